@@ -202,7 +202,7 @@ def prepare(c, seed):
         def buffers(fill):
             if not c["flat"]:
                 return [fill(n, DT[k]) for n, k in kinds]
-            flat = {k: fill(sum(n for n, kk in kinds if kk == k), DT[k]) for k in {k for _, k in kinds}}
+            flat = {k: fill(sum(n for n, kk in kinds if kk == k), DT[k]) for k in sorted({k for _, k in kinds})}
             at, views = {k: 0 for k in flat}, []
             for n, k in kinds:
                 views.append(flat[k][at[k]: at[k] + n])
