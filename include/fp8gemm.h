@@ -18,6 +18,9 @@
  *   backward (e5m2 gradients)
  *                  fp8_quantize_1x128_e5m2, fp8_gemm_nt_dgrad, fp8_grouped_gemm_contiguous_dgrad,
  *                  fp8_grouped_gemm_wgrad
+ *   training operators around the grouped GEMMs (bf16 / fp32)
+ *                  fp8g_layer_norm, fp8g_layer_norm_backward, fp8g_moe_gate, fp8g_moe_gate_backward,
+ *                  fp8g_moe_combine, fp8g_moe_combine_backward, fp8g_grad_norm, fp8g_clip_grad_norm
  *   status         fp8g_get_status, fp8g_status_string, fp8g_selftest_bounded_waits, fp8g_last_config,
  *                  fp8g_last_split, fp8g_last_swap_ab, fp8g_last_cluster_k
  *
@@ -389,6 +392,154 @@ int fp8_grouped_gemm_contiguous_dgrad(const void* A, const float* sA, int64_t ld
 int fp8_grouped_gemm_wgrad(const void* A, int64_t lda, const float* sA, int64_t ld_sa, const void* B,
                            int64_t ldb, const float* sB, int64_t ld_sb, void* D, const int32_t* offsets,
                            int32_t E, int64_t M, int64_t N, int64_t T, void* stream);
+
+/*
+ * Training operators around the grouped GEMMs: the norm before a MoE block, the gate that chooses the
+ * experts, the combine that brings the experts' rows back to their tokens, the gradients of all three, and the
+ * global gradient norm with clipping.  Tensors are bf16 or fp32 (an fp8g_dtype each); every sum, softmax
+ * and statistic is fp32, and a bf16 result is rounded once, at the end.  Results do not depend on the order in
+ * which CTAs run: two calls on the same inputs give the same bits.  Where a call needs scratch memory, its
+ * _workspace function (host only, no device needed) gives the bytes and the caller passes a buffer of at least
+ * that size, 16-byte aligned, free to be reused once the stream has passed the call.
+ */
+typedef enum { FP8G_BF16 = 0, FP8G_F32 = 1 } fp8g_dtype;
+
+/*
+ * fp8g_layer_norm -- for every row m of x:
+ *     mean[m] = sum_n x / N,  rstd[m] = 1 / sqrt(sum_n (x - mean)^2 / N + eps),
+ *     y[m, n] = (x[m, n] - mean[m]) * rstd[m] * weight[n] + bias[n]
+ *
+ *   x       [M, N], row stride ldx elements (ldx >= N)
+ *   weight, bias  [N], both of type w_dtype; either may be null (1 and 0)
+ *   y       [M, N], row stride ldy elements (ldy >= N); may be x itself when the types are the same
+ *   mean, rstd  fp32 [M], for the backward call; either may be null
+ *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31, eps >= 0.  Pointers aligned to their element; rows that are
+ *   16-byte aligned (base and stride) and N a multiple of 8 take the faster paths.
+ */
+int fp8g_layer_norm(const void* x, int32_t x_dtype, int64_t M, int64_t N, int64_t ldx, const void* weight,
+                    const void* bias, int32_t w_dtype, float eps, void* y, int32_t y_dtype, int64_t ldy,
+                    float* mean, float* rstd, void* stream);
+
+/* fp8g_layer_norm_backward_workspace -- scratch bytes of fp8g_layer_norm_backward with dweight or dbias. */
+int fp8g_layer_norm_backward_workspace(int64_t M, int64_t N, int64_t* bytes);
+
+/*
+ * fp8g_layer_norm_backward -- with h = (x - mean) * rstd and g = dy * weight:
+ *     dx = rstd * (g - sum_n g / N - h * sum_n (g * h) / N),  dweight = sum_m dy * h,  dbias = sum_m dy
+ *
+ *   dy      [M, N] (dy_dtype), x and dx [M, N] (x_dtype), row strides lddy, ldx, lddx >= N.  dx may not
+ *           overlap x or dy.
+ *   weight  [N] (w_dtype) or null; mean, rstd  fp32 [M], as fp8g_layer_norm wrote them
+ *   dweight, dbias  fp32 [N], overwritten (M == 0: zeros); either may be null.  Where both are, no workspace is
+ *           needed and it may be null.
+ *   Sizes and alignment as fp8g_layer_norm.
+ */
+int fp8g_layer_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x, int32_t x_dtype,
+                             int64_t ldx, const void* weight, int32_t w_dtype, const float* mean,
+                             const float* rstd, int64_t M, int64_t N, void* dx, int64_t lddx, float* dweight,
+                             float* dbias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* fp8g_moe_gate_workspace -- scratch bytes of fp8g_moe_gate. */
+int fp8g_moe_gate_workspace(int64_t T, int32_t E, int64_t* bytes);
+
+/*
+ * fp8g_moe_gate -- the router: softmax over the experts, the topk best, per-expert counts and the balance loss.
+ *     p[t] = softmax(logits[t]);  topk_ids[t] = the topk largest logits of the row, in descending order, ties to the
+ *     lower index;  topk_weights[t, j] = p[t, topk_ids[t, j]], divided by their sum over j if renormalize
+ *     counts[e] = how many (t, j) of the unmasked tokens chose e;  Tv = how many tokens are unmasked
+ *     loss = loss_coef * E * sum_e (counts[e] / (topk * Tv)) * (sum over unmasked t of p[t, e]) / Tv
+ * (1 * loss_coef for a uniform choice; 0 when no token is unmasked).
+ *
+ *   logits      [T, E] (dtype), row stride ldl elements (ldl >= E).  -inf rules an expert out: it has p = 0 and is
+ *               taken, with weight 0, only where fewer than topk others are left.  A row of nothing but -inf has
+ *               p = 0 everywhere and the ids 0 .. topk-1.  A NaN makes its row's weights NaN and ranks first, so
+ *               the ids stay in range.
+ *   token_mask  bytes [T] or null: 0 = a padding token.  It gets ids like any other (the routed layout needs them in
+ *               range) and weights 0, and is left out of counts and loss whatever its logits hold.
+ *   topk_ids    int32 [T, topk], topk_weights fp32 [T, topk], counts int32 [E], loss fp32 [1] or null
+ *   0 <= T < 2^31 (T == 0: counts and loss are zeros), 1 <= E <= 2048, 1 <= topk <= min(E, 32),
+ *   T * topk < 2^31, renormalize 0 or 1.  Pointers aligned to their element.
+ */
+int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl, int32_t topk,
+                  int32_t renormalize, const uint8_t* token_mask, float loss_coef, int32_t* topk_ids,
+                  float* topk_weights, int32_t* counts, float* loss, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/*
+ * fp8g_moe_gate_backward -- the gradient of topk_weights and loss with respect to the logits (the choice and the
+ * counts are held fixed):
+ *     G[t, e] = dloss * loss_coef * E * counts[e] / (topk * Tv^2) + sum_j [topk_ids[t, j] == e] dp[t, j]
+ *     dp[t, j] = dweights[t, j], or (dweights[t, j] - sum_i dweights[t, i] * w[t, i]) / sum_i p[t, topk_ids[t, i]]
+ *     if renormalize;   dlogits[t, e] = p[t, e] * (G[t, e] - sum_e' G[t, e'] * p[t, e'])
+ *
+ *   logits, dtype, T, E, ldl, topk, renormalize, token_mask, loss_coef, topk_ids, counts  as in the forward call
+ *   (Tv is the sum of counts over topk).  Masked tokens get zeros.  Ids outside [0, E) have no gradient.
+ *   dweights  fp32 [T, topk] or null (0);  dloss  fp32 [1], device memory, or null (0)
+ *   dlogits   [T, E] (dtype), row stride ldd >= E; may be logits itself
+ */
+int fp8g_moe_gate_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl, int32_t topk,
+                           int32_t renormalize, const uint8_t* token_mask, float loss_coef,
+                           const int32_t* topk_ids, const int32_t* counts, const float* dweights,
+                           const float* dloss, void* dlogits, int64_t ldd, void* stream);
+
+/*
+ * fp8g_moe_combine -- the experts' rows back to their tokens:
+ *     out[t] = residual[t] + sum_j weights[t, j] * D[entry_row[t, j]]
+ *
+ *   D          bf16 [M, N], row stride ldd elements: a grouped GEMM's output in the routed layout
+ *   entry_row  int32 [T, topk], as fp8_route_gather_quantize_1x128 writes it; a negative row is a dropped entry and
+ *              adds nothing, a row >= M is left out and sets FP8G_ERR_DEVICE_ASSERT
+ *   weights    fp32 [T, topk] or null (1: the plain sum, which is the gradient of the gather)
+ *   residual   [T, N] of out's type, row stride ldr, or null; may be out itself
+ *   out        [T, N] (out_dtype), row stride ldo
+ *   0 <= M, T < 2^31 (T == 0: no-op), T * topk < 2^31, N % 8 == 0.  D, residual, out 16-byte aligned, their
+ *   strides multiples of 8 elements and at least N.
+ */
+int fp8g_moe_combine(const void* D, int64_t M, int64_t N, int64_t ldd, const int32_t* entry_row, int64_t T,
+                     int32_t topk, const float* weights, const void* residual, int64_t ldr, void* out,
+                     int32_t out_dtype, int64_t ldo, void* stream);
+
+/*
+ * fp8g_moe_combine_backward -- dD[entry_row[t, j]] = weights[t, j] * dout[t],
+ * dweights[t, j] = sum_n dout[t, n] * D[entry_row[t, j], n] (0 for a dropped entry); rows with row_token < 0 (padding,
+ * and past the last group) get zeros, so that dD can be quantised and multiplied like any activation.
+ *
+ *   dout       [T, N] (dout_dtype), row stride lddo;  D as in the forward call (null if dweights is)
+ *   entry_row, row_token  int32 [T, topk] and [M], as fp8_route_gather_quantize_1x128 writes them
+ *   weights    fp32 [T, topk] or null (1);  dD  bf16 [M, N], row stride lddd;  dweights  fp32 [T, topk] or null
+ *   Sizes, alignment and out-of-range rows as fp8g_moe_combine.  dD may not overlap D or dout.
+ */
+int fp8g_moe_combine_backward(const void* dout, int32_t dout_dtype, int64_t lddo, const void* D, int64_t M,
+                              int64_t N, int64_t ldd, const int32_t* entry_row, const int32_t* row_token, int64_t T,
+                              int32_t topk, const float* weights, void* dD, int64_t lddd, float* dweights,
+                              void* stream);
+
+/* fp8g_grad_norm_workspace -- scratch bytes of fp8g_grad_norm and fp8g_clip_grad_norm for n tensors. */
+int fp8g_grad_norm_workspace(int32_t n, int64_t* bytes);
+
+/*
+ * fp8g_grad_norm -- norm[0] = sqrt(sum over all n tensors of g^2).
+ *
+ *   grads, numels, dtypes  HOST arrays of n: each tensor's device address, its number of (contiguous) values and its
+ *           fp8g_dtype.  Read during the call only; they travel as kernel arguments, so a captured graph keeps
+ *           the addresses it was captured with.  Empty tensors may be null.
+ *   norm    fp32 [1], device memory
+ *   0 <= n <= 2^20, at most 2^42 values together.  Pointers aligned to their element.  Squares are summed in fp32:
+ *   values beyond about 1.8e19 give an infinite norm.
+ */
+int fp8g_grad_norm(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, float* norm,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8g_clip_grad_norm -- norm as fp8g_grad_norm, and out = grad * min(1, max_norm / (norm + eps)) for every tensor.
+ *
+ *   outs    HOST array of n device addresses, each of its gradient's size and type: either the gradient itself (in
+ *           place, where nothing is written if nothing needs scaling) or memory that overlaps no gradient
+ *   max_norm >= 0, eps >= 0.  A NaN norm makes every output NaN, an infinite one makes finite values 0.
+ */
+int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,
+                        int32_t n, float max_norm, float eps, float* norm, void* workspace,
+                        int64_t workspace_bytes, void* stream);
 
 /*
  * fp8g_get_status -- synchronise `stream`, then return and clear the current

@@ -20,6 +20,10 @@ functions here carry the same names and take torch tensors:
     fp8_grouped_gemm_contiguous_dgrad(A, sA, B, sB, D, group_offsets)   grouped data gradient
     fp8_grouped_gemm_wgrad(A, sA, B, sB, D, offsets)   weight gradient per expert over its tokens
 
+The training operators around the grouped GEMMs, on bf16 and fp32 tensors (``block_ops.py``): ``layer_norm``,
+``moe_gate`` (top-k, counts and balance loss), ``moe_combine``, their ``_backward`` calls, ``grad_norm`` and
+``clip_grad_norm``.
+
 e4m3 tensors may be torch.uint8 or torch.float8_e4m3fn.  Work is enqueued on the
 current CUDA stream of the tensors' device.  A non-zero status raises Fp8GemmError.
 Convenience wrappers (``quantize_1x128``, ``quantize_128x128``, ``gemm_nt``) allocate
@@ -53,7 +57,7 @@ class Fp8GemmError(RuntimeError):
 
 _lib = None
 
-_I64, _I32, _P, _FP = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p
+_I64, _I32, _P, _FP, _F32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float
 _SIGNATURES = {
     "fp8_quantize_1x128": [_P, _I64, _I64, _I64, _P, _I64, _FP, _I64, _P],
     "fp8_quantize_128x128": [_P, _I64, _I64, _I64, _P, _FP, _P],
@@ -73,6 +77,18 @@ _SIGNATURES = {
     "fp8_gemm_nt_dgrad": [_P, _I64, _FP, _I64, _P, _I64, _FP, _P, _I64, _I64, _I64, _I64, _P],
     "fp8_grouped_gemm_contiguous_dgrad": [_P, _FP, _I64, _P, _FP, _P, _P, _I32, _I64, _I64, _I64, _P],
     "fp8_grouped_gemm_wgrad": [_P, _I64, _FP, _I64, _P, _I64, _FP, _I64, _P, _P, _I32, _I64, _I64, _I64, _P],
+    "fp8g_layer_norm": [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _F32, _P, _I32, _I64, _FP, _FP, _P],
+    "fp8g_layer_norm_backward_workspace": [_I64, _I64, ctypes.POINTER(ctypes.c_int64)],
+    "fp8g_layer_norm_backward": [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _FP, _FP, _I64, _I64, _P, _I64, _FP, _FP,
+                                 _P, _I64, _P],
+    "fp8g_moe_gate_workspace": [_I64, _I32, ctypes.POINTER(ctypes.c_int64)],
+    "fp8g_moe_gate": [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _F32, _P, _FP, _P, _FP, _P, _I64, _P],
+    "fp8g_moe_gate_backward": [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _F32, _P, _P, _FP, _FP, _P, _I64, _P],
+    "fp8g_moe_combine": [_P, _I64, _I64, _I64, _P, _I64, _I32, _FP, _P, _I64, _P, _I32, _I64, _P],
+    "fp8g_moe_combine_backward": [_P, _I32, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I32, _FP, _P, _I64, _FP, _P],
+    "fp8g_grad_norm_workspace": [_I32, ctypes.POINTER(ctypes.c_int64)],
+    "fp8g_grad_norm": [_P, _P, _P, _I32, _FP, _P, _I64, _P],
+    "fp8g_clip_grad_norm": [_P, _P, _P, _P, _I32, _F32, _F32, _FP, _P, _I64, _P],
     "fp8g_selftest_bounded_waits": [_I64, _P, _P],
     "fp8g_get_status": [_P],
     "fp8g_last_config": [ctypes.POINTER(ctypes.c_int)] * 3,
@@ -528,3 +544,11 @@ def gemm_nt_scaled(A, sA, B, sB) -> torch.Tensor:
     D = torch.empty((A.shape[0], B.shape[0]), dtype=torch.bfloat16, device=A.device)
     fp8_gemm_nt_scaled(A, sA, B, sB, D)
     return D
+
+
+# ------------------------------------------------------------------ training operators (bf16 / fp32)
+
+from .block_ops import (  # noqa: E402 -- they use the helpers above
+    GradList, clip_grad_norm, fp8g_clip_grad_norm, fp8g_grad_norm, fp8g_layer_norm, fp8g_layer_norm_backward,
+    fp8g_moe_combine, fp8g_moe_combine_backward, fp8g_moe_gate, fp8g_moe_gate_backward, grad_norm, layer_norm,
+    layer_norm_backward, moe_combine, moe_combine_backward, moe_gate, moe_gate_backward)

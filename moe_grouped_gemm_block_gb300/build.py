@@ -20,7 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfp8gemm.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "noalloc.cu", "norm.cu", "moe.cu", "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -21,6 +21,8 @@ Modules:
   e5m2      -- the e5m2 (OCP "E5M2") codec for gradients
   backward  -- 1x128 e5m2 gradient quantisation, the data-gradient GEMM (e5m2 x e4m3) and the
                K-grouped weight-gradient GEMM of a grouped MoE layer
+  block_ops -- layer norm, the MoE gate with its balance loss, the combine, their gradients and
+               gradient clipping, in float64
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 invariants, brute force on tiny inputs and library routines; none is "parity
 unpinned".

@@ -1,0 +1,214 @@
+"""The training operators' argument checks, in the library (before anything is launched) and in the binding; and the
+calls that have nothing to do.  No GPU needed."""
+
+import ctypes
+
+import pytest
+import torch
+
+import moe_grouped_gemm_block_gb300 as g
+
+INVALID, ALIGN = 1, 2
+P = 1 << 20  # an aligned fake device address, never dereferenced
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return g.lib()
+
+
+def _args(defaults, kw):
+    assert set(kw) <= set(defaults)
+    return tuple({**defaults, **kw}.values())
+
+
+NORM = dict(x=P, xd=0, M=4, N=64, ldx=64, w=P, b=P, wd=1, eps=1e-5, y=P, yd=0, ldy=64, mean=P, rstd=P, s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xd=2), INVALID), (dict(yd=-1), INVALID), (dict(wd=7), INVALID), (dict(M=-1), INVALID), (dict(N=0), INVALID),
+    (dict(ldx=63), INVALID), (dict(ldy=63), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(M=1 << 31), INVALID),
+    (dict(x=P + 1), ALIGN), (dict(w=P + 2), ALIGN), (dict(mean=P + 2), ALIGN), (dict(y=P + 2, yd=1), ALIGN),
+    (dict(M=0, x=None, y=None), 0),
+])
+def test_layer_norm(lib, kw, want):
+    assert lib.fp8g_layer_norm(*_args(NORM, kw)) == want
+
+
+NORM_BWD = dict(dy=P, yd=0, lddy=64, x=P, xd=0, ldx=64, w=P, wd=1, mean=P, rstd=P, M=4, N=64, dx=P, lddx=64, dw=P,
+                db=P, ws=P, wsb=BIG, s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(yd=3), INVALID), (dict(lddy=8), INVALID), (dict(lddx=8), INVALID), (dict(mean=None), INVALID),
+    (dict(dx=None), INVALID), (dict(ws=None), INVALID), (dict(wsb=16), INVALID), (dict(M=-1), INVALID),
+    (dict(ws=P + 8), ALIGN), (dict(dw=P + 1), ALIGN), (dict(dx=P + 1), ALIGN),
+    (dict(M=0, dy=None, x=None, mean=None, rstd=None, dx=None, dw=None, db=None, ws=None), 0),
+])
+def test_layer_norm_backward(lib, kw, want):
+    assert lib.fp8g_layer_norm_backward(*_args(NORM_BWD, kw)) == want
+
+
+GATE = dict(l=P, d=1, T=4, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, w=P, counts=P, loss=P, ws=P, wsb=BIG,
+            s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(d=2), INVALID), (dict(E=0), INVALID), (dict(E=2049, ldl=2049), INVALID), (dict(ldl=7), INVALID),
+    (dict(k=0), INVALID), (dict(k=9), INVALID), (dict(E=64, ldl=64, k=33), INVALID), (dict(renorm=2), INVALID),
+    (dict(T=-1), INVALID), (dict(T=(1 << 31) - 1, k=8), INVALID), (dict(counts=None), INVALID),
+    (dict(ids=None), INVALID), (dict(ws=None), INVALID), (dict(wsb=8), INVALID),
+    (dict(ids=P + 2), ALIGN), (dict(l=P + 2), ALIGN), (dict(ws=P + 4), ALIGN),
+])
+def test_gate(lib, kw, want):
+    assert lib.fp8g_moe_gate(*_args(GATE, kw)) == want
+
+
+GATE_BWD = dict(l=P, d=1, T=4, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, counts=P, dw=P, dloss=P, dl=P,
+                ldd=8, s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(d=2), INVALID), (dict(ldd=7), INVALID), (dict(k=9), INVALID), (dict(ids=None), INVALID),
+    (dict(dl=None), INVALID), (dict(dl=P + 2), ALIGN), (dict(dw=P + 1), ALIGN), (dict(T=0, l=None, dl=None), 0),
+])
+def test_gate_backward(lib, kw, want):
+    assert lib.fp8g_moe_gate_backward(*_args(GATE_BWD, kw)) == want
+
+
+COMBINE = dict(D=P, M=128, N=64, ldd=64, rows=P, T=4, k=2, w=P, res=None, ldr=0, out=P, od=0, ldo=64, s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(N=60, ldd=64, ldo=64), INVALID), (dict(ldd=56), INVALID), (dict(ldo=56), INVALID), (dict(k=0), INVALID),
+    (dict(od=5), INVALID), (dict(D=None), INVALID), (dict(rows=None), INVALID), (dict(res=P, ldr=32), INVALID),
+    (dict(M=-1), INVALID), (dict(T=1 << 30, k=4), INVALID),
+    (dict(D=P + 8), ALIGN), (dict(out=P + 2), ALIGN), (dict(ldd=68), ALIGN), (dict(res=P + 4, ldr=64), ALIGN),
+    (dict(T=0, D=None, out=None, rows=None), 0),
+])
+def test_combine(lib, kw, want):
+    assert lib.fp8g_moe_combine(*_args(COMBINE, kw)) == want
+
+
+COMBINE_BWD = dict(dout=P, dd=0, lddo=64, D=P, M=128, N=64, ldd=64, rows=P, tokens=P, T=4, k=2, w=P, dD=P, lddd=64,
+                   dw=P, s=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(N=60), INVALID), (dict(lddd=56), INVALID), (dict(lddo=56), INVALID), (dict(tokens=None), INVALID),
+    (dict(D=None), INVALID), (dict(dD=None), INVALID), (dict(dout=None), INVALID), (dict(dd=2), INVALID),
+    (dict(dD=P + 8), ALIGN), (dict(lddo=68), ALIGN), (dict(dw=P + 2), ALIGN),
+    (dict(M=0, T=0, dout=None, D=None, dD=None, rows=None, tokens=None), 0),
+])
+def test_combine_backward(lib, kw, want):
+    assert lib.fp8g_moe_combine_backward(*_args(COMBINE_BWD, kw)) == want
+
+
+def _clip(lib, ptrs=(P, P), numels=(8, 8), dtypes=(1, 0), outs=(P, P), max_norm=1.0, eps=1e-6, norm=P, ws=P, wsb=BIG):
+    n = len(numels)
+    return lib.fp8g_clip_grad_norm((ctypes.c_void_p * n)(*ptrs), (ctypes.c_void_p * n)(*outs),
+                                   (ctypes.c_int64 * n)(*numels), (ctypes.c_int32 * n)(*dtypes), n, max_norm, eps, norm,
+                                   ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(numels=(8, -1)), INVALID), (dict(dtypes=(1, 2)), INVALID), (dict(ptrs=(P, None)), INVALID),
+    (dict(outs=(None, P)), INVALID), (dict(max_norm=-1.0), INVALID), (dict(max_norm=float("nan")), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(norm=None), INVALID), (dict(ws=None), INVALID), (dict(wsb=64), INVALID),
+    (dict(numels=(1 << 42, 1)), INVALID),
+    (dict(ptrs=(P + 2, P)), ALIGN), (dict(outs=(P, P + 1)), ALIGN), (dict(ws=P + 4), ALIGN), (dict(norm=P + 1), ALIGN),
+])
+def test_clip(lib, kw, want):
+    assert _clip(lib, **kw) == want
+
+
+def test_null_tables(lib):
+    assert lib.fp8g_grad_norm(None, None, None, 2, P, P, BIG, None) == INVALID
+    assert lib.fp8g_grad_norm(None, None, None, -1, P, P, BIG, None) == INVALID
+    assert lib.fp8g_grad_norm_workspace(4, None) == INVALID
+    assert lib.fp8g_moe_gate_workspace(4, 0, ctypes.byref(ctypes.c_int64())) == INVALID
+    assert lib.fp8g_layer_norm_backward_workspace(4, 0, ctypes.byref(ctypes.c_int64())) == INVALID
+
+
+def test_valid_arguments_without_a_gpu_report_an_error(lib):
+    if torch.cuda.is_available():
+        pytest.skip("GPU present: covered by the GPU tests")
+    for name, args in (("fp8g_layer_norm", NORM), ("fp8g_layer_norm_backward", NORM_BWD), ("fp8g_moe_gate", GATE),
+                       ("fp8g_moe_gate_backward", GATE_BWD), ("fp8g_moe_combine", COMBINE),
+                       ("fp8g_moe_combine_backward", COMBINE_BWD)):
+        assert getattr(lib, name)(*args.values()) in (3, 4), name
+    assert _clip(lib) in (3, 4)
+
+
+# ---- the binding: ValueError before the library is called
+
+def _f32(*shape):
+    return torch.zeros(shape)
+
+
+def _bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_binding_layer_norm():
+    with pytest.raises(ValueError, match="x: bf16 or f32"):
+        g.layer_norm(torch.zeros(4, 8, dtype=torch.float16))
+    with pytest.raises(ValueError, match="weight"):
+        g.layer_norm(_f32(4, 8), _f32(7))
+    with pytest.raises(ValueError, match="one type"):
+        g.layer_norm(_f32(4, 8), _f32(8), _bf16(8))
+    with pytest.raises(ValueError, match="rows contiguous"):
+        g.layer_norm(_f32(8, 4).t())
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        g.layer_norm(_f32(4, 8), _f32(8), _f32(8))
+    with pytest.raises(ValueError, match="mean"):
+        g.layer_norm_backward(_f32(4, 8), _f32(4, 8), _f32(8), _f32(3), _f32(4))
+    with pytest.raises(ValueError, match="x's shape"):
+        g.layer_norm_backward(_f32(4, 7), _f32(4, 8), _f32(8), _f32(4), _f32(4))
+
+
+def test_binding_gate():
+    with pytest.raises(ValueError, match="logits"):
+        g.moe_gate(torch.zeros(4, 8, dtype=torch.float64), 2)
+    with pytest.raises(ValueError, match="token_mask"):
+        g.moe_gate(_f32(4, 8), 2, token_mask=torch.ones(3, dtype=torch.bool))
+    with pytest.raises(ValueError, match="topk_ids"):
+        g.fp8g_moe_gate(_f32(4, 8), 2, _i32(4, 3), _f32(4, 2), _i32(8))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        g.moe_gate(_f32(4, 8), 2)
+    with pytest.raises(ValueError, match="counts"):
+        g.moe_gate_backward(_f32(4, 8), _i32(4, 2), _i32(7), _f32(4, 2))
+    with pytest.raises(ValueError, match="dweights"):
+        g.moe_gate_backward(_f32(4, 8), _i32(4, 2), _i32(8), _f32(4, 3))
+
+
+def test_binding_combine():
+    with pytest.raises(ValueError, match="D: bf16"):
+        g.moe_combine(_f32(128, 64), _i32(4, 2), _f32(4, 2), out_dtype=torch.float32)
+    with pytest.raises(ValueError, match="weights"):
+        g.moe_combine(_bf16(128, 64), _i32(4, 2), _f32(4, 3))
+    with pytest.raises(ValueError, match="residual"):
+        g.moe_combine(_bf16(128, 64), _i32(4, 2), _f32(4, 2), residual=_f32(4, 32))
+    with pytest.raises(ValueError, match="row_token"):
+        g.moe_combine_backward(_bf16(4, 64), _bf16(128, 64), _i32(4, 2), _i32(64), _f32(4, 2))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        g.moe_combine(_bf16(128, 64), _i32(4, 2), _f32(4, 2))
+
+
+def test_binding_clip():
+    with pytest.raises(ValueError, match="at least one"):
+        g.clip_grad_norm([], 1.0)
+    with pytest.raises(ValueError, match="contiguous"):
+        g.clip_grad_norm([_f32(4, 8).t()], 1.0)
+    with pytest.raises(ValueError, match="bf16 or f32"):
+        g.grad_norm([torch.zeros(4, dtype=torch.float64)])
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        g.clip_grad_norm([_f32(8)], 1.0)
+    with pytest.raises(ValueError, match="a tensor for each"):
+        g.GradList([_f32(8)], [])
