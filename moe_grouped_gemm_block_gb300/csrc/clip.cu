@@ -2,39 +2,47 @@
 //
 //     norm = sqrt(sum over all tensors of g^2),   out = g min(1, max_norm / (norm + eps))
 //
-// The tensors' addresses, sizes and types travel as kernel arguments (up to kClipCap tensors a launch), so
-// nothing is copied to the device and a call can be captured into a graph.  Each tensor is cut into chunks;
-// a CTA works through the chunks blockIdx.x, blockIdx.x + gridDim.x, ...  Sums of squares are fp32 within a
-// CTA and fp64 over the CTAs, in a fixed order.
+// Two passes over the data, both bound by memory: one reads everything and leaves a partial sum per CTA, the
+// other sums those (each CTA all of them, in the same order), reads everything again and writes it scaled.  The
+// tensors' addresses, sizes and types travel as kernel arguments (up to kClipCap tensors a launch), so nothing is
+// copied to the device and a call can be captured into a graph.
+//
+// Every tensor is cut into chunks of kClipGroups 16-byte groups on the 16-byte grid of its addresses, whatever its own
+// alignment: only a tensor's first and last group can be partial, and those are taken value by value.
 
 #include <algorithm>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace fp8g {
 namespace {
 
 constexpr int kClipThreads = 256;
+constexpr int kClipUnroll = 8;       // 16-byte loads in flight per thread
+constexpr int kClipGroups = kClipThreads * kClipUnroll;
 constexpr int kClipCap = 1024;       // tensors a launch
+constexpr int kClipSmallCap = 64;    // tensors a launch with the small table (2 KB of arguments instead of 30)
 constexpr int kClipMaxCtas = 608;    // partial sums a launch
-constexpr int64_t kClipChunk = 8192; // values a chunk
 constexpr int32_t kClipMaxTensors = 1 << 20;
 constexpr int64_t kClipMaxValues = int64_t{1} << 42;  // of all tensors together
 
+template <int CAP>
 struct ClipTable {
-  const void* grad[kClipCap];
-  void* out[kClipCap];
-  int64_t numel[kClipCap];
-  uint32_t end[kClipCap];  // chunks of the tensors up to and with this one
-  uint8_t dtype[kClipCap];
+  const void* grad[CAP];
+  void* out[CAP];
+  int64_t numel[CAP];
+  uint32_t end[CAP];  // chunks of the tensors up to and with this one
+  uint8_t dtype[CAP];
   int32_t n;
 };
-static_assert(sizeof(ClipTable) <= 32000, "kernel arguments hold 32764 bytes");
+static_assert(sizeof(ClipTable<kClipCap>) <= 32000, "kernel arguments hold 32764 bytes");
 
 // The tensor that chunk c belongs to.
-__device__ __forceinline__ int find_tensor(const ClipTable& t, uint32_t c) {
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const ClipTable<CAP>& t, uint32_t c) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -44,19 +52,86 @@ __device__ __forceinline__ int find_tensor(const ClipTable& t, uint32_t c) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __grid_constant__ ClipTable t,
+// A chunk of tensor i: values [lo, hi) of the tensor; the value at lo + k lies k values after a 16-byte boundary
+// (lo is negative in a first chunk whose tensor does not start on one).
+template <typename T>
+struct Chunk {
+  static constexpr int kPer = 16 / sizeof(T);  // values a group
+  const T* g;
+  T* o;
+  int64_t lo, hi, numel;
+  bool whole;
+  template <int CAP>
+  __device__ __forceinline__ Chunk(const ClipTable<CAP>& t, int i, uint32_t c) {
+    g = static_cast<const T*>(t.grad[i]);
+    o = static_cast<T*>(t.out[i]);
+    numel = t.numel[i];
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(T));
+    lo = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * (kClipGroups * kPer) - mis;
+    hi = min(lo + kClipGroups * kPer, numel);
+    whole = lo >= 0 && hi == lo + kClipGroups * kPer;
+  }
+};
+
+__device__ __forceinline__ float square_sum(const uint4& v, float) {
+  const float a = __uint_as_float(v.x), b = __uint_as_float(v.y), c = __uint_as_float(v.z), d = __uint_as_float(v.w);
+  return (a * a + b * b) + (c * c + d * d);
+}
+__device__ __forceinline__ float square_sum(const uint4& v, __nv_bfloat16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
+    s[0] = fmaf(a, a, s[0]);
+    s[1] = fmaf(b, b, s[1]);
+  }
+  return s[0] + s[1];
+}
+
+// A thread's share of a chunk's sum of squares: its eight groups' sums, joined in a tree.
+template <typename T, int CAP>
+__device__ __forceinline__ float chunk_square_sum(const ClipTable<CAP>& t, int i, uint32_t c) {
+  const Chunk<T> ch(t, i, c);
+  float s[kClipUnroll] = {};
+  if (ch.whole) {
+    const uint4* p = reinterpret_cast<const uint4*>(ch.g + ch.lo) + threadIdx.x;
+    uint4 v[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) v[u] = __ldg(p + u * kClipThreads);
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) s[u] = square_sum(v[u], T());
+  } else {
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+      const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * Chunk<T>::kPer;
+      if (k >= 0 && k + Chunk<T>::kPer <= ch.hi) {
+        s[u] = square_sum(__ldg(reinterpret_cast<const uint4*>(ch.g + k)), T());
+      } else {
+        for (int64_t q = max(k, int64_t{0}); q < min(k + Chunk<T>::kPer, ch.hi); ++q) {
+          const float f = to_f32(ch.g[q]);
+          s[u] = fmaf(f, f, s[u]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kClipUnroll; d *= 2)
+#pragma unroll
+    for (int u = 0; u + d < kClipUnroll; u += 2 * d) s[u] += s[u + d];
+  return s[0];
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __grid_constant__ ClipTable<CAP> t,
                                                                       float* __restrict__ parts) {
   __shared__ float red[2 * kClipThreads / 32];
+  griddep_launch_dependents();  // the scaling pass may start (it waits for this grid's sums)
   float s[1] = {0.0f};
   const uint32_t chunks = t.end[t.n - 1];
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = find_tensor(t, c);
-    const int64_t lo = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * kClipChunk;
-    const int64_t hi = min(lo + kClipChunk, t.numel[i]);
-    for (int64_t k = lo + threadIdx.x; k < hi; k += kClipThreads) {
-      const float v = load_any(t.grad[i], t.dtype[i], k);
-      s[0] += v * v;
-    }
+    s[0] += t.dtype[i] == FP8G_F32 ? chunk_square_sum<float>(t, i, c) : chunk_square_sum<__nv_bfloat16>(t, i, c);
   }
   cta_sum<kClipThreads / 32>(s, red, 0);
   if (threadIdx.x == 0) parts[blockIdx.x] = s[0];
@@ -82,37 +157,77 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_join_kernel(const floa
   if (threadIdx.x == 0) *norm = n;
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_constant__ ClipTable t,
+__device__ __forceinline__ uint4 scaled(const uint4& v, float c, float) {
+  return make_uint4(__float_as_uint(__uint_as_float(v.x) * c), __float_as_uint(__uint_as_float(v.y) * c),
+                    __float_as_uint(__uint_as_float(v.z) * c), __float_as_uint(__uint_as_float(v.w) * c));
+}
+__device__ __forceinline__ uint32_t scaled2(uint32_t w, float c) {
+  return pack2(__uint_as_float(w << 16) * c, __uint_as_float(w & 0xFFFF0000u) * c);
+}
+__device__ __forceinline__ uint4 scaled(const uint4& v, float c, __nv_bfloat16) {
+  return make_uint4(scaled2(v.x, c), scaled2(v.y, c), scaled2(v.z, c), scaled2(v.w, c));
+}
+
+template <typename T, int CAP>
+__device__ __forceinline__ void chunk_scale(const ClipTable<CAP>& t, int i, uint32_t c, float coef) {
+  const Chunk<T> ch(t, i, c);
+  // 16-byte stores where the result's groups lie on its own 16-byte grid too
+  const bool same = ((reinterpret_cast<uintptr_t>(ch.g) ^ reinterpret_cast<uintptr_t>(ch.o)) & 15u) == 0;
+  if (ch.whole && same) {
+    const uint4* p = reinterpret_cast<const uint4*>(ch.g + ch.lo) + threadIdx.x;
+    uint4* q = reinterpret_cast<uint4*>(ch.o + ch.lo) + threadIdx.x;
+    uint4 v[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) v[u] = __ldcs(p + u * kClipThreads);
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) __stcs(q + u * kClipThreads, scaled(v[u], coef, T()));
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kClipUnroll; ++u) {
+    const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * Chunk<T>::kPer;
+    if (same && k >= 0 && k + Chunk<T>::kPer <= ch.hi) {
+      *reinterpret_cast<uint4*>(ch.o + k) = scaled(*reinterpret_cast<const uint4*>(ch.g + k), coef, T());
+    } else {
+      for (int64_t q = max(k, int64_t{0}); q < min(k + Chunk<T>::kPer, ch.hi); ++q)
+        ch.o[q] = from_f32<T>(to_f32(ch.g[q]) * coef);
+    }
+  }
+}
+
+// The chunks in descending order: the first pass ended with the last ones, so some of them are still in L2.
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_constant__ ClipTable<CAP> t,
                                                                  const float* __restrict__ parts, int32_t P,
                                                                  float max_norm, float eps,
                                                                  float* __restrict__ norm) {
+  griddep_wait();
   const float n = join_norm(parts, P);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = n;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float coef = n + eps <= max_norm ? 1.0f : max_norm / (n + eps);  // a NaN norm makes every output NaN
   const uint32_t chunks = t.end[t.n - 1];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const uint32_t c = chunks - 1 - b;
     const int i = find_tensor(t, c);
     if (coef == 1.0f && t.out[i] == t.grad[i]) continue;  // in place and nothing to scale
-    const int64_t lo = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * kClipChunk;
-    const int64_t hi = min(lo + kClipChunk, t.numel[i]);
-    for (int64_t k = lo + threadIdx.x; k < hi; k += kClipThreads) {
-      const float v = load_any(t.grad[i], t.dtype[i], k) * coef;
-      if (t.dtype[i] == FP8G_F32) static_cast<float*>(t.out[i])[k] = v;
-      else static_cast<__nv_bfloat16*>(t.out[i])[k] = __float2bfloat16_rn(v);
-    }
+    if (t.dtype[i] == FP8G_F32) chunk_scale<float>(t, i, c, coef);
+    else chunk_scale<__nv_bfloat16>(t, i, c, coef);
   }
 }
 
 // Fills one launch's table from the tensors first, first + 1, ...; empty tensors are left out.  Returns the
 // tensor after the last one taken.  (check_tensors bounds the chunks of all tensors together below 2^31.)
-int32_t fill_table(ClipTable& t, const void* const* grads, void* const* outs, const int64_t* numels,
+template <int CAP>
+int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
                    const int32_t* dtypes, int32_t first, int32_t n) {
   t.n = 0;
   uint64_t chunks = 0;
   int32_t i = first;
-  for (; i < n && t.n < kClipCap; ++i) {
+  for (; i < n && t.n < CAP; ++i) {
     if (numels[i] == 0) continue;
-    chunks += static_cast<uint64_t>((numels[i] + kClipChunk - 1) / kClipChunk);
+    const int64_t size = dtypes[i] == FP8G_F32 ? 4 : 2, per = kClipGroups * (16 / size);
+    const int64_t mis = static_cast<int64_t>(reinterpret_cast<uintptr_t>(grads[i]) & 15u) / size;
+    chunks += static_cast<uint64_t>((numels[i] + mis + per - 1) / per);
     t.grad[t.n] = grads[i];
     t.out[t.n] = outs ? outs[i] : nullptr;
     t.numel[t.n] = numels[i];
@@ -143,18 +258,62 @@ int check_tensors(const void* const* grads, void* const* outs, const int64_t* nu
 }
 
 // Partial sums of all the tensors; *P is how many were written.
-int norm_parts_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
-                      float* parts, int32_t* P, cudaStream_t s) {
+template <int CAP>
+int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
+                      const int32_t* dtypes, int32_t n, float* parts, int32_t* P, cudaStream_t s) {
   *P = 0;
-  ClipTable t;
   for (int32_t i = 0; i < n;) {
-    i = fill_table(t, grads, nullptr, numels, dtypes, i, n);
+    i = fill_table(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
     const uint32_t ctas = std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas);
-    grad_norm_part_kernel<<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
+    grad_norm_part_kernel<CAP><<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
     *P += static_cast<int32_t>(ctas);
   }
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+template <int CAP>
+int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, float* norm,
+                     float* parts, cudaStream_t s) {
+  ClipTable<CAP> t;
+  int32_t P = 0;
+  const int st = norm_parts_launch(t, grads, nullptr, numels, dtypes, n, parts, &P, s);
+  if (st != FP8G_OK) return st;
+  grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, P, norm);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+template <int CAP>
+int clip_launch(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes, int32_t n,
+                float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
+  ClipTable<CAP> t;
+  int32_t P = 0;
+  const int st = norm_parts_launch(t, grads, outs, numels, dtypes, n, parts, &P, s);
+  if (st != FP8G_OK) return st;
+  if (P == 0) {  // no values at all
+    grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, 0, norm);
+    return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  }
+  const bool one = n <= CAP;  // then the table is already the whole one
+  for (int32_t i = 0; i < n;) {
+    i = one ? n : fill_table(t, grads, outs, numels, dtypes, i, n);
+    if (t.n == 0) continue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas));
+    cfg.blockDim = dim3(kClipThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = one ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<CAP>, t, static_cast<const float*>(parts), P, max_norm, eps, norm) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return FP8G_ERR_CUDA;
+    }
+  }
+  return FP8G_OK;
 }
 
 }  // namespace
@@ -178,13 +337,8 @@ extern "C" int fp8g_grad_norm(const void* const* grads, const int64_t* numels, c
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* parts = static_cast<float*>(workspace);
-  int32_t P = 0;
-  st = norm_parts_launch(grads, numels, dtypes, n, parts, &P, s);
-  if (st != FP8G_OK) return st;
-  grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, P, norm);
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  auto go = n <= kClipSmallCap ? grad_norm_launch<kClipSmallCap> : grad_norm_launch<kClipCap>;
+  return go(grads, numels, dtypes, n, norm, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
@@ -199,21 +353,7 @@ extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, 
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* parts = static_cast<float*>(workspace);
-  int32_t P = 0;
-  st = norm_parts_launch(grads, numels, dtypes, n, parts, &P, s);
-  if (st != FP8G_OK) return st;
-  if (P == 0) {  // no values at all
-    grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, 0, norm);
-    return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
-  }
-  ClipTable t;
-  for (int32_t i = 0; i < n;) {
-    i = fill_table(t, grads, outs, numels, dtypes, i, n);
-    if (t.n == 0) continue;
-    const uint32_t ctas = std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas);
-    grad_clip_kernel<<<ctas, kClipThreads, 0, s>>>(t, parts, P, max_norm, eps, norm);
-  }
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  auto go = n <= kClipSmallCap ? clip_launch<kClipSmallCap> : clip_launch<kClipCap>;
+  return go(grads, outs, numels, dtypes, n, max_norm, eps, norm, static_cast<float*>(workspace),
+            static_cast<cudaStream_t>(stream));
 }
