@@ -138,10 +138,10 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_join_kernel(
 // (S_t = the selected probabilities' sum).  Masked tokens get zeros.  One warp a row.
 template <typename TL>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(
-    const TL* __restrict__ logits, int64_t T, int32_t E, int64_t ldl, int32_t topk, int32_t renorm,
+    const TL* logits, int64_t T, int32_t E, int64_t ldl, int32_t topk, int32_t renorm,
     const uint8_t* __restrict__ mask, float coef, const int32_t* __restrict__ ids,
     const int32_t* __restrict__ counts, const float* __restrict__ dweights, const float* __restrict__ dloss,
-    TL* __restrict__ dlogits, int64_t ldd) {
+    TL* dlogits, int64_t ldd) {
   extern __shared__ float smem[];
   __shared__ float red[2 * kGateWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -227,8 +227,8 @@ __device__ __forceinline__ int32_t entry(const int32_t* __restrict__ entry_row, 
 template <typename TO>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
     const __nv_bfloat16* __restrict__ D, int64_t M, int64_t N, int64_t ldd, const int32_t* __restrict__ entry_row,
-    int32_t topk, const float* __restrict__ weights, const TO* __restrict__ residual, int64_t ldr,
-    TO* __restrict__ out, int64_t ldo, unsigned int* status) {
+    int32_t topk, const float* __restrict__ weights, const TO* residual, int64_t ldr,
+    TO* out, int64_t ldo, unsigned int* status) {
   const int64_t t = blockIdx.x;
   for (int64_t n = threadIdx.x * 8; n < N; n += kCombineThreads * 8) {
     float acc[8] = {};

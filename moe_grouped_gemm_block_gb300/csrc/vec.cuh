@@ -20,10 +20,10 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// A value of a tensor whose type is known only at run time (uniform over the launch).
-__device__ __forceinline__ float load_any(const void* p, int32_t dtype, int64_t i) {
-  return dtype == FP8G_F32 ? static_cast<const float*>(p)[i]
-                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// A value of a tensor that the kernel only reads and whose type is known only at run time (bit 0 of `kind`).
+__device__ __forceinline__ float load_any(const void* p, int32_t kind, int64_t i) {
+  return kind & FP8G_F32 ? __ldg(static_cast<const float*>(p) + i)
+                         : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
 }
 
 // Eight values at a time, 16-byte aligned.
