@@ -531,14 +531,24 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_grad_ring_kernel(c
   const float inv_n = 1.0f / static_cast<float>(a.N);
   int s = 0;
   uint32_t parity = 0;
-  float nmu = a.mean[blockIdx.x], nr = a.rstd[blockIdx.x];
+  // the statistics of 32 rows at a time, one row a lane (loaded 32 rows ahead: no row waits for them)
+  const int lane = tid & 31;
+  float mu32 = 0.0f, r32 = 0.0f, next_mu = 0.0f, next_r = 0.0f;
+  auto stats = [&](int64_t i) {
+    if (i + lane >= rows) return;
+    next_mu = a.mean[blockIdx.x + (i + lane) * P];
+    next_r = a.rstd[blockIdx.x + (i + lane) * P];
+  };
+  stats(0);
   for (int64_t i = 0; i < rows; ++i) {
     const int64_t m = blockIdx.x + i * P;
-    const float mu = nmu, r = nr;
-    if (i + 1 < rows) {
-      nmu = a.mean[m + P];
-      nr = a.rstd[m + P];
+    if ((i & 31) == 0) {
+      mu32 = next_mu;
+      r32 = next_r;
+      stats(i + 32);
     }
+    const float mu = __shfl_sync(0xffffffffu, mu32, static_cast<int>(i & 31));
+    const float r = __shfl_sync(0xffffffffu, r32, static_cast<int>(i & 31));
     ring_wait(smem_u32(&full_bar[s]), parity, a, &s_dead);
     const uint8_t* stage = ring + static_cast<size_t>(s) * (xb + yb);
     GradPairs p[NV];
@@ -682,33 +692,35 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_dw_any_kernel(
   parts[p * 2 * N + N + n] = db;
 }
 
-// dw and db (either may be null) from the P partial rows [2][N].  A CTA takes 32 columns, its 8 warps an eighth of
-// the rows each: the additions' order follows from P alone.
-constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ parts, int32_t P,
-                                                                          int64_t N, float* __restrict__ dw,
-                                                                          float* __restrict__ db) {
-  __shared__ float sums[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// dw and db (either may be null) from the P partial rows [2][N].  A CTA takes 32 columns, its warps an equal share of
+// the rows each: the additions' order follows from P alone.  The sums are short and the rows' addresses far apart, so
+// the time is the loads' latency: eight in flight per lane, and many warps (P = 152, N = 7168: 6.3 us with 8 warps).
+constexpr int kJoinMaxWarps = 32;
+constexpr int kJoinUnroll = 8;
+__global__ void __launch_bounds__(32 * kJoinMaxWarps) layer_norm_join_kernel(const float* __restrict__ parts, int32_t P,
+                                                                             int64_t N, float* __restrict__ dw,
+                                                                             float* __restrict__ db) {
+  __shared__ float sums[kJoinMaxWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   griddep_wait();
-  const int lo = static_cast<int>(static_cast<int64_t>(P) * warp / kJoinWarps);
-  const int hi = static_cast<int>(static_cast<int64_t>(P) * (warp + 1) / kJoinWarps);
-  float s[4] = {};
+  const int lo = static_cast<int>(static_cast<int64_t>(P) * warp / warps);
+  const int hi = static_cast<int>(static_cast<int64_t>(P) * (warp + 1) / warps);
+  float s = 0.0f;
   if (i < 2 * N) {
-    const float* p = parts + lo * 2 * N + i;
-    int k = lo;
-    for (; k + 4 <= hi; k += 4, p += 8 * N)
+    for (int k = lo; k < hi; k += kJoinUnroll) {
+      float v[kJoinUnroll];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) s[u] += __ldcg(p + u * 2 * N);
-    for (; k < hi; ++k, p += 2 * N) s[0] += __ldcg(p);
+      for (int u = 0; u < kJoinUnroll; ++u)
+        v[u] = k + u < hi ? __ldcg(parts + static_cast<int64_t>(k + u) * 2 * N + i) : 0.0f;
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
   }
-  sums[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || i >= 2 * N) return;
   float t = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) t += sums[w][lane];
+  for (int w = 0; w < warps; ++w) t += sums[w][lane];
   if (i < N) {
     if (dw) dw[i] = t;
   } else if (db) {
@@ -839,7 +851,8 @@ int layer_norm_backward_launch(NormGrad a, float* dw, float* db, const DeviceInf
   if (!a.parts) return FP8G_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((2 * N + 31) / 32));
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.blockDim = dim3(32 * static_cast<unsigned>(std::min<int64_t>(
+                                kJoinMaxWarps, (P + kJoinUnroll - 1) / kJoinUnroll)));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
