@@ -7,17 +7,21 @@
 // All sums are taken in fp32; the variance is the mean of the squared differences from the mean
 // (a second pass over the row), not the difference of two large sums.
 //
-// Forms, by the row's length and alignment (rows on 16-byte boundaries whose length is a multiple of 8 go in
-// vectors of 8 values):
+// Forms, by the row's length (rows go in vectors of 8 values on the 16-byte grid, see RowShape):
 //   warp     up to 1024 values: a row (or 2, 4 at once) per warp, all in registers, no barriers
-//   cta      longer rows: a CTA per row, the row in registers
-//   ring     longer rows, backward: one resident CTA walks over its rows, which bulk copies bring into a ring of
-//            shared-memory stages ahead of it; the weight gradients' sums stay in its registers
-//   scalar   rows off the 16-byte grid: a CTA per row (backward: resident), value by value in registers
+//   ring     longer rows: resident CTAs (clusters of two beyond 8192 values) walk over their rows, which bulk copies
+//            bring into a ring of shared-memory stages ahead of them; some warps form a row's sums, the others the
+//            results, with the weights and (backward) the weight gradients' sums in registers
+//   cta      forward, rows longer than the ring takes: a CTA per row, the row in registers
+//   scalar   rows that share no grid: a CTA per row (backward: resident), value by value in registers
 //   any      rows longer than those hold
+// The form follows from N, the types and the alignment alone, never from M: a row's result does not depend on how
+// many rows the call has.  (A CTA per row with all its threads on the sums, for few rows, would save less than a
+// microsecond of the kernel: 64 x 7168 bf16.)
 
 #include <algorithm>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -38,6 +42,21 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void load_stream(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // value j by value j from memory where the mask has it, zero elsewhere
+  __device__ __forceinline__ void gather(const __nv_bfloat16* p, uint32_t mask) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = mask >> j & 1u ? h[j] : 0u;
+    v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  // keeps the values that the mask has, zeroes the others
+  __device__ __forceinline__ void keep(uint32_t mask) {
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] &= (mask >> (2 * j) & 1u ? 0xFFFFu : 0u) | (mask >> (2 * j + 1) & 1u ? 0xFFFF0000u : 0u);
+  }
   __device__ __forceinline__ void get(float2 (&f)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -56,6 +75,19 @@ struct Raw8<float> {
     b = __ldcs(reinterpret_cast<const float4*>(p + 4));
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void gather(const float* p, uint32_t mask) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = mask >> j & 1u ? p[j] : 0.0f;
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  __device__ __forceinline__ void keep(uint32_t mask) {
+    a.x = mask & 1u ? a.x : 0.0f, a.y = mask & 2u ? a.y : 0.0f;
+    a.z = mask & 4u ? a.z : 0.0f, a.w = mask & 8u ? a.w : 0.0f;
+    b.x = mask & 16u ? b.x : 0.0f, b.y = mask & 32u ? b.y : 0.0f;
+    b.z = mask & 64u ? b.z : 0.0f, b.w = mask & 128u ? b.w : 0.0f;
+  }
   __device__ __forceinline__ void get(float2 (&f)[4]) const {
     f[0] = make_float2(a.x, a.y);
     f[1] = make_float2(a.z, a.w);
@@ -73,14 +105,62 @@ __device__ __forceinline__ void store_pairs(float* p, const float2 (&f)[4]) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Eight weights (or biases) from column n on (a multiple of 8); `fill` where there are none.  w_kind: the type, and
-// kWeightVectors where the weights lie on 16-byte boundaries.
-constexpr int32_t kWeightVectors = 2;
-__device__ __forceinline__ void weights8(const void* w, int32_t w_kind, int64_t n, float fill, float2 (&f)[4]) {
-  if (!w) {
+// How a row falls into vectors of 8.  Where every row starts on the grid of its matrix's 8-value groups (SHIFT
+// false), vector v holds columns 8 v .. 8 v + 7.  Else row m starts q = (m ld) mod 8 values after a group's start and
+// vector v holds columns 8 v - q ..: its first and last vectors reach into the neighbouring rows, whose values are
+// left out.  q repeats every 8 rows, so a thread that steps by multiples of 8 rows keeps its columns, and with
+// them its weights and its sums of the weight gradients.  Every matrix of a call has the same q (the host checks).
+template <bool SHIFT>
+struct RowShape {
+  int N, q;
+  __device__ __forceinline__ RowShape(int n, int64_t m, int64_t ld)
+      : N(n), q(SHIFT ? static_cast<int>((m & 7) * (ld & 7)) & 7 : 0) {}
+  __device__ __forceinline__ int vectors() const { return (N + q + 7) >> 3; }
+  __device__ __forceinline__ int col(int v) const { return 8 * v - q; }
+  // The columns of vector v that exist, a bit each.
+  __device__ __forceinline__ uint32_t mask(int v) const {
+    const int c = col(v);
+    if (!SHIFT) return c < N ? 0xFFu : 0u;
+    uint32_t k = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = both(fill);
-  } else if (w_kind == (FP8G_F32 | kWeightVectors)) {
+    for (int j = 0; j < 8; ++j) k |= (c + j >= 0 && c + j < N ? 1u : 0u) << j;
+    return k;
+  }
+};
+
+// The values of a vector that the mask has.
+template <typename T>
+__device__ __forceinline__ void store_masked(T* p, const float2 (&f)[4], uint32_t mask) {
+  if (mask == 0xFFu) {
+    store_pairs(p, f);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (mask >> j & 1u) p[j] = from_f32<T>(j & 1 ? f[j / 2].y : f[j / 2].x);
+}
+
+// A vector of a row, read once: 16-byte loads where all of it may be read (`inside`: it lies within its matrix,
+// neighbouring rows included), value by value where it would reach past the matrix's end.
+template <typename T>
+__device__ __forceinline__ void load_vector(Raw8<T>& r, const T* p, uint32_t mask, bool inside) {
+  if (mask == 0xFFu || (mask && inside)) {
+    r.load_stream(p);
+    if (mask != 0xFFu) r.keep(mask);
+  } else {
+    r.gather(p, mask);
+  }
+}
+
+// Eight weights (or biases) from column n on, where the mask has them; `fill` where there are none.  w_kind: the
+// type, and kWeightVectors where the weights lie on 16-byte boundaries (and n is a multiple of 8).
+constexpr int32_t kWeightVectors = 2;
+__device__ __forceinline__ void weights8(const void* w, int32_t w_kind, int n, uint32_t mask, float fill,
+                                         float2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = both(fill);
+  if (!w || !mask) return;
+  if (w_kind == (FP8G_F32 | kWeightVectors)) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + n);
     const float4 a = __ldg(p), b = __ldg(p + 1);
     f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
@@ -91,7 +171,10 @@ __device__ __forceinline__ void weights8(const void* w, int32_t w_kind, int64_t 
     r.get(f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float2(load_any(w, w_kind, n + 2 * i), load_any(w, w_kind, n + 2 * i + 1));
+    for (int i = 0; i < 4; ++i) {
+      if (mask >> (2 * i) & 1u) f[i].x = load_any(w, w_kind, n + 2 * i);
+      if (mask >> (2 * i + 1) & 1u) f[i].y = load_any(w, w_kind, n + 2 * i + 1);
+    }
   }
 }
 
@@ -122,18 +205,20 @@ __device__ __forceinline__ float block_sum(float v, float2 (*red)[32], int phase
   return warp_sum(lane < warps ? red[phase & 1][lane].x : 0.0f);
 }
 
-// The sum of (x - mu)^2 over NV vectors, without the vectors past the row's end.
+// The sum of (x - mu)^2 over the existing values of NV vectors.
 template <typename T, int NV>
-__device__ __forceinline__ float spread_sum(const Raw8<T> (&raw)[NV], const bool (&live)[NV], float mu) {
+__device__ __forceinline__ float spread_sum(const Raw8<T> (&raw)[NV], const uint32_t (&mask)[NV], float mu) {
   float2 s = both(0.0f);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (!live[v]) continue;
+    if (!mask[v]) continue;
     float2 f[4];
     raw[v].get(f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 d = __fadd2_rn(f[i], both(-mu));
+      float2 d = __fadd2_rn(f[i], both(-mu));
+      if (mask[v] != 0xFFu)
+        d = make_float2(mask[v] >> (2 * i) & 1u ? d.x : 0.0f, mask[v] >> (2 * i + 1) & 1u ? d.y : 0.0f);
       s = __ffma2_rn(d, d, s);
     }
   }
@@ -151,105 +236,459 @@ __device__ __forceinline__ float value_sum(const Raw8<T> (&raw)[NV]) {
   return s.x + s.y;
 }
 
-// ---------------------------------------------------------------- forward
-// (y may be x itself: a row is read before it is written)
-// warp form: LPR lanes a row, lane l of a row holds the vectors l, l + LPR, ...
-template <typename TX, typename TY, int LPR, int NV>
-__global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(
-    const TX* x, int64_t M, int32_t N, int64_t ldx, const void* __restrict__ w,
-    const void* __restrict__ b, int32_t w_kind, float eps, TY* y, int64_t ldy,
-    float* __restrict__ mean, float* __restrict__ rstd) {
-  constexpr int kRows = kNormThreads / LPR;  // rows a CTA at once
-  const int sub = threadIdx.x % LPR;
-  bool live[NV];
-  float2 wf[NV][4], bf[NV][4];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int col = (v * LPR + sub) * 8;
-    live[v] = col < N;
-    if (live[v]) {
-      weights8(w, w_kind, col, 1.0f, wf[v]);
-      weights8(b, w_kind, col, 0.0f, bf[v]);
+// ---------------------------------------------------------------- the ring of row stages
+// Roles of a CTA's warps: column warps own kRingVecs vectors a thread of every row, sum warps take whole rows in
+// turn and form their sums, one thread of the last warp issues the copies.  A row's stage goes full (its copies have
+// landed) -> ready (its sums are in `slot`) -> empty (every column warp has read it); nothing else orders the warps,
+// so the latencies of one row's sums lie under the columns' work on others.  (With all warps of the CTA taking
+// a row together, sums through a barrier, a row cost about 2000 cycles of latency: 4096 x 7168 bf16 rows took 42 us
+// forward and 43 us backward, and 29 and 36 us with two to four rows at a time.)
+constexpr int kRingMaxStages = 16;
+constexpr int kRingVecs = 2;
+constexpr int kRingMaxColumnWarps = 16;
+constexpr int kRingMaxSumWarps = 3;
+constexpr int kRingMaxThreads = 32 * (kRingMaxColumnWarps + kRingMaxSumWarps + 1);  // 20 warps: 96 registers a thread
+
+struct RingShared {
+  uint64_t full[kRingMaxStages], ready[kRingMaxStages], empty[kRingMaxStages];
+  float4 slot[kRingMaxStages][2];  // a row's sums from each CTA of the cluster
+  int dead;
+};
+
+// Waits for a barrier's phase, at most `budget` cycles; past that it records the status and nobody in the CTA waits
+// any more (the results are void, the kernel ends).  CLUSTER: what the other CTA wrote before it arrived is seen too.
+template <bool CLUSTER = false>
+__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity, long long budget, unsigned int* status,
+                                          volatile int* dead) {
+  const uint32_t b = smem_u32(bar);
+  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity); };
+  if (done()) return;
+  const long long t0 = clock64();
+  while (!done()) {
+    if (*dead) return;
+    if (clock64() - t0 > budget) {
+      *dead = 1;
+      record_status(status, FP8G_ERR_TIMEOUT);
+      return;
     }
   }
-  const float inv_n = 1.0f / static_cast<float>(N);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// This CTA's share of every row: the vectors first .. first + count - 1 of the row's.
+struct Share {
+  int first, count;
+  template <bool SHIFT>
+  __device__ __forceinline__ Share(const RowShape<SHIFT>& shape, int rank, int ranks) {
+    const int all = shape.vectors(), each = (all + ranks - 1) / ranks;
+    first = rank * each;
+    count = min(each, all - first);
+  }
+};
+
+// The vectors of the share that a stage's copy holds: a last row's last vector may reach past the matrix, and is left
+// out (the threads that need it read its values themselves).
+template <bool SHIFT>
+__device__ __forceinline__ int copied(const RowShape<SHIFT>& shape, const Share& sh, bool last_row) {
+  const bool past = SHIFT && last_row && (shape.N + shape.q) % 8 != 0 && sh.first + sh.count == shape.vectors();
+  return sh.count - (past ? 1 : 0);
+}
+// Vector v of the share from its stage; the values that do not exist are zero.
+template <bool SHIFT, typename T>
+__device__ __forceinline__ void stage_vector(Raw8<T>& r, const T* stage, int v, uint32_t mask, bool last_row,
+                                             const T* row) {
+  if (SHIFT && mask != 0xFFu && last_row) {
+    r.gather(row + v * 8, mask);  // row: the share's first vector in memory
+  } else {
+    r.load(stage + v * 8);
+    if (SHIFT && mask != 0xFFu) r.keep(mask);
+  }
+}
+
+// The vectors of a share that are whole in every row; off the grid its first and last one may not be.  (A ring's rows
+// have more than 64 vectors a share.)
+template <bool SHIFT>
+struct Inner {
+  int lo, hi;
+  __device__ __forceinline__ Inner(const Share& sh) : lo(SHIFT ? 1 : 0), hi(sh.count - (SHIFT ? 1 : 0)) {}
+};
+constexpr int kSumUnroll = 4;  // vectors in flight per lane of a sum warp
+
+// The rows of sum warp w: those in the stages w, w + warps, ... in every round, so that it sees each round of its
+// stages' barriers (a wait tells the round only by its parity).
+struct SumRows {
+  int stage, round, w, warps, stages;
+  __device__ __forceinline__ SumRows(int w_, int warps_, int stages_)
+      : stage(w_), round(0), w(w_), warps(warps_), stages(stages_) {}
+  __device__ __forceinline__ int64_t row() const { return static_cast<int64_t>(round) * stages + stage; }
+  __device__ __forceinline__ void next() {
+    stage += warps;
+    if (stage >= stages) {
+      stage = w;
+      ++round;
+    }
+  }
+};
+
+template <int CL>
+__device__ __forceinline__ void ring_init(RingShared& sm, int stages, int column_warps) {
+  if (threadIdx.x == 0) {
+    sm.dead = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.ready[s]), CL);
+      mbar_init(smem_u32(&sm.empty[s]), CL * column_warps);
+    }
+    fence_mbar_init();
+  }
+}
+
+// The copying thread: row after row into the ring, each stage once it is empty.  `load` copies row i into stage s and
+// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.
+template <typename Load>
+__device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, bool cluster, long long budget,
+                                            unsigned int* status, Load load) {
+  int s = 0, i = 0;
+  uint32_t parity = 1;  // the first round of `empty` counts as complete
+  for (; i < rows; ++i) {
+    if (i >= stages) {
+      if (cluster) ring_wait<true>(&sm.empty[s], parity, budget, status, &sm.dead);
+      else ring_wait<false>(&sm.empty[s], parity, budget, status, &sm.dead);
+      if (*const_cast<volatile int*>(&sm.dead)) break;
+    }
+    load(i, s);
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+  if (!*const_cast<volatile int*>(&sm.dead)) return;
+  const long long t0 = clock64();
+  for (int k = max(0, i - stages); k < i; ++k)
+    while (!mbar_try_wait(smem_u32(&sm.full[k % stages]), (k / stages) & 1) && clock64() - t0 <= budget) {
+    }
+}
+
+// A sum warp hands its row on: the sums to every CTA of the cluster, then the arrival.
+template <int CL>
+__device__ __forceinline__ void ring_ready(RingShared& sm, int s, int rank, float4 v) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (CL == 1) {
+    if (lane == 0) {
+      sm.slot[s][0] = v;
+      mbar_arrive(smem_u32(&sm.ready[s]));
+    }
+  } else if (lane < CL) {
+    st_cluster4(mapa_shared(smem_u32(&sm.slot[s][rank]), lane), v);
+    mbar_arrive_cluster(mapa_shared(smem_u32(&sm.ready[s]), lane));
+  }
+}
+// A column warp has read the stage and the slot.
+template <int CL>
+__device__ __forceinline__ void ring_empty(RingShared& sm, int s) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if constexpr (CL == 1) {
+    if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
+  } else {
+    if (lane < CL) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.empty[s]), lane));
+  }
+}
+
+// ---------------------------------------------------------------- forward
+// (y may be x itself: a row is read before it is written)
+struct NormArgs {
+  const void* x;
+  void* y;
+  const void* w;
+  const void* b;
+  float* mean;  // mean and rstd may be null
+  float* rstd;
+  int64_t M, ldx, ldy;
+  int32_t N, w_kind;
+  float eps;
+  unsigned int* status;
+  long long budget;
+};
+
+__device__ __forceinline__ void norm_vector(float2 (&f)[4], float mu, float r, const float2 (&w)[4],
+                                            const float2 (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i], both(-mu)), both(r)), w[i], b[i]);
+}
+
+// warp form: LPR lanes a row, lane l of a row holds the vectors l, l + LPR, ...  The next row is on its way while one
+// is worked on.
+template <typename TX, typename TY, int LPR, int NV, bool SHIFT>
+__global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const NormArgs a) {
+  constexpr int kRows = kNormThreads / LPR;  // rows a CTA at once: a multiple of 8
+  const int sub = threadIdx.x % LPR;
+  const TX* x = static_cast<const TX*>(a.x);
+  TY* y = static_cast<TY*>(a.y);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   // the loop runs for whole warps (m0 is the warp's first row): the sums are taken by all its lanes
   int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + (threadIdx.x & ~31) / LPR;
   const int64_t off = (threadIdx.x & 31) / LPR;
+  const RowShape<SHIFT> shape(a.N, m0 + off, a.ldx);
+  uint32_t mask[NV];
+  float2 wf[NV][4], bf[NV][4];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    mask[v] = shape.mask(v * LPR + sub);
+    weights8(a.w, a.w_kind, shape.col(v * LPR + sub), mask[v], 1.0f, wf[v]);
+    weights8(a.b, a.w_kind, shape.col(v * LPR + sub), mask[v], 0.0f, bf[v]);
+  }
+  const float inv_n = 1.0f / static_cast<float>(a.N);
   Raw8<TX> next[NV];
   auto fetch = [&](int64_t m) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (live[v] && m < M) next[v].load_stream(x + m * ldx + (v * LPR + sub) * 8);
-      else next[v].zero();
-    }
+    for (int v = 0; v < NV; ++v)
+      load_vector(next[v], x + m * a.ldx + shape.col(v * LPR + sub), m < a.M ? mask[v] : 0u, m + 1 < a.M);
   };
   fetch(m0 + off);
-  for (; m0 < M; m0 += stride) {
+  for (; m0 < a.M; m0 += stride) {
     const int64_t m = m0 + off;
     Raw8<TX> raw[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) raw[v] = next[v];
-    if (m0 + stride < M) fetch(m + stride);
+    if (m0 + stride < a.M) fetch(m + stride);
     const float mu = lanes_sum<LPR>(value_sum(raw)) * inv_n;
-    const float var = lanes_sum<LPR>(spread_sum(raw, live, mu)) * inv_n;
-    const float r = 1.0f / sqrtf(var + eps);
-    if (m >= M) continue;
+    const float var = lanes_sum<LPR>(spread_sum(raw, mask, mu)) * inv_n;
+    const float r = 1.0f / sqrtf(var + a.eps);
+    if (m >= a.M) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!live[v]) continue;
+      if (!mask[v]) continue;
       float2 f[4];
       raw[v].get(f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i], both(-mu)), both(r)), wf[v][i], bf[v][i]);
-      store_pairs(y + m * ldy + (v * LPR + sub) * 8, f);
+      norm_vector(f, mu, r, wf[v], bf[v]);
+      store_masked(y + m * a.ldy + shape.col(v * LPR + sub), f, mask[v]);
     }
     if (sub == 0) {
-      if (mean) mean[m] = mu;
-      if (rstd) rstd[m] = r;
+      if (a.mean) a.mean[m] = mu;
+      if (a.rstd) a.rstd[m] = r;
     }
   }
 }
 
-// cta form: thread t holds the vectors t, t + blockDim.x, ...
-template <typename TX, typename TY, int NV>
-__global__ void __launch_bounds__(1024) layer_norm_cta_kernel(
-    const TX* x, int32_t N, int64_t ldx, const void* __restrict__ w, const void* __restrict__ b,
-    int32_t w_kind, float eps, TY* y, int64_t ldy, float* __restrict__ mean,
-    float* __restrict__ rstd) {
-  __shared__ float2 red[2][32];
+// The sums of a warp's values: their sum and, about their own mean, their squared differences.  `count`: the values
+// that the warp holds.
+template <typename T, int NV>
+__device__ __forceinline__ float2 warp_moments(const Raw8<T> (&raw)[NV], const uint32_t (&mask)[NV], float inv_count) {
+  const float s = warp_sum(value_sum(raw));
+  return make_float2(s, warp_sum(spread_sum(raw, mask, s * inv_count)));
+}
+// A row's mean and 1 / sqrt(variance + eps) from its warps' sums, lane i holding warp i's: the squared differences
+// about the row's mean are those about each warp's own plus count (difference of the means)^2.
+__device__ __forceinline__ float2 join_moments(float2 v, float count, float inv_count, float inv_n, float eps) {
+  const float mu = warp_sum(v.x) * inv_n;
+  const float d = v.x * inv_count - mu;
+  const float var = warp_sum(fmaf(count * d, d, v.y)) * inv_n;
+  return make_float2(mu, 1.0f / sqrtf(var + eps));
+}
+// The values that the calling warp's masks have.
+template <int NV>
+__device__ __forceinline__ int warp_count(const uint32_t (&mask)[NV]) {
+  int n = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) n += __popc(mask[v]);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// cta form: a CTA a row, thread t holds the vectors t, t + blockDim.x, ...
+template <typename TX, typename TY, int NV, bool SHIFT>
+__global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) {
+  __shared__ float2 red[32];
+  __shared__ float cnt[32];
   const int64_t m = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+  const RowShape<SHIFT> shape(a.N, m, a.ldx);
   Raw8<TX> raw[NV];
-  bool live[NV];
+  uint32_t mask[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int col = (v * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-    live[v] = col < N;
-    if (live[v]) raw[v].load_stream(x + m * ldx + col);
-    else raw[v].zero();
+    const int i = v * threads + static_cast<int>(threadIdx.x);
+    mask[v] = shape.mask(i);
+    load_vector(raw[v], static_cast<const TX*>(a.x) + m * a.ldx + shape.col(i), mask[v], m + 1 < a.M);
   }
-  const float inv_n = 1.0f / static_cast<float>(N);
-  const float mu = block_sum(value_sum(raw), red, 0) * inv_n;
-  const float var = block_sum(spread_sum(raw, live, mu), red, 1) * inv_n;
-  const float r = 1.0f / sqrtf(var + eps);
+  const int n = warp_count(mask);
+  const float2 own = warp_moments(raw, mask, n ? 1.0f / static_cast<float>(n) : 0.0f);
+  if (lane == 0) {
+    red[warp] = own;
+    cnt[warp] = static_cast<float>(n);
+  }
+  __syncthreads();
+  const bool in = lane < threads / 32;
+  const float c = in ? cnt[lane] : 0.0f;
+  const float2 st = join_moments(in ? red[lane] : both(0.0f), c, c > 0.0f ? 1.0f / c : 0.0f,
+                                 1.0f / static_cast<float>(a.N), a.eps);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (!live[v]) continue;
-    const int col = (v * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+    if (!mask[v]) continue;
+    const int col = shape.col(v * threads + static_cast<int>(threadIdx.x));
     float2 f[4], wf[4], bf[4];
-    weights8(w, w_kind, col, 1.0f, wf);
-    weights8(b, w_kind, col, 0.0f, bf);
+    weights8(a.w, a.w_kind, col, mask[v], 1.0f, wf);
+    weights8(a.b, a.w_kind, col, mask[v], 0.0f, bf);
     raw[v].get(f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i], both(-mu)), both(r)), wf[i], bf[i]);
-    store_pairs(y + m * ldy + col, f);
+    norm_vector(f, st.x, st.y, wf, bf);
+    store_masked(static_cast<TY*>(a.y) + m * a.ldy + col, f, mask[v]);
   }
   if (threadIdx.x == 0) {
-    if (mean) mean[m] = mu;
-    if (rstd) rstd[m] = r;
+    if (a.mean) a.mean[m] = st.x;
+    if (a.rstd) a.rstd[m] = st.y;
   }
+}
+
+// ring form.  A sum warp takes the differences from K, the mean of 256 values at the row's start (of its CTA's share):
+// variance = mean (x - K)^2 - (mean (x - K))^2 then loses little to cancellation, as (K - mean)^2 is at most N / 256
+// variances whatever the values.
+template <typename TX, typename TY, int CL, bool SHIFT>
+__global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_ring_kernel(const NormArgs a, int32_t stages,
+                                                                             int32_t stage_bytes, int32_t column_warps,
+                                                                             int32_t sum_warps) {
+  constexpr int NV = kRingVecs;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ RingShared sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, columns = column_warps * 32;
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int P = static_cast<int>(gridDim.x) / CL, first = static_cast<int>(blockIdx.x) / CL;
+  const int rows = static_cast<int>((a.M - first + P - 1) / P);  // rows first, first + P, ...
+  const RowShape<SHIFT> shape(a.N, first, a.ldx);
+  const Share share(shape, rank, CL);
+  const TX* x = static_cast<const TX*>(a.x) + shape.col(share.first);
+  ring_init<CL>(sm, stages, column_warps);
+  if constexpr (CL == 1) __syncthreads();
+  else cluster_sync();  // every CTA of the cluster runs before it is written to
+  if (warp == column_warps + sum_warps) {
+    if (lane == 0)
+      ring_copies(sm, rows, stages, CL > 1, a.budget, a.status, [&](int i, int s) {
+        const int64_t m = first + static_cast<int64_t>(i) * P;
+        const uint32_t bar = smem_u32(&sm.full[s]);
+        const uint32_t bytes = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8 * sizeof(TX);
+        mbar_arrive_expect_tx(true, bar, bytes);
+        if (bytes) bulk_load(smem_u32(ring) + s * stage_bytes, x + m * a.ldx, bytes, bar);
+      });
+  } else if (warp >= column_warps) {
+    // the values that the share holds
+    const int held = min(a.N, shape.col(share.first + share.count)) - max(0, shape.col(share.first));
+    const float n = static_cast<float>(held), inv_n = 1.0f / n;
+    for (SumRows it(warp - column_warps, sum_warps, stages); it.row() < rows; it.next()) {
+      const int s = it.stage;
+      const int64_t m = first + it.row() * P;
+      ring_wait(&sm.full[s], it.round & 1, a.budget, a.status, &sm.dead);
+      const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
+      const Inner<SHIFT> in(share);
+      float2 f[4], d1 = both(0.0f), d2 = both(0.0f), e1 = both(0.0f), e2 = both(0.0f);
+      Raw8<TX> r[kSumUnroll];
+      r[0].load(stage + (in.lo + lane) * 8);
+      r[0].get(f);
+      const float2 t = __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3]));
+      const float K = warp_sum(t.x + t.y) * (1.0f / 256.0f);
+      auto add = [&](const Raw8<TX>& raw) {
+        raw.get(f);
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float2 p = __fadd2_rn(f[k], both(-K)), q = __fadd2_rn(f[k + 1], both(-K));
+          d1 = __fadd2_rn(d1, p);
+          d2 = __ffma2_rn(p, p, d2);
+          e1 = __fadd2_rn(e1, q);
+          e2 = __ffma2_rn(q, q, e2);
+        }
+      };
+      int v = in.lo + lane;
+      for (; v + 32 * (kSumUnroll - 1) < in.hi; v += 32 * kSumUnroll) {
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) r[u].load(stage + (v + 32 * u) * 8);
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) add(r[u]);
+      }
+      for (; v < in.hi; v += 32) {
+        r[0].load(stage + v * 8);
+        add(r[0]);
+      }
+      if (SHIFT && lane < 2) {  // the first and the last vector
+        v = lane == 0 ? 0 : share.count - 1;
+        const uint32_t mask = shape.mask(share.first + v);
+        stage_vector<SHIFT>(r[0], stage, v, mask, m + 1 == a.M, x + m * a.ldx);
+        r[0].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = mask >> j & 1u ? (j & 1 ? f[j / 2].y : f[j / 2].x) - K : 0.0f;
+          d1.x += d;
+          d2.x = fmaf(d, d, d2.x);
+        }
+      }
+      d1 = __fadd2_rn(d1, e1);
+      d2 = __fadd2_rn(d2, e2);
+      const float s1 = warp_sum(d1.x + d1.y), s2 = warp_sum(d2.x + d2.y);
+      float4 st = make_float4(fmaf(s1, inv_n, K), fmaf(-s1 * inv_n, s1, s2), n, 0.0f);
+      if (st.y < 0.0f) st.y = 0.0f;  // a NaN stays one
+      if constexpr (CL == 1) {
+        st.y = rsqrtf(st.y * inv_n + a.eps);
+        if (lane == 0) {
+          if (a.mean) a.mean[m] = st.x;
+          if (a.rstd) a.rstd[m] = st.y;
+        }
+      }
+      ring_ready<CL>(sm, s, rank, st);
+    }
+  } else {
+    TY* y = static_cast<TY*>(a.y) + shape.col(share.first);
+    uint32_t mask[NV];
+    float2 wf[NV][4], bf[NV][4];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = v * columns + tid;
+      mask[v] = i < share.count ? shape.mask(share.first + i) : 0u;
+      weights8(a.w, a.w_kind, shape.col(share.first + i), mask[v], 1.0f, wf[v]);
+      weights8(a.b, a.w_kind, shape.col(share.first + i), mask[v], 0.0f, bf[v]);
+    }
+    const float inv_n = 1.0f / static_cast<float>(a.N);
+    int s = 0;
+    uint32_t parity = 0;
+    for (int i = 0; i < rows; ++i) {
+      const int64_t m = first + static_cast<int64_t>(i) * P;
+      ring_wait(&sm.full[s], parity, a.budget, a.status, &sm.dead);
+      ring_wait<(CL > 1)>(&sm.ready[s], parity, a.budget, a.status, &sm.dead);
+      const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
+      const float4 st = sm.slot[s][0];
+      float mu = st.x, r = st.y;
+      if constexpr (CL == 2) {  // the two halves' means and spreads, each about its own mean
+        const float4 su = sm.slot[s][1];
+        const float d = su.x - st.x;
+        mu = (st.x * st.z + su.x * su.z) * inv_n;
+        r = rsqrtf(fmaf(d * d, st.z * su.z * inv_n, st.y + su.y) * inv_n + a.eps);
+        if (rank == 0 && tid == 0) {
+          if (a.mean) a.mean[m] = mu;
+          if (a.rstd) a.rstd[m] = r;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        Raw8<TX> raw;
+        if (mask[v]) stage_vector<SHIFT>(raw, stage, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
+        if (v == NV - 1) ring_empty<CL>(sm, s);
+        if (!mask[v]) continue;
+        float2 f[4];
+        raw.get(f);
+        norm_vector(f, mu, r, wf[v], bf[v]);
+        store_masked(y + m * a.ldy + (v * columns + tid) * 8, f, mask[v]);
+      }
+      if (++s == stages) {
+        s = 0;
+        parity ^= 1u;
+      }
+    }
+  }
+  if constexpr (CL > 1) cluster_sync();  // nobody leaves while another CTA may still write to it
 }
 
 // scalar form: thread t holds the values t, t + blockDim.x, ...
@@ -330,133 +769,144 @@ struct NormGrad {  // arguments of every backward form
   const void* w;
   const float* mean;
   const float* rstd;
-  float* parts;  // [gridDim.x][2][N]: each CTA's sums of dy h and of dy; null where none are wanted
+  float* parts;  // [CTAs or clusters][2][N]: each one's sums of dy h and of dy; null where none are wanted
   int64_t M, lddy, ldx, lddx;
   int32_t N, w_kind;
   unsigned int* status;
   long long budget;
 };
 
-// One vector of a row: h = (x - mu) r and g = dy w, their row sums, and the weight gradients' terms.
-struct GradPairs {
-  float2 h[4], g[4];
-};
-__device__ __forceinline__ void grad_terms(const float2 (&xf)[4], const float2 (&yf)[4], const float2 (&wf)[4],
-                                           float mu, float r, GradPairs& p, float2& s1, float2& s2,
-                                           float2 (&dw)[4], float2 (&db)[4]) {
+// One vector of a row: h = (x - mu) r and g = dy w ...
+__device__ __forceinline__ void grad_hg(const float2 (&xf)[4], const float2 (&yf)[4], const float2 (&wf)[4], float mu,
+                                        float r, float2 (&h)[4], float2 (&g)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    p.h[i] = __fmul2_rn(__fadd2_rn(xf[i], both(-mu)), both(r));
-    p.g[i] = __fmul2_rn(yf[i], wf[i]);
-    s1 = __fadd2_rn(s1, p.g[i]);
-    s2 = __ffma2_rn(p.g[i], p.h[i], s2);
-    dw[i] = __ffma2_rn(yf[i], p.h[i], dw[i]);
+    h[i] = __fmul2_rn(__fadd2_rn(xf[i], both(-mu)), both(r));
+    g[i] = __fmul2_rn(yf[i], wf[i]);
+  }
+}
+// ... the row's sums of g and g h, and the weight gradients' terms ...
+__device__ __forceinline__ void grad_sums(const float2 (&h)[4], const float2 (&g)[4], const float2 (&yf)[4], float2& s1,
+                                          float2& s2, float2 (&dw)[4], float2 (&db)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s1 = __fadd2_rn(s1, g[i]);
+    s2 = __ffma2_rn(g[i], h[i], s2);
+    dw[i] = __ffma2_rn(yf[i], h[i], dw[i]);
     db[i] = __fadd2_rn(db[i], yf[i]);
   }
 }
-// dx = r (g - c1 - h c2)
-__device__ __forceinline__ void grad_dx(const GradPairs& p, float c1, float c2, float r, float2 (&f)[4]) {
+// ... and dx = r (g - c1 - h c2), with rc = r c.
+__device__ __forceinline__ void grad_dx(const float2 (&h)[4], const float2 (&g)[4], float rc1, float rc2, float r,
+                                        float2 (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = __fmul2_rn(__ffma2_rn(p.h[i], both(-c2), __fadd2_rn(p.g[i], both(-c1))), both(r));
+  for (int i = 0; i < 4; ++i) f[i] = __ffma2_rn(g[i], both(r), __ffma2_rn(h[i], both(-rc2), both(-rc1)));
 }
-__device__ __forceinline__ void store_part(float* p, const float2 (&f)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+__device__ __forceinline__ void store_part(float* p, const float2 (&f)[4], uint32_t mask, bool grid) {
+  if (mask == 0xFFu && grid) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (mask >> j & 1u) p[j] = j & 1 ? f[j / 2].y : f[j / 2].x;
+  }
 }
 
 // warp form, as forward; the CTA's warps add their sums up in shared memory, one after another.
 constexpr int kNormGradThreads = 128;
-template <typename TX, typename TY, int LPR, int NV>
+template <typename TX, typename TY, int LPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(const NormGrad a) {
-  constexpr int kRows = kNormGradThreads / LPR;
-  __shared__ __align__(16) float sums[2 * LPR * NV * 8];
+  constexpr int kRows = kNormGradThreads / LPR;  // a multiple of 4; the grid is even, so steps are multiples of 8
+  constexpr int kCols = LPR * NV * 8;
+  __shared__ __align__(16) float sums[2 * kCols];
   griddep_launch_dependents();
   const int sub = threadIdx.x % LPR;
   const TX* x = static_cast<const TX*>(a.x);
   const TY* dy = static_cast<const TY*>(a.dy);
-  bool live[NV];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + (threadIdx.x & ~31) / LPR;
+  const int64_t off = (threadIdx.x & 31) / LPR;
+  const RowShape<SHIFT> shape(a.N, m0 + off, a.ldx);
+  uint32_t mask[NV];
   float2 wf[NV][4], dw[NV][4], db[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    live[v] = (v * LPR + sub) * 8 < a.N;
-    weights8(live[v] ? a.w : nullptr, a.w_kind, (v * LPR + sub) * 8, 1.0f, wf[v]);
+    mask[v] = shape.mask(v * LPR + sub);
+    weights8(a.w, a.w_kind, shape.col(v * LPR + sub), mask[v], 1.0f, wf[v]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[v][i] = db[v][i] = both(0.0f);
   }
   const float inv_n = 1.0f / static_cast<float>(a.N);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + (threadIdx.x & ~31) / LPR;
-  const int64_t off = (threadIdx.x & 31) / LPR;
   Raw8<TX> nx[NV];
   Raw8<TY> ny[NV];
   float nmu = 0.0f, nr = 0.0f;
-  auto fetch = [&](int64_t m) {  // rows past the end are zeros, which add nothing
+  auto fetch = [&](int64_t m) {  // what lies past a row's or the matrix's end is zero and adds nothing
     const bool in = m < a.M;
     nmu = in ? a.mean[m] : 0.0f;
     nr = in ? a.rstd[m] : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      nx[v].zero();
-      ny[v].zero();
-      if (live[v] && in) {
-        nx[v].load_stream(x + m * a.ldx + (v * LPR + sub) * 8);
-        ny[v].load_stream(dy + m * a.lddy + (v * LPR + sub) * 8);
-      }
+      load_vector(nx[v], x + m * a.ldx + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
+      load_vector(ny[v], dy + m * a.lddy + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
     }
   };
   fetch(m0 + off);
   for (; m0 < a.M; m0 += stride) {
     const int64_t m = m0 + off;
     const float mu = nmu, r = nr;
-    GradPairs p[NV];
-    float2 s1 = both(0.0f), s2 = both(0.0f);
+    float2 h[NV][4], g[NV][4], s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float2 xf[4], yf[4];
       nx[v].get(xf);
       ny[v].get(yf);
-      if (!live[v])
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xf[i] = both(mu);  // h = 0 past the row's end
-      grad_terms(xf, yf, wf[v], mu, r, p[v], s1, s2, dw[v], db[v]);
+      grad_hg(xf, yf, wf[v], mu, r, h[v], g[v]);
+      grad_sums(h[v], g[v], yf, s1, s2, dw[v], db[v]);
     }
     if (m0 + stride < a.M) fetch(m + stride);
-    const float c1 = lanes_sum<LPR>(s1.x + s1.y) * inv_n, c2 = lanes_sum<LPR>(s2.x + s2.y) * inv_n;
+    const float rc1 = lanes_sum<LPR>(s1.x + s1.y) * inv_n * r, rc2 = lanes_sum<LPR>(s2.x + s2.y) * inv_n * r;
     if (m >= a.M) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!live[v]) continue;
+      if (!mask[v]) continue;
       float2 f[4];
-      grad_dx(p[v], c1, c2, r, f);
-      store_pairs(static_cast<TX*>(a.dx) + m * a.lddx + (v * LPR + sub) * 8, f);
+      grad_dx(h[v], g[v], rc1, rc2, r, f);
+      store_masked(static_cast<TX*>(a.dx) + m * a.lddx + shape.col(v * LPR + sub), f, mask[v]);
     }
   }
   if (!a.parts) return;
-  // over the rows that the warp's lanes shared, then over the warps
+  // over the rows that the warp's lanes shared (rows of one shape each), then over the warps
+  if constexpr (!SHIFT) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int o = 16; o >= LPR; o >>= 1) {
-        dw[v][i].x += __shfl_xor_sync(0xffffffffu, dw[v][i].x, o);
-        dw[v][i].y += __shfl_xor_sync(0xffffffffu, dw[v][i].y, o);
-        db[v][i].x += __shfl_xor_sync(0xffffffffu, db[v][i].x, o);
-        db[v][i].y += __shfl_xor_sync(0xffffffffu, db[v][i].y, o);
-      }
-  constexpr int kCols = LPR * NV * 8;
-  for (int w = 0; w < kNormGradThreads / 32; ++w) {
-    if (threadIdx.x / 32 == w && (threadIdx.x & 31) < LPR) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2* sw = reinterpret_cast<float2*>(sums + (v * LPR + sub) * 8 + 2 * i);
-          float2* sb = reinterpret_cast<float2*>(sums + kCols + (v * LPR + sub) * 8 + 2 * i);
-          *sw = w == 0 ? dw[v][i] : __fadd2_rn(*sw, dw[v][i]);
-          *sb = w == 0 ? db[v][i] : __fadd2_rn(*sb, db[v][i]);
+        for (int o = 16; o >= LPR; o >>= 1) {
+          dw[v][i].x += __shfl_xor_sync(0xffffffffu, dw[v][i].x, o);
+          dw[v][i].y += __shfl_xor_sync(0xffffffffu, dw[v][i].y, o);
+          db[v][i].x += __shfl_xor_sync(0xffffffffu, db[v][i].x, o);
+          db[v][i].y += __shfl_xor_sync(0xffffffffu, db[v][i].y, o);
         }
+  }
+  for (int n = threadIdx.x; n < 2 * kCols; n += kNormGradThreads) sums[n] = 0.0f;
+  __syncthreads();
+  constexpr int kGroups = SHIFT ? kNormGradThreads / LPR : kNormGradThreads / 32;
+  for (int t = 0; t < kGroups; ++t) {
+    const int own = SHIFT ? static_cast<int>(threadIdx.x) / LPR
+                          : (threadIdx.x & 31) < LPR ? static_cast<int>(threadIdx.x) / 32 : -1;
+    if (own == t) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float* sw = sums + shape.col(v * LPR + sub);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (mask[v] >> j & 1u) {
+            sw[j] += j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
+            sw[kCols + j] += j & 1 ? db[v][j / 2].y : db[v][j / 2].x;
+          }
+      }
     }
     __syncthreads();
   }
@@ -467,133 +917,185 @@ __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(
   }
 }
 
-// ring form.  The x and dy rows of `stages` rows ahead are in flight as bulk copies; a row's stage is filled again
-// once every thread has passed the barrier of the row after it.
-constexpr int kRingMaxStages = 8;
-constexpr int kRingThreads = 512;
-
-// Waits for a stage, at most `budget` cycles; past that it records the status and nobody waits any more (the
-// results are void, the kernel ends).
-__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity, const NormGrad& a, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*dead) return;
-    if (clock64() - t0 > a.budget) {
-      *dead = 1;
-      record_status(a.status, FP8G_ERR_TIMEOUT);
-      return;
-    }
-  }
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-template <typename TX, typename TY, int NV>
-__global__ void __launch_bounds__(kRingThreads, 1) layer_norm_grad_ring_kernel(const NormGrad a, int32_t stages) {
+// ring form, as forward with the x and dy rows in a stage.  The sum warps read the weights from shared memory, in the
+// order of the row's vectors: the first four values of every vector, then the other four (16-byte reads without
+// bank conflicts).
+template <typename TX, typename TY, int CL, bool SHIFT>
+__global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_grad_ring_kernel(
+    const NormGrad a, int32_t stages, int32_t stage_bytes, int32_t x_bytes, int32_t column_warps, int32_t sum_warps) {
+  constexpr int NV = kRingVecs;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t full_bar[kRingMaxStages];
-  __shared__ float2 red[2][32];
-  __shared__ int s_dead;
+  __shared__ RingShared sm;
   griddep_launch_dependents();
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const uint32_t xb = static_cast<uint32_t>(a.N) * sizeof(TX), yb = static_cast<uint32_t>(a.N) * sizeof(TY);
-  const int64_t P = gridDim.x;
-  const int64_t rows = (a.M - blockIdx.x + P - 1) / P;  // rows blockIdx.x, blockIdx.x + P, ...
-  if (tid == 0) {
-    s_dead = 0;
-    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full_bar[s]), 1);
-    fence_mbar_init();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, columns = column_warps * 32;
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int P = static_cast<int>(gridDim.x) / CL, first = static_cast<int>(blockIdx.x) / CL;
+  const int rows = static_cast<int>((a.M - first + P - 1) / P);  // rows first, first + P, ...
+  const RowShape<SHIFT> shape(a.N, first, a.ldx);
+  const Share share(shape, rank, CL);
+  const TX* x = static_cast<const TX*>(a.x) + shape.col(share.first);
+  const TY* dy = static_cast<const TY*>(a.dy) + shape.col(share.first);
+  float4* ws = reinterpret_cast<float4*>(ring + stages * stage_bytes);  // [2][share.count]
+  ring_init<CL>(sm, stages, column_warps);
+  for (int v = tid; v < share.count; v += blockDim.x) {
+    float2 f[4];
+    weights8(a.w, a.w_kind, shape.col(share.first + v), shape.mask(share.first + v), 1.0f, f);
+    ws[v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    ws[share.count + v] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
-  __syncthreads();
-  auto fill = [&](int64_t i) {  // one thread: the copies of this CTA's i-th row
-    const int s = static_cast<int>(i % stages);
-    const int64_t m = blockIdx.x + i * P;
-    const uint32_t bar = smem_u32(&full_bar[s]), dst = smem_u32(ring) + static_cast<uint32_t>(s) * (xb + yb);
-    mbar_arrive_expect_tx(true, bar, xb + yb);
-    bulk_load(dst, static_cast<const TX*>(a.x) + m * a.ldx, xb, bar);
-    bulk_load(dst + xb, static_cast<const TY*>(a.dy) + m * a.lddy, yb, bar);
-  };
-  if (tid == 0)
-    for (int64_t i = 0; i < stages && i < rows; ++i) fill(i);
-  bool live[NV];
-  float2 wf[NV][4], dw[NV][4], db[NV][4];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    live[v] = (v * threads + tid) * 8 < a.N;
-    weights8(live[v] ? a.w : nullptr, a.w_kind, (v * threads + tid) * 8, 1.0f, wf[v]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dw[v][i] = db[v][i] = both(0.0f);
-  }
+  if constexpr (CL == 1) __syncthreads();
+  else cluster_sync();  // every CTA of the cluster runs before it is written to
   const float inv_n = 1.0f / static_cast<float>(a.N);
-  int s = 0;
-  uint32_t parity = 0;
-  // the statistics of 32 rows at a time, one row a lane (loaded 32 rows ahead: no row waits for them)
-  const int lane = tid & 31;
-  float mu32 = 0.0f, r32 = 0.0f, next_mu = 0.0f, next_r = 0.0f;
-  auto stats = [&](int64_t i) {
-    if (i + lane >= rows) return;
-    next_mu = a.mean[blockIdx.x + (i + lane) * P];
-    next_r = a.rstd[blockIdx.x + (i + lane) * P];
-  };
-  stats(0);
-  for (int64_t i = 0; i < rows; ++i) {
-    const int64_t m = blockIdx.x + i * P;
-    if ((i & 31) == 0) {
-      mu32 = next_mu;
-      r32 = next_r;
-      stats(i + 32);
-    }
-    const float mu = __shfl_sync(0xffffffffu, mu32, static_cast<int>(i & 31));
-    const float r = __shfl_sync(0xffffffffu, r32, static_cast<int>(i & 31));
-    ring_wait(smem_u32(&full_bar[s]), parity, a, &s_dead);
-    const uint8_t* stage = ring + static_cast<size_t>(s) * (xb + yb);
-    GradPairs p[NV];
-    float2 s1 = both(0.0f), s2 = both(0.0f);
+  if (warp == column_warps + sum_warps) {
+    if (lane == 0)
+      ring_copies(sm, rows, stages, CL > 1, a.budget, a.status, [&](int i, int s) {
+        const int64_t m = first + static_cast<int64_t>(i) * P;
+        const uint32_t bar = smem_u32(&sm.full[s]), dst = smem_u32(ring) + s * stage_bytes;
+        const uint32_t n = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8;
+        mbar_arrive_expect_tx(true, bar, n * (sizeof(TX) + sizeof(TY)));
+        if (n) {
+          bulk_load(dst, x + m * a.ldx, n * sizeof(TX), bar);
+          bulk_load(dst + x_bytes, dy + m * a.lddy, n * sizeof(TY), bar);
+        }
+      });
+  } else if (warp >= column_warps) {
+    SumRows it(warp - column_warps, sum_warps, stages);
+    float nmu = 0.0f, nr = 0.0f;  // the next row's statistics
+    auto stats = [&] {
+      if (it.row() >= rows) return;
+      nmu = a.mean[first + it.row() * P];
+      nr = a.rstd[first + it.row() * P];
+    };
+    stats();
+    while (it.row() < rows) {
+      const int s = it.stage, round = it.round;
+      const int64_t m = first + it.row() * P;
+      const float mu = nmu, r = nr;
+      it.next();
+      stats();
+      ring_wait(&sm.full[s], round & 1, a.budget, a.status, &sm.dead);
+      const TX* xs = reinterpret_cast<const TX*>(ring + s * stage_bytes);
+      const TY* ys = reinterpret_cast<const TY*>(ring + s * stage_bytes + x_bytes);
+      const Inner<SHIFT> in(share);
+      float2 s1[2] = {both(0.0f), both(0.0f)}, s2[2] = {both(0.0f), both(0.0f)};
+      auto add = [&](const Raw8<TX>& rx, const Raw8<TY>& ry, const float4& wa, const float4& wb) {
+        const float2 w[4] = {make_float2(wa.x, wa.y), make_float2(wa.z, wa.w), make_float2(wb.x, wb.y),
+                             make_float2(wb.z, wb.w)};
+        float2 xf[4], yf[4];
+        rx.get(xf);
+        ry.get(yf);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (!live[v]) continue;
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = __fmul2_rn(yf[k], w[k]);
+          s1[k & 1] = __fadd2_rn(s1[k & 1], g);
+          s2[k & 1] = __ffma2_rn(g, __fadd2_rn(xf[k], both(-mu)), s2[k & 1]);
+        }
+      };
+      constexpr int U = kSumUnroll / 2;
+      int v = in.lo + lane;
+      for (; v + 32 * (U - 1) < in.hi; v += 32 * U) {
+        Raw8<TX> rx[U];
+        Raw8<TY> ry[U];
+        float4 wa[U], wb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          rx[u].load(xs + (v + 32 * u) * 8);
+          ry[u].load(ys + (v + 32 * u) * 8);
+          wa[u] = ws[v + 32 * u];
+          wb[u] = ws[share.count + v + 32 * u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(rx[u], ry[u], wa[u], wb[u]);
+      }
       Raw8<TX> rx;
       Raw8<TY> ry;
-      rx.load(reinterpret_cast<const TX*>(stage) + (v * threads + tid) * 8);
-      ry.load(reinterpret_cast<const TY*>(stage + xb) + (v * threads + tid) * 8);
-      float2 xf[4], yf[4];
-      rx.get(xf);
-      ry.get(yf);
-      grad_terms(xf, yf, wf[v], mu, r, p[v], s1, s2, dw[v], db[v]);
+      for (; v < in.hi; v += 32) {
+        rx.load(xs + v * 8);
+        ry.load(ys + v * 8);
+        add(rx, ry, ws[v], ws[share.count + v]);
+      }
+      if (SHIFT && lane < 2) {  // the first and the last vector; dy is zero where they do not exist
+        v = lane == 0 ? 0 : share.count - 1;
+        const uint32_t mask = shape.mask(share.first + v);
+        stage_vector<SHIFT>(rx, xs, v, mask, m + 1 == a.M, x + m * a.ldx);
+        stage_vector<SHIFT>(ry, ys, v, mask, m + 1 == a.M, dy + m * a.lddy);
+        add(rx, ry, ws[v], ws[share.count + v]);
+      }
+      s1[0] = __fadd2_rn(s1[0], s1[1]);
+      s2[0] = __fadd2_rn(s2[0], s2[1]);
+      const float c1 = warp_sum(s1[0].x + s1[0].y) * inv_n * r;
+      const float c2 = warp_sum(s2[0].x + s2[0].y) * inv_n * r * r;
+      ring_ready<CL>(sm, s, rank, make_float4(mu, r, c1, c2));
     }
-    const float2 c = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), red, static_cast<int>(i & 1));
-    // every thread has now read the row before this one
-    if (tid == 0 && i > 0 && i - 1 + stages < rows) fill(i - 1 + stages);
-    const float c1 = c.x * inv_n, c2 = c.y * inv_n;
+  } else {
+    TX* out = static_cast<TX*>(a.dx) + shape.col(share.first);
+    uint32_t mask[NV];
+    float2 wf[NV][4], dw[NV][4], db[NV][4];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (!live[v]) continue;
-      float2 f[4];
-      grad_dx(p[v], c1, c2, r, f);
-      store_pairs(static_cast<TX*>(a.dx) + m * a.lddx + (v * threads + tid) * 8, f);
-    }
-    if (++s == stages) {
-      s = 0;
-      parity ^= 1u;
-    }
-  }
-  if (!a.parts) return;
-  float* part = a.parts + blockIdx.x * 2 * static_cast<int64_t>(a.N);
+      const int i = v * columns + tid;
+      mask[v] = i < share.count ? shape.mask(share.first + i) : 0u;
+      weights8(a.w, a.w_kind, shape.col(share.first + i), mask[v], 1.0f, wf[v]);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if (!live[v]) continue;
-    store_part(part + (v * threads + tid) * 8, dw[v]);
-    store_part(part + a.N + (v * threads + tid) * 8, db[v]);
+      for (int k = 0; k < 4; ++k) dw[v][k] = db[v][k] = both(0.0f);
+    }
+    int s = 0;
+    uint32_t parity = 0;
+    for (int i = 0; i < rows; ++i) {
+      const int64_t m = first + static_cast<int64_t>(i) * P;
+      ring_wait(&sm.full[s], parity, a.budget, a.status, &sm.dead);
+      ring_wait<(CL > 1)>(&sm.ready[s], parity, a.budget, a.status, &sm.dead);
+      const TX* xs = reinterpret_cast<const TX*>(ring + s * stage_bytes);
+      const TY* ys = reinterpret_cast<const TY*>(ring + s * stage_bytes + x_bytes);
+      float4 st = sm.slot[s][0];
+      if constexpr (CL == 2) {
+        const float4 su = sm.slot[s][1];
+        st.z += su.z;
+        st.w += su.w;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        Raw8<TX> rx;
+        Raw8<TY> ry;
+        if (mask[v]) {
+          stage_vector<SHIFT>(rx, xs, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
+          stage_vector<SHIFT>(ry, ys, v * columns + tid, mask[v], m + 1 == a.M, dy + m * a.lddy);
+        }
+        if (v == NV - 1) ring_empty<CL>(sm, s);
+        if (!mask[v]) continue;
+        float2 xf[4], yf[4], h[4], g[4], f[4];
+        rx.get(xf);
+        ry.get(yf);
+        grad_hg(xf, yf, wf[v], st.x, st.y, h, g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dw[v][k] = __ffma2_rn(yf[k], h[k], dw[v][k]);
+          db[v][k] = __fadd2_rn(db[v][k], yf[k]);
+        }
+        grad_dx(h, g, st.z, st.w, st.y, f);
+        store_masked(out + m * a.lddx + (v * columns + tid) * 8, f, mask[v]);
+      }
+      if (++s == stages) {
+        s = 0;
+        parity ^= 1u;
+      }
+    }
+    if (a.parts) {
+      float* part = a.parts + first * 2 * static_cast<int64_t>(a.N);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int col = shape.col(share.first + v * columns + tid);
+        store_part(part + col, dw[v], mask[v], !SHIFT);
+        store_part(part + a.N + col, db[v], mask[v], !SHIFT);
+      }
+    }
   }
+  if constexpr (CL > 1) cluster_sync();  // nobody leaves while another CTA may still write to it
 }
 
 // scalar form: resident CTAs, thread t holds the columns t, t + blockDim.x, ...
 template <typename TX, typename TY, int NV>
-__global__ void __launch_bounds__(kRingThreads) layer_norm_grad_scalar_kernel(const NormGrad a) {
+__global__ void __launch_bounds__(512) layer_norm_grad_scalar_kernel(const NormGrad a) {
   __shared__ float2 red[2][32];
   griddep_launch_dependents();
   const int tid = threadIdx.x, threads = blockDim.x;
@@ -732,103 +1234,177 @@ bool dtype_ok(int32_t d) { return d == FP8G_BF16 || d == FP8G_F32; }
 int dtype_size(int32_t d) { return d == FP8G_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t kWarpMaxN = 1024;    // warp form: up to 4 vectors a lane
-constexpr int64_t kCtaMaxN = 32768;    // cta form: up to 4 vectors a thread
-constexpr int64_t kScalarMaxN = 16384; // scalar form, forward: up to 16 values a thread
-constexpr int64_t kGradScalarMaxN = 8192;
-constexpr int64_t kRingMaxN = 8192;    // ring form: up to 2 vectors a thread
-constexpr int kRingBytes = 200 * 1024; // shared memory of a ring's stages, at most
+constexpr int64_t kWarpMaxN = 1024;      // warp form: up to 4 vectors a lane
+constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice that in clusters of two
+constexpr int64_t kCtaMaxN = 32768;      // cta form: up to 4 vectors a thread
+constexpr int64_t kScalarMaxN = 16384;   // scalar form: up to 16 values a thread, forward ...
+constexpr int64_t kGradScalarMaxN = 8192;  // ... and backward
+constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM's stages, at most
+constexpr int64_t kNormMaxParts = 608;
 
 // Rows of partial sums that the workspace has room for: the largest grid of any backward form.
-int64_t norm_parts(int64_t M) { return std::min<int64_t>(M, 608); }
+int64_t norm_parts(int64_t M) { return std::min<int64_t>(M, kNormMaxParts); }
 
-// Whether rows of N values of `size` bytes, `ld` apart, can be taken in vectors of 8.
-bool vectors(const void* p, int size, int64_t N, int64_t ld) {
-  return N % 8 == 0 && aligned16(p) && (ld * size) % 16 == 0;
+enum Grid { kNone, kGrid, kShifted };  // see RowShape
+struct Rows {
+  const void* p;
+  int64_t ld;
+};
+// How the rows of all a call's matrices fall on the 16-byte grid: all on it, all equally off it, or neither.
+Grid row_grid(int64_t M, int64_t N, std::initializer_list<Rows> all) {
+  bool on = N % 8 == 0, same = true;
+  const int64_t ld0 = all.begin()->ld & 7;
+  for (const Rows& r : all) {
+    if (!aligned16(r.p)) return kNone;
+    on &= M == 1 || (r.ld & 7) == 0;
+    same &= M == 1 || (r.ld & 7) == ld0;
+  }
+  return on ? kGrid : same ? kShifted : kNone;
 }
 // The weights' type as the kernels take it.
-int32_t weight_kind(const void* w, const void* b, int32_t dtype) {
-  return dtype | (aligned16(w) && aligned16(b) ? kWeightVectors : 0);
+int32_t weight_kind(const void* w, const void* b, int32_t dtype, Grid grid) {
+  return dtype | (aligned16(w) && aligned16(b) && grid == kGrid ? kWeightVectors : 0);
 }
 // Threads for `items` items a row at `each` a thread.
 int row_threads(int64_t items, int each) { return static_cast<int>((items + each * 32 - 1) / (each * 32) * 32); }
+// Vectors a row takes, at most.
+int64_t row_vectors(int64_t N, Grid grid) { return (N + (grid == kShifted ? 7 : 0) + 7) / 8; }
 
-template <typename TX, typename TY>
-int layer_norm_launch(const void* xv, int64_t M, int64_t N, int64_t ldx, const void* w, const void* b,
-                      int32_t w_kind, float eps, void* yv, int64_t ldy, float* mean, float* rstd,
-                      const DeviceInfo* dev, cudaStream_t s) {
-  const TX* x = static_cast<const TX*>(xv);
-  TY* y = static_cast<TY*>(yv);
-  const int n = static_cast<int>(N);
-  const unsigned rows = static_cast<unsigned>(M);
-  const bool vec = vectors(x, sizeof(TX), N, ldx) && vectors(y, sizeof(TY), N, ldy);
-  if (vec && N <= kWarpMaxN) {
-    auto go = N <= 64    ? layer_norm_warp_kernel<TX, TY, 8, 1>
-              : N <= 128 ? layer_norm_warp_kernel<TX, TY, 16, 1>
-              : N <= 256 ? layer_norm_warp_kernel<TX, TY, 32, 1>
-              : N <= 512 ? layer_norm_warp_kernel<TX, TY, 32, 2>
-                         : layer_norm_warp_kernel<TX, TY, 32, 4>;
-    const int64_t per = kNormThreads / (N <= 64 ? 8 : N <= 128 ? 16 : 32);
-    const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 8 * static_cast<int64_t>(dev->sm_count));
-    go<<<static_cast<unsigned>(ctas), kNormThreads, 0, s>>>(x, M, n, ldx, w, b, w_kind, eps, y, ldy, mean, rstd);
-  } else if (vec && N <= kCtaMaxN) {
-    const int64_t items = N / 8;
-    // few rows: one vector a thread, for the latency; many: more a thread
-    const int nv = M <= 2 * dev->sm_count && items <= 1024 ? 1 : items <= 1024 ? 2 : items <= 2048 ? 2 : 4;
-    auto go = nv == 1   ? layer_norm_cta_kernel<TX, TY, 1>
-              : nv == 2 ? layer_norm_cta_kernel<TX, TY, 2>
-                        : layer_norm_cta_kernel<TX, TY, 4>;
-    go<<<rows, row_threads(items, nv), 0, s>>>(x, n, ldx, w, b, w_kind, eps, y, ldy, mean, rstd);
-  } else if (N <= kScalarMaxN) {
-    const int nv = N <= 1024 ? 4 : N <= 4096 ? 8 : 16;
-    auto go = nv == 4   ? layer_norm_scalar_kernel<TX, TY, 4>
-              : nv == 8 ? layer_norm_scalar_kernel<TX, TY, 8>
-                        : layer_norm_scalar_kernel<TX, TY, 16>;
-    go<<<rows, row_threads(N, nv), 0, s>>>(x, n, ldx, w, b, w_kind, eps, y, ldy, mean, rstd);
-  } else {
-    layer_norm_any_kernel<TX, TY><<<rows, kNormThreads, 0, s>>>(x, N, ldx, w, b, w_kind, eps, y, ldy, mean, rstd);
-  }
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+struct RingPlan {
+  int cluster, column_warps, sum_warps, stages, threads;
+  int32_t each, stage_bytes;  // vectors a CTA holds of a row, at most; bytes of a stage
+  int64_t rows_at_once;       // CTAs or clusters
+};
+// A ring for rows of `vecs` vectors, `size` bytes a value over all matrices of a stage; `extra` bytes of shared memory
+// a vector beside the stages.  As many CTAs an SM as its registers hold at 96 a thread: short rows take several.
+RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, Grid grid, int sms) {
+  RingPlan p;
+  p.cluster = vecs * 8 <= kRingMaxN ? 1 : 2;
+  p.each = static_cast<int32_t>((vecs + p.cluster - 1) / p.cluster);
+  p.column_warps = row_threads(p.each, kRingVecs) / 32;
+  p.sum_warps = p.column_warps > 6 ? kRingMaxSumWarps : 2;
+  const int per_sm = std::max(1, std::min(4, 65536 / (32 * (p.column_warps + p.sum_warps + 1) * 96)));
+  p.stage_bytes = p.each * 8 * size;
+  p.stages = static_cast<int>(
+      std::min<int64_t>(kRingMaxStages, (kRingBytes / per_sm - static_cast<int64_t>(p.each) * extra) / p.stage_bytes));
+  p.sum_warps = std::min(p.sum_warps, p.stages);  // (a sum warp has stages of its own)
+  p.threads = 32 * (p.column_warps + p.sum_warps + 1);
+  p.rows_at_once = std::min<int64_t>(static_cast<int64_t>(sms) * per_sm / p.cluster, kNormMaxParts);
+  if (grid == kShifted) p.rows_at_once = p.rows_at_once / 8 * 8;  // a CTA's rows are multiples of 8 apart
+  p.rows_at_once = std::min(M, p.rows_at_once);
+  return p;
 }
-
-// The ring's resident CTAs per SM: one of 512 threads, more of shorter rows (their barriers and latencies overlap).
-int ring_per_sm(int threads) { return std::max(1, std::min(4, 768 / threads)); }
-
-template <typename TX, typename TY, int NV>
-int ring_launch(const NormGrad& a, int threads, int64_t grid, cudaStream_t s) {
-  const int stage = a.N * static_cast<int>(sizeof(TX) + sizeof(TY));
-  const int stages = std::min(kRingMaxStages, kRingBytes / ring_per_sm(threads) / stage);
-  auto kern = layer_norm_grad_ring_kernel<TX, TY, NV>;
+template <typename Kernel, typename... Args>
+int ring_launch(Kernel kern, const RingPlan& p, int64_t smem, cudaStream_t s, Args... args) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess) {
     cudaGetLastError();
     return FP8G_ERR_CUDA;
   }
-  kern<<<static_cast<unsigned>(grid), threads, stages * stage, s>>>(a, stages);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows_at_once * p.cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(p.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  return FP8G_OK;
+}
+
+template <typename TX, typename TY, bool SHIFT>
+int layer_norm_vectors(const NormArgs& a, Grid grid, const DeviceInfo* dev, cudaStream_t s) {
+  const int64_t M = a.M, vecs = row_vectors(a.N, grid);
+  const int sms = dev->sm_count;
+  if (vecs * 8 <= kWarpMaxN) {
+    auto go = vecs <= 8    ? layer_norm_warp_kernel<TX, TY, 8, 1, SHIFT>
+              : vecs <= 16 ? layer_norm_warp_kernel<TX, TY, 16, 1, SHIFT>
+              : vecs <= 32 ? layer_norm_warp_kernel<TX, TY, 32, 1, SHIFT>
+              : vecs <= 64 ? layer_norm_warp_kernel<TX, TY, 32, 2, SHIFT>
+                           : layer_norm_warp_kernel<TX, TY, 32, 4, SHIFT>;
+    const int64_t per = kNormThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
+    const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 8 * static_cast<int64_t>(sms));
+    go<<<static_cast<unsigned>(ctas), kNormThreads, 0, s>>>(a);
+  } else if (vecs * 8 <= 2 * kRingMaxN) {
+    const RingPlan p = ring_plan(M, vecs, sizeof(TX), 0, grid, sms);
+    auto go = p.cluster == 1 ? layer_norm_ring_kernel<TX, TY, 1, SHIFT> : layer_norm_ring_kernel<TX, TY, 2, SHIFT>;
+    return ring_launch(go, p, static_cast<int64_t>(p.stages) * p.stage_bytes, s, a, p.stages, p.stage_bytes,
+                       p.column_warps, p.sum_warps);
+  } else {
+    layer_norm_cta_kernel<TX, TY, 4, SHIFT><<<static_cast<unsigned>(M), row_threads(vecs, 4), 0, s>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+template <typename TX, typename TY>
+int layer_norm_launch(NormArgs a, const DeviceInfo* dev, cudaStream_t s) {
+  const Grid grid = row_grid(a.M, a.N, {{a.x, a.ldx}, {a.y, a.ldy}});
+  const int32_t dtype = a.w_kind;
+  a.w_kind = weight_kind(a.w, a.b, dtype, grid);
+  if (grid != kNone && row_vectors(a.N, grid) * 8 <= kCtaMaxN)
+    return grid == kGrid ? layer_norm_vectors<TX, TY, false>(a, grid, dev, s)
+                         : layer_norm_vectors<TX, TY, true>(a, grid, dev, s);
+  const TX* x = static_cast<const TX*>(a.x);
+  TY* y = static_cast<TY*>(a.y);
+  const unsigned rows = static_cast<unsigned>(a.M);
+  if (a.N <= kScalarMaxN) {
+    const int nv = a.N <= 1024 ? 4 : a.N <= 4096 ? 8 : 16;
+    auto go = nv == 4   ? layer_norm_scalar_kernel<TX, TY, 4>
+              : nv == 8 ? layer_norm_scalar_kernel<TX, TY, 8>
+                        : layer_norm_scalar_kernel<TX, TY, 16>;
+    go<<<rows, row_threads(a.N, nv), 0, s>>>(x, a.N, a.ldx, a.w, a.b, dtype, a.eps, y, a.ldy, a.mean, a.rstd);
+  } else {
+    layer_norm_any_kernel<TX, TY><<<rows, kNormThreads, 0, s>>>(x, a.N, a.ldx, a.w, a.b, dtype, a.eps, y, a.ldy, a.mean,
+                                                                a.rstd);
+  }
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+// The backward forms; *P is how many partial rows they write.
+template <typename TX, typename TY, bool SHIFT>
+int layer_norm_grad_vectors(const NormGrad& a, Grid grid, int64_t* P, const DeviceInfo* dev, cudaStream_t s) {
+  const int64_t M = a.M, vecs = row_vectors(a.N, grid);
+  const int sms = dev->sm_count;
+  if (vecs * 8 <= kWarpMaxN) {
+    auto go = vecs <= 8    ? layer_norm_grad_warp_kernel<TX, TY, 8, 1, SHIFT>
+              : vecs <= 16 ? layer_norm_grad_warp_kernel<TX, TY, 16, 1, SHIFT>
+              : vecs <= 32 ? layer_norm_grad_warp_kernel<TX, TY, 32, 1, SHIFT>
+              : vecs <= 64 ? layer_norm_grad_warp_kernel<TX, TY, 32, 2, SHIFT>
+                           : layer_norm_grad_warp_kernel<TX, TY, 32, 4, SHIFT>;
+    const int64_t per = kNormGradThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
+    *P = std::min<int64_t>((M + per - 1) / per, std::min<int64_t>(4 * static_cast<int64_t>(sms), kNormMaxParts) / 2 * 2);
+    go<<<static_cast<unsigned>(*P), kNormGradThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  }
+  const RingPlan p = ring_plan(M, vecs, sizeof(TX) + sizeof(TY), 32, grid, sms);
+  *P = p.rows_at_once;
+  auto go = p.cluster == 1 ? layer_norm_grad_ring_kernel<TX, TY, 1, SHIFT>
+                           : layer_norm_grad_ring_kernel<TX, TY, 2, SHIFT>;
+  return ring_launch(go, p, static_cast<int64_t>(p.stages) * p.stage_bytes + static_cast<int64_t>(p.each) * 32, s, a,
+                     p.stages, p.stage_bytes, static_cast<int32_t>(p.each * 8 * sizeof(TX)), p.column_warps,
+                     p.sum_warps);
 }
 
 template <typename TX, typename TY>
 int layer_norm_backward_launch(NormGrad a, float* dw, float* db, const DeviceInfo* dev, cudaStream_t s) {
   const int64_t M = a.M, N = a.N;
-  const bool vec = vectors(a.x, sizeof(TX), N, a.ldx) && vectors(a.dy, sizeof(TY), N, a.lddy) &&
-                   vectors(a.dx, sizeof(TX), N, a.lddx);
   const int sms = dev->sm_count;
+  const Grid grid = row_grid(M, N, {{a.x, a.ldx}, {a.dy, a.lddy}, {a.dx, a.lddx}});
+  const int32_t dtype = a.w_kind;
+  a.w_kind = weight_kind(a.w, nullptr, dtype, grid);
   int64_t P = 0;
-  if (vec && N <= kWarpMaxN) {
-    auto go = N <= 64    ? layer_norm_grad_warp_kernel<TX, TY, 8, 1>
-              : N <= 128 ? layer_norm_grad_warp_kernel<TX, TY, 16, 1>
-              : N <= 256 ? layer_norm_grad_warp_kernel<TX, TY, 32, 1>
-              : N <= 512 ? layer_norm_grad_warp_kernel<TX, TY, 32, 2>
-                         : layer_norm_grad_warp_kernel<TX, TY, 32, 4>;
-    const int64_t per = kNormGradThreads / (N <= 64 ? 8 : N <= 128 ? 16 : 32);
-    P = std::min<int64_t>({(M + per - 1) / per, 4 * static_cast<int64_t>(sms), norm_parts(M)});
-    go<<<static_cast<unsigned>(P), kNormGradThreads, 0, s>>>(a);
-  } else if (vec && N <= kRingMaxN) {
-    const int nv = N <= 4096 ? 1 : 2, threads = row_threads(N / 8, nv);
-    P = std::min<int64_t>(M, static_cast<int64_t>(sms) * ring_per_sm(threads));
-    const int st = nv == 1 ? ring_launch<TX, TY, 1>(a, threads, P, s) : ring_launch<TX, TY, 2>(a, threads, P, s);
+  if (grid != kNone && row_vectors(N, grid) * 8 <= 2 * kRingMaxN) {
+    const int st = grid == kGrid ? layer_norm_grad_vectors<TX, TY, false>(a, grid, &P, dev, s)
+                                 : layer_norm_grad_vectors<TX, TY, true>(a, grid, &P, dev, s);
     if (st != FP8G_OK) return st;
   } else if (N <= kGradScalarMaxN) {
+    a.w_kind = dtype;
     const int nv = N <= 1024 ? 4 : N <= 4096 ? 8 : 16;
     const int threads = row_threads(N, nv);
     P = std::min<int64_t>({M, static_cast<int64_t>(sms) * std::max(1, std::min(4, 1024 / threads)), norm_parts(M)});
@@ -838,12 +1414,12 @@ int layer_norm_backward_launch(NormGrad a, float* dw, float* db, const DeviceInf
     go<<<static_cast<unsigned>(P), threads, 0, s>>>(a);
   } else {
     layer_norm_dx_any_kernel<TX, TY><<<static_cast<unsigned>(M), kNormThreads, 0, s>>>(
-        static_cast<const TY*>(a.dy), a.lddy, static_cast<const TX*>(a.x), a.ldx, a.w, a.w_kind, a.mean, a.rstd, N,
+        static_cast<const TY*>(a.dy), a.lddy, static_cast<const TX*>(a.x), a.ldx, a.w, dtype, a.mean, a.rstd, N,
         static_cast<TX*>(a.dx), a.lddx);
     if (a.parts) {
       P = norm_parts(M);
-      const dim3 grid(static_cast<unsigned>((N + kNormThreads - 1) / kNormThreads), static_cast<unsigned>(P));
-      layer_norm_dw_any_kernel<TX, TY><<<grid, kNormThreads, 0, s>>>(
+      const dim3 ctas(static_cast<unsigned>((N + kNormThreads - 1) / kNormThreads), static_cast<unsigned>(P));
+      layer_norm_dw_any_kernel<TX, TY><<<ctas, kNormThreads, 0, s>>>(
           static_cast<const TY*>(a.dy), a.lddy, static_cast<const TX*>(a.x), a.ldx, a.mean, a.rstd, M, N, a.parts);
     }
   }
@@ -851,8 +1427,7 @@ int layer_norm_backward_launch(NormGrad a, float* dw, float* db, const DeviceInf
   if (!a.parts) return FP8G_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((2 * N + 31) / 32));
-  cfg.blockDim = dim3(32 * static_cast<unsigned>(std::min<int64_t>(
-                                kJoinMaxWarps, (P + kJoinUnroll - 1) / kJoinUnroll)));
+  cfg.blockDim = dim3(32 * static_cast<unsigned>(std::min<int64_t>(kJoinMaxWarps, (P + kJoinUnroll - 1) / kJoinUnroll)));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -891,8 +1466,12 @@ extern "C" int fp8g_layer_norm(const void* x, int32_t x_dtype, int64_t M, int64_
                 ? (y_dtype == FP8G_F32 ? layer_norm_launch<float, float> : layer_norm_launch<float, __nv_bfloat16>)
                 : (y_dtype == FP8G_F32 ? layer_norm_launch<__nv_bfloat16, float>
                                        : layer_norm_launch<__nv_bfloat16, __nv_bfloat16>);
-  return go(x, M, N, ldx, weight, bias, weight_kind(weight, bias, w_dtype), eps, y, ldy, mean, rstd, dev,
-            static_cast<cudaStream_t>(stream));
+  NormArgs a{};
+  a.x = x, a.y = y, a.w = weight, a.b = bias, a.mean = mean, a.rstd = rstd;
+  a.M = M, a.ldx = ldx, a.ldy = ldy;
+  a.N = static_cast<int32_t>(N), a.w_kind = w_dtype, a.eps = eps;
+  a.status = dev->status, a.budget = wait_budget_cycles();
+  return go(a, dev, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp8g_layer_norm_backward_workspace(int64_t M, int64_t N, int64_t* bytes) {
@@ -938,7 +1517,7 @@ extern "C" int fp8g_layer_norm_backward(const void* dy, int32_t dy_dtype, int64_
   a.dy = dy, a.x = x, a.dx = dx, a.w = weight, a.mean = mean, a.rstd = rstd;
   a.parts = dweight || dbias ? static_cast<float*>(workspace) : nullptr;
   a.M = M, a.lddy = lddy, a.ldx = ldx, a.lddx = lddx;
-  a.N = static_cast<int32_t>(N), a.w_kind = weight_kind(weight, nullptr, w_dtype);
+  a.N = static_cast<int32_t>(N), a.w_kind = w_dtype;
   a.status = dev->status, a.budget = wait_budget_cycles();
   return go(a, dweight, dbias, dev, s);
 }

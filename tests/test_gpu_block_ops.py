@@ -189,6 +189,28 @@ def test_layer_norm_many_short_rows():
     _check_norm_grads(dx, dw, db, dy, x, w, mean, rstd, "bf16")
 
 
+# many rows a resident CTA, so that its ring of row stages goes round many times; the last ones have a ring of two
+# stages, and rows that two CTAs share
+@pytest.mark.parametrize("M,N,xd,yd", [(3001, 1032, "bf16", "bf16"), (4000, 2048, "f32", "bf16"), (2500, 7168, "bf16", "bf16"),
+                                       (3000, 1531, "bf16", "bf16"), (2000, 5003, "f32", "f32"), (1300, 8190, "bf16", "f32"),
+                                       (1500, 16384, "f32", "f32"), (1111, 12001, "bf16", "bf16"),
+                                       (5000, 1020, "bf16", "bf16"), (9000, 333, "f32", "bf16")])
+def test_layer_norm_many_rows(M, N, xd, yd):
+    x, dy, w = _draw((M, N), xd, 15, 1.0, 0.3), _draw((M, N), yd, 16, 0.1), _draw((N,), "f32", 17)
+    y, mean, rstd = g.layer_norm(x, w, out_dtype=DT[yd])
+    ry, rmean, rrstd = ob.layer_norm(_np(x), _np(w))
+    k = (N / 256 + 16) * U
+    _within(mean, rmean, k * np.abs(_np(x)).mean(1), "f32", "mean")
+    _within(y, ry, _norm_bounds(_np(x), _np(w), None, rmean, rrstd, N) + 4 * k * np.abs(ry), yd, "y")
+    dx, dw, db = g.layer_norm_backward(dy, x, w, mean, rstd)
+    _check_norm_grads(dx, dw, db, dy, x, w, mean, rstd, xd)
+    check_status()  # no wait ran out
+    # a row's result does not depend on how many rows the call has (here: rows on the 16-byte grid)
+    if N % 8 == 0:
+        assert torch.equal(g.layer_norm(x[-5:], w, out_dtype=DT[yd])[0], y[-5:])
+        assert torch.equal(g.layer_norm_backward(dy[-5:], x[-5:], w, mean[-5:], rstd[-5:])[0], dx[-5:])
+
+
 # ------------------------------------------------------------------ gate
 
 def _gate_k(E, spread):
