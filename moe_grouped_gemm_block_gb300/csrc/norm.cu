@@ -246,8 +246,8 @@ __device__ __forceinline__ float value_sum(const Raw8<T> (&raw)[NV]) {
 constexpr int kRingMaxStages = 16;
 constexpr int kRingVecs = 2;
 constexpr int kRingMaxColumnWarps = 16;
-constexpr int kRingMaxSumWarps = 3;
-constexpr int kRingMaxThreads = 32 * (kRingMaxColumnWarps + kRingMaxSumWarps + 1);  // 20 warps: 96 registers a thread
+// With 16 column warps: forward 24 warps of 80 registers, backward 20 warps of 96.
+constexpr int kRingThreads = 32 * 24, kRingGradThreads = 32 * 20;
 
 struct RingShared {
   uint64_t full[kRingMaxStages], ready[kRingMaxStages], empty[kRingMaxStages];
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
 // variance = mean (x - K)^2 - (mean (x - K))^2 then loses little to cancellation, as (K - mean)^2 is at most N / 256
 // variances whatever the values.
 template <typename TX, typename TY, int CL, bool SHIFT>
-__global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_ring_kernel(const NormArgs a, int32_t stages,
+__global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const NormArgs a, int32_t stages,
                                                                              int32_t stage_bytes, int32_t column_warps,
                                                                              int32_t sum_warps) {
   constexpr int NV = kRingVecs;
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(
 // order of the row's vectors: the first four values of every vector, then the other four (16-byte reads without
 // bank conflicts).
 template <typename TX, typename TY, int CL, bool SHIFT>
-__global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_grad_ring_kernel(
+__global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kernel(
     const NormGrad a, int32_t stages, int32_t stage_bytes, int32_t x_bytes, int32_t column_warps, int32_t sum_warps) {
   constexpr int NV = kRingVecs;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -937,12 +937,6 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_grad_ring_kerne
   const TY* dy = static_cast<const TY*>(a.dy) + shape.col(share.first);
   float4* ws = reinterpret_cast<float4*>(ring + stages * stage_bytes);  // [2][share.count]
   ring_init<CL>(sm, stages, column_warps);
-  for (int v = tid; v < share.count; v += blockDim.x) {
-    float2 f[4];
-    weights8(a.w, a.w_kind, shape.col(share.first + v), shape.mask(share.first + v), 1.0f, f);
-    ws[v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    ws[share.count + v] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-  }
   if constexpr (CL == 1) __syncthreads();
   else cluster_sync();  // every CTA of the cluster runs before it is written to
   const float inv_n = 1.0f / static_cast<float>(a.N);
@@ -959,6 +953,14 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) layer_norm_grad_ring_kerne
         }
       });
   } else if (warp >= column_warps) {
+    // the weights, in the order of the row's vectors; the first copies are already under way
+    for (int v = tid - columns; v < share.count; v += sum_warps * 32) {
+      float2 f[4];
+      weights8(a.w, a.w_kind, shape.col(share.first + v), shape.mask(share.first + v), 1.0f, f);
+      ws[v] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      ws[share.count + v] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    }
+    asm volatile("bar.sync 1, %0;" ::"r"(sum_warps * 32) : "memory");  // the sum warps among themselves
     SumRows it(warp - column_warps, sum_warps, stages);
     float nmu = 0.0f, nr = 0.0f;  // the next row's statistics
     auto stats = [&] {
@@ -1276,14 +1278,19 @@ struct RingPlan {
   int64_t rows_at_once;       // CTAs or clusters
 };
 // A ring for rows of `vecs` vectors, `size` bytes a value over all matrices of a stage; `extra` bytes of shared memory
-// a vector beside the stages.  As many CTAs an SM as its registers hold at 96 a thread: short rows take several.
-RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, Grid grid, int sms) {
+// a vector beside the stages (backward).  As many CTAs an SM as its registers hold: short rows take several.
+RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, int max_threads, Grid grid, int sms) {
   RingPlan p;
   p.cluster = vecs * 8 <= kRingMaxN ? 1 : 2;
   p.each = static_cast<int32_t>((vecs + p.cluster - 1) / p.cluster);
   p.column_warps = row_threads(p.each, kRingVecs) / 32;
-  p.sum_warps = p.column_warps > 6 ? kRingMaxSumWarps : 2;
-  const int per_sm = std::max(1, std::min(4, 65536 / (32 * (p.column_warps + p.sum_warps + 1) * 96)));
+  const int warps = max_threads / 32;  // what an SM's registers hold
+  // about a sum warp for two column warps, as far as there is room for them
+  p.sum_warps = std::max(2, std::min(warps - 1 - p.column_warps, (p.column_warps + 2) / 2));
+  // Short rows take several CTAs an SM.  Backward each of them writes its partial sums: with 16384 rows of 2048 bf16
+  // values two are 20% faster than one (48 against 58 us), with 2560 (fp32 rows) 13% slower (84 against 74).
+  int per_sm = std::max(1, std::min(4, warps / (p.column_warps + p.sum_warps + 1)));
+  if (extra && p.column_warps > 4) per_sm = 1;
   p.stage_bytes = p.each * 8 * size;
   p.stages = static_cast<int>(
       std::min<int64_t>(kRingMaxStages, (kRingBytes / per_sm - static_cast<int64_t>(p.each) * extra) / p.stage_bytes));
@@ -1332,7 +1339,7 @@ int layer_norm_vectors(const NormArgs& a, Grid grid, const DeviceInfo* dev, cuda
     const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 8 * static_cast<int64_t>(sms));
     go<<<static_cast<unsigned>(ctas), kNormThreads, 0, s>>>(a);
   } else if (vecs * 8 <= 2 * kRingMaxN) {
-    const RingPlan p = ring_plan(M, vecs, sizeof(TX), 0, grid, sms);
+    const RingPlan p = ring_plan(M, vecs, sizeof(TX), 0, kRingThreads, grid, sms);
     auto go = p.cluster == 1 ? layer_norm_ring_kernel<TX, TY, 1, SHIFT> : layer_norm_ring_kernel<TX, TY, 2, SHIFT>;
     return ring_launch(go, p, static_cast<int64_t>(p.stages) * p.stage_bytes, s, a, p.stages, p.stage_bytes,
                        p.column_warps, p.sum_warps);
@@ -1382,7 +1389,7 @@ int layer_norm_grad_vectors(const NormGrad& a, Grid grid, int64_t* P, const Devi
     go<<<static_cast<unsigned>(*P), kNormGradThreads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
   }
-  const RingPlan p = ring_plan(M, vecs, sizeof(TX) + sizeof(TY), 32, grid, sms);
+  const RingPlan p = ring_plan(M, vecs, sizeof(TX) + sizeof(TY), 32, kRingGradThreads, grid, sms);
   *P = p.rows_at_once;
   auto go = p.cluster == 1 ? layer_norm_grad_ring_kernel<TX, TY, 1, SHIFT>
                            : layer_norm_grad_ring_kernel<TX, TY, 2, SHIFT>;
