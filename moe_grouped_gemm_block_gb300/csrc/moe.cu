@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -19,15 +20,29 @@ namespace {
 //
 // A row is held by LPR lanes of a warp, VPL consecutive logits each (a warp works on 32 / LPR rows at once, 32 for 8
 // experts), so the whole of it stays in registers.  The k best are taken by merging the lanes' sorted lists: each
-// round finds the largest head, whose lane drops it.  The kernel is bound by those instructions, not by memory:
-// 65536 x 256 bf16 logits, top-8, 33 MB.
+// round finds the largest head, whose lane goes on to its next one.  The kernels are bound by their instructions,
+// not by memory.
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateMaxExperts = 2048;  // the routed layout's limit
 constexpr int kGateMaxTopk = 32;
-constexpr int kGateCluster = 8;        // CTAs that add their sums up before they write them
-constexpr int kGateMaxClusters = 76;   // partial sums
+constexpr int kGateCluster = 8;        // CTAs of a small call, which finish it together
+constexpr int kGateMaxParts = 608;     // CTAs, and partial sums, of a larger one
 constexpr int kGateBackwardCtas = 1216;
+
+// 2^x (relative error 2^-22; results below the normal range are 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float recip_approx(float x) {  // 1 / x to one unit in the last place
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// e^(v - mx) for v <= mx; the difference first, which cannot overflow to anything but -inf.
+__device__ __forceinline__ float exp_below(float v, float mx) { return exp2_approx((v - mx) * 1.4426950408889634f); }
 
 // The order of the selection as an unsigned integer: ascending in the value, NaN above everything (as a
 // descending sort has it), -0 equal to +0 (the addition turns -0 into +0 and every NaN into the positive one).
@@ -38,6 +53,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+// The same for two bf16 values in a word, 16 bits each.
+__device__ __forceinline__ uint32_t order_key2(uint32_t w) {
+  const __nv_bfloat162 z = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(0.0f, 0.0f));
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&z);
+  const uint32_t neg = u >> 15 & 0x00010001u;
+  return u ^ ((neg << 16) - neg | 0x80008000u);
 }
 
 template <int LPR>
@@ -68,10 +90,49 @@ __device__ __forceinline__ void sort8(Exchange ex) {
   ex(1, 2), ex(3, 4), ex(5, 6);
 }
 
-// The lane's logits by rank.  next(): the row's best that is left (its value and index, the same in all the row's
-// lanes), taken out of the list of the lane that has it.
+// VPL logits of a row as they lie in memory; -inf past the row's end.
+template <typename TL, int VPL>
+struct Logits {
+  Raw8<TL> raw[VPL / 8];
+  // vec: the row's groups of 8 lie on 16-byte boundaries and E is a multiple of 8
+  __device__ __forceinline__ void load(const TL* row, int base, int E, bool vec) {
+#pragma unroll
+    for (int v = 0; v < VPL / 8; ++v) {
+      const int c = base + 8 * v;
+      if (vec && c < E) {
+        raw[v].load(row + c);
+      } else {
+        TL f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < E ? row[c + i] : from_f32<TL>(-INFINITY);
+        raw[v].set(f);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[VPL]) const {
+#pragma unroll
+    for (int v = 0; v < VPL / 8; ++v) {
+      float2 p[4];
+      raw[v].get(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[8 * v + 2 * i] = p[i].x;
+        f[8 * v + 2 * i + 1] = p[i].y;
+      }
+    }
+  }
+};
+
+// The lane's logits by rank.  next(): the row's best that is left (the same in all the row's lanes), taken out of the
+// list of the lane that has it; value() and id() of what next() gave.  `list`: kListWords words of shared memory of
+// the lane's own, the last of them 0 (init_list).
 //
-// More than 256 experts: the lane keeps its largest key and looks for the next one when it is taken.
+// The general form, beyond 256 experts: the lane keeps its largest key and looks for the next one when it is taken.
+struct Pick {
+  uint32_t key;
+  int id;
+};
+constexpr int kListWords = 12;  // eight keys and the end; lanes 12 words apart write 16 bytes without bank conflicts
 template <typename TL, int VPL, int LPR>
 struct Ranking {
   static_assert(LPR == 32, "rows of a whole warp");
@@ -83,13 +144,15 @@ struct Ranking {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) head = max(head, key[i]);
   }
-  __device__ __forceinline__ void init(const float (&f)[VPL], int base_, int E) {
+  __device__ __forceinline__ void init(const Logits<TL, VPL>& l, int base_, int E, uint32_t*) {
     base = base_;
+    float f[VPL];
+    l.get(f);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = base + i < E ? order_key(f[i]) : 0u;
     find();
   }
-  __device__ __forceinline__ void next(float& v, int& id) {
+  __device__ __forceinline__ Pick next() {
     const uint32_t top = row_max<32>(head);
     const int from = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;
     int at = 0;
@@ -100,108 +163,115 @@ struct Ranking {
       for (int i = 0; i < VPL; ++i) key[i] = i == at ? 0u : key[i];
       find();
     }
-    id = __shfl_sync(0xffffffffu, base + at, from);
-    v = key_value(top);
+    return {top, __shfl_sync(0xffffffffu, base + at, from)};
   }
+  static __device__ __forceinline__ float value(const Pick& p) { return key_value(p.key); }
+  static __device__ __forceinline__ int id(const Pick& p) { return p.id; }
 };
 
-// bf16: the key's 16 bits and the index are one word, unlike any other of the row.
+// bf16: the key's 16 bits and the index are one word, unlike any other of the row.  The sorted list lies in shared
+// memory, its head in a register.
 template <int LPR>
 struct Ranking<__nv_bfloat16, 8, LPR> {
-  uint32_t key[8];
-  __device__ __forceinline__ void init(const float (&f)[8], int base, int E) {
+  uint32_t head;
+  const uint32_t* at;
+  __device__ __forceinline__ void init(const Logits<__nv_bfloat16, 8>& l, int base, int E, uint32_t* list) {
+    const uint32_t w[4] = {l.raw[0].v.x, l.raw[0].v.y, l.raw[0].v.z, l.raw[0].v.w};
+    uint32_t key[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      key[i] = base + i < E ? (order_key(f[i]) & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(base + i)) : 0u;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t k = order_key2(w[i]), c = 0xFFFFu - static_cast<uint32_t>(base + 2 * i);
+      key[2 * i] = __byte_perm(k, c, 0x1054);          // the low key over the place
+      key[2 * i + 1] = __byte_perm(k, c - 1u, 0x3254);  // the high one
+    }
+    if (base + 8 > E) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = base + i < E ? key[i] : 0u;
+    }
     sort8([&](int a, int b) {
       const uint32_t hi = max(key[a], key[b]), lo = min(key[a], key[b]);
       key[a] = hi;
       key[b] = lo;
     });
+    head = key[0];
+    at = list;
+    reinterpret_cast<uint4*>(list)[0] = make_uint4(key[0], key[1], key[2], key[3]);
+    reinterpret_cast<uint4*>(list)[1] = make_uint4(key[4], key[5], key[6], key[7]);
   }
-  __device__ __forceinline__ void next(float& v, int& id) {
-    const uint32_t top = row_max<LPR>(key[0]);
-    if (key[0] == top) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i) key[i] = key[i + 1];
-      key[7] = 0u;
-    }
-    id = static_cast<int>(0xFFFFu - (top & 0xFFFFu));
-    v = __uint_as_float(__float_as_uint(key_value(top & 0xFFFF0000u)) & 0xFFFF0000u);
+  __device__ __forceinline__ Pick next() {
+    const uint32_t top = row_max<LPR>(head);
+    if (head == top) head = *++at;
+    return {top, 0};
   }
+  static __device__ __forceinline__ float value(const Pick& p) {
+    return __uint_as_float(__float_as_uint(key_value(p.key & 0xFFFF0000u)) & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ int id(const Pick& p) { return static_cast<int>(0xFFFFu - (p.key & 0xFFFFu)); }
 };
 
 // fp32: keys sorted with their places; of equal keys the lower place comes first, of equal heads the lower lane.
 template <int LPR>
 struct Ranking<float, 8, LPR> {
-  uint32_t key[8];
+  uint32_t head;
   uint32_t places;  // a hexadecimal digit each, the head's lowest
+  const uint32_t* at;
   int base;
-  __device__ __forceinline__ void init(const float (&f)[8], int base_, int E) {
+  __device__ __forceinline__ void init(const Logits<float, 8>& l, int base_, int E, uint32_t* list) {
     base = base_;
-    uint32_t at[8];
+    float f[8];
+    l.get(f);
+    uint32_t key[8], place[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      key[i] = base + i < E ? order_key(f[i]) : 0u;
-      at[i] = i;
+      key[i] = order_key(f[i]);
+      place[i] = i;
+    }
+    if (base + 8 > E) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = base + i < E ? key[i] : 0u;
     }
     sort8([&](int a, int b) {
-      const bool swap = key[a] < key[b] || (key[a] == key[b] && at[a] > at[b]);
-      const uint32_t k = key[a], p = at[a];
+      const bool swap = key[a] < key[b] || (key[a] == key[b] && place[a] > place[b]);
+      const uint32_t k = key[a], p = place[a];
       key[a] = swap ? key[b] : k;
       key[b] = swap ? k : key[b];
-      at[a] = swap ? at[b] : p;
-      at[b] = swap ? p : at[b];
+      place[a] = swap ? place[b] : p;
+      place[b] = swap ? p : place[b];
     });
     places = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) places |= at[i] << (4 * i);
+    for (int i = 0; i < 8; ++i) places |= place[i] << (4 * i);
+    head = key[0];
+    at = list;
+    reinterpret_cast<uint4*>(list)[0] = make_uint4(key[0], key[1], key[2], key[3]);
+    reinterpret_cast<uint4*>(list)[1] = make_uint4(key[4], key[5], key[6], key[7]);
   }
-  __device__ __forceinline__ void next(float& v, int& id) {
+  __device__ __forceinline__ Pick next() {
     const int lane = threadIdx.x & 31;
-    const uint32_t top = row_max<LPR>(key[0]);
-    int from = lane;
+    const uint32_t top = row_max<LPR>(head);
+    int from = lane, id = base + static_cast<int>(places & 7u);
     if constexpr (LPR > 1) {
       const uint32_t row = (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u) << (lane & ~(LPR - 1) & 31);
-      from = __ffs(__ballot_sync(0xffffffffu, key[0] == top) & row) - 1;
+      from = __ffs(__ballot_sync(0xffffffffu, head == top) & row) - 1;
+      id = __shfl_sync(0xffffffffu, id, from);
     }
-    id = base + static_cast<int>(places & 7u);
-    if constexpr (LPR > 1) id = __shfl_sync(0xffffffffu, id, from);
-    v = key_value(top);
     if (lane == from) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i) key[i] = key[i + 1];
-      key[7] = 0u;
+      head = *++at;
       places >>= 4;
     }
+    return {top, id};
   }
+  static __device__ __forceinline__ float value(const Pick& p) { return key_value(p.key); }
+  static __device__ __forceinline__ int id(const Pick& p) { return p.id; }
 };
-
-// Logits base .. base + VPL - 1 of a row; -inf past its end.  vec: the row's groups of 8 lie on 16-byte boundaries and
-// E is a multiple of 8.
-template <int VPL, typename TL>
-__device__ __forceinline__ void load_logits(const TL* row, int base, int E, bool vec, float (&f)[VPL]) {
-#pragma unroll
-  for (int v = 0; v < VPL; v += 8) {
-    if (vec && base + v < E) {
-      float g[8];
-      load8(row + base + v, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[v + i] = g[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[v + i] = base + v + i < E ? to_f32(row[base + v + i]) : -INFINITY;
-    }
-  }
-}
 
 struct GateArgs {
   const void* logits;
   const uint8_t* mask;
   int32_t* ids;
   float* weights;
-  float* part_p;    // [clusters][E]
-  int32_t* part_c;  // [clusters][E]
+  float* part_p;    // [CTAs][E]
+  int32_t* part_c;  // [CTAs][E]
   int32_t* counts;
   float* loss;
   int64_t T, ldl;
@@ -226,31 +296,37 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return n;
 }
 
-// Shared memory of the forward kernel: [E] sums of p and [E] counts of the CTA, then per warp its rows' selection
-// (ids, exponentials) and factors; the warps' sums of p [WARPS][E] take that room at the end.
+// Shared memory of the forward kernel: [E] sums of p and [E] counts of the CTA, then per warp the lanes' lists and its
+// rows' picks (keys, ids, weights) and factors; the warps' sums of p [WARPS][E] take that room at the end.
 template <int LPR>
-__host__ __device__ constexpr int gate_warp_words(int topk) { return (32 / LPR) * (2 * topk + 1); }
+__host__ __device__ constexpr int gate_warp_words(int topk) {
+  return 32 * kListWords + ((32 / LPR) * (3 * topk + 1) + 3) / 4 * 4;
+}
 template <int LPR>
 size_t gate_smem(int E, int topk) {
-  return 4 * (2 * static_cast<size_t>(E) + std::max(kGateWarps * E, kGateWarps * gate_warp_words<LPR>(topk)));
+  return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + std::max(kGateWarps * E, kGateWarps * gate_warp_words<LPR>(topk)));
 }
 
 // A warp's rows, and so each partial sum's terms and their order, follow from the grid alone.
 template <typename TL, int VPL, int LPR>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_kernel(const GateArgs a) {
   constexpr int G = 32 / LPR;  // rows a warp at once
-  extern __shared__ float smem[];
+  using Rank = Ranking<TL, VPL, LPR>;
+  extern __shared__ __align__(16) float smem[];
   __shared__ float2 s_loss[kGateCluster];
   __shared__ float red[2 * 2 * kGateWarps];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
-  const int E = a.E, topk = a.topk;
+  const int E = a.E, topk = a.topk, padded = (E + 3) / 4 * 4;
   float* sum_p = smem;
-  int32_t* cnt = reinterpret_cast<int32_t*>(smem + E);
-  float* rest = smem + 2 * E;
-  int32_t* sel_id = reinterpret_cast<int32_t*>(rest + warp * gate_warp_words<LPR>(topk));
-  float* sel_e = reinterpret_cast<float*>(sel_id + G * topk);
-  float* factor = sel_e + G * topk;
+  int32_t* cnt = reinterpret_cast<int32_t*>(smem + padded);
+  float* rest = smem + 2 * padded;
+  uint32_t* list = reinterpret_cast<uint32_t*>(rest) + warp * gate_warp_words<LPR>(topk) + lane * kListWords;
+  uint32_t* pick_key = reinterpret_cast<uint32_t*>(rest) + warp * gate_warp_words<LPR>(topk) + 32 * kListWords;
+  int32_t* pick_id = reinterpret_cast<int32_t*>(pick_key + G * topk);
+  float* pick_w = reinterpret_cast<float*>(pick_id + G * topk);
+  float* factor = pick_w + G * topk;
+  list[8] = 0u;  // the end of every list
   for (int e = threadIdx.x; e < E; e += kGateThreads) cnt[e] = 0;
   __syncthreads();
   const TL* logits = static_cast<const TL*>(a.logits);
@@ -259,49 +335,66 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_kernel(const GateArgs a
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps * G;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * G; t0 < a.T; t0 += stride) {
-    const int64_t t = t0 + grp;
-    const bool in = t < a.T;
-    const bool real = in && (!a.mask || a.mask[t]);
-    float f[VPL];
-    load_logits(logits + (in ? t : t0) * a.ldl, base, E, a.vec, f);
-    Ranking<TL, VPL, LPR> rank;
-    rank.init(f, base, E);
-    float mx = 0.0f, picked = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-      float v;
-      int id;
-      rank.next(v, id);
-      if (j == 0) mx = v == -INFINITY ? 0.0f : v;  // every expert ruled out: the exponentials are all 0
-      const float e = __expf(v - mx);
-      picked += e;
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * G;
+  Logits<TL, VPL> next;
+  bool next_real = false;
+  auto fetch = [&](int64_t at) {
+    const int64_t t = at + grp < a.T ? at + grp : a.T - 1;
+    next_real = at + grp < a.T && (!a.mask || a.mask[t]);
+    next.load(logits + t * a.ldl, base, E, a.vec);
+  };
+  if (t0 < a.T) fetch(t0);
+  for (; t0 < a.T; t0 += stride) {
+    Logits<TL, VPL> l = next;
+    const bool real = next_real;
+    if (t0 + stride < a.T) fetch(t0 + stride);
+    Rank rank;
+    rank.init(l, base, E, list);
+    Pick first = rank.next();
+    for (int j = 0;; ) {
       if (sub == 0) {
-        sel_id[grp * topk + j] = id;
-        sel_e[grp * topk + j] = e;
+        pick_key[grp * topk + j] = first.key;
+        if constexpr (!std::is_same_v<TL, __nv_bfloat16> || VPL != 8) pick_id[grp * topk + j] = first.id;
       }
+      if (++j == topk) break;
+      first = rank.next();
     }
-    float s = 0.0f;
+    __syncwarp();
+    float mx = Rank::value({pick_key[grp * topk], 0});
+    if (mx == -INFINITY) mx = 0.0f;  // every expert ruled out: the exponentials are all 0
+    // the row's picks, a lane each (or several)
+    float picked = 0.0f;
+    for (int j = sub; j < topk; j += LPR) {
+      Pick p{pick_key[grp * topk + j], 0};
+      const float e = exp_below(Rank::value(p), mx);
+      picked += e;
+      if constexpr (std::is_same_v<TL, __nv_bfloat16> && VPL == 8) pick_id[grp * topk + j] = Rank::id(p);
+      pick_w[grp * topk + j] = e;
+    }
+    picked = row_sum<LPR>(picked);
+    float f[VPL], s = 0.0f;
+    l.get(f);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      f[i] = __expf(f[i] - mx);
+      f[i] = exp_below(f[i], mx);
       s += f[i];
     }
     s = row_sum<LPR>(s);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+    const float inv = s == 0.0f ? 0.0f : recip_approx(s);
     if (real) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[i] = fmaf(f[i], inv, acc[i]);
     }
-    if (sub == 0) factor[grp] = !real ? -1.0f : a.renorm ? (picked == 0.0f ? 0.0f : 1.0f / picked) : inv;
+    if (sub == 0) factor[grp] = !real ? -1.0f : a.renorm ? (picked == 0.0f ? 0.0f : recip_approx(picked)) : inv;
     __syncwarp();
     // the warp's rows are neighbours: their results go out in one piece
     for (int q = lane; q < G * topk; q += 32) {
       const int g = G == 1 ? 0 : static_cast<int>((static_cast<float>(q) + 0.5f) * inv_k);
       if (t0 + g >= a.T) break;
-      const int id = sel_id[q];
+      const int id = pick_id[q];
       const float w = factor[g];
       a.ids[t0 * topk + q] = id;
-      a.weights[t0 * topk + q] = w == -1.0f ? 0.0f : sel_e[q] * w;
+      a.weights[t0 * topk + q] = w == -1.0f ? 0.0f : pick_w[q] * w;
       if (w != -1.0f) atomicAdd(cnt + id, 1);  // whole numbers: the order does not matter
     }
     __syncwarp();
@@ -324,7 +417,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_kernel(const GateArgs a
     for (int w = 0; w < kGateWarps; ++w) s += rest[w * E + e];
     sum_p[e] = s;
   }
-  // the cluster's: each CTA takes a share of the experts
+  // a cluster's: each CTA takes a share of the experts
   const int ranks = static_cast<int>(cluster_size()), me = static_cast<int>(cluster_ctarank());
   const int each = (E + ranks - 1) / ranks, lo = me * each, hi = min(E, lo + each);
   cluster_sync();
@@ -365,8 +458,8 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_kernel(const GateArgs a
   }
 }
 
-// Counts and loss from the clusters' partial sums, in their order: 32 experts a warp, the warps beside each other
-// taking a share of the partial sums.
+// Counts and loss from the CTAs' partial sums, in their order.  One cluster; a CTA takes 32 experts at a time, its warps
+// a share of the partial sums each.
 constexpr int kGateJoinThreads = 1024;
 __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int32_t P, int32_t E, int32_t topk,
@@ -374,18 +467,18 @@ __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
   constexpr int W = kGateJoinThreads / 32;
   __shared__ float s_p[W][32];
   __shared__ int32_t s_c[W][32];
-  __shared__ float red[2 * 2 * W];
+  __shared__ float2 s_loss[kGateCluster];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cols = min(W, (E + 31) / 32), slices = W / cols;  // columns of 32 experts at once, warps for each
-  const int col = warp % cols, slice = warp / cols;
-  float v[2] = {0.0f, 0.0f};  // sum_e c_e sum_t p_te, sum_e c_e
+  const int ranks = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+  float v[2] = {0.0f, 0.0f};  // warp 0: sum_e c_e sum_t p_te, sum_e c_e
+  cluster_sync();             // every CTA runs before it is written to
   griddep_wait();
-  for (int e0 = 0; e0 < E; e0 += 32 * cols) {
-    const int e = e0 + 32 * col + lane;
+  for (int e0 = 32 * me; e0 < E; e0 += 32 * ranks) {
+    const int e = e0 + lane;
     float p = 0.0f;
     int32_t c = 0;
-    if (slice < slices && e < E) {
-      const int lo = P * slice / slices, hi = P * (slice + 1) / slices;
+    if (e < E) {
+      const int lo = P * warp / W, hi = P * (warp + 1) / W;
 #pragma unroll 4
       for (int i = lo; i < hi; ++i) {
         p += __ldcg(part_p + static_cast<int64_t>(i) * E + e);
@@ -395,10 +488,11 @@ __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     s_p[warp][lane] = p;
     s_c[warp][lane] = c;
     __syncthreads();
-    if (slice == 0 && e < E) {
-      for (int i = 1; i < slices; ++i) {
-        p += s_p[col + i * cols][lane];
-        c += s_c[col + i * cols][lane];
+    if (warp == 0 && e < E) {
+#pragma unroll
+      for (int i = 1; i < W; ++i) {
+        p += s_p[i][lane];
+        c += s_c[i][lane];
       }
       counts[e] = c;
       v[0] += static_cast<float>(c) * p;
@@ -406,17 +500,29 @@ __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     }
     __syncthreads();
   }
-  cta_sum<W>(v, red, 0);
-  if (threadIdx.x == 0 && loss) *loss = balance_loss(v[0], v[1], E, topk, coef);
+  if (warp == 0) {
+    const float cp = warp_sum(v[0]), c = warp_sum(v[1]);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(mapa_shared(smem_u32(&s_loss[me]), 0)), "f"(cp),
+                   "f"(c)
+                   : "memory");
+  }
+  cluster_sync();
+  if (me == 0 && threadIdx.x == 0 && loss) {
+    float cp = 0.0f, c = 0.0f;
+    for (int r = 0; r < ranks; ++r) {
+      cp += s_loss[r].x;
+      c += s_loss[r].y;
+    }
+    *loss = balance_loss(cp, c, E, topk, coef);
+  }
 }
 
 // dl_te = p_te (G_te - sum_e G_te p_te),  G_te = g_e + sum_j [ids_tj = e] dp_tj,
 // g_e = dloss coef E c_e / (k Tv^2),  dp_tj = dw_tj, or (dw_tj - sum_i dw_ti w_ti) / S_t where renormalised
-// (S_t = the selected probabilities' sum).  Masked tokens get zeros.  Rows as in the forward kernel; the selected
-// experts' dw come to their lanes through a row of shared memory, where this pattern (a NaN that no arithmetic makes)
-// marks an expert that was not selected.
-constexpr uint32_t kNotSelected = 0xFFFFDEADu;
-
+// (S_t = the selected probabilities' sum).  Masked tokens get zeros.  Rows as in the forward kernel.  Every lane writes
+// p (g - inner product) for its logits; the selected experts' values, a few a row, are worked out by a lane each (it
+// reads their logits again) and written over them.
 struct GateGrad {
   const void* logits;
   const uint8_t* mask;
@@ -433,15 +539,14 @@ struct GateGrad {
 template <typename TL, int VPL, int LPR>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const GateGrad a) {
   constexpr int G = 32 / LPR;
+  constexpr int kPicks = LPR >= kGateMaxTopk ? 1 : LPR * 8 >= kGateMaxTopk ? kGateMaxTopk / LPR : 8;  // a lane's, at most
   __shared__ float red[2 * kGateWarps];
-  extern __shared__ float smem[];  // per warp: G rows of LPR * VPL
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
   const int E = a.E, topk = a.topk;
-  float* row = smem + warp * (32 * VPL);
   float n[1] = {0.0f};
   for (int e = threadIdx.x; e < E; e += kGateThreads) n[0] += static_cast<float>(a.counts[e]);
   cta_sum<kGateWarps>(n, red, 0);
-  const float k = static_cast<float>(topk), tv = n[0] / k, inv_k = 1.0f / k;
+  const float k = static_cast<float>(topk), tv = n[0] / k;
   const float scale = a.dloss && tv > 0.0f ? *a.dloss * a.coef * static_cast<float>(E) / (k * tv * tv) : 0.0f;
   float g[VPL];
 #pragma unroll
@@ -449,84 +554,108 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
   const TL* logits = static_cast<const TL*>(a.logits);
   TL* dlogits = static_cast<TL*>(a.dlogits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps * G;
-  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * G; t0 < a.T; t0 += stride) {
-    const int64_t t = t0 + grp;
-    const bool in = t < a.T;
-    const bool real = in && (!a.mask || a.mask[t]);
-    float f[VPL], d[VPL];
-    load_logits(logits + (in ? t : t0) * a.ldl, base, E, a.vec, f);
-    if (a.dweights) {
-      uint4* mine = reinterpret_cast<uint4*>(row + lane * VPL);
-#pragma unroll
-      for (int i = 0; i < VPL / 4; ++i) mine[i] = make_uint4(kNotSelected, kNotSelected, kNotSelected, kNotSelected);
-      __syncwarp();
-      for (int q = lane; q < G * topk; q += 32) {
-        const int r = G == 1 ? 0 : static_cast<int>((static_cast<float>(q) + 0.5f) * inv_k);
-        if (t0 + r >= a.T) break;
-        const int id = a.ids[t0 * topk + q];
-        if (id >= 0 && id < E) row[r * (LPR * VPL) + id] = a.dweights[t0 * topk + q];
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) d[i] = row[lane * VPL + i];
-      __syncwarp();
+  // the next row's logits and this lane's (first) selected expert and gradient are on their way while a row is worked on
+  Logits<TL, VPL> next;
+  bool next_real = false;
+  int next_id = -1;
+  float next_dw = 0.0f;
+  auto fetch = [&](int64_t t) {  // t < a.T, or a row past the end, of which nothing is used
+    const int64_t r = min(t, a.T - 1);
+    next_real = t < a.T && (!a.mask || a.mask[r]);
+    next.load(logits + r * a.ldl, base, E, a.vec);
+    if (a.dweights && sub < topk) {
+      next_id = a.ids[r * topk + sub];
+      next_dw = a.dweights[r * topk + sub];
     }
+  };
+  int64_t t = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * G + grp;
+  if (t - grp < a.T) fetch(t);
+  for (; t - grp < a.T; t += stride) {
+    const Logits<TL, VPL> l = next;
+    const bool real = next_real;
+    const int id0 = next_id;
+    const float dw0 = next_dw;
+    if (t - grp + stride < a.T) fetch(t + stride);
+    const TL* row = logits + min(t, a.T - 1) * a.ldl;
+    // the lane's selected experts, the row's sub, sub + LPR, ...: their logits, or id -1 for none
+    int id[kPicks];
+    float dw[kPicks], e[kPicks];
+#pragma unroll
+    for (int j = 0; j < kPicks; ++j) {
+      const int q = j * LPR + sub;
+      id[j] = -1;
+      dw[j] = 0.0f;
+      e[j] = -INFINITY;
+      if (a.dweights && q < topk) {
+        id[j] = j == 0 ? id0 : a.ids[min(t, a.T - 1) * topk + q];
+        dw[j] = j == 0 ? dw0 : a.dweights[min(t, a.T - 1) * topk + q];
+        if (id[j] >= 0 && id[j] < E) e[j] = to_f32(row[id[j]]);
+        else id[j] = -1;
+      }
+    }
+    float f[VPL];
+    l.get(f);
     float mx = f[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, f[i]);
 #pragma unroll
     for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     if (mx == -INFINITY) mx = 0.0f;
-    float s = 0.0f;
+    // sums over the exponentials f = s p: all of them, with g, the selected ones, and with their dw
+    float s = 0.0f, sum_g = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      f[i] = __expf(f[i] - mx);
+      f[i] = exp_below(f[i], mx);
       s += f[i];
+      sum_g = fmaf(g[i], f[i], sum_g);
     }
-    s = row_sum<LPR>(s);
-    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+    float sel = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) f[i] *= inv;
-    float G_[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) G_[i] = g[i];
-    if (a.dweights) {
-      float total = 0.0f, dot = 0.0f;
-      if (a.renorm) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (__float_as_uint(d[i]) != kNotSelected) {
-            total += f[i];
-            dot = fmaf(d[i], f[i], dot);
-          }
-        total = row_sum<LPR>(total);
-        dot = row_sum<LPR>(dot);
-        total = total == 0.0f ? 0.0f : 1.0f / total;
-        dot *= total;
-      }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (__float_as_uint(d[i]) != kNotSelected) G_[i] += a.renorm ? (d[i] - dot) * total : d[i];
+    for (int j = 0; j < kPicks; ++j) {
+      if (j * LPR >= topk) break;
+      e[j] = exp_below(e[j], mx);
+      sel += e[j];
+      if (id[j] >= 0) dot = fmaf(dw[j], e[j], dot);
     }
-    float inner = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) inner = fmaf(G_[i], f[i], inner);
-    inner = row_sum<LPR>(inner);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) f[i] = real ? f[i] * (G_[i] - inner) : 0.0f;
-    if (!in) continue;
+    for (int off = LPR / 2; off > 0; off >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, off);
+      sum_g += __shfl_xor_sync(0xffffffffu, sum_g, off);
+      sel += __shfl_xor_sync(0xffffffffu, sel, off);
+      dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    }
+    const float inv = !real || s == 0.0f ? 0.0f : recip_approx(s);
+    const float inv_sel = sel == 0.0f ? 0.0f : recip_approx(sel);
+    // renormalised, the weights' gradient has no component along the weights: the inner product is g's alone
+    const float inner = inv * (a.renorm ? sum_g : sum_g + dot);
+    const float per = a.renorm ? s * inv_sel : 1.0f;         // 1 / S_t
+    const float mean = a.renorm ? dot * inv_sel : 0.0f;      // sum_i dw_i w_i
     TL* out = dlogits + t * a.ldd;
+    if (t < a.T) {
 #pragma unroll
-    for (int v = 0; v < VPL; v += 8) {
-      if (a.vec && base + v < E) {
-        float o[8];
+      for (int i = 0; i < VPL; ++i) f[i] = real ? f[i] * inv * (g[i] - inner) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = f[v + i];
-        store8(out + base + v, o);
-      } else {
+      for (int v = 0; v < VPL; v += 8) {
+        if (a.vec && base + v < E) {
+          float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (base + v + i < E) out[base + v + i] = from_f32<TL>(f[v + i]);
+          for (int i = 0; i < 8; ++i) o[i] = f[v + i];
+          store8(out + base + v, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (base + v + i < E) out[base + v + i] = from_f32<TL>(f[v + i]);
+        }
+      }
+    }
+    if (!a.dweights) continue;
+    __syncwarp();  // over what the row's lanes have written
+#pragma unroll
+    for (int j = 0; j < kPicks; ++j) {
+      if (j * LPR >= topk) break;
+      if (real && id[j] >= 0) {
+        const float own = fmaf(per, dw[j] - mean, scale * static_cast<float>(a.counts[id[j]]));
+        out[id[j]] = from_f32<TL>(e[j] * inv * (own - inner));
       }
     }
   }
@@ -624,28 +753,39 @@ int allow_smem(Kernel kern, size_t bytes) {
   return FP8G_OK;
 }
 
-// The clusters of a forward call, at most (each writes a row of partial sums).
-int64_t gate_clusters(int64_t T) {
-  return std::min<int64_t>(kGateMaxClusters, (T + kGateCluster * kGateWarps - 1) / (kGateCluster * kGateWarps));
+// The CTAs of a forward call, at most (each writes a row of partial sums).
+int64_t gate_parts(int64_t T) { return std::min<int64_t>(kGateMaxParts, (T + kGateWarps - 1) / kGateWarps); }
+
+template <typename Kernel>
+int resident_ctas(Kernel kern, size_t smem, const DeviceInfo* dev) {
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGateThreads, smem) != cudaSuccess || per_sm < 1) {
+    cudaGetLastError();
+    per_sm = 1;
+  }
+  return per_sm * dev->sm_count;
 }
 
 template <typename TL, int VPL, int LPR>
-int gate_launch(const GateArgs& a, cudaStream_t s) {
+int gate_launch(const GateArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   auto kern = moe_gate_kernel<TL, VPL, LPR>;
   const size_t smem = gate_smem<LPR>(a.E, a.topk);
   int st = allow_smem(kern, smem);
   if (st != FP8G_OK) return st;
-  // one CTA for a few rounds of its warps' rows (its latency is below a cluster's), else clusters
+  // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs as
+  // are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38).
   const int64_t at_once = kGateWarps * (32 / LPR);
-  const int cluster = a.T <= 2 * at_once ? 1 : kGateCluster;
-  const int64_t clusters =
-      cluster == 1 ? 1 : std::min<int64_t>(kGateMaxClusters, (a.T + cluster * at_once - 1) / (cluster * at_once));
+  const bool few = a.T <= 2 * kGateCluster * at_once;
+  const int cluster = a.T <= 2 * at_once || !few ? 1 : kGateCluster;
+  const int64_t ctas = few ? cluster
+                           : std::min<int64_t>({(a.T + at_once - 1) / at_once, resident_ctas(kern, smem, dev),
+                                                gate_parts(a.T)});
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kGateThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -655,14 +795,17 @@ int gate_launch(const GateArgs& a, cudaStream_t s) {
     cudaGetLastError();
     return FP8G_ERR_CUDA;
   }
-  if (clusters == 1) return FP8G_OK;  // the cluster has finished the counts and the loss itself
-  cfg.gridDim = dim3(1);
+  if (few) return FP8G_OK;
+  const int joins = std::min(kGateCluster, (a.E + 31) / 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(joins));
   cfg.blockDim = dim3(kGateJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(joins);
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, moe_gate_join_kernel, static_cast<const float*>(a.part_p),
-                         static_cast<const int32_t*>(a.part_c), static_cast<int32_t>(clusters), a.E, a.topk, a.coef,
+                         static_cast<const int32_t*>(a.part_c), static_cast<int32_t>(ctas), a.E, a.topk, a.coef,
                          a.counts, a.loss) != cudaSuccess) {
     cudaGetLastError();
     return FP8G_ERR_CUDA;
@@ -673,12 +816,9 @@ int gate_launch(const GateArgs& a, cudaStream_t s) {
 template <typename TL, int VPL, int LPR>
 int gate_backward_launch(const GateGrad& a, cudaStream_t s) {
   auto kern = moe_gate_backward_kernel<TL, VPL, LPR>;
-  const size_t smem = static_cast<size_t>(kGateWarps) * 32 * VPL * 4;
-  int st = allow_smem(kern, smem);
-  if (st != FP8G_OK) return st;
   const int64_t at_once = kGateWarps * (32 / LPR);
   const int64_t ctas = std::min<int64_t>((a.T + at_once - 1) / at_once, kGateBackwardCtas);
-  kern<<<static_cast<unsigned>(ctas), kGateThreads, smem, s>>>(a);
+  kern<<<static_cast<unsigned>(ctas), kGateThreads, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
@@ -717,7 +857,7 @@ using namespace fp8g;
 
 extern "C" int fp8g_moe_gate_workspace(int64_t T, int32_t E, int64_t* bytes) {
   if (T < 0 || T > 0x7FFFFFFF || E < 1 || E > kGateMaxExperts || !bytes) return FP8G_ERR_INVALID_ARG;
-  *bytes = gate_clusters(T) * E * 8;
+  *bytes = gate_parts(T) * E * 8;
   return FP8G_OK;
 }
 
@@ -729,7 +869,7 @@ extern "C" int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32
       topk > kGateMaxTopk || topk > E || (renormalize != 0 && renormalize != 1) || T * topk > 0x7FFFFFFF)
     return FP8G_ERR_INVALID_ARG;
   if (!counts || (T > 0 && (!logits || !topk_ids || !topk_weights))) return FP8G_ERR_INVALID_ARG;
-  if (T > 0 && (!workspace || workspace_bytes < gate_clusters(T) * E * 8)) return FP8G_ERR_INVALID_ARG;
+  if (T > 0 && (!workspace || workspace_bytes < gate_parts(T) * E * 8)) return FP8G_ERR_INVALID_ARG;
   if (!aligned_to(logits, dtype_size(dtype)) || !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) ||
       !aligned_to(counts, 4) || !aligned_to(loss, 4) || !aligned16(workspace))
     return FP8G_ERR_ALIGNMENT;
@@ -748,10 +888,10 @@ extern "C" int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32
   GateArgs a{};
   a.logits = logits, a.mask = token_mask, a.ids = topk_ids, a.weights = topk_weights, a.counts = counts, a.loss = loss;
   a.part_p = static_cast<float*>(workspace);
-  a.part_c = reinterpret_cast<int32_t*>(a.part_p + gate_clusters(T) * E);
+  a.part_c = reinterpret_cast<int32_t*>(a.part_p + gate_parts(T) * E);
   a.T = T, a.ldl = ldl, a.E = E, a.topk = topk, a.renorm = renormalize, a.coef = loss_coef;
   a.vec = logit_vectors(logits, ldl, E, dtype);
-  return (dtype == FP8G_F32 ? gate_form<float>(E) : gate_form<__nv_bfloat16>(E))(a, s);
+  return (dtype == FP8G_F32 ? gate_form<float>(E) : gate_form<__nv_bfloat16>(E))(a, dev, s);
 }
 
 extern "C" int fp8g_moe_gate_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl,

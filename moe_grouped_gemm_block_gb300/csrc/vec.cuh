@@ -56,6 +56,76 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// Eight values as they lie in memory, and as four pairs for the two-wide fp32 instructions.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_stream(const __nv_bfloat16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void set(const __nv_bfloat16 (&f)[8]) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(f);
+    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+  // value j by value j from memory where the mask has it, zero elsewhere
+  __device__ __forceinline__ void gather(const __nv_bfloat16* p, uint32_t mask) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = mask >> j & 1u ? h[j] : 0u;
+    v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  // keeps the values that the mask has, zeroes the others
+  __device__ __forceinline__ void keep(uint32_t mask) {
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] &= (mask >> (2 * j) & 1u ? 0xFFFFu : 0u) | (mask >> (2 * j + 1) & 1u ? 0xFFFF0000u : 0u);
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void load_stream(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  __device__ __forceinline__ void gather(const float* p, uint32_t mask) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = mask >> j & 1u ? p[j] : 0.0f;
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  __device__ __forceinline__ void keep(uint32_t mask) {
+    a.x = mask & 1u ? a.x : 0.0f, a.y = mask & 2u ? a.y : 0.0f;
+    a.z = mask & 4u ? a.z : 0.0f, a.w = mask & 8u ? a.w : 0.0f;
+    b.x = mask & 16u ? b.x : 0.0f, b.y = mask & 32u ? b.y : 0.0f;
+    b.z = mask & 64u ? b.z : 0.0f, b.w = mask & 128u ? b.w : 0.0f;
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    f[0] = make_float2(a.x, a.y);
+    f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y);
+    f[3] = make_float2(b.z, b.w);
+  }
+};
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
