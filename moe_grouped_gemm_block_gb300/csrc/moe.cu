@@ -663,12 +663,14 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
 
 // ---------------------------------------------------------------- combine
 //     out_t = residual_t + sum_j w_tj D[row_tj]
+// Both directions are bound by memory: 16-byte loads, the rows of several entries in flight per thread.
 constexpr int kCombineThreads = 128;
+constexpr int kCombineSpan = kCombineThreads * 8;  // columns a CTA takes at once
 
 // The row of an entry, or -1 where it is dropped or out of range (the latter is flagged).
 __device__ __forceinline__ int32_t entry(const int32_t* __restrict__ entry_row, int64_t i, int64_t M,
                                          unsigned int* status) {
-  const int32_t r = entry_row[i];
+  const int32_t r = __ldg(entry_row + i);
   if (r >= M) {
     record_status(status, FP8G_ERR_DEVICE_ASSERT);
     return -1;
@@ -676,68 +678,124 @@ __device__ __forceinline__ int32_t entry(const int32_t* __restrict__ entry_row, 
   return r;
 }
 
-template <typename TO>
+// A CTA (blockIdx.x, blockIdx.y) takes token blockIdx.x and every gridDim.y-th span of columns; JN entries' rows are in
+// flight at once.
+template <typename TO, int JN>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(
-    const __nv_bfloat16* __restrict__ D, int64_t M, int64_t N, int64_t ldd, const int32_t* __restrict__ entry_row,
-    int32_t topk, const float* __restrict__ weights, const TO* residual, int64_t ldr,
-    TO* out, int64_t ldo, unsigned int* status) {
+    const __nv_bfloat16* __restrict__ D, int64_t M, int32_t N, int64_t ldd, const int32_t* __restrict__ entry_row,
+    int32_t topk, const float* __restrict__ weights, const TO* residual, int64_t ldr, TO* out, int64_t ldo,
+    unsigned int* status) {
   const int64_t t = blockIdx.x;
-  for (int64_t n = threadIdx.x * 8; n < N; n += kCombineThreads * 8) {
+  for (int64_t n = static_cast<int64_t>(blockIdx.y) * kCombineSpan + threadIdx.x * 8; n < N;
+       n += static_cast<int64_t>(gridDim.y) * kCombineSpan) {
+    Raw8<TO> res;
+    if (residual) res.load_stream(residual + t * ldr + n);
     float acc[8] = {};
-    if (residual) load8(residual + t * ldr + n, acc);
-    for (int j = 0; j < topk; ++j) {
-      const int32_t r = entry(entry_row, t * topk + j, M, status);
-      if (r < 0) continue;
-      const float w = weights ? weights[t * topk + j] : 1.0f;
-      float f[8];
-      load8(D + r * ldd + n, f);
+    for (int j0 = 0; j0 < topk; j0 += JN) {
+      uint4 raw[JN];
+      float w[JN];
+      int32_t r[JN];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += w * f[i];
+      for (int u = 0; u < JN; ++u) {
+        r[u] = j0 + u < topk ? entry(entry_row, t * topk + j0 + u, M, status) : -1;
+        w[u] = r[u] >= 0 && weights ? __ldg(weights + t * topk + j0 + u) : 1.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < JN; ++u)
+        if (r[u] >= 0) raw[u] = __ldg(reinterpret_cast<const uint4*>(D + static_cast<int64_t>(r[u]) * ldd + n));
+#pragma unroll
+      for (int u = 0; u < JN; ++u) {
+        if (r[u] < 0) continue;
+        const uint32_t q[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[2 * i] = fmaf(w[u], __uint_as_float(q[i] << 16), acc[2 * i]);
+          acc[2 * i + 1] = fmaf(w[u], __uint_as_float(q[i] & 0xFFFF0000u), acc[2 * i + 1]);
+        }
+      }
     }
-    store8(out + t * ldo + n, acc);
+    if (residual) {
+      float2 f[4];
+      res.get(f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * i] += f[i].x;
+        acc[2 * i + 1] += f[i].y;
+      }
+    }
+    store8_stream(out + t * ldo + n, acc);
   }
 }
 
-// dD[row_tj] = w_tj dout_t,  dw_tj = <dout_t, D[row_tj]>; rows without a token are zero.  One CTA a token;
-// the rows' zeros are written by the CTAs in turn.
-template <typename TO>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_backward_kernel(
-    const TO* __restrict__ dout, int64_t lddo, const __nv_bfloat16* __restrict__ D, int64_t M, int64_t N, int64_t ldd,
-    const int32_t* __restrict__ entry_row, const int32_t* __restrict__ row_token, int64_t T, int32_t topk,
+// dD[row_tj] = w_tj dout_t,  dw_tj = <dout_t, D[row_tj]>; rows without a token are zero.  The first `zero_ctas` CTAs
+// write those: a warp looks at 32 rows at a time, far apart so that the runs of padding rows spread over the warps.
+// Each of the others takes a token, JN of its entries at a time: its dout is read once for them.
+template <typename TO, int JN, int THREADS>
+__global__ void __launch_bounds__(THREADS) moe_combine_backward_kernel(
+    const TO* __restrict__ dout, int64_t lddo, const __nv_bfloat16* __restrict__ D, int64_t M, int32_t N, int64_t ldd,
+    const int32_t* __restrict__ entry_row, const int32_t* __restrict__ row_token, int32_t zero_ctas, int32_t topk,
     const float* __restrict__ weights, __nv_bfloat16* __restrict__ dD, int64_t lddd, float* __restrict__ dweights,
     unsigned int* status) {
-  __shared__ float red[2 * kCombineThreads / 32];
-  int phase = 0;
-  const int64_t t = blockIdx.x;
-  if (t < T) {
-    for (int j = 0; j < topk; ++j) {
-      const int32_t r = entry(entry_row, t * topk + j, M, status);
-      float dot[1] = {0.0f};
-      if (r >= 0) {
-        const float w = weights ? weights[t * topk + j] : 1.0f;
-        for (int64_t n = threadIdx.x * 8; n < N; n += kCombineThreads * 8) {
-          float f[8], g[8];
-          load8(dout + t * lddo + n, g);
-          if (dweights) {
-            load8(D + r * ldd + n, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dot[0] += f[i] * g[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] *= w;
-          store8(dD + r * lddd + n, g);
-        }
-      }
-      if (dweights) {
-        cta_sum<kCombineThreads / 32>(dot, red, phase++);
-        if (threadIdx.x == 0) dweights[t * topk + j] = dot[0];
+  constexpr int kWarps = THREADS / 32;
+  __shared__ float red[2 * kWarps * JN];
+  if (static_cast<int>(blockIdx.x) < zero_ctas) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(zero_ctas) * kWarps;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; r0 < M; r0 += 32 * warps) {
+      const int64_t r = r0 + lane * warps;
+      unsigned empty = __ballot_sync(0xffffffffu, r < M && __ldg(row_token + r) < 0);
+      for (; empty; empty &= empty - 1) {
+        __nv_bfloat16* p = dD + (r0 + (__ffs(empty) - 1) * warps) * lddd;
+        for (int64_t n = lane * 8; n < N; n += 256) __stcs(reinterpret_cast<uint4*>(p + n), make_uint4(0u, 0u, 0u, 0u));
       }
     }
+    return;
   }
-  const float zero[8] = {};
-  for (int64_t r = blockIdx.x; r < M; r += gridDim.x)
-    if (row_token[r] < 0)
-      for (int64_t n = threadIdx.x * 8; n < N; n += kCombineThreads * 8) store8(dD + r * lddd + n, zero);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) - zero_ctas;
+  int phase = 0;
+  for (int j0 = 0; j0 < topk; j0 += JN) {
+    int32_t r[JN];
+    float w[JN], dot[JN];
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+      r[j] = j0 + j < topk ? entry(entry_row, t * topk + j0 + j, M, status) : -1;
+      w[j] = r[j] >= 0 && weights ? __ldg(weights + t * topk + j0 + j) : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t n = threadIdx.x * 8; n < N; n += THREADS * 8) {
+      Raw8<TO> graw;
+      Raw8<__nv_bfloat16> d[JN];
+      graw.load(dout + t * lddo + n);
+      if (dweights) {
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+          if (r[j] >= 0) d[j].load_stream(D + static_cast<int64_t>(r[j]) * ldd + n);
+      }
+      float2 g[4];
+      graw.get(g);
+#pragma unroll
+      for (int j = 0; j < JN; ++j) {
+        if (r[j] < 0) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack2(w[j] * g[i].x, w[j] * g[i].y);
+        __stcs(reinterpret_cast<uint4*>(dD + static_cast<int64_t>(r[j]) * lddd + n), make_uint4(o[0], o[1], o[2], o[3]));
+        if (dweights) {
+          float2 f[4], s = make_float2(0.0f, 0.0f);
+          d[j].get(f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s = __ffma2_rn(f[i], g[i], s);
+          dot[j] += s.x + s.y;
+        }
+      }
+    }
+    if (dweights) {
+      cta_sum<kWarps>(dot, red, phase++);
+#pragma unroll
+      for (int j = 0; j < JN; ++j)
+        if (static_cast<int>(threadIdx.x) == j && j0 + j < topk) dweights[t * topk + j0 + j] = dot[j];
+    }
+  }
 }
 
 bool dtype_ok(int32_t d) { return d == FP8G_BF16 || d == FP8G_F32; }
@@ -850,6 +908,29 @@ bool logit_vectors(const void* p, int64_t ld, int32_t E, int32_t dtype) {
   return E % 8 == 0 && aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
 }
 
+template <typename TO>
+int combine_backward_launch(const void* dout, int64_t lddo, const __nv_bfloat16* D, int64_t M, int32_t N, int64_t ldd,
+                            const int32_t* entry_row, const int32_t* row_token, int64_t T, int32_t topk,
+                            const float* weights, __nv_bfloat16* dD, int64_t lddd, float* dweights,
+                            const DeviceInfo* dev, cudaStream_t s) {
+  // more threads a token where there are few tokens
+  const bool few = T < 2 * dev->sm_count && N > 2048;
+  auto kern = few          ? (topk <= 2   ? moe_combine_backward_kernel<TO, 2, 512>
+                              : topk <= 4 ? moe_combine_backward_kernel<TO, 4, 512>
+                                          : moe_combine_backward_kernel<TO, 8, 512>)
+              : topk <= 2 ? moe_combine_backward_kernel<TO, 2, 128>
+              : topk <= 4 ? moe_combine_backward_kernel<TO, 4, 128>
+                          : moe_combine_backward_kernel<TO, 8, 128>;
+  const int threads = few ? 512 : 128;
+  // CTAs for the zero rows: down to a row a warp, two CTAs an SM at most
+  const int warps = threads / 32;
+  const int64_t zero = std::min<int64_t>((M + warps - 1) / warps, 2 * static_cast<int64_t>(dev->sm_count));
+  kern<<<static_cast<unsigned>(zero + T), threads, 0, s>>>(static_cast<const TO*>(dout), lddo, D, M, N, ldd, entry_row,
+                                                          row_token, static_cast<int32_t>(zero), topk, weights, dD,
+                                                          lddd, dweights, dev->status);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace fp8g
 
@@ -934,15 +1015,22 @@ extern "C" int fp8g_moe_combine(const void* D, int64_t M, int64_t N, int64_t ldd
   DeviceInfo* dev = nullptr;
   int st = current_device(&dev);
   if (st != FP8G_OK) return st;
+  // A CTA a token; few tokens are split by columns too, so that every SM has a few CTAs (64 tokens of 8 x 7168: 33 us
+  // in whole rows).
+  const int64_t spans = (N + kCombineSpan - 1) / kCombineSpan;
+  const dim3 grid(static_cast<unsigned>(T),
+                  static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(spans, 8 * dev->sm_count / T))));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto launch = [&](auto kern, auto type) {
+    using TO = decltype(type);
+    kern<<<grid, kCombineThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(D), M, static_cast<int32_t>(N), ldd, entry_row,
+                                          topk, weights, static_cast<const TO*>(residual), ldr, static_cast<TO*>(out),
+                                          ldo, dev->status);
+  };
   if (out_dtype == FP8G_F32)
-    moe_combine_kernel<float><<<static_cast<unsigned>(T), kCombineThreads, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(D), M, N, ldd, entry_row, topk, weights,
-        static_cast<const float*>(residual), ldr, static_cast<float*>(out), ldo, dev->status);
+    launch(topk <= 2 ? moe_combine_kernel<float, 2> : moe_combine_kernel<float, 4>, float());
   else
-    moe_combine_kernel<__nv_bfloat16><<<static_cast<unsigned>(T), kCombineThreads, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(D), M, N, ldd, entry_row, topk, weights,
-        static_cast<const __nv_bfloat16*>(residual), ldr, static_cast<__nv_bfloat16*>(out), ldo, dev->status);
+    launch(topk <= 2 ? moe_combine_kernel<__nv_bfloat16, 2> : moe_combine_kernel<__nv_bfloat16, 4>, __nv_bfloat16());
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
@@ -951,7 +1039,7 @@ extern "C" int fp8g_moe_combine_backward(const void* dout, int32_t dout_dtype, i
                                          const int32_t* row_token, int64_t T, int32_t topk, const float* weights,
                                          void* dD, int64_t lddd, float* dweights, void* stream) {
   if (!dtype_ok(dout_dtype) || M < 0 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFFF || N % 8 != 0 || lddd < N ||
-      T < 0 || T > 0x7FFFFFFF || topk < 1 || T * topk > 0x7FFFFFFF || lddo < N || (dweights && ldd < N))
+      T < 0 || T > 0x7FFFFFFF - 4096 /* beside the CTAs of the zero rows */ || topk < 1 || T * topk > 0x7FFFFFFF || lddo < N || (dweights && ldd < N))
     return FP8G_ERR_INVALID_ARG;
   if (M == 0 && T == 0) return FP8G_OK;
   if ((M > 0 && (!dD || !row_token || (dweights && !D))) || (T > 0 && (!entry_row || !dout)))
@@ -963,15 +1051,7 @@ extern "C" int fp8g_moe_combine_backward(const void* dout, int32_t dout_dtype, i
   DeviceInfo* dev = nullptr;
   int st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(T, std::min<int64_t>(M, 1216)));
-  if (dout_dtype == FP8G_F32)
-    moe_combine_backward_kernel<float><<<grid, kCombineThreads, 0, s>>>(
-        static_cast<const float*>(dout), lddo, static_cast<const __nv_bfloat16*>(D), M, N, ldd, entry_row, row_token, T,
-        topk, weights, static_cast<__nv_bfloat16*>(dD), lddd, dweights, dev->status);
-  else
-    moe_combine_backward_kernel<__nv_bfloat16><<<grid, kCombineThreads, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(dout), lddo, static_cast<const __nv_bfloat16*>(D), M, N, ldd, entry_row,
-        row_token, T, topk, weights, static_cast<__nv_bfloat16*>(dD), lddd, dweights, dev->status);
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  return (dout_dtype == FP8G_F32 ? combine_backward_launch<float> : combine_backward_launch<__nv_bfloat16>)(
+      dout, lddo, static_cast<const __nv_bfloat16*>(D), M, static_cast<int32_t>(N), ldd, entry_row, row_token, T, topk,
+      weights, static_cast<__nv_bfloat16*>(dD), lddd, dweights, dev, static_cast<cudaStream_t>(stream));
 }

@@ -56,6 +56,16 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// The same for results that the caller's next kernel reads, not this one: they need not stay in the near caches.
+__device__ __forceinline__ void store8_stream(__nv_bfloat16* p, const float (&f)[8]) {
+  __stcs(reinterpret_cast<uint4*>(p),
+         make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
+}
+__device__ __forceinline__ void store8_stream(float* p, const float (&f)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+  __stcs(reinterpret_cast<float4*>(p + 4), make_float4(f[4], f[5], f[6], f[7]));
+}
+
 // Eight values as they lie in memory, and as four pairs for the two-wide fp32 instructions.
 template <typename T>
 struct Raw8;
