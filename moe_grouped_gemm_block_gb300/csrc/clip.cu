@@ -7,8 +7,13 @@
 // tensors' addresses, sizes and types travel as kernel arguments (up to kClipCap tensors a launch), so nothing is
 // copied to the device and a call can be captured into a graph.
 //
-// Every tensor is cut into chunks of kClipGroups 16-byte groups on the 16-byte grid of its addresses, whatever its own
-// alignment: only a tensor's first and last group can be partial, and those are taken value by value.
+// Every tensor is cut into chunks of U 16-byte groups a thread on the 16-byte grid of its addresses, whatever its own
+// alignment: only a tensor's first and last group can be partial, and those are taken value by value.  U = 16 keeps
+// more loads in flight, U = 4 gives a few megabytes to more CTAs (clip_unroll).
+//
+// 470 MB of bf16 gradients: 222 us with U = 16 and 8 CTAs an SM, 238 with U = 8 and 4; the first pass reads at the copy
+// rate, the second moves 800 MB (77 MB of its reads are still in L2), reads and writes mixed, at 85% of it.  Cache hints
+// on either side and the order of the chunks changed nothing beyond 1%.
 
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -21,11 +26,9 @@ namespace fp8g {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipUnroll = 8;       // 16-byte loads in flight per thread
-constexpr int kClipGroups = kClipThreads * kClipUnroll;
-constexpr int kClipCap = 1024;       // tensors a launch
-constexpr int kClipSmallCap = 64;    // tensors a launch with the small table (2 KB of arguments instead of 30)
-constexpr int kClipMaxCtas = 608;    // partial sums a launch
+constexpr int kClipCap = 1024;       // tensors a launch; tables of 64 and 256 are there for their size (the arguments'
+                                     // copies are most of a small call's host time)
+constexpr int kClipMaxCtas = 1216;   // partial sums a launch
 constexpr int32_t kClipMaxTensors = 1 << 20;
 constexpr int64_t kClipMaxValues = int64_t{1} << 42;  // of all tensors together
 
@@ -54,8 +57,9 @@ __device__ __forceinline__ int find_tensor(const ClipTable<CAP>& t, uint32_t c) 
 
 // A chunk of tensor i: values [lo, hi) of the tensor; the value at lo + k lies k values after a 16-byte boundary
 // (lo is negative in a first chunk whose tensor does not start on one).
-template <typename T>
+template <typename T, int U>
 struct Chunk {
+  static constexpr int kGroups = kClipThreads * U;
   static constexpr int kPer = 16 / sizeof(T);  // values a group
   const T* g;
   T* o;
@@ -67,9 +71,9 @@ struct Chunk {
     o = static_cast<T*>(t.out[i]);
     numel = t.numel[i];
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(g) & 15u) / sizeof(T));
-    lo = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * (kClipGroups * kPer) - mis;
-    hi = min(lo + kClipGroups * kPer, numel);
-    whole = lo >= 0 && hi == lo + kClipGroups * kPer;
+    lo = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * (kGroups * kPer) - mis;
+    hi = min(lo + kGroups * kPer, numel);
+    whole = lo >= 0 && hi == lo + kGroups * kPer;
   }
 };
 
@@ -89,26 +93,26 @@ __device__ __forceinline__ float square_sum(const uint4& v, __nv_bfloat16) {
   return s[0] + s[1];
 }
 
-// A thread's share of a chunk's sum of squares: its eight groups' sums, joined in a tree.
-template <typename T, int CAP>
+// A thread's share of a chunk's sum of squares: its groups' sums, joined in a tree.
+template <typename T, int U, int CAP>
 __device__ __forceinline__ float chunk_square_sum(const ClipTable<CAP>& t, int i, uint32_t c) {
-  const Chunk<T> ch(t, i, c);
-  float s[kClipUnroll] = {};
+  const Chunk<T, U> ch(t, i, c);
+  float s[U] = {};
   if (ch.whole) {
     const uint4* p = reinterpret_cast<const uint4*>(ch.g + ch.lo) + threadIdx.x;
-    uint4 v[kClipUnroll];
+    uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) v[u] = __ldg(p + u * kClipThreads);
+    for (int u = 0; u < U; ++u) v[u] = __ldg(p + u * kClipThreads);
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) s[u] = square_sum(v[u], T());
+    for (int u = 0; u < U; ++u) s[u] = square_sum(v[u], T());
   } else {
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) {
-      const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * Chunk<T>::kPer;
-      if (k >= 0 && k + Chunk<T>::kPer <= ch.hi) {
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * ch.kPer;
+      if (k >= 0 && k + ch.kPer <= ch.hi) {
         s[u] = square_sum(__ldg(reinterpret_cast<const uint4*>(ch.g + k)), T());
       } else {
-        for (int64_t q = max(k, int64_t{0}); q < min(k + Chunk<T>::kPer, ch.hi); ++q) {
+        for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q) {
           const float f = to_f32(ch.g[q]);
           s[u] = fmaf(f, f, s[u]);
         }
@@ -116,13 +120,13 @@ __device__ __forceinline__ float chunk_square_sum(const ClipTable<CAP>& t, int i
     }
   }
 #pragma unroll
-  for (int d = 1; d < kClipUnroll; d *= 2)
+  for (int d = 1; d < U; d *= 2)
 #pragma unroll
-    for (int u = 0; u + d < kClipUnroll; u += 2 * d) s[u] += s[u + d];
+    for (int u = 0; u + d < U; u += 2 * d) s[u] += s[u + d];
   return s[0];
 }
 
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __grid_constant__ ClipTable<CAP> t,
                                                                       float* __restrict__ parts) {
   __shared__ float red[2 * kClipThreads / 32];
@@ -131,7 +135,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __gr
   const uint32_t chunks = t.end[t.n - 1];
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = find_tensor(t, c);
-    s[0] += t.dtype[i] == FP8G_F32 ? chunk_square_sum<float>(t, i, c) : chunk_square_sum<__nv_bfloat16>(t, i, c);
+    s[0] += t.dtype[i] == FP8G_F32 ? chunk_square_sum<float, U>(t, i, c)
+                                    : chunk_square_sum<__nv_bfloat16, U>(t, i, c);
   }
   cta_sum<kClipThreads / 32>(s, red, 0);
   if (threadIdx.x == 0) parts[blockIdx.x] = s[0];
@@ -168,35 +173,35 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, float c, __nv_bfloat16) 
   return make_uint4(scaled2(v.x, c), scaled2(v.y, c), scaled2(v.z, c), scaled2(v.w, c));
 }
 
-template <typename T, int CAP>
+template <typename T, int U, int CAP>
 __device__ __forceinline__ void chunk_scale(const ClipTable<CAP>& t, int i, uint32_t c, float coef) {
-  const Chunk<T> ch(t, i, c);
+  const Chunk<T, U> ch(t, i, c);
   // 16-byte stores where the result's groups lie on its own 16-byte grid too
   const bool same = ((reinterpret_cast<uintptr_t>(ch.g) ^ reinterpret_cast<uintptr_t>(ch.o)) & 15u) == 0;
   if (ch.whole && same) {
     const uint4* p = reinterpret_cast<const uint4*>(ch.g + ch.lo) + threadIdx.x;
     uint4* q = reinterpret_cast<uint4*>(ch.o + ch.lo) + threadIdx.x;
-    uint4 v[kClipUnroll];
+    uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) v[u] = __ldcs(p + u * kClipThreads);
+    for (int u = 0; u < U; ++u) v[u] = __ldcs(p + u * kClipThreads);
 #pragma unroll
-    for (int u = 0; u < kClipUnroll; ++u) __stcs(q + u * kClipThreads, scaled(v[u], coef, T()));
+    for (int u = 0; u < U; ++u) __stcs(q + u * kClipThreads, scaled(v[u], coef, T()));
     return;
   }
 #pragma unroll
-  for (int u = 0; u < kClipUnroll; ++u) {
-    const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * Chunk<T>::kPer;
-    if (same && k >= 0 && k + Chunk<T>::kPer <= ch.hi) {
+  for (int u = 0; u < U; ++u) {
+    const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * ch.kPer;
+    if (same && k >= 0 && k + ch.kPer <= ch.hi) {
       *reinterpret_cast<uint4*>(ch.o + k) = scaled(*reinterpret_cast<const uint4*>(ch.g + k), coef, T());
     } else {
-      for (int64_t q = max(k, int64_t{0}); q < min(k + Chunk<T>::kPer, ch.hi); ++q)
+      for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q)
         ch.o[q] = from_f32<T>(to_f32(ch.g[q]) * coef);
     }
   }
 }
 
 // The chunks in descending order: the first pass ended with the last ones, so some of them are still in L2.
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_constant__ ClipTable<CAP> t,
                                                                  const float* __restrict__ parts, int32_t P,
                                                                  float max_norm, float eps,
@@ -210,14 +215,14 @@ __global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_co
     const uint32_t c = chunks - 1 - b;
     const int i = find_tensor(t, c);
     if (coef == 1.0f && t.out[i] == t.grad[i]) continue;  // in place and nothing to scale
-    if (t.dtype[i] == FP8G_F32) chunk_scale<float>(t, i, c, coef);
-    else chunk_scale<__nv_bfloat16>(t, i, c, coef);
+    if (t.dtype[i] == FP8G_F32) chunk_scale<float, U>(t, i, c, coef);
+    else chunk_scale<__nv_bfloat16, U>(t, i, c, coef);
   }
 }
 
 // Fills one launch's table from the tensors first, first + 1, ...; empty tensors are left out.  Returns the
 // tensor after the last one taken.  (check_tensors bounds the chunks of all tensors together below 2^31.)
-template <int CAP>
+template <int CAP, int U>
 int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
                    const int32_t* dtypes, int32_t first, int32_t n) {
   t.n = 0;
@@ -225,7 +230,7 @@ int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* out
   int32_t i = first;
   for (; i < n && t.n < CAP; ++i) {
     if (numels[i] == 0) continue;
-    const int64_t size = dtypes[i] == FP8G_F32 ? 4 : 2, per = kClipGroups * (16 / size);
+    const int64_t size = dtypes[i] == FP8G_F32 ? 4 : 2, per = static_cast<int64_t>(kClipThreads) * U * (16 / size);
     const int64_t mis = static_cast<int64_t>(reinterpret_cast<uintptr_t>(grads[i]) & 15u) / size;
     chunks += static_cast<uint64_t>((numels[i] + mis + per - 1) / per);
     t.grad[t.n] = grads[i];
@@ -236,6 +241,13 @@ int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* out
     ++t.n;
   }
   return i;
+}
+
+// Whether the chunks are small: up to 64 MB, where 16 KB chunks give every SM some.
+bool small_chunks(const int64_t* numels, const int32_t* dtypes, int32_t n) {
+  int64_t bytes = 0;
+  for (int32_t i = 0; i < n; ++i) bytes += numels[i] * (dtypes[i] == FP8G_F32 ? 4 : 2);
+  return bytes <= int64_t{64} << 20;
 }
 
 int64_t clip_launches(int32_t n) { return (static_cast<int64_t>(n) + kClipCap - 1) / kClipCap; }
@@ -258,37 +270,37 @@ int check_tensors(const void* const* grads, void* const* outs, const int64_t* nu
 }
 
 // Partial sums of all the tensors; *P is how many were written.
-template <int CAP>
+template <int CAP, int U>
 int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
                       const int32_t* dtypes, int32_t n, float* parts, int32_t* P, cudaStream_t s) {
   *P = 0;
   for (int32_t i = 0; i < n;) {
-    i = fill_table(t, grads, outs, numels, dtypes, i, n);
+    i = fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
     const uint32_t ctas = std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas);
-    grad_norm_part_kernel<CAP><<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
+    grad_norm_part_kernel<CAP, U><<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
     *P += static_cast<int32_t>(ctas);
   }
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
-template <int CAP>
+template <int CAP, int U>
 int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, float* norm,
                      float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch(t, grads, nullptr, numels, dtypes, n, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, nullptr, numels, dtypes, n, parts, &P, s);
   if (st != FP8G_OK) return st;
   grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, P, norm);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
-template <int CAP>
+template <int CAP, int U>
 int clip_launch(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes, int32_t n,
                 float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch(t, grads, outs, numels, dtypes, n, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, outs, numels, dtypes, n, parts, &P, s);
   if (st != FP8G_OK) return st;
   if (P == 0) {  // no values at all
     grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, 0, norm);
@@ -296,7 +308,7 @@ int clip_launch(const void* const* grads, void* const* outs, const int64_t* nume
   }
   const bool one = n <= CAP;  // then the table is already the whole one
   for (int32_t i = 0; i < n;) {
-    i = one ? n : fill_table(t, grads, outs, numels, dtypes, i, n);
+    i = one ? n : fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas));
@@ -307,7 +319,7 @@ int clip_launch(const void* const* grads, void* const* outs, const int64_t* nume
     attr[0].val.programmaticStreamSerializationAllowed = one ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<CAP>, t, static_cast<const float*>(parts), P, max_norm, eps, norm) !=
+    if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<CAP, U>, t, static_cast<const float*>(parts), P, max_norm, eps, norm) !=
         cudaSuccess) {
       cudaGetLastError();
       return FP8G_ERR_CUDA;
@@ -337,7 +349,10 @@ extern "C" int fp8g_grad_norm(const void* const* grads, const int64_t* numels, c
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  auto go = n <= kClipSmallCap ? grad_norm_launch<kClipSmallCap> : grad_norm_launch<kClipCap>;
+  const bool small = small_chunks(numels, dtypes, n);
+  auto go = n <= 64    ? (small ? grad_norm_launch<64, 4> : grad_norm_launch<64, 16>)
+            : n <= 256 ? (small ? grad_norm_launch<256, 4> : grad_norm_launch<256, 16>)
+                       : (small ? grad_norm_launch<kClipCap, 4> : grad_norm_launch<kClipCap, 16>);
   return go(grads, numels, dtypes, n, norm, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
@@ -353,7 +368,10 @@ extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, 
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  auto go = n <= kClipSmallCap ? clip_launch<kClipSmallCap> : clip_launch<kClipCap>;
+  const bool small = small_chunks(numels, dtypes, n);
+  auto go = n <= 64    ? (small ? clip_launch<64, 4> : clip_launch<64, 16>)
+            : n <= 256 ? (small ? clip_launch<256, 4> : clip_launch<256, 16>)
+                       : (small ? clip_launch<kClipCap, 4> : clip_launch<kClipCap, 16>);
   return go(grads, outs, numels, dtypes, n, max_norm, eps, norm, static_cast<float*>(workspace),
             static_cast<cudaStream_t>(stream));
 }
