@@ -439,7 +439,7 @@ int fp8g_layer_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, con
                              const float* rstd, int64_t M, int64_t N, void* dx, int64_t lddx, float* dweight,
                              float* dbias, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* fp8g_moe_gate_workspace -- scratch bytes of fp8g_moe_gate. */
+/* fp8g_moe_gate_workspace -- scratch bytes of fp8g_moe_gate; 0 for few tokens, whose workspace may be null. */
 int fp8g_moe_gate_workspace(int64_t T, int32_t E, int64_t* bytes);
 
 /*

@@ -86,10 +86,12 @@ def _raise(code: int, what: str):
     raise Fp8GemmError(code, what)
 
 
-def _workspace(name: str, device, *sizes) -> torch.Tensor:
+def _workspace(name: str, device, *sizes) -> torch.Tensor | None:
     n = ctypes.c_int64()
-    _check(getattr(lib(), name)(*sizes, ctypes.byref(n)), name)
-    return _empty(max(n.value, 16), dtype=_U8, device=device)
+    code = getattr(lib(), name)(*sizes, ctypes.byref(n))
+    if code:
+        _raise(code, name)
+    return _empty(n.value, dtype=_U8, device=device) if n.value else None
 
 
 def _scratch(t: torch.Tensor) -> None:
@@ -113,84 +115,95 @@ def _norm_weights(weight, bias, n: int) -> int:
 
 def fp8g_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5) -> None:
     """x [M,N] -> y [M,N] (bf16 or f32 each), mean and rstd f32 [M] (or None); weight, bias [N] or None."""
-    xd, yd, ldx, ldy = _dtype(x, "x"), _dtype(y, "y"), _rows(x, "x"), _rows(y, "y")
-    M, N = x.shape
     if y.shape != x.shape:
         _refuse("y: x's shape")
-    wd = _norm_weights(weight, bias, N)
+    ldy = _rows(y, "y")
     if mean is not None:
-        _vector(mean, M, _F32, "mean")
+        _vector(mean, x.shape[0], _F32, "mean")
     if rstd is not None:
-        _vector(rstd, M, _F32, "rstd")
+        _vector(rstd, x.shape[0], _F32, "rstd")
+    _one_device(x.get_device(), y, mean, rstd)
+    _norm(x, weight, bias, y, ldy, _opt(mean), _opt(rstd), eps)
+
+
+def _norm(x, weight, bias, y, ldy: int, mean: int | None, rstd: int | None, eps: float) -> None:
+    """The inputs' checks and the call."""
+    xd, ldx, yd = _dtype(x, "x"), _rows(x, "x"), _dtype(y, "y")
+    M, N = x.shape
+    wd = 1 if weight is None and bias is None else _norm_weights(weight, bias, N)
     dev = x.get_device()
-    _one_device(dev, weight, bias, y, mean, rstd)
+    _one_device(dev, weight, bias)
     code = lib().fp8g_layer_norm(x.data_ptr(), xd, M, N, ldx, _opt(weight), _opt(bias), wd, eps, y.data_ptr(), yd, ldy,
-                                 _opt(mean), _opt(rstd), _on(x, dev))
+                                 mean, rstd, _on(x, dev))
     if code:
         _raise(code, "fp8g_layer_norm")
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=None):
     """x [M,N] bf16 or f32 -> (y [M,N] of out_dtype (x's), mean f32 [M], rstd f32 [M])."""
-    dev = x.device
-    y = _empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
-    mean = _empty(x.shape[0], dtype=_F32, device=dev)
-    rstd = _empty(x.shape[0], dtype=_F32, device=dev)
-    fp8g_layer_norm(x, weight, bias, y, mean, rstd, eps)
+    dev, shape = x.device, x.shape
+    y = _empty(shape, dtype=out_dtype or x.dtype, device=dev)
+    mean = _empty(shape[0], dtype=_F32, device=dev)
+    rstd = _empty(shape[0], dtype=_F32, device=dev)
+    _norm(x, weight, bias, y, shape[-1], mean.data_ptr(), rstd.data_ptr(), eps)
     return y, mean, rstd
 
 
 def fp8g_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None) -> None:
     """dy [M,N], x [M,N], weight [N] or None, mean and rstd f32 [M] -> dx [M,N] of x's type, dweight and dbias f32 [N]
     (or None).  workspace: a uint8 tensor of fp8g_layer_norm_backward_workspace bytes (allocated if None)."""
+    if dx.shape != x.shape or dx.dtype != x.dtype:
+        _refuse("dx: x's shape and type")
+    lddx = _rows(dx, "dx")
+    if dweight is not None:
+        _vector(dweight, x.shape[1], _F32, "dweight")
+    if dbias is not None:
+        _vector(dbias, x.shape[1], _F32, "dbias")
+    if workspace is not None:
+        _scratch(workspace)
+    _one_device(x.get_device(), dx, dweight, dbias, workspace)
+    _norm_grad(dy, x, weight, mean, rstd, dx, lddx, dweight, dbias, workspace)
+
+
+def _norm_grad(dy, x, weight, mean, rstd, dx, lddx: int, dweight, dbias, workspace) -> None:
+    """The inputs' checks and the call."""
     yd, xd = _dtype(dy, "dy"), _dtype(x, "x")
-    lddy, ldx, lddx = _rows(dy, "dy"), _rows(x, "x"), _rows(dx, "dx")
+    lddy, ldx = _rows(dy, "dy"), _rows(x, "x")
     M, N = shape = x.shape
-    if dy.shape != shape or dx.shape != shape or dx.dtype != x.dtype:
-        _refuse("dy, dx: x's shape; dx: x's type")
-    wd = _norm_weights(weight, None, N)
+    if dy.shape != shape:
+        _refuse("dy: x's shape")
+    wd = 1 if weight is None else _norm_weights(weight, None, N)
     if mean is None or rstd is None:
         _refuse("mean, rstd: as layer_norm returned them")
     _vector(mean, M, _F32, "mean")
     _vector(rstd, M, _F32, "rstd")
-    if dweight is not None:
-        _vector(dweight, N, _F32, "dweight")
-    if dbias is not None:
-        _vector(dbias, N, _F32, "dbias")
-    ws, bytes_ = None, 0
-    if workspace is not None:
-        _scratch(workspace)
-    elif dweight is not None or dbias is not None:
-        workspace = _workspace("fp8g_layer_norm_backward_workspace", x.device, M, N)
-    if workspace is not None:
-        ws, bytes_ = workspace.data_ptr(), workspace.numel()
     dev = x.get_device()
-    _one_device(dev, dy, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _one_device(dev, dy, weight, mean, rstd)
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = _workspace("fp8g_layer_norm_backward_workspace", x.device, M, N)
     code = lib().fp8g_layer_norm_backward(dy.data_ptr(), yd, lddy, x.data_ptr(), xd, ldx, _opt(weight), wd,
                                           mean.data_ptr(), rstd.data_ptr(), M, N, dx.data_ptr(), lddx, _opt(dweight),
-                                          _opt(dbias), ws, bytes_, _on(x, dev))
+                                          _opt(dbias), _opt(workspace), 0 if workspace is None else workspace.numel(),
+                                          _on(x, dev))
     if code:
         _raise(code, "fp8g_layer_norm_backward")
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, weight_grads: bool = True):
     """-> (dx of x's type, dweight f32 [N], dbias f32 [N]); the last two are None without weight_grads."""
-    dev = x.device
-    dx = _empty(x.shape, dtype=x.dtype, device=dev)
+    dev, shape = x.device, x.shape
+    dx = _empty(shape, dtype=x.dtype, device=dev)
     dw = db = None
     if weight_grads:
-        N = x.shape[-1]
-        dw = _empty(N, dtype=_F32, device=dev)
-        db = _empty(N, dtype=_F32, device=dev)
-    fp8g_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db)
+        dw = _empty(shape[-1], dtype=_F32, device=dev)
+        db = _empty(shape[-1], dtype=_F32, device=dev)
+    _norm_grad(dy, x, weight, mean, rstd, dx, shape[-1], dw, db, None)
     return dx, dw, db
 
 
 # ------------------------------------------------------------------ gate
 
-def _mask(mask, T: int) -> int | None:
-    if mask is None:
-        return None
+def _mask(mask, T: int) -> int:
     if mask.dtype not in (torch.bool, _U8) or mask.numel() != T or not mask.is_contiguous():
         _refuse(f"token_mask: bool or uint8 [{T}], contiguous")
     return mask.data_ptr()
@@ -199,24 +212,33 @@ def _mask(mask, T: int) -> int | None:
 def fp8g_moe_gate(logits, topk: int, topk_ids, topk_weights, counts, loss=None, renormalize: bool = True,
                   loss_coef: float = 0.01, token_mask=None, workspace=None) -> None:
     """logits [T,E] bf16 or f32 -> topk_ids int32 [T,topk], topk_weights f32 [T,topk], counts int32 [E], loss f32 [1]
-    (or None).  token_mask: bool or uint8 [T], False for padding tokens."""
-    code, ld = _dtype(logits, "logits"), _rows(logits, "logits")
+    (or None).  token_mask: bool or uint8 [T], False for padding tokens.  workspace: a uint8 tensor of
+    fp8g_moe_gate_workspace bytes (allocated if None)."""
+    _need(logits.dim() == 2, "logits: [T,E]")
     T, E = logits.shape
     _vector(topk_ids, T * topk, _I32, "topk_ids")
     _vector(topk_weights, T * topk, _F32, "topk_weights")
     _vector(counts, E, _I32, "counts")
     if loss is not None:
         _vector(loss, 1, _F32, "loss")
-    mask = _mask(token_mask, T)
+    if workspace is not None:
+        _scratch(workspace)
+    _one_device(logits.get_device(), topk_ids, topk_weights, counts, loss, workspace)
+    _gate(logits, topk, topk_ids, topk_weights, counts, loss, renormalize, loss_coef, token_mask, workspace)
+
+
+def _gate(logits, topk, topk_ids, topk_weights, counts, loss, renormalize, loss_coef, token_mask, workspace) -> None:
+    """The inputs' checks and the call."""
+    code, ld = _dtype(logits, "logits"), _rows(logits, "logits")
+    T, E = logits.shape
+    mask = None if token_mask is None else _mask(token_mask, T)
     dev = logits.get_device()
-    _one_device(dev, topk_ids, topk_weights, counts, loss, token_mask, workspace)
+    _one_device(dev, token_mask)
     if workspace is None:
         workspace = _workspace("fp8g_moe_gate_workspace", logits.device, T, E)
-    else:
-        _scratch(workspace)
     st = lib().fp8g_moe_gate(logits.data_ptr(), code, T, E, ld, topk, 1 if renormalize else 0, mask, loss_coef,
                              topk_ids.data_ptr(), topk_weights.data_ptr(), counts.data_ptr(), _opt(loss),
-                             workspace.data_ptr(), workspace.numel(), _on(logits, dev))
+                             _opt(workspace), 0 if workspace is None else workspace.numel(), _on(logits, dev))
     if st:
         _raise(st, "fp8g_moe_gate")
 
@@ -230,17 +252,24 @@ def moe_gate(logits, topk: int, renormalize: bool = True, loss_coef: float = 0.0
     w = _empty((T, topk), dtype=_F32, device=dev)
     counts = _empty(E, dtype=_I32, device=dev)
     loss = _empty(1, dtype=_F32, device=dev)
-    fp8g_moe_gate(logits, topk, ids, w, counts, loss, renormalize, loss_coef, token_mask)
+    _gate(logits, topk, ids, w, counts, loss, renormalize, loss_coef, token_mask, None)
     return ids, w, counts, loss
 
 
 def fp8g_moe_gate_backward(logits, topk_ids, counts, dweights, dloss, dlogits, renormalize: bool = True,
                            loss_coef: float = 0.01, token_mask=None) -> None:
     """dweights f32 [T,topk] and dloss f32 [1] (either may be None) -> dlogits [T,E] of logits' type."""
-    code, ld, ldd = _dtype(logits, "logits"), _rows(logits, "logits"), _rows(dlogits, "dlogits")
-    T, E = logits.shape
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         _refuse("dlogits: logits' shape and type")
+    ldd = _rows(dlogits, "dlogits")
+    _one_device(logits.get_device(), dlogits)
+    _gate_grad(logits, topk_ids, counts, dweights, dloss, dlogits, ldd, renormalize, loss_coef, token_mask)
+
+
+def _gate_grad(logits, topk_ids, counts, dweights, dloss, dlogits, ldd, renormalize, loss_coef, token_mask) -> None:
+    """The inputs' checks and the call."""
+    code, ld = _dtype(logits, "logits"), _rows(logits, "logits")
+    T, E = logits.shape
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         _refuse("topk_ids: int32 [T,topk]")
     topk = topk_ids.shape[1]
@@ -250,9 +279,9 @@ def fp8g_moe_gate_backward(logits, topk_ids, counts, dweights, dloss, dlogits, r
         _vector(dweights, T * topk, _F32, "dweights")
     if dloss is not None:
         _vector(dloss, 1, _F32, "dloss")
-    mask = _mask(token_mask, T)
+    mask = None if token_mask is None else _mask(token_mask, T)
     dev = logits.get_device()
-    _one_device(dev, topk_ids, counts, dweights, dloss, dlogits, token_mask)
+    _one_device(dev, topk_ids, counts, dweights, dloss, token_mask)
     st = lib().fp8g_moe_gate_backward(logits.data_ptr(), code, T, E, ld, topk, 1 if renormalize else 0, mask, loss_coef,
                                       topk_ids.data_ptr(), counts.data_ptr(), _opt(dweights), _opt(dloss),
                                       dlogits.data_ptr(), ldd, _on(logits, dev))
@@ -264,7 +293,7 @@ def moe_gate_backward(logits, topk_ids, counts, dweights=None, dloss=None, renor
                       loss_coef: float = 0.01, token_mask=None):
     """The gradient of moe_gate's weights and loss with respect to the logits -> dlogits [T,E]."""
     dlogits = _empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    fp8g_moe_gate_backward(logits, topk_ids, counts, dweights, dloss, dlogits, renormalize, loss_coef, token_mask)
+    _gate_grad(logits, topk_ids, counts, dweights, dloss, dlogits, logits.shape[-1], renormalize, loss_coef, token_mask)
     return dlogits
 
 
@@ -273,25 +302,32 @@ def moe_gate_backward(logits, topk_ids, counts, dweights=None, dloss=None, renor
 def fp8g_moe_combine(D, entry_row, weights, out, residual=None) -> None:
     """D bf16 [M,N], entry_row int32 [T,topk], weights f32 [T,topk] or None (1) -> out [T,N] bf16 or f32, plus
     residual [T,N] of out's type."""
+    if out.dim() != 2 or out.shape[0] != entry_row.shape[0] or out.shape[1] != D.shape[-1]:
+        _refuse("out: [T,N]")
+    ldo = _rows(out, "out")
+    _one_device(D.get_device(), out)
+    _combine(D, entry_row, weights, out, ldo, residual)
+
+
+def _combine(D, entry_row, weights, out, ldo: int, residual) -> None:
+    """The inputs' checks and the call."""
     if D.dtype != torch.bfloat16:
         _refuse("D: bf16 [M,N]")
-    code, ldd, ldo = _dtype(out, "out"), _rows(D, "D"), _rows(out, "out")
+    code, ldd = _dtype(out, "out"), _rows(D, "D")
     M, N = D.shape
     if entry_row.dim() != 2:
         _refuse("entry_row: int32 [T,topk]")
     T, topk = entry_row.shape
-    if out.shape != (T, N):
-        _refuse("out: [T,N]")
     _vector(entry_row, T * topk, _I32, "entry_row")
     if weights is not None:
         _vector(weights, T * topk, _F32, "weights")
     ldr, res = 0, None
     if residual is not None:
         ldr, res = _rows(residual, "residual"), residual.data_ptr()
-        if residual.shape != out.shape or residual.dtype != out.dtype:
+        if residual.shape != (T, N) or residual.dtype != out.dtype:
             _refuse("residual: out's shape and type")
     dev = D.get_device()
-    _one_device(dev, entry_row, weights, out, residual)
+    _one_device(dev, entry_row, weights, residual)
     st = lib().fp8g_moe_combine(D.data_ptr(), M, N, ldd, entry_row.data_ptr(), T, topk, _opt(weights), res, ldr,
                                 out.data_ptr(), code, ldo, _on(D, dev))
     if st:
@@ -301,8 +337,9 @@ def fp8g_moe_combine(D, entry_row, weights, out, residual=None) -> None:
 def moe_combine(D, entry_row, weights=None, residual=None, out_dtype=None):
     """The experts' rows D back to their tokens -> out [T,N] of out_dtype (the residual's type, or bf16)."""
     dtype = out_dtype or (D.dtype if residual is None else residual.dtype)
-    out = _empty((entry_row.shape[0], D.shape[1]), dtype=dtype, device=D.device)
-    fp8g_moe_combine(D, entry_row, weights, out, residual)
+    N = D.shape[-1]
+    out = _empty((entry_row.shape[0], N), dtype=dtype, device=D.device)
+    _combine(D, entry_row, weights, out, N, residual)
     return out
 
 
@@ -395,8 +432,8 @@ def _norm_buffers(g: GradList, norm, workspace):
 def fp8g_grad_norm(grads: GradList, norm, workspace=None) -> None:
     """norm f32 [1] = the 2-norm of all gradients together."""
     ws = _norm_buffers(grads, norm, workspace)
-    st = lib().fp8g_grad_norm(grads.ptrs, grads.numels, grads.dtypes, grads.n, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                              _on(norm, grads.device_index))
+    st = lib().fp8g_grad_norm(grads.ptrs, grads.numels, grads.dtypes, grads.n, norm.data_ptr(), ws.data_ptr(),
+                              ws.numel(), _on(norm, grads.device_index))
     if st:
         _raise(st, "fp8g_grad_norm")
 

@@ -6,7 +6,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdlib>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "common.cuh"
 
@@ -82,6 +84,30 @@ int encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, cons
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+int allow_shared_memory(const void* kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return FP8G_OK;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  static std::mutex mutex;
+  static std::map<std::pair<int, const void*>, size_t> allowed;
+  std::lock_guard<std::mutex> lock(mutex);
+  const std::pair<int, const void*> key{dev, kernel};
+  const auto it = allowed.find(key);
+  if (it != allowed.end() && it->second >= bytes) return FP8G_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  try {
+    allowed[key] = bytes;
+  } catch (...) {  // not remembered: asked again next time
+  }
+  return FP8G_OK;
 }
 
 long long wait_budget_cycles() {

@@ -27,6 +27,10 @@ int encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, cons
                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                 CUtensorMapSwizzle swizzle);
 
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device.  The runtime is asked only the first time
+// that a kernel needs more than before (the call costs about as much as a launch).
+int allow_shared_memory(const void* kernel, size_t bytes);
+
 // Cycle budget of every device-side wait (clock64 ticks).  FP8G_WAIT_BUDGET_CYCLES overrides.
 long long wait_budget_cycles();
 

@@ -307,9 +307,12 @@ size_t gate_smem(int E, int topk) {
   return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + std::max(kGateWarps * E, kGateWarps * gate_warp_words<LPR>(topk)));
 }
 
+// CTAs that are resident on an SM at once.
+__host__ __device__ constexpr int gate_per_sm(int vpl) { return vpl == 8 ? 4 : vpl == 16 ? 2 : 1; }
+
 // A warp's rows, and so each partial sum's terms and their order, follow from the grid alone.
 template <typename TL, int VPL, int LPR>
-__global__ void __launch_bounds__(kGateThreads) moe_gate_kernel(const GateArgs a) {
+__global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kernel(const GateArgs a) {
   constexpr int G = 32 / LPR;  // rows a warp at once
   using Rank = Ranking<TL, VPL, LPR>;
   extern __shared__ __align__(16) float smem[];
@@ -801,43 +804,33 @@ __global__ void __launch_bounds__(THREADS) moe_combine_backward_kernel(
 bool dtype_ok(int32_t d) { return d == FP8G_BF16 || d == FP8G_F32; }
 uintptr_t dtype_size(int32_t d) { return d == FP8G_F32 ? 4 : 2; }
 
-template <typename Kernel>
-int allow_smem(Kernel kern, size_t bytes) {
-  if (bytes <= 48 * 1024) return FP8G_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
-    cudaGetLastError();
-    return FP8G_ERR_CUDA;
-  }
-  return FP8G_OK;
+// Rows that a CTA has at once, by the lanes a row takes.
+int64_t gate_rows(int E) {
+  int lpr = 1;
+  while (lpr < 32 && lpr * 8 < E) lpr *= 2;
+  return kGateWarps * (32 / lpr);
 }
-
-// The CTAs of a forward call, at most (each writes a row of partial sums).
-int64_t gate_parts(int64_t T) { return std::min<int64_t>(kGateMaxParts, (T + kGateWarps - 1) / kGateWarps); }
-
-template <typename Kernel>
-int resident_ctas(Kernel kern, size_t smem, const DeviceInfo* dev) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGateThreads, smem) != cudaSuccess || per_sm < 1) {
-    cudaGetLastError();
-    per_sm = 1;
-  }
-  return per_sm * dev->sm_count;
+// Whether a call is finished by one CTA or cluster, without partial sums.
+bool gate_few(int64_t T, int E) { return T <= 2 * kGateCluster * gate_rows(E); }
+// The CTAs of a larger call, at most (each writes a row of partial sums).
+int64_t gate_parts(int64_t T, int E) {
+  return gate_few(T, E) ? 0 : std::min<int64_t>(kGateMaxParts, (T + gate_rows(E) - 1) / gate_rows(E));
 }
 
 template <typename TL, int VPL, int LPR>
 int gate_launch(const GateArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   auto kern = moe_gate_kernel<TL, VPL, LPR>;
   const size_t smem = gate_smem<LPR>(a.E, a.topk);
-  int st = allow_smem(kern, smem);
+  const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), smem);
   if (st != FP8G_OK) return st;
   // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs as
   // are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38).
   const int64_t at_once = kGateWarps * (32 / LPR);
-  const bool few = a.T <= 2 * kGateCluster * at_once;
+  const bool few = gate_few(a.T, a.E);
   const int cluster = a.T <= 2 * at_once || !few ? 1 : kGateCluster;
   const int64_t ctas = few ? cluster
-                           : std::min<int64_t>({(a.T + at_once - 1) / at_once, resident_ctas(kern, smem, dev),
-                                                gate_parts(a.T)});
+                           : std::min<int64_t>(gate_parts(a.T, a.E),
+                                               static_cast<int64_t>(gate_per_sm(VPL)) * dev->sm_count);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kGateThreads);
@@ -938,7 +931,7 @@ using namespace fp8g;
 
 extern "C" int fp8g_moe_gate_workspace(int64_t T, int32_t E, int64_t* bytes) {
   if (T < 0 || T > 0x7FFFFFFF || E < 1 || E > kGateMaxExperts || !bytes) return FP8G_ERR_INVALID_ARG;
-  *bytes = gate_parts(T) * E * 8;
+  *bytes = gate_parts(T, E) * E * 8;
   return FP8G_OK;
 }
 
@@ -950,7 +943,8 @@ extern "C" int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32
       topk > kGateMaxTopk || topk > E || (renormalize != 0 && renormalize != 1) || T * topk > 0x7FFFFFFF)
     return FP8G_ERR_INVALID_ARG;
   if (!counts || (T > 0 && (!logits || !topk_ids || !topk_weights))) return FP8G_ERR_INVALID_ARG;
-  if (T > 0 && (!workspace || workspace_bytes < gate_parts(T) * E * 8)) return FP8G_ERR_INVALID_ARG;
+  const int64_t scratch = gate_parts(T, E) * E * 8;
+  if (scratch > 0 && (!workspace || workspace_bytes < scratch)) return FP8G_ERR_INVALID_ARG;
   if (!aligned_to(logits, dtype_size(dtype)) || !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) ||
       !aligned_to(counts, 4) || !aligned_to(loss, 4) || !aligned16(workspace))
     return FP8G_ERR_ALIGNMENT;
@@ -969,7 +963,7 @@ extern "C" int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32
   GateArgs a{};
   a.logits = logits, a.mask = token_mask, a.ids = topk_ids, a.weights = topk_weights, a.counts = counts, a.loss = loss;
   a.part_p = static_cast<float*>(workspace);
-  a.part_c = reinterpret_cast<int32_t*>(a.part_p + gate_parts(T) * E);
+  a.part_c = reinterpret_cast<int32_t*>(a.part_p + gate_parts(T, E) * E);
   a.T = T, a.ldl = ldl, a.E = E, a.topk = topk, a.renorm = renormalize, a.coef = loss_coef;
   a.vec = logit_vectors(logits, ldl, E, dtype);
   return (dtype == FP8G_F32 ? gate_form<float>(E) : gate_form<__nv_bfloat16>(E))(a, dev, s);

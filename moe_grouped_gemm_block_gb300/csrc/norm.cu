@@ -1241,10 +1241,8 @@ RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, int max_threads
 }
 template <typename Kernel, typename... Args>
 int ring_launch(Kernel kern, const RingPlan& p, int64_t smem, cudaStream_t s, Args... args) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess) {
-    cudaGetLastError();
-    return FP8G_ERR_CUDA;
-  }
+  const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), kRingBytes);
+  if (st != FP8G_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows_at_once * p.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(p.threads));

@@ -51,7 +51,7 @@ def test_layer_norm_backward(lib, kw, want):
     assert lib.fp8g_layer_norm_backward(*_args(NORM_BWD, kw)) == want
 
 
-GATE = dict(l=P, d=1, T=4, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, w=P, counts=P, loss=P, ws=P, wsb=BIG,
+GATE = dict(l=P, d=1, T=50000, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, w=P, counts=P, loss=P, ws=P, wsb=BIG,
             s=None)
 
 
@@ -129,6 +129,9 @@ def test_null_tables(lib):
     assert lib.fp8g_grad_norm(None, None, None, -1, P, P, BIG, None) == INVALID
     assert lib.fp8g_grad_norm_workspace(4, None) == INVALID
     assert lib.fp8g_moe_gate_workspace(4, 0, ctypes.byref(ctypes.c_int64())) == INVALID
+    n = ctypes.c_int64(-1)
+    assert lib.fp8g_moe_gate_workspace(4, 8, ctypes.byref(n)) == 0 and n.value == 0  # few tokens: none needed
+    assert lib.fp8g_moe_gate_workspace(50000, 8, ctypes.byref(n)) == 0 and n.value > 0
     assert lib.fp8g_layer_norm_backward_workspace(4, 0, ctypes.byref(ctypes.c_int64())) == INVALID
 
 
