@@ -4,11 +4,12 @@
 //     with h = (x - mu) r and g = dy w:
 //     dx = r (g - mean_n g - h mean_n (g h)),   dw = sum_m dy h,   db = sum_m dy
 //
-// All sums are taken in fp32; the variance is the mean of the squared differences from the mean
-// (a second pass over the row), not the difference of two large sums.
+// All sums are taken in fp32.  The variance is the mean of the squared differences from the mean (a second pass over the
+// values in registers), or in the ring from a value near it with a bound on what cancels; never the difference of
+// two large sums.
 //
 // Forms, by the row's length (rows go in vectors of 8 values on the 16-byte grid, see RowShape):
-//   warp     up to 1024 values: a row (or 2, 4 at once) per warp, all in registers, no barriers
+//   warp     short rows: a row (or 2, 4 at once) per warp, all in registers, no barriers
 //   ring     longer rows: resident CTAs (clusters of two beyond 8192 values) walk over their rows, which bulk copies
 //            bring into a ring of shared-memory stages ahead of them; some warps form a row's sums, the others the
 //            results, with the weights and (backward) the weight gradients' sums in registers
@@ -67,9 +68,9 @@ struct RowShape {
 };
 
 // The values of a vector that the mask has.
-template <typename T>
+template <bool SHIFT, typename T>
 __device__ __forceinline__ void store_masked(T* p, const float2 (&f)[4], uint32_t mask) {
-  if (mask == 0xFFu) {
+  if (!SHIFT || mask == 0xFFu) {
     store_pairs(p, f);
     return;
   }
@@ -80,9 +81,12 @@ __device__ __forceinline__ void store_masked(T* p, const float2 (&f)[4], uint32_
 
 // A vector of a row, read once: 16-byte loads where all of it may be read (`inside`: it lies within its matrix,
 // neighbouring rows included), value by value where it would reach past the matrix's end.
-template <typename T>
+template <bool SHIFT, typename T>
 __device__ __forceinline__ void load_vector(Raw8<T>& r, const T* p, uint32_t mask, bool inside) {
-  if (mask == 0xFFu || (mask && inside)) {
+  if constexpr (!SHIFT) {  // a vector is there or not
+    if (mask) r.load_stream(p);
+    else r.zero();
+  } else if (mask == 0xFFu || (mask && inside)) {
     r.load_stream(p);
     if (mask != 0xFFu) r.keep(mask);
   } else {
@@ -144,7 +148,7 @@ __device__ __forceinline__ float block_sum(float v, float2 (*red)[32], int phase
 }
 
 // The sum of (x - mu)^2 over the existing values of NV vectors.
-template <typename T, int NV>
+template <bool SHIFT, typename T, int NV>
 __device__ __forceinline__ float spread_sum(const Raw8<T> (&raw)[NV], const uint32_t (&mask)[NV], float mu) {
   float2 s = both(0.0f);
 #pragma unroll
@@ -155,7 +159,7 @@ __device__ __forceinline__ float spread_sum(const Raw8<T> (&raw)[NV], const uint
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 d = __fadd2_rn(f[i], both(-mu));
-      if (mask[v] != 0xFFu)
+      if (SHIFT && mask[v] != 0xFFu)
         d = make_float2(mask[v] >> (2 * i) & 1u ? d.x : 0.0f, mask[v] >> (2 * i + 1) & 1u ? d.y : 0.0f);
       s = __ffma2_rn(d, d, s);
     }
@@ -252,7 +256,7 @@ __device__ __forceinline__ void stage_vector(Raw8<T>& r, const T* stage, int v, 
 }
 
 // The vectors of a share that are whole in every row; off the grid its first and last one may not be.  (A ring's rows
-// have more than 64 vectors a share.)
+// have more than 33 vectors a share.)
 template <bool SHIFT>
 struct Inner {
   int lo, hi;
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const Nor
   auto fetch = [&](int64_t m) {
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      load_vector(next[v], x + m * a.ldx + shape.col(v * LPR + sub), m < a.M ? mask[v] : 0u, m + 1 < a.M);
+      load_vector<SHIFT>(next[v], x + m * a.ldx + shape.col(v * LPR + sub), m < a.M ? mask[v] : 0u, m + 1 < a.M);
   };
   fetch(m0 + off);
   for (; m0 < a.M; m0 += stride) {
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const Nor
     for (int v = 0; v < NV; ++v) raw[v] = next[v];
     if (m0 + stride < a.M) fetch(m + stride);
     const float mu = lanes_sum<LPR>(value_sum(raw)) * inv_n;
-    const float var = lanes_sum<LPR>(spread_sum(raw, mask, mu)) * inv_n;
+    const float var = lanes_sum<LPR>(spread_sum<SHIFT>(raw, mask, mu)) * inv_n;
     const float r = 1.0f / sqrtf(var + a.eps);
     if (m >= a.M) continue;
 #pragma unroll
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const Nor
       float2 f[4];
       raw[v].get(f);
       norm_vector(f, mu, r, wf[v], bf[v]);
-      store_masked(y + m * a.ldy + shape.col(v * LPR + sub), f, mask[v]);
+      store_masked<SHIFT>(y + m * a.ldy + shape.col(v * LPR + sub), f, mask[v]);
     }
     if (sub == 0) {
       if (a.mean) a.mean[m] = mu;
@@ -419,10 +423,10 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const Nor
 
 // The sums of a warp's values: their sum and, about their own mean, their squared differences.  `count`: the values
 // that the warp holds.
-template <typename T, int NV>
+template <bool SHIFT, typename T, int NV>
 __device__ __forceinline__ float2 warp_moments(const Raw8<T> (&raw)[NV], const uint32_t (&mask)[NV], float inv_count) {
   const float s = warp_sum(value_sum(raw));
-  return make_float2(s, warp_sum(spread_sum(raw, mask, s * inv_count)));
+  return make_float2(s, warp_sum(spread_sum<SHIFT>(raw, mask, s * inv_count)));
 }
 // A row's mean and 1 / sqrt(variance + eps) from its warps' sums, lane i holding warp i's: the squared differences
 // about the row's mean are those about each warp's own plus count (difference of the means)^2.
@@ -455,10 +459,10 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
   for (int v = 0; v < NV; ++v) {
     const int i = v * threads + static_cast<int>(threadIdx.x);
     mask[v] = shape.mask(i);
-    load_vector(raw[v], static_cast<const TX*>(a.x) + m * a.ldx + shape.col(i), mask[v], m + 1 < a.M);
+    load_vector<SHIFT>(raw[v], static_cast<const TX*>(a.x) + m * a.ldx + shape.col(i), mask[v], m + 1 < a.M);
   }
   const int n = warp_count(mask);
-  const float2 own = warp_moments(raw, mask, n ? 1.0f / static_cast<float>(n) : 0.0f);
+  const float2 own = warp_moments<SHIFT>(raw, mask, n ? 1.0f / static_cast<float>(n) : 0.0f);
   if (lane == 0) {
     red[warp] = own;
     cnt[warp] = static_cast<float>(n);
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
     weights8(a.b, a.w_kind, col, mask[v], 0.0f, bf);
     raw[v].get(f);
     norm_vector(f, st.x, st.y, wf, bf);
-    store_masked(static_cast<TY*>(a.y) + m * a.ldy + col, f, mask[v]);
+    store_masked<SHIFT>(static_cast<TY*>(a.y) + m * a.ldy + col, f, mask[v]);
   }
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[m] = st.x;
@@ -618,7 +622,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
         float2 f[4];
         raw.get(f);
         norm_vector(f, mu, r, wf[v], bf[v]);
-        store_masked(y + m * a.ldy + (v * columns + tid) * 8, f, mask[v]);
+        store_masked<SHIFT>(y + m * a.ldy + (v * columns + tid) * 8, f, mask[v]);
       }
       if (++s == stages) {
         s = 0;
@@ -751,13 +755,19 @@ __device__ __forceinline__ void store_part(float* p, const float2 (&f)[4], uint3
   }
 }
 
-// warp form, as forward; the CTA's warps add their sums up in shared memory, one after another.
-constexpr int kNormGradThreads = 128;
+// warp form, as forward.  One CTA an SM, of as many warps as its registers hold, so that there are few partial sums:
+// the warps add theirs up in shared memory, kSumBuffers of them at a time.
+constexpr int kSumBuffers = 4;
+template <typename TX, typename TY, int NV, bool SHIFT>
+__host__ __device__ constexpr int grad_warps() {
+  return NV == 4 ? 8 : NV == 2 ? (sizeof(TX) + sizeof(TY) > 4 ? 12 : 16) : SHIFT ? 16 : 20;
+}
 template <typename TX, typename TY, int LPR, int NV, bool SHIFT>
-__global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(const NormGrad a) {
-  constexpr int kRows = kNormGradThreads / LPR;  // a multiple of 4; the grid is even, so steps are multiples of 8
+__global__ void __launch_bounds__(32 * grad_warps<TX, TY, NV, SHIFT>(), 1) layer_norm_grad_warp_kernel(const NormGrad a) {
+  constexpr int kNormGradThreads = 32 * grad_warps<TX, TY, NV, SHIFT>();
+  constexpr int kRows = kNormGradThreads / LPR;  // (times a grid that is a multiple of 8, or the whole matrix)
   constexpr int kCols = LPR * NV * 8;
-  __shared__ __align__(16) float sums[2 * kCols];
+  __shared__ __align__(16) float sums[kSumBuffers][2 * kCols];
   griddep_launch_dependents();
   const int sub = threadIdx.x % LPR;
   const TX* x = static_cast<const TX*>(a.x);
@@ -785,8 +795,8 @@ __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(
     nr = in ? a.rstd[m] : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      load_vector(nx[v], x + m * a.ldx + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
-      load_vector(ny[v], dy + m * a.lddy + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
+      load_vector<SHIFT>(nx[v], x + m * a.ldx + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
+      load_vector<SHIFT>(ny[v], dy + m * a.lddy + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
     }
   };
   fetch(m0 + off);
@@ -810,7 +820,7 @@ __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(
       if (!mask[v]) continue;
       float2 f[4];
       grad_dx(h[v], g[v], rc1, rc2, r, f);
-      store_masked(static_cast<TX*>(a.dx) + m * a.lddx + shape.col(v * LPR + sub), f, mask[v]);
+      store_masked<SHIFT>(static_cast<TX*>(a.dx) + m * a.lddx + shape.col(v * LPR + sub), f, mask[v]);
     }
   }
   if (!a.parts) return;
@@ -828,30 +838,40 @@ __global__ void __launch_bounds__(kNormGradThreads) layer_norm_grad_warp_kernel(
           db[v][i].y += __shfl_xor_sync(0xffffffffu, db[v][i].y, o);
         }
   }
-  for (int n = threadIdx.x; n < 2 * kCols; n += kNormGradThreads) sums[n] = 0.0f;
+  for (int n = threadIdx.x; n < kSumBuffers * 2 * kCols; n += kNormGradThreads) sums[0][n] = 0.0f;
   __syncthreads();
+  // on the grid a warp's lanes hold each column once; off it every row group has columns of its own
   constexpr int kGroups = SHIFT ? kNormGradThreads / LPR : kNormGradThreads / 32;
-  for (int t = 0; t < kGroups; ++t) {
-    const int own = SHIFT ? static_cast<int>(threadIdx.x) / LPR
-                          : (threadIdx.x & 31) < LPR ? static_cast<int>(threadIdx.x) / 32 : -1;
-    if (own == t) {
+  const int own = SHIFT ? static_cast<int>(threadIdx.x) / LPR
+                        : (threadIdx.x & 31) < LPR ? static_cast<int>(threadIdx.x) / 32 : -1;
+  for (int t = 0; t < kGroups; t += kSumBuffers) {
+    if (own >= t && own < t + kSumBuffers) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float* sw = sums + shape.col(v * LPR + sub);
+        float* sw = sums[own - t] + shape.col(v * LPR + sub);
+        if (!SHIFT || mask[v] == 0xFFu) {
+          if (!mask[v]) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (mask[v] >> j & 1u) {
+          for (int j = 0; j < 8; ++j) {
             sw[j] += j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
             sw[kCols + j] += j & 1 ? db[v][j / 2].y : db[v][j / 2].x;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (mask[v] >> j & 1u) {
+              sw[j] += j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
+              sw[kCols + j] += j & 1 ? db[v][j / 2].y : db[v][j / 2].x;
+            }
+        }
       }
     }
     __syncthreads();
   }
   float* part = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
   for (int n = threadIdx.x; n < a.N; n += kNormGradThreads) {
-    part[n] = sums[n];
-    part[a.N + n] = sums[kCols + n];
+    part[n] = (sums[0][n] + sums[1][n]) + (sums[2][n] + sums[3][n]);
+    part[a.N + n] = (sums[0][kCols + n] + sums[1][kCols + n]) + (sums[2][kCols + n] + sums[3][kCols + n]);
   }
 }
 
@@ -1013,7 +1033,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
           db[v][k] = __fadd2_rn(db[v][k], yf[k]);
         }
         grad_dx(h, g, st.z, st.w, st.y, f);
-        store_masked(out + m * a.lddx + (v * columns + tid) * 8, f, mask[v]);
+        store_masked<SHIFT>(out + m * a.lddx + (v * columns + tid) * 8, f, mask[v]);
       }
       if (++s == stages) {
         s = 0;
@@ -1174,7 +1194,10 @@ bool dtype_ok(int32_t d) { return d == FP8G_BF16 || d == FP8G_F32; }
 int dtype_size(int32_t d) { return d == FP8G_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t kWarpMaxN = 1024;      // warp form: up to 4 vectors a lane
+// The warp form's vectors a row, at most, on the 16-byte grid and off it.  Beyond them a lane's registers (weights, next
+// row, backward the sums) leave too few warps an SM: 16384 x 1000 bf16 forward 30 us against 21 in the ring,
+// backward 29 against 33; 16384 x 501 forward 30 against 25, backward 41 against 38.
+constexpr int64_t kWarpVectors = 64, kWarpGradVectors = 128, kWarpShiftVectors = 32;
 constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice that in clusters of two
 constexpr int64_t kCtaMaxN = 32768;      // cta form: up to 4 vectors a thread
 constexpr int64_t kScalarMaxN = 16384;   // scalar form: up to 16 values a thread, forward ...
@@ -1265,12 +1288,11 @@ template <typename TX, typename TY, bool SHIFT>
 int layer_norm_vectors(const NormArgs& a, Grid grid, const DeviceInfo* dev, cudaStream_t s) {
   const int64_t M = a.M, vecs = row_vectors(a.N, grid);
   const int sms = dev->sm_count;
-  if (vecs * 8 <= kWarpMaxN) {
+  if (vecs <= (SHIFT ? kWarpShiftVectors : kWarpVectors)) {
     auto go = vecs <= 8    ? layer_norm_warp_kernel<TX, TY, 8, 1, SHIFT>
               : vecs <= 16 ? layer_norm_warp_kernel<TX, TY, 16, 1, SHIFT>
               : vecs <= 32 ? layer_norm_warp_kernel<TX, TY, 32, 1, SHIFT>
-              : vecs <= 64 ? layer_norm_warp_kernel<TX, TY, 32, 2, SHIFT>
-                           : layer_norm_warp_kernel<TX, TY, 32, 4, SHIFT>;
+                           : layer_norm_warp_kernel<TX, TY, 32, 2, false>;
     const int64_t per = kNormThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
     const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 8 * static_cast<int64_t>(sms));
     go<<<static_cast<unsigned>(ctas), kNormThreads, 0, s>>>(a);
@@ -1314,15 +1336,18 @@ template <typename TX, typename TY, bool SHIFT>
 int layer_norm_grad_vectors(const NormGrad& a, Grid grid, int64_t* P, const DeviceInfo* dev, cudaStream_t s) {
   const int64_t M = a.M, vecs = row_vectors(a.N, grid);
   const int sms = dev->sm_count;
-  if (vecs * 8 <= kWarpMaxN) {
+  if (vecs <= (SHIFT ? kWarpShiftVectors : kWarpGradVectors)) {
     auto go = vecs <= 8    ? layer_norm_grad_warp_kernel<TX, TY, 8, 1, SHIFT>
               : vecs <= 16 ? layer_norm_grad_warp_kernel<TX, TY, 16, 1, SHIFT>
               : vecs <= 32 ? layer_norm_grad_warp_kernel<TX, TY, 32, 1, SHIFT>
-              : vecs <= 64 ? layer_norm_grad_warp_kernel<TX, TY, 32, 2, SHIFT>
-                           : layer_norm_grad_warp_kernel<TX, TY, 32, 4, SHIFT>;
-    const int64_t per = kNormGradThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
-    *P = std::min<int64_t>((M + per - 1) / per, std::min<int64_t>(4 * static_cast<int64_t>(sms), kNormMaxParts) / 2 * 2);
-    go<<<static_cast<unsigned>(*P), kNormGradThreads, 0, s>>>(a);
+              : vecs <= 64 ? layer_norm_grad_warp_kernel<TX, TY, 32, 2, false>
+                           : layer_norm_grad_warp_kernel<TX, TY, 32, 4, false>;
+    const int threads = 32 * (vecs <= 32   ? grad_warps<TX, TY, 1, SHIFT>()
+                              : vecs <= 64 ? grad_warps<TX, TY, 2, false>()
+                                           : grad_warps<TX, TY, 4, false>());
+    const int64_t per = threads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
+    *P = std::min<int64_t>((M + per - 1) / per, std::min<int64_t>(sms, kNormMaxParts) / 8 * 8);
+    go<<<static_cast<unsigned>(*P), threads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
   }
   const RingPlan p = ring_plan(M, vecs, sizeof(TX) + sizeof(TY), 32, kRingGradThreads, grid, sms);
