@@ -9,11 +9,11 @@
 //
 // Every tensor is cut into chunks of U 16-byte groups a thread on the 16-byte grid of its addresses, whatever its own
 // alignment: only a tensor's first and last group can be partial, and those are taken value by value.  U = 16 keeps
-// more loads in flight, U = 4 gives a few megabytes to more CTAs (clip_unroll).
+// more loads in flight, U = 4 gives fewer megabytes to more CTAs (clip_plan).
 //
 // 470 MB of bf16 gradients: 222 us with U = 16 and 8 CTAs an SM, 238 with U = 8 and 4; the first pass reads at the copy
-// rate, the second moves 800 MB (77 MB of its reads are still in L2), reads and writes mixed, at 85% of it.  Cache hints
-// on either side and the order of the chunks changed nothing beyond 1%.
+// rate, the second moves 800 MB (77 MB of its reads are still in L2), reads and writes mixed, at 85% of it.  Cache
+// hints on either side and the order of the chunks changed nothing beyond 1%.
 
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -43,10 +43,9 @@ struct ClipTable {
 };
 static_assert(sizeof(ClipTable<kClipCap>) <= 32000, "kernel arguments hold 32764 bytes");
 
-// The tensor that chunk c belongs to.
+// The tensor that chunk c belongs to: among [lo, hi].
 template <int CAP>
-__device__ __forceinline__ int find_tensor(const ClipTable<CAP>& t, uint32_t c) {
-  int lo = 0, hi = t.n - 1;
+__device__ __forceinline__ int find_tensor(const ClipTable<CAP>& t, uint32_t c, int lo, int hi) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (c < t.end[mid]) hi = mid;
@@ -133,8 +132,9 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __gr
   griddep_launch_dependents();  // the scaling pass may start (it waits for this grid's sums)
   float s[1] = {0.0f};
   const uint32_t chunks = t.end[t.n - 1];
+  int i = 0;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = find_tensor(t, c);
+    i = c < t.end[i] ? i : find_tensor(t, c, i, t.n - 1);
     s[0] += t.dtype[i] == FP8G_F32 ? chunk_square_sum<float, U>(t, i, c)
                                     : chunk_square_sum<__nv_bfloat16, U>(t, i, c);
   }
@@ -144,16 +144,24 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __gr
 
 // The norm from the partial sums: the same value in every CTA that calls it.
 __device__ __forceinline__ float join_norm(const float* __restrict__ parts, int32_t P) {
-  __shared__ double s_sum[kClipThreads];
+  __shared__ double s_sum[kClipThreads / 32];
   double s = 0.0;
-  for (int i = threadIdx.x; i < P; i += kClipThreads) s += static_cast<double>(parts[i]);
-  s_sum[threadIdx.x] = s;
-  __syncthreads();
-  for (int off = kClipThreads / 2; off > 0; off >>= 1) {
-    if (threadIdx.x < off) s_sum[threadIdx.x] += s_sum[threadIdx.x + off];
-    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < (kClipMaxCtas + kClipThreads - 1) / kClipThreads; ++i) {
+    const int k = i * kClipThreads + static_cast<int>(threadIdx.x);
+    s += k < P ? static_cast<double>(__ldcg(parts + k)) : 0.0;
   }
-  return static_cast<float>(sqrt(s_sum[0]));
+  for (int k = kClipMaxCtas / kClipThreads * kClipThreads + kClipThreads + static_cast<int>(threadIdx.x); k < P;
+       k += kClipThreads)  // (more than one launch's)
+    s += static_cast<double>(__ldcg(parts + k));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = s_sum[0];
+#pragma unroll
+  for (int w = 1; w < kClipThreads / 32; ++w) s += s_sum[w];
+  return static_cast<float>(sqrt(s));
 }
 
 __global__ void __launch_bounds__(kClipThreads) grad_norm_join_kernel(const float* __restrict__ parts, int32_t P,
@@ -211,9 +219,10 @@ __global__ void __launch_bounds__(kClipThreads) grad_clip_kernel(const __grid_co
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float coef = n + eps <= max_norm ? 1.0f : max_norm / (n + eps);  // a NaN norm makes every output NaN
   const uint32_t chunks = t.end[t.n - 1];
+  int i = t.n - 1;
   for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
     const uint32_t c = chunks - 1 - b;
-    const int i = find_tensor(t, c);
+    i = i == 0 || c >= t.end[i - 1] ? i : find_tensor(t, c, 0, i);
     if (coef == 1.0f && t.out[i] == t.grad[i]) continue;  // in place and nothing to scale
     if (t.dtype[i] == FP8G_F32) chunk_scale<float, U>(t, i, c, coef);
     else chunk_scale<__nv_bfloat16, U>(t, i, c, coef);
@@ -243,11 +252,18 @@ int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* out
   return i;
 }
 
-// Whether the chunks are small: up to 64 MB, where 16 KB chunks give every SM some.
-bool small_chunks(const int64_t* numels, const int32_t* dtypes, int32_t n) {
+// Chunk size and CTAs by the bytes of all tensors.  16 KB chunks (U = 4) up to 256 MB: 36 MB of bf16 took 34 us and
+// 17 MB of odd tensors 23 us, with 64 KB chunks 35 and 25; beyond, 64 KB ones (470 MB: 224 us, 238 with 32 KB).  Every
+// CTA of the second pass sums all partial sums first: 608 of them up to 24 MB (23 us for 17 MB, 29 with 1216), more
+// where there is more to hide that under (157 MB: 92 us with 608, 84 with 1216).
+struct ClipPlan {
+  bool small_chunks;
+  uint32_t ctas;
+};
+ClipPlan clip_plan(const int64_t* numels, const int32_t* dtypes, int32_t n) {
   int64_t bytes = 0;
   for (int32_t i = 0; i < n; ++i) bytes += numels[i] * (dtypes[i] == FP8G_F32 ? 4 : 2);
-  return bytes <= int64_t{64} << 20;
+  return {bytes <= int64_t{256} << 20, bytes <= int64_t{24} << 20 ? kClipMaxCtas / 2u : kClipMaxCtas};
 }
 
 int64_t clip_launches(int32_t n) { return (static_cast<int64_t>(n) + kClipCap - 1) / kClipCap; }
@@ -272,12 +288,12 @@ int check_tensors(const void* const* grads, void* const* outs, const int64_t* nu
 // Partial sums of all the tensors; *P is how many were written.
 template <int CAP, int U>
 int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
-                      const int32_t* dtypes, int32_t n, float* parts, int32_t* P, cudaStream_t s) {
+                      const int32_t* dtypes, int32_t n, uint32_t max_ctas, float* parts, int32_t* P, cudaStream_t s) {
   *P = 0;
   for (int32_t i = 0; i < n;) {
     i = fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
-    const uint32_t ctas = std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas);
+    const uint32_t ctas = std::min(t.end[t.n - 1], max_ctas);
     grad_norm_part_kernel<CAP, U><<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
     *P += static_cast<int32_t>(ctas);
   }
@@ -285,11 +301,11 @@ int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* 
 }
 
 template <int CAP, int U>
-int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, float* norm,
-                     float* parts, cudaStream_t s) {
+int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
+                     uint32_t max_ctas, float* norm, float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch<CAP, U>(t, grads, nullptr, numels, dtypes, n, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, nullptr, numels, dtypes, n, max_ctas, parts, &P, s);
   if (st != FP8G_OK) return st;
   grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, P, norm);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
@@ -297,10 +313,10 @@ int grad_norm_launch(const void* const* grads, const int64_t* numels, const int3
 
 template <int CAP, int U>
 int clip_launch(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes, int32_t n,
-                float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
+                uint32_t max_ctas, float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch<CAP, U>(t, grads, outs, numels, dtypes, n, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, outs, numels, dtypes, n, max_ctas, parts, &P, s);
   if (st != FP8G_OK) return st;
   if (P == 0) {  // no values at all
     grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, 0, norm);
@@ -311,7 +327,7 @@ int clip_launch(const void* const* grads, void* const* outs, const int64_t* nume
     i = one ? n : fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas));
+    cfg.gridDim = dim3(std::min(t.end[t.n - 1], max_ctas));
     cfg.blockDim = dim3(kClipThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -319,8 +335,8 @@ int clip_launch(const void* const* grads, void* const* outs, const int64_t* nume
     attr[0].val.programmaticStreamSerializationAllowed = one ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<CAP, U>, t, static_cast<const float*>(parts), P, max_norm, eps, norm) !=
-        cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, grad_clip_kernel<CAP, U>, t, static_cast<const float*>(parts), P, max_norm, eps,
+                           norm) != cudaSuccess) {
       cudaGetLastError();
       return FP8G_ERR_CUDA;
     }
@@ -349,11 +365,12 @@ extern "C" int fp8g_grad_norm(const void* const* grads, const int64_t* numels, c
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  const bool small = small_chunks(numels, dtypes, n);
-  auto go = n <= 64    ? (small ? grad_norm_launch<64, 4> : grad_norm_launch<64, 16>)
-            : n <= 256 ? (small ? grad_norm_launch<256, 4> : grad_norm_launch<256, 16>)
-                       : (small ? grad_norm_launch<kClipCap, 4> : grad_norm_launch<kClipCap, 16>);
-  return go(grads, numels, dtypes, n, norm, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+  const ClipPlan plan = clip_plan(numels, dtypes, n);
+  auto go = n <= 64    ? (plan.small_chunks ? grad_norm_launch<64, 4> : grad_norm_launch<64, 16>)
+            : n <= 256 ? (plan.small_chunks ? grad_norm_launch<256, 4> : grad_norm_launch<256, 16>)
+                       : (plan.small_chunks ? grad_norm_launch<kClipCap, 4> : grad_norm_launch<kClipCap, 16>);
+  return go(grads, numels, dtypes, n, plan.ctas, norm, static_cast<float*>(workspace),
+            static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
@@ -368,10 +385,10 @@ extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, 
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  const bool small = small_chunks(numels, dtypes, n);
-  auto go = n <= 64    ? (small ? clip_launch<64, 4> : clip_launch<64, 16>)
-            : n <= 256 ? (small ? clip_launch<256, 4> : clip_launch<256, 16>)
-                       : (small ? clip_launch<kClipCap, 4> : clip_launch<kClipCap, 16>);
-  return go(grads, outs, numels, dtypes, n, max_norm, eps, norm, static_cast<float*>(workspace),
+  const ClipPlan plan = clip_plan(numels, dtypes, n);
+  auto go = n <= 64    ? (plan.small_chunks ? clip_launch<64, 4> : clip_launch<64, 16>)
+            : n <= 256 ? (plan.small_chunks ? clip_launch<256, 4> : clip_launch<256, 16>)
+                       : (plan.small_chunks ? clip_launch<kClipCap, 4> : clip_launch<kClipCap, 16>);
+  return go(grads, outs, numels, dtypes, n, plan.ctas, max_norm, eps, norm, static_cast<float*>(workspace),
             static_cast<cudaStream_t>(stream));
 }
