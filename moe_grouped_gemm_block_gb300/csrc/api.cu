@@ -99,7 +99,8 @@ int allow_shared_memory(const void* kernel, size_t bytes) {
   const std::pair<int, const void*> key{dev, kernel};
   const auto it = allowed.find(key);
   if (it != allowed.end() && it->second >= bytes) return FP8G_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+      cudaSuccess) {
     cudaGetLastError();
     return FP8G_ERR_CUDA;
   }

@@ -304,7 +304,7 @@ __host__ __device__ constexpr int gate_warp_words(int topk) {
 }
 template <int LPR>
 size_t gate_smem(int E, int topk) {
-  return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + std::max(kGateWarps * E, kGateWarps * gate_warp_words<LPR>(topk)));
+  return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + kGateWarps * std::max(E, gate_warp_words<LPR>(topk)));
 }
 
 // CTAs that are resident on an SM at once.
@@ -315,6 +315,7 @@ template <typename TL, int VPL, int LPR>
 __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kernel(const GateArgs a) {
   constexpr int G = 32 / LPR;  // rows a warp at once
   using Rank = Ranking<TL, VPL, LPR>;
+  constexpr bool kOneWord = std::is_same_v<TL, __nv_bfloat16> && VPL == 8;  // a pick's key holds its index
   extern __shared__ __align__(16) float smem[];
   __shared__ float2 s_loss[kGateCluster];
   __shared__ float red[2 * 2 * kGateWarps];
@@ -353,27 +354,40 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
     if (t0 + stride < a.T) fetch(t0 + stride);
     Rank rank;
     rank.init(l, base, E, list);
-    Pick first = rank.next();
-    for (int j = 0;; ) {
-      if (sub == 0) {
-        pick_key[grp * topk + j] = first.key;
-        if constexpr (!std::is_same_v<TL, __nv_bfloat16> || VPL != 8) pick_id[grp * topk + j] = first.id;
-      }
-      if (++j == topk) break;
-      first = rank.next();
-    }
-    __syncwarp();
-    float mx = Rank::value({pick_key[grp * topk], 0});
+    // the row's picks go to a lane each (of a whole warp's row), or through shared memory to the row's lanes in turn
+    Pick mine = rank.next();
+    float mx = Rank::value(mine);
     if (mx == -INFINITY) mx = 0.0f;  // every expert ruled out: the exponentials are all 0
-    // the row's picks, a lane each (or several)
-    float picked = 0.0f;
-    for (int j = sub; j < topk; j += LPR) {
-      Pick p{pick_key[grp * topk + j], 0};
-      const float e = exp_below(Rank::value(p), mx);
-      picked += e;
-      if constexpr (std::is_same_v<TL, __nv_bfloat16> && VPL == 8) pick_id[grp * topk + j] = Rank::id(p);
-      pick_w[grp * topk + j] = e;
+    if constexpr (G == 1) {
+#pragma unroll 2
+      for (int j = 1; j < topk; ++j) {
+        const Pick p = rank.next();
+        if (lane == j) mine = p;
+      }
+    } else {
+      for (int j = 0;;) {
+        if (sub == 0) {
+          pick_key[grp * topk + j] = mine.key;
+          if constexpr (!kOneWord) pick_id[grp * topk + j] = mine.id;
+        }
+        if (++j == topk) break;
+        mine = rank.next();
+      }
+      __syncwarp();
     }
+    float picked = 0.0f;
+    if constexpr (G == 1) {
+      if (lane < topk) picked = exp_below(Rank::value(mine), mx);
+    } else {
+      for (int j = sub; j < topk; j += LPR) {
+        const Pick p{pick_key[grp * topk + j], 0};
+        const float e = exp_below(Rank::value(p), mx);
+        picked += e;
+        if constexpr (kOneWord) pick_id[grp * topk + j] = Rank::id(p);
+        pick_w[grp * topk + j] = e;
+      }
+    }
+    const float own = picked;
     picked = row_sum<LPR>(picked);
     float f[VPL], s = 0.0f;
     l.get(f);
@@ -388,19 +402,29 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
 #pragma unroll
       for (int i = 0; i < VPL; ++i) acc[i] = fmaf(f[i], inv, acc[i]);
     }
-    if (sub == 0) factor[grp] = !real ? -1.0f : a.renorm ? (picked == 0.0f ? 0.0f : recip_approx(picked)) : inv;
-    __syncwarp();
-    // the warp's rows are neighbours: their results go out in one piece
-    for (int q = lane; q < G * topk; q += 32) {
-      const int g = G == 1 ? 0 : static_cast<int>((static_cast<float>(q) + 0.5f) * inv_k);
-      if (t0 + g >= a.T) break;
-      const int id = pick_id[q];
-      const float w = factor[g];
-      a.ids[t0 * topk + q] = id;
-      a.weights[t0 * topk + q] = w == -1.0f ? 0.0f : pick_w[q] * w;
-      if (w != -1.0f) atomicAdd(cnt + id, 1);  // whole numbers: the order does not matter
+    const float scale = a.renorm ? (picked == 0.0f ? 0.0f : recip_approx(picked)) : inv;
+    if constexpr (G == 1) {
+      if (lane < topk) {
+        const int id = Rank::id(mine);
+        a.ids[t0 * topk + lane] = id;
+        a.weights[t0 * topk + lane] = real ? own * scale : 0.0f;
+        if (real) atomicAdd(cnt + id, 1);  // whole numbers: the order does not matter
+      }
+    } else {
+      if (sub == 0) factor[grp] = real ? scale : -1.0f;
+      __syncwarp();
+      // the warp's rows are neighbours: their results go out in one piece
+      for (int q = lane; q < G * topk; q += 32) {
+        const int g = static_cast<int>((static_cast<float>(q) + 0.5f) * inv_k);
+        if (t0 + g >= a.T) break;
+        const int id = pick_id[q];
+        const float w = factor[g];
+        a.ids[t0 * topk + q] = id;
+        a.weights[t0 * topk + q] = w == -1.0f ? 0.0f : pick_w[q] * w;
+        if (w != -1.0f) atomicAdd(cnt + id, 1);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
   // the CTA's sums: over the rows that a warp's lanes shared, then over the warps
 #pragma unroll
@@ -461,8 +485,8 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
   }
 }
 
-// Counts and loss from the CTAs' partial sums, in their order.  One cluster; a CTA takes 32 experts at a time, its warps
-// a share of the partial sums each.
+// Counts and loss from the CTAs' partial sums, in their order.  One cluster; a CTA takes 32 experts at a time, its
+// warps a share of the partial sums each.
 constexpr int kGateJoinThreads = 1024;
 __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int32_t P, int32_t E, int32_t topk,
@@ -542,7 +566,8 @@ struct GateGrad {
 template <typename TL, int VPL, int LPR>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const GateGrad a) {
   constexpr int G = 32 / LPR;
-  constexpr int kPicks = LPR >= kGateMaxTopk ? 1 : LPR * 8 >= kGateMaxTopk ? kGateMaxTopk / LPR : 8;  // a lane's, at most
+  // a lane's selected experts, at most
+  constexpr int kPicks = LPR >= kGateMaxTopk ? 1 : LPR * 8 >= kGateMaxTopk ? kGateMaxTopk / LPR : 8;
   __shared__ float red[2 * kGateWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
   const int E = a.E, topk = a.topk;
@@ -557,7 +582,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
   const TL* logits = static_cast<const TL*>(a.logits);
   TL* dlogits = static_cast<TL*>(a.dlogits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps * G;
-  // the next row's logits and this lane's (first) selected expert and gradient are on their way while a row is worked on
+  // the next row's logits and this lane's (first) selected expert and gradient are on their way meanwhile
   Logits<TL, VPL> next;
   bool next_real = false;
   int next_id = -1;
@@ -782,7 +807,8 @@ __global__ void __launch_bounds__(THREADS) moe_combine_backward_kernel(
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack2(w[j] * g[i].x, w[j] * g[i].y);
-        __stcs(reinterpret_cast<uint4*>(dD + static_cast<int64_t>(r[j]) * lddd + n), make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4*>(dD + static_cast<int64_t>(r[j]) * lddd + n),
+               make_uint4(o[0], o[1], o[2], o[3]));
         if (dweights) {
           float2 f[4], s = make_float2(0.0f, 0.0f);
           d[j].get(f);
@@ -823,8 +849,8 @@ int gate_launch(const GateArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   const size_t smem = gate_smem<LPR>(a.E, a.topk);
   const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), smem);
   if (st != FP8G_OK) return st;
-  // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs as
-  // are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38).
+  // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs
+  // as are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38).
   const int64_t at_once = kGateWarps * (32 / LPR);
   const bool few = gate_few(a.T, a.E);
   const int cluster = a.T <= 2 * at_once || !few ? 1 : kGateCluster;
@@ -1017,9 +1043,9 @@ extern "C" int fp8g_moe_combine(const void* D, int64_t M, int64_t N, int64_t ldd
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto launch = [&](auto kern, auto type) {
     using TO = decltype(type);
-    kern<<<grid, kCombineThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(D), M, static_cast<int32_t>(N), ldd, entry_row,
-                                          topk, weights, static_cast<const TO*>(residual), ldr, static_cast<TO*>(out),
-                                          ldo, dev->status);
+    kern<<<grid, kCombineThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(D), M, static_cast<int32_t>(N), ldd,
+                                          entry_row, topk, weights, static_cast<const TO*>(residual), ldr,
+                                          static_cast<TO*>(out), ldo, dev->status);
   };
   if (out_dtype == FP8G_F32)
     launch(topk <= 2 ? moe_combine_kernel<float, 2> : moe_combine_kernel<float, 4>, float());
@@ -1033,7 +1059,8 @@ extern "C" int fp8g_moe_combine_backward(const void* dout, int32_t dout_dtype, i
                                          const int32_t* row_token, int64_t T, int32_t topk, const float* weights,
                                          void* dD, int64_t lddd, float* dweights, void* stream) {
   if (!dtype_ok(dout_dtype) || M < 0 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFFF || N % 8 != 0 || lddd < N ||
-      T < 0 || T > 0x7FFFFFFF - 4096 /* beside the CTAs of the zero rows */ || topk < 1 || T * topk > 0x7FFFFFFF || lddo < N || (dweights && ldd < N))
+      T < 0 || T > 0x7FFFFFFF - 4096 /* beside the CTAs of the zero rows */ || topk < 1 || T * topk > 0x7FFFFFFF ||
+      lddo < N || (dweights && ldd < N))
     return FP8G_ERR_INVALID_ARG;
   if (M == 0 && T == 0) return FP8G_OK;
   if ((M > 0 && (!dD || !row_token || (dweights && !D))) || (T > 0 && (!entry_row || !dout)))

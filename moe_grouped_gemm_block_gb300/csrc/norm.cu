@@ -4,9 +4,9 @@
 //     with h = (x - mu) r and g = dy w:
 //     dx = r (g - mean_n g - h mean_n (g h)),   dw = sum_m dy h,   db = sum_m dy
 //
-// All sums are taken in fp32.  The variance is the mean of the squared differences from the mean (a second pass over the
-// values in registers), or in the ring from a value near it with a bound on what cancels; never the difference of
-// two large sums.
+// All sums are taken in fp32.  The variance is the mean of the squared differences from the mean (a second pass over
+// the values in registers), or in the ring from a value near it with a bound on what cancels; never the difference
+// of two large sums.
 //
 // Forms, by the row's length (rows go in vectors of 8 values on the 16-byte grid, see RowShape):
 //   warp     short rows: a row (or 2, 4 at once) per warp, all in registers, no barriers
@@ -763,7 +763,8 @@ __host__ __device__ constexpr int grad_warps() {
   return NV == 4 ? 8 : NV == 2 ? (sizeof(TX) + sizeof(TY) > 4 ? 12 : 16) : SHIFT ? 16 : 20;
 }
 template <typename TX, typename TY, int LPR, int NV, bool SHIFT>
-__global__ void __launch_bounds__(32 * grad_warps<TX, TY, NV, SHIFT>(), 1) layer_norm_grad_warp_kernel(const NormGrad a) {
+__global__ void __launch_bounds__(32 * grad_warps<TX, TY, NV, SHIFT>(), 1)
+    layer_norm_grad_warp_kernel(const NormGrad a) {
   constexpr int kNormGradThreads = 32 * grad_warps<TX, TY, NV, SHIFT>();
   constexpr int kRows = kNormGradThreads / LPR;  // (times a grid that is a multiple of 8, or the whole matrix)
   constexpr int kCols = LPR * NV * 8;
@@ -1134,7 +1135,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_dx_any_kernel(
   }
 }
 
-// Partial sums of the weight gradients, any length and alignment: thread = column, CTA row blockIdx.y = a range of rows.
+// Partial sums of the weight gradients, any length and alignment: thread = column, blockIdx.y = a range of rows.
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_dw_any_kernel(
     const TY* __restrict__ dy, int64_t lddy, const TX* __restrict__ x, int64_t ldx,
@@ -1194,8 +1195,8 @@ bool dtype_ok(int32_t d) { return d == FP8G_BF16 || d == FP8G_F32; }
 int dtype_size(int32_t d) { return d == FP8G_F32 ? 4 : 2; }
 
 // ---------------------------------------------------------------- launches
-// The warp form's vectors a row, at most, on the 16-byte grid and off it.  Beyond them a lane's registers (weights, next
-// row, backward the sums) leave too few warps an SM: 16384 x 1000 bf16 forward 30 us against 21 in the ring,
+// The warp form's vectors a row, at most, on the 16-byte grid and off it.  Beyond them a lane's registers (weights,
+// next row, backward the sums) leave too few warps an SM: 16384 x 1000 bf16 forward 30 us against 21 in the ring,
 // backward 29 against 33; 16384 x 501 forward 30 against 25, backward 41 against 38.
 constexpr int64_t kWarpVectors = 64, kWarpGradVectors = 128, kWarpShiftVectors = 32;
 constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice that in clusters of two
@@ -1395,7 +1396,8 @@ int layer_norm_backward_launch(NormGrad a, float* dw, float* db, const DeviceInf
   if (!a.parts) return FP8G_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((2 * N + 31) / 32));
-  cfg.blockDim = dim3(32 * static_cast<unsigned>(std::min<int64_t>(kJoinMaxWarps, (P + kJoinUnroll - 1) / kJoinUnroll)));
+  const int64_t join_warps = std::min<int64_t>(kJoinMaxWarps, (P + kJoinUnroll - 1) / kJoinUnroll);
+  cfg.blockDim = dim3(32 * static_cast<unsigned>(join_warps));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

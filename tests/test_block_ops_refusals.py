@@ -51,8 +51,8 @@ def test_layer_norm_backward(lib, kw, want):
     assert lib.fp8g_layer_norm_backward(*_args(NORM_BWD, kw)) == want
 
 
-GATE = dict(l=P, d=1, T=50000, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, w=P, counts=P, loss=P, ws=P, wsb=BIG,
-            s=None)
+GATE = dict(l=P, d=1, T=50000, E=8, ldl=8, k=2, renorm=1, mask=None, coef=0.01, ids=P, w=P, counts=P, loss=P, ws=P,
+            wsb=BIG, s=None)
 
 
 @pytest.mark.parametrize("kw,want", [

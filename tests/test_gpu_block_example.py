@@ -57,7 +57,8 @@ def test_gradients_agree_with_autograd(T, hidden, E, topk, masked):
     ids, real = saved[5].long(), torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask
     wts = p.gather(1, ids)
     wts = wts / wts.sum(1, keepdim=True) * real[:, None]
-    ref = x_ + (torch.einsum("eno,to->ten", e_, y)[torch.arange(T, device="cuda")[:, None], ids] * wts[..., None]).sum(1)
+    every = torch.einsum("eno,to->ten", e_, y)[torch.arange(T, device="cuda")[:, None], ids]
+    ref = x_ + (every * wts[..., None]).sum(1)
     counts, tv = saved[7].float(), real.sum()
     ref_balance = 0.5 * E * (counts / (topk * tv) * p[real].sum(0) / tv).sum()
     ((ref * dout).sum() + ref_balance).backward()

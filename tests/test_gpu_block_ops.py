@@ -72,8 +72,8 @@ def _norm_bounds(x, w, b, mean, rstd, N):
 
 
 NORM_SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 31), (3, 64), (7, 127), (130, 128), (3, 129), (9, 264), (2, 1000),
-              (33, 1024), (2, 1025), (3, 2048), (5, 4099), (4, 4096), (3, 7168), (161, 7168), (2, 8200), (3, 16384), (2, 20001),
-              (2, 40000), (1, 70008)]
+              (33, 1024), (2, 1025), (3, 2048), (5, 4099), (4, 4096), (3, 7168), (161, 7168), (2, 8200), (3, 16384),
+              (2, 20001), (2, 40000), (1, 70008)]
 
 
 @pytest.mark.parametrize("M,N", NORM_SIZES)
@@ -191,8 +191,9 @@ def test_layer_norm_many_short_rows():
 
 # many rows a resident CTA, so that its ring of row stages goes round many times; the last ones have a ring of two
 # stages, and rows that two CTAs share
-@pytest.mark.parametrize("M,N,xd,yd", [(3001, 1032, "bf16", "bf16"), (4000, 2048, "f32", "bf16"), (2500, 7168, "bf16", "bf16"),
-                                       (3000, 1531, "bf16", "bf16"), (2000, 5003, "f32", "f32"), (1300, 8190, "bf16", "f32"),
+@pytest.mark.parametrize("M,N,xd,yd", [(3001, 1032, "bf16", "bf16"), (4000, 2048, "f32", "bf16"),
+                                       (2500, 7168, "bf16", "bf16"), (3000, 1531, "bf16", "bf16"),
+                                       (2000, 5003, "f32", "f32"), (1300, 8190, "bf16", "f32"),
                                        (1500, 16384, "f32", "f32"), (1111, 12001, "bf16", "bf16"),
                                        (5000, 1020, "bf16", "bf16"), (9000, 333, "f32", "bf16")])
 def test_layer_norm_many_rows(M, N, xd, yd):
@@ -395,7 +396,8 @@ def _rows_of(T, topk, E, drop, seed):
 
 
 @pytest.mark.parametrize("T,topk,E,N", [(1, 1, 1, 8), (2, 2, 4, 16), (5, 3, 4, 24), (64, 8, 32, 256), (37, 2, 8, 1000),
-                                        (9, 12, 16, 136), (40, 4, 8, 4096), (3, 5, 6, 7168), (300, 2, 3, 64), (7, 2, 4, 16400)])
+                                        (9, 12, 16, 136), (40, 4, 8, 4096), (3, 5, 6, 7168), (300, 2, 3, 64),
+                                        (7, 2, 4, 16400)])
 @pytest.mark.parametrize("yd", ["bf16", "f32"])
 @pytest.mark.parametrize("drop,residual,weighted", [(0, False, True), (5, True, True), (5, True, False)])
 def test_combine_and_gradient(T, topk, E, N, yd, drop, residual, weighted):
@@ -475,7 +477,8 @@ def test_combine_no_tokens_and_no_rows():
     assert not g.moe_combine(D, er).any()  # every entry dropped
     big = torch.full((256, 64), 3.0, dtype=torch.bfloat16, device="cuda")
     rt = torch.full((256,), -1, dtype=torch.int32, device="cuda")
-    dD, dw = g.moe_combine_backward(torch.empty((0, 64), device="cuda"), big, none, rt, torch.empty((0, 2), device="cuda"))
+    dD, dw = g.moe_combine_backward(torch.empty((0, 64), device="cuda"), big, none, rt,
+                                    torch.empty((0, 2), device="cuda"))
     assert dD.shape == (256, 64) and not dD.any() and dw.numel() == 0
 
 
