@@ -19,6 +19,7 @@ Work is enqueued on the current CUDA stream of the tensors' device; nothing sync
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -86,12 +87,18 @@ def _raise(code: int, what: str):
     raise Fp8GemmError(code, what)
 
 
-def _workspace(name: str, device, *sizes) -> torch.Tensor | None:
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *sizes) -> int:
     n = ctypes.c_int64()
     code = getattr(lib(), name)(*sizes, ctypes.byref(n))
     if code:
         _raise(code, name)
-    return _empty(n.value, dtype=_U8, device=device) if n.value else None
+    return n.value
+
+
+def _workspace(name: str, device, *sizes) -> torch.Tensor | None:
+    n = _workspace_bytes(name, *sizes)
+    return _empty(n, dtype=_U8, device=device) if n else None
 
 
 def _scratch(t: torch.Tensor) -> None:

@@ -104,19 +104,27 @@ __device__ __forceinline__ float chunk_square_sum(const ClipTable<CAP>& t, int i
     for (int u = 0; u < U; ++u) v[u] = __ldg(p + u * kClipThreads);
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] = square_sum(v[u], T());
-  } else {
+  } else {  // four groups at a time: the whole ones' loads together, then the partial ones (two of a tensor, at most)
+#pragma unroll 1
+    for (int u0 = 0; u0 < U; u0 += 4) {
+      uint4 v[4];
+      float e = 0.0f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * ch.kPer;
-      if (k >= 0 && k + ch.kPer <= ch.hi) {
-        s[u] = square_sum(__ldg(reinterpret_cast<const uint4*>(ch.g + k)), T());
-      } else {
-        for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q) {
-          const float f = to_f32(ch.g[q]);
-          s[u] = fmaf(f, f, s[u]);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t k = ch.lo + ((u0 + u) * kClipThreads + threadIdx.x) * ch.kPer;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (k >= 0 && k + ch.kPer <= ch.hi) {
+          v[u] = __ldg(reinterpret_cast<const uint4*>(ch.g + k));
+        } else {
+          for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q) {
+            const float f = to_f32(ch.g[q]);
+            e = fmaf(f, f, e);
+          }
         }
       }
+      s[0] += e + ((square_sum(v[0], T()) + square_sum(v[1], T())) + (square_sum(v[2], T()) + square_sum(v[3], T())));
     }
+    return s[0];
   }
 #pragma unroll
   for (int d = 1; d < U; d *= 2)
@@ -196,14 +204,25 @@ __device__ __forceinline__ void chunk_scale(const ClipTable<CAP>& t, int i, uint
     for (int u = 0; u < U; ++u) __stcs(q + u * kClipThreads, scaled(v[u], coef, T()));
     return;
   }
+#pragma unroll 1
+  for (int u0 = 0; u0 < U; u0 += 4) {  // as in the sum; without a common grid value by value
+    uint4 v[4];
+    bool full[4];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t k = ch.lo + (u * kClipThreads + threadIdx.x) * ch.kPer;
-    if (same && k >= 0 && k + ch.kPer <= ch.hi) {
-      *reinterpret_cast<uint4*>(ch.o + k) = scaled(*reinterpret_cast<const uint4*>(ch.g + k), coef, T());
-    } else {
-      for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q)
-        ch.o[q] = from_f32<T>(to_f32(ch.g[q]) * coef);
+    for (int u = 0; u < 4; ++u) {
+      const int64_t k = ch.lo + ((u0 + u) * kClipThreads + threadIdx.x) * ch.kPer;
+      full[u] = same && k >= 0 && k + ch.kPer <= ch.hi;
+      if (full[u]) v[u] = __ldcs(reinterpret_cast<const uint4*>(ch.g + k));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t k = ch.lo + ((u0 + u) * kClipThreads + threadIdx.x) * ch.kPer;
+      if (full[u]) {
+        *reinterpret_cast<uint4*>(ch.o + k) = scaled(v[u], coef, T());
+      } else {
+        for (int64_t q = max(k, int64_t{0}); q < min(k + ch.kPer, ch.hi); ++q)
+          ch.o[q] = from_f32<T>(to_f32(ch.g[q]) * coef);
+      }
     }
   }
 }
