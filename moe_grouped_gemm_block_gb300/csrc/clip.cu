@@ -29,6 +29,7 @@ constexpr int kClipThreads = 256;
 constexpr int kClipCap = 1024;       // tensors a launch; tables of 64 and 256 are there for their size (the arguments'
                                      // copies are most of a small call's host time)
 constexpr int kClipMaxCtas = 1216;   // partial sums a launch
+constexpr int kClipJoinLoads = (kClipMaxCtas + kClipThreads - 1) / kClipThreads;
 constexpr int32_t kClipMaxTensors = 1 << 20;
 constexpr int64_t kClipMaxValues = int64_t{1} << 42;  // of all tensors together
 
@@ -150,26 +151,41 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_part_kernel(const __gr
   if (threadIdx.x == 0) parts[blockIdx.x] = s[0];
 }
 
-// The norm from the partial sums: the same value in every CTA that calls it.
-__device__ __forceinline__ float join_norm(const float* __restrict__ parts, int32_t P) {
-  __shared__ double s_sum[kClipThreads / 32];
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < (kClipMaxCtas + kClipThreads - 1) / kClipThreads; ++i) {
-    const int k = i * kClipThreads + static_cast<int>(threadIdx.x);
-    s += k < P ? static_cast<double>(__ldcg(parts + k)) : 0.0;
+// A sum and what its roundings lost: the exact sum of two floats is their rounded sum and its error (Knuth).
+struct Sum2 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v, float v_lo) {
+    const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)), v_lo));
+    hi = s;
   }
-  for (int k = kClipMaxCtas / kClipThreads * kClipThreads + kClipThreads + static_cast<int>(threadIdx.x); k < P;
-       k += kClipThreads)  // (more than one launch's)
-    s += static_cast<double>(__ldcg(parts + k));
+};
+
+// The norm from the partial sums: the same value in every CTA that calls it.  The sums are pairs of floats, not doubles:
+// every CTA of the second pass takes them, and this GPU's fp64 rate made that 15 us of a 26 MB call's 30.
+__device__ __forceinline__ float join_norm(const float* __restrict__ parts, int32_t P) {
+  __shared__ Sum2 s_sum[kClipThreads / 32];
+  float v[kClipJoinLoads];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  for (int i = 0; i < kClipJoinLoads; ++i) {
+    const int k = i * kClipThreads + static_cast<int>(threadIdx.x);
+    v[i] = k < P ? __ldcg(parts + k) : 0.0f;
+  }
+  Sum2 s{0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kClipJoinLoads; ++i) s.add(v[i], 0.0f);
+  for (int k = kClipJoinLoads * kClipThreads + static_cast<int>(threadIdx.x); k < P; k += kClipThreads)
+    s.add(__ldcg(parts + k), 0.0f);  // (more than one launch's)
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    s.add(__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off));
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
   __syncthreads();
   s = s_sum[0];
 #pragma unroll
-  for (int w = 1; w < kClipThreads / 32; ++w) s += s_sum[w];
-  return static_cast<float>(sqrt(s));
+  for (int w = 1; w < kClipThreads / 32; ++w) s.add(s_sum[w].hi, s_sum[w].lo);
+  // (an infinite sum's error is not a number)
+  return sqrtf(isinf(s.hi) ? s.hi : s.hi + s.lo);
 }
 
 __global__ void __launch_bounds__(kClipThreads) grad_norm_join_kernel(const float* __restrict__ parts, int32_t P,
