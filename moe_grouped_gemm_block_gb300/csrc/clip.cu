@@ -9,11 +9,11 @@
 //
 // Every tensor is cut into chunks of U 16-byte groups a thread on the 16-byte grid of its addresses, whatever its own
 // alignment: only a tensor's first and last group can be partial, and those are taken value by value.  U = 16 keeps
-// more loads in flight, U = 4 gives fewer megabytes to more CTAs (clip_plan).
+// more loads in flight, U = 4 gives fewer megabytes to more CTAs (small_chunks).
 //
-// 470 MB of bf16 gradients: 222 us with U = 16 and 8 CTAs an SM, 238 with U = 8 and 4; the first pass reads at the copy
-// rate, the second moves 800 MB (77 MB of its reads are still in L2), reads and writes mixed, at 85% of it.  Cache
-// hints on either side and the order of the chunks changed nothing beyond 1%.
+// 470 MB of bf16 gradients: 220 us.  The first pass reads at the copy rate, the second moves 800 MB (77 MB of its reads
+// are still in L2), reads and writes mixed, at 85% of it.  Cache hints on either side and the order of the chunks
+// changed nothing beyond 1%.
 
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -28,7 +28,7 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kClipCap = 1024;       // tensors a launch; tables of 64 and 256 are there for their size (the arguments'
                                      // copies are most of a small call's host time)
-constexpr int kClipMaxCtas = 1216;   // partial sums a launch
+constexpr int kClipMaxCtas = 608;    // partial sums a launch: 4 CTAs an SM (8 are within 1% of it, or slower)
 constexpr int kClipJoinLoads = (kClipMaxCtas + kClipThreads - 1) / kClipThreads;
 constexpr int32_t kClipMaxTensors = 1 << 20;
 constexpr int64_t kClipMaxValues = int64_t{1} << 42;  // of all tensors together
@@ -161,8 +161,8 @@ struct Sum2 {
   }
 };
 
-// The norm from the partial sums: the same value in every CTA that calls it.  The sums are pairs of floats, not doubles:
-// every CTA of the second pass takes them, and this GPU's fp64 rate made that 15 us of a 26 MB call's 30.
+// The norm from the partial sums: the same value in every CTA that calls it.  The sums are pairs of floats, not
+// doubles: every CTA of the second pass takes them, and this GPU's fp64 rate made that 15 us of a 26 MB call's 30.
 __device__ __forceinline__ float join_norm(const float* __restrict__ parts, int32_t P) {
   __shared__ Sum2 s_sum[kClipThreads / 32];
   float v[kClipJoinLoads];
@@ -287,18 +287,12 @@ int32_t fill_table(ClipTable<CAP>& t, const void* const* grads, void* const* out
   return i;
 }
 
-// Chunk size and CTAs by the bytes of all tensors.  16 KB chunks (U = 4) up to 256 MB: 36 MB of bf16 took 34 us and
-// 17 MB of odd tensors 23 us, with 64 KB chunks 35 and 25; beyond, 64 KB ones (470 MB: 224 us, 238 with 32 KB).  Every
-// CTA of the second pass sums all partial sums first: 608 of them up to 24 MB (23 us for 17 MB, 29 with 1216), more
-// where there is more to hide that under (157 MB: 92 us with 608, 84 with 1216).
-struct ClipPlan {
-  bool small_chunks;
-  uint32_t ctas;
-};
-ClipPlan clip_plan(const int64_t* numels, const int32_t* dtypes, int32_t n) {
+// Whether the chunks are the 16 KB ones (U = 4): up to 256 MB.  17 MB of odd tensors took 14.5 us with them and 19 with
+// 64 KB chunks, 36 MB of bf16 21 and 23, 470 MB 230 and 220.
+bool small_chunks(const int64_t* numels, const int32_t* dtypes, int32_t n) {
   int64_t bytes = 0;
   for (int32_t i = 0; i < n; ++i) bytes += numels[i] * (dtypes[i] == FP8G_F32 ? 4 : 2);
-  return {bytes <= int64_t{256} << 20, bytes <= int64_t{24} << 20 ? kClipMaxCtas / 2u : kClipMaxCtas};
+  return bytes <= int64_t{256} << 20;
 }
 
 int64_t clip_launches(int32_t n) { return (static_cast<int64_t>(n) + kClipCap - 1) / kClipCap; }
@@ -323,12 +317,12 @@ int check_tensors(const void* const* grads, void* const* outs, const int64_t* nu
 // Partial sums of all the tensors; *P is how many were written.
 template <int CAP, int U>
 int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* outs, const int64_t* numels,
-                      const int32_t* dtypes, int32_t n, uint32_t max_ctas, float* parts, int32_t* P, cudaStream_t s) {
+                      const int32_t* dtypes, int32_t n, float* parts, int32_t* P, cudaStream_t s) {
   *P = 0;
   for (int32_t i = 0; i < n;) {
     i = fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
-    const uint32_t ctas = std::min(t.end[t.n - 1], max_ctas);
+    const uint32_t ctas = std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas);
     grad_norm_part_kernel<CAP, U><<<ctas, kClipThreads, 0, s>>>(t, parts + *P);
     *P += static_cast<int32_t>(ctas);
   }
@@ -336,11 +330,11 @@ int norm_parts_launch(ClipTable<CAP>& t, const void* const* grads, void* const* 
 }
 
 template <int CAP, int U>
-int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n,
-                     uint32_t max_ctas, float* norm, float* parts, cudaStream_t s) {
+int grad_norm_launch(const void* const* grads, const int64_t* numels, const int32_t* dtypes, int32_t n, float* norm,
+                     float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch<CAP, U>(t, grads, nullptr, numels, dtypes, n, max_ctas, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, nullptr, numels, dtypes, n, parts, &P, s);
   if (st != FP8G_OK) return st;
   grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, P, norm);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
@@ -348,10 +342,10 @@ int grad_norm_launch(const void* const* grads, const int64_t* numels, const int3
 
 template <int CAP, int U>
 int clip_launch(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes, int32_t n,
-                uint32_t max_ctas, float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
+                float max_norm, float eps, float* norm, float* parts, cudaStream_t s) {
   ClipTable<CAP> t;
   int32_t P = 0;
-  const int st = norm_parts_launch<CAP, U>(t, grads, outs, numels, dtypes, n, max_ctas, parts, &P, s);
+  const int st = norm_parts_launch<CAP, U>(t, grads, outs, numels, dtypes, n, parts, &P, s);
   if (st != FP8G_OK) return st;
   if (P == 0) {  // no values at all
     grad_norm_join_kernel<<<1, kClipThreads, 0, s>>>(parts, 0, norm);
@@ -362,7 +356,7 @@ int clip_launch(const void* const* grads, void* const* outs, const int64_t* nume
     i = one ? n : fill_table<CAP, U>(t, grads, outs, numels, dtypes, i, n);
     if (t.n == 0) continue;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(std::min(t.end[t.n - 1], max_ctas));
+    cfg.gridDim = dim3(std::min<uint32_t>(t.end[t.n - 1], kClipMaxCtas));
     cfg.blockDim = dim3(kClipThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -400,12 +394,11 @@ extern "C" int fp8g_grad_norm(const void* const* grads, const int64_t* numels, c
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  const ClipPlan plan = clip_plan(numels, dtypes, n);
-  auto go = n <= 64    ? (plan.small_chunks ? grad_norm_launch<64, 4> : grad_norm_launch<64, 16>)
-            : n <= 256 ? (plan.small_chunks ? grad_norm_launch<256, 4> : grad_norm_launch<256, 16>)
-                       : (plan.small_chunks ? grad_norm_launch<kClipCap, 4> : grad_norm_launch<kClipCap, 16>);
-  return go(grads, numels, dtypes, n, plan.ctas, norm, static_cast<float*>(workspace),
-            static_cast<cudaStream_t>(stream));
+  const bool small = small_chunks(numels, dtypes, n);
+  auto go = n <= 64    ? (small ? grad_norm_launch<64, 4> : grad_norm_launch<64, 16>)
+            : n <= 256 ? (small ? grad_norm_launch<256, 4> : grad_norm_launch<256, 16>)
+                       : (small ? grad_norm_launch<kClipCap, 4> : grad_norm_launch<kClipCap, 16>);
+  return go(grads, numels, dtypes, n, norm, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
@@ -420,10 +413,10 @@ extern "C" int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, 
   DeviceInfo* dev = nullptr;
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
-  const ClipPlan plan = clip_plan(numels, dtypes, n);
-  auto go = n <= 64    ? (plan.small_chunks ? clip_launch<64, 4> : clip_launch<64, 16>)
-            : n <= 256 ? (plan.small_chunks ? clip_launch<256, 4> : clip_launch<256, 16>)
-                       : (plan.small_chunks ? clip_launch<kClipCap, 4> : clip_launch<kClipCap, 16>);
-  return go(grads, outs, numels, dtypes, n, plan.ctas, max_norm, eps, norm, static_cast<float*>(workspace),
+  const bool small = small_chunks(numels, dtypes, n);
+  auto go = n <= 64    ? (small ? clip_launch<64, 4> : clip_launch<64, 16>)
+            : n <= 256 ? (small ? clip_launch<256, 4> : clip_launch<256, 16>)
+                       : (small ? clip_launch<kClipCap, 4> : clip_launch<kClipCap, 16>);
+  return go(grads, outs, numels, dtypes, n, max_norm, eps, norm, static_cast<float*>(workspace),
             static_cast<cudaStream_t>(stream));
 }
