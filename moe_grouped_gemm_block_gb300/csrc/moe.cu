@@ -28,7 +28,7 @@ constexpr int kGateMaxExperts = 2048;  // the routed layout's limit
 constexpr int kGateMaxTopk = 32;
 constexpr int kGateCluster = 8;        // CTAs of a small call, which finish it together
 constexpr int kGateMaxParts = 608;     // CTAs, and partial sums, of a larger one
-constexpr int kGateBackwardCtas = 1216;
+constexpr int kGateBackwardCtas = 608;
 
 // 2^x (relative error 2^-22; results below the normal range are 0).
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -43,6 +43,19 @@ __device__ __forceinline__ float recip_approx(float x) {  // 1 / x to one unit i
 }
 // e^(v - mx) for v <= mx; the difference first, which cannot overflow to anything but -inf.
 __device__ __forceinline__ float exp_below(float v, float mx) { return exp2_approx((v - mx) * 1.4426950408889634f); }
+// The same for all of f, in place, and their sum.
+template <int H>
+__device__ __forceinline__ float exp_below(float2 (&f)[H], float mx) {
+  const float2 m = make_float2(-mx, -mx), k = make_float2(1.4426950408889634f, 1.4426950408889634f);
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    const float2 d = __fmul2_rn(__fadd2_rn(f[i], m), k);
+    f[i] = make_float2(exp2_approx(d.x), exp2_approx(d.y));
+    s = __fadd2_rn(s, f[i]);
+  }
+  return s.x + s.y;
+}
 
 // The order of the selection as an unsigned integer: ascending in the value, NaN above everything (as a
 // descending sort has it), -0 equal to +0 (the addition turns -0 into +0 and every NaN into the positive one).
@@ -73,10 +86,39 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   }
 }
 template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (LPR == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+  }
+}
+template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
+}
+// Four sums at once: each half of the row's lanes goes on with two of them, each quarter with one (10 shuffles of a
+// whole warp's row instead of 20).
+template <int LPR>
+__device__ __forceinline__ float4 row_sum4(float a, float b, float c, float d) {
+  if constexpr (LPR < 8) {
+    return make_float4(row_sum<LPR>(a), row_sum<LPR>(b), row_sum<LPR>(c), row_sum<LPR>(d));
+  } else {
+    const int lane = threadIdx.x & 31;
+    const bool half = lane & (LPR / 2), quarter = lane & (LPR / 4);
+    float v = (half ? c : a) + __shfl_xor_sync(0xffffffffu, half ? a : c, LPR / 2);
+    const float w = (half ? d : b) + __shfl_xor_sync(0xffffffffu, half ? b : d, LPR / 2);
+    v = (quarter ? w : v) + __shfl_xor_sync(0xffffffffu, quarter ? v : w, LPR / 4);
+    v = row_sum<LPR / 4>(v);
+    return make_float4(__shfl_sync(0xffffffffu, v, 0, LPR), __shfl_sync(0xffffffffu, v, LPR / 4, LPR),
+                       __shfl_sync(0xffffffffu, v, LPR / 2, LPR), __shfl_sync(0xffffffffu, v, 3 * LPR / 4, LPR));
+  }
 }
 
 // A sorting network for eight (19 exchanges, descending).
@@ -109,30 +151,22 @@ struct Logits {
       }
     }
   }
-  __device__ __forceinline__ void get(float (&f)[VPL]) const {
+  __device__ __forceinline__ void get(float2 (&f)[VPL / 2]) const {
 #pragma unroll
-    for (int v = 0; v < VPL / 8; ++v) {
-      float2 p[4];
-      raw[v].get(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[8 * v + 2 * i] = p[i].x;
-        f[8 * v + 2 * i + 1] = p[i].y;
-      }
-    }
+    for (int v = 0; v < VPL / 8; ++v) raw[v].get(reinterpret_cast<float2(&)[4]>(f[4 * v]));
   }
 };
 
 // The lane's logits by rank.  next(): the row's best that is left (the same in all the row's lanes), taken out of the
 // list of the lane that has it; value() and id() of what next() gave.  `list`: kListWords words of shared memory of
-// the lane's own, the last of them 0 (init_list).
+// the lane's own, of which words 8 and 9 are 0.
 //
 // The general form, beyond 256 experts: the lane keeps its largest key and looks for the next one when it is taken.
 struct Pick {
   uint32_t key;
   int id;
 };
-constexpr int kListWords = 12;  // eight keys and the end; lanes 12 words apart write 16 bytes without bank conflicts
+constexpr int kListWords = 12;  // eight keys and two for the end; lanes 12 words apart write 16 bytes without bank conflicts
 template <typename TL, int VPL, int LPR>
 struct Ranking {
   static_assert(LPR == 32, "rows of a whole warp");
@@ -146,10 +180,10 @@ struct Ranking {
   }
   __device__ __forceinline__ void init(const Logits<TL, VPL>& l, int base_, int E, uint32_t*) {
     base = base_;
-    float f[VPL];
+    float2 f[VPL / 2];
     l.get(f);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = base + i < E ? order_key(f[i]) : 0u;
+    for (int i = 0; i < VPL; ++i) key[i] = base + i < E ? order_key(i & 1 ? f[i / 2].y : f[i / 2].x) : 0u;
     find();
   }
   __device__ __forceinline__ Pick next() {
@@ -170,10 +204,10 @@ struct Ranking {
 };
 
 // bf16: the key's 16 bits and the index are one word, unlike any other of the row.  The sorted list lies in shared
-// memory, its head in a register.
+// memory, its next two in registers (a round need not wait for the load of the one before).
 template <int LPR>
 struct Ranking<__nv_bfloat16, 8, LPR> {
-  uint32_t head;
+  uint32_t head, second;
   const uint32_t* at;
   __device__ __forceinline__ void init(const Logits<__nv_bfloat16, 8>& l, int base, int E, uint32_t* list) {
     const uint32_t w[4] = {l.raw[0].v.x, l.raw[0].v.y, l.raw[0].v.z, l.raw[0].v.w};
@@ -194,14 +228,26 @@ struct Ranking<__nv_bfloat16, 8, LPR> {
       key[b] = lo;
     });
     head = key[0];
-    at = list;
+    second = key[1];
+    at = list + 1;
     reinterpret_cast<uint4*>(list)[0] = make_uint4(key[0], key[1], key[2], key[3]);
     reinterpret_cast<uint4*>(list)[1] = make_uint4(key[4], key[5], key[6], key[7]);
   }
   __device__ __forceinline__ Pick next() {
     const uint32_t top = row_max<LPR>(head);
-    if (head == top) head = *++at;
+    if (head == top) {
+      head = second;
+      second = *++at;
+    }
     return {top, 0};
+  }
+  __device__ __forceinline__ void next(uint32_t* to) {  // which the lane that has it writes
+    const uint32_t top = row_max<LPR>(head);
+    if (head == top) {
+      *to = top;
+      head = second;
+      second = *++at;
+    }
   }
   static __device__ __forceinline__ float value(const Pick& p) {
     return __uint_as_float(__float_as_uint(key_value(p.key & 0xFFFF0000u)) & 0xFFFF0000u);
@@ -212,18 +258,18 @@ struct Ranking<__nv_bfloat16, 8, LPR> {
 // fp32: keys sorted with their places; of equal keys the lower place comes first, of equal heads the lower lane.
 template <int LPR>
 struct Ranking<float, 8, LPR> {
-  uint32_t head;
+  uint32_t head, second;
   uint32_t places;  // a hexadecimal digit each, the head's lowest
   const uint32_t* at;
   int base;
   __device__ __forceinline__ void init(const Logits<float, 8>& l, int base_, int E, uint32_t* list) {
     base = base_;
-    float f[8];
+    float2 f[4];
     l.get(f);
     uint32_t key[8], place[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      key[i] = order_key(f[i]);
+      key[i] = order_key(i & 1 ? f[i / 2].y : f[i / 2].x);
       place[i] = i;
     }
     if (base + 8 > E) {
@@ -242,7 +288,8 @@ struct Ranking<float, 8, LPR> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) places |= place[i] << (4 * i);
     head = key[0];
-    at = list;
+    second = key[1];
+    at = list + 1;
     reinterpret_cast<uint4*>(list)[0] = make_uint4(key[0], key[1], key[2], key[3]);
     reinterpret_cast<uint4*>(list)[1] = make_uint4(key[4], key[5], key[6], key[7]);
   }
@@ -256,7 +303,8 @@ struct Ranking<float, 8, LPR> {
       id = __shfl_sync(0xffffffffu, id, from);
     }
     if (lane == from) {
-      head = *++at;
+      head = second;
+      second = *++at;
       places >>= 4;
     }
     return {top, id};
@@ -303,22 +351,24 @@ __host__ __device__ constexpr int gate_warp_words(int topk) {
   return 32 * kListWords + ((32 / LPR) * (3 * topk + 1) + 3) / 4 * 4;
 }
 template <int LPR>
-size_t gate_smem(int E, int topk) {
-  return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + kGateWarps * std::max(E, gate_warp_words<LPR>(topk)));
+size_t gate_smem(int E, int topk, int warps) {
+  return 4 * (2 * static_cast<size_t>((E + 3) / 4 * 4) + warps * std::max(E, gate_warp_words<LPR>(topk)));
 }
 
 // CTAs that are resident on an SM at once.
 __host__ __device__ constexpr int gate_per_sm(int vpl) { return vpl == 8 ? 4 : vpl == 16 ? 2 : 1; }
 
 // A warp's rows, and so each partial sum's terms and their order, follow from the grid alone.
-template <typename TL, int VPL, int LPR>
-__global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kernel(const GateArgs a) {
+template <typename TL, int VPL, int LPR, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, gate_per_sm(VPL) * kGateWarps / WARPS)
+    moe_gate_kernel(const GateArgs a) {
+  constexpr int kThreads = 32 * WARPS;
   constexpr int G = 32 / LPR;  // rows a warp at once
   using Rank = Ranking<TL, VPL, LPR>;
   constexpr bool kOneWord = std::is_same_v<TL, __nv_bfloat16> && VPL == 8;  // a pick's key holds its index
   extern __shared__ __align__(16) float smem[];
   __shared__ float2 s_loss[kGateCluster];
-  __shared__ float red[2 * 2 * kGateWarps];
+  __shared__ float red[2 * 2 * WARPS];
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
   const int E = a.E, topk = a.topk, padded = (E + 3) / 4 * 4;
@@ -330,16 +380,16 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
   int32_t* pick_id = reinterpret_cast<int32_t*>(pick_key + G * topk);
   float* pick_w = reinterpret_cast<float*>(pick_id + G * topk);
   float* factor = pick_w + G * topk;
-  list[8] = 0u;  // the end of every list
-  for (int e = threadIdx.x; e < E; e += kGateThreads) cnt[e] = 0;
+  list[8] = list[9] = 0u;  // the end of every list
+  for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
   __syncthreads();
   const TL* logits = static_cast<const TL*>(a.logits);
   const float inv_k = 1.0f / static_cast<float>(topk);
-  float acc[VPL];
+  float2 acc[VPL / 2];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps * G;
-  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * G;
+  for (int i = 0; i < VPL / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * WARPS * G;
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * G;
   Logits<TL, VPL> next;
   bool next_real = false;
   auto fetch = [&](int64_t at) {
@@ -358,7 +408,14 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
     Pick mine = rank.next();
     float mx = Rank::value(mine);
     if (mx == -INFINITY) mx = 0.0f;  // every expert ruled out: the exponentials are all 0
-    if constexpr (G == 1) {
+    if constexpr (G == 1 && kOneWord) {
+      if (lane == 0) pick_key[0] = mine.key;
+#pragma unroll 2
+      for (int j = 1; j < topk; ++j) rank.next(pick_key + j);
+      __syncwarp();
+      if (lane < topk) mine.key = pick_key[lane];
+      __syncwarp();
+    } else if constexpr (G == 1) {
 #pragma unroll 2
       for (int j = 1; j < topk; ++j) {
         const Pick p = rank.next();
@@ -389,18 +446,13 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
     }
     const float own = picked;
     picked = row_sum<LPR>(picked);
-    float f[VPL], s = 0.0f;
+    float2 f[VPL / 2];
     l.get(f);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      f[i] = exp_below(f[i], mx);
-      s += f[i];
-    }
-    s = row_sum<LPR>(s);
+    const float s = row_sum<LPR>(exp_below(f, mx));
     const float inv = s == 0.0f ? 0.0f : recip_approx(s);
     if (real) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = fmaf(f[i], inv, acc[i]);
+      for (int i = 0; i < VPL / 2; ++i) acc[i] = __ffma2_rn(f[i], make_float2(inv, inv), acc[i]);
     }
     const float scale = a.renorm ? (picked == 0.0f ? 0.0f : recip_approx(picked)) : inv;
     if constexpr (G == 1) {
@@ -428,20 +480,23 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
   }
   // the CTA's sums: over the rows that a warp's lanes shared, then over the warps
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
+  for (int i = 0; i < VPL / 2; ++i)
 #pragma unroll
-    for (int off = 16; off >= LPR; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    for (int off = 16; off >= LPR; off >>= 1) {
+      acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, off);
+      acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, off);
+    }
   __syncthreads();
   if (lane < LPR) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (base + i < E) rest[warp * E + base + i] = acc[i];
+      if (base + i < E) rest[warp * E + base + i] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kGateThreads) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kGateWarps; ++w) s += rest[w * E + e];
+    for (int w = 0; w < WARPS; ++w) s += rest[w * E + e];
     sum_p[e] = s;
   }
   // a cluster's: each CTA takes a share of the experts
@@ -451,7 +506,7 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
   const bool single = static_cast<int>(gridDim.x) == ranks;
   const int64_t part = static_cast<int64_t>(blockIdx.x / ranks) * E;
   float v[2] = {0.0f, 0.0f};
-  for (int e = lo + static_cast<int>(threadIdx.x); e < hi; e += kGateThreads) {
+  for (int e = lo + static_cast<int>(threadIdx.x); e < hi; e += kThreads) {
     float p = 0.0f;
     int32_t c = 0;
     for (int r = 0; r < ranks; ++r) {
@@ -468,7 +523,7 @@ __global__ void __launch_bounds__(kGateThreads, gate_per_sm(VPL)) moe_gate_kerne
     }
   }
   if (single) {
-    cta_sum<kGateWarps>(v, red, 0);
+    cta_sum<WARPS>(v, red, 0);
     if (threadIdx.x == 0) {
       const uint32_t to = mapa_shared(smem_u32(&s_loss[me]), 0);
       asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v[0]), "f"(v[1]) : "memory");
@@ -492,6 +547,7 @@ __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int32_t P, int32_t E, int32_t topk,
     float coef, int32_t* __restrict__ counts, float* __restrict__ loss) {
   constexpr int W = kGateJoinThreads / 32;
+  constexpr int kLoads = 10;  // a warp's share, 19 rows at most, in two trips to L2
   __shared__ float s_p[W][32];
   __shared__ int32_t s_c[W][32];
   __shared__ float2 s_loss[kGateCluster];
@@ -506,10 +562,19 @@ __global__ void __launch_bounds__(kGateJoinThreads) moe_gate_join_kernel(
     int32_t c = 0;
     if (e < E) {
       const int lo = P * warp / W, hi = P * (warp + 1) / W;
-#pragma unroll 4
-      for (int i = lo; i < hi; ++i) {
-        p += __ldcg(part_p + static_cast<int64_t>(i) * E + e);
-        c += __ldcg(part_c + static_cast<int64_t>(i) * E + e);
+      for (int i0 = lo; i0 < hi; i0 += kLoads) {
+        float pi[kLoads];
+        int32_t ci[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          pi[i] = i0 + i < hi ? __ldcg(part_p + static_cast<int64_t>(i0 + i) * E + e) : 0.0f;
+          ci[i] = i0 + i < hi ? __ldcg(part_c + static_cast<int64_t>(i0 + i) * E + e) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          p += pi[i];
+          c += ci[i];
+        }
       }
     }
     s_p[warp][lane] = p;
@@ -576,9 +641,10 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
   cta_sum<kGateWarps>(n, red, 0);
   const float k = static_cast<float>(topk), tv = n[0] / k;
   const float scale = a.dloss && tv > 0.0f ? *a.dloss * a.coef * static_cast<float>(E) / (k * tv * tv) : 0.0f;
-  float g[VPL];
+  float2 g[VPL / 2];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) g[i] = base + i < E ? scale * static_cast<float>(a.counts[base + i]) : 0.0f;
+  for (int i = 0; i < VPL; ++i)
+    (i & 1 ? g[i / 2].y : g[i / 2].x) = base + i < E ? scale * static_cast<float>(a.counts[base + i]) : 0.0f;
   const TL* logits = static_cast<const TL*>(a.logits);
   TL* dlogits = static_cast<TL*>(a.dlogits);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateWarps * G;
@@ -621,22 +687,18 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
         else id[j] = -1;
       }
     }
-    float f[VPL];
+    float2 f[VPL / 2];
     l.get(f);
-    float mx = f[0];
+    float mx = fmaxf(f[0].x, f[0].y);
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, f[i]);
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    for (int i = 1; i < VPL / 2; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
+    mx = row_max<LPR>(mx);
     if (mx == -INFINITY) mx = 0.0f;
     // sums over the exponentials f = s p: all of them, with g, the selected ones, and with their dw
-    float s = 0.0f, sum_g = 0.0f;
+    const float own_s = exp_below(f, mx);
+    float2 own_g = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      f[i] = exp_below(f[i], mx);
-      s += f[i];
-      sum_g = fmaf(g[i], f[i], sum_g);
-    }
+    for (int i = 0; i < VPL / 2; ++i) own_g = __ffma2_rn(g[i], f[i], own_g);
     float sel = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < kPicks; ++j) {
@@ -645,13 +707,10 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
       sel += e[j];
       if (id[j] >= 0) dot = fmaf(dw[j], e[j], dot);
     }
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, off);
-      sum_g += __shfl_xor_sync(0xffffffffu, sum_g, off);
-      sel += __shfl_xor_sync(0xffffffffu, sel, off);
-      dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    }
+    const float4 sums = row_sum4<LPR>(own_s, own_g.x + own_g.y, sel, dot);
+    const float s = sums.x, sum_g = sums.y;
+    sel = sums.z;
+    dot = sums.w;
     const float inv = !real || s == 0.0f ? 0.0f : recip_approx(s);
     const float inv_sel = sel == 0.0f ? 0.0f : recip_approx(sel);
     // renormalised, the weights' gradient has no component along the weights: the inner product is g's alone
@@ -661,18 +720,21 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
     TL* out = dlogits + t * a.ldd;
     if (t < a.T) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) f[i] = real ? f[i] * inv * (g[i] - inner) : 0.0f;
+      for (int i = 0; i < VPL / 2; ++i) {
+        const float2 p = __fmul2_rn(f[i], make_float2(inv, inv));
+        f[i] = real ? __fmul2_rn(p, __fadd2_rn(g[i], make_float2(-inner, -inner))) : make_float2(0.0f, 0.0f);
+      }
 #pragma unroll
       for (int v = 0; v < VPL; v += 8) {
-        if (a.vec && base + v < E) {
-          float o[8];
+        float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = f[v + i];
+        for (int i = 0; i < 8; ++i) o[i] = i & 1 ? f[(v + i) / 2].y : f[(v + i) / 2].x;
+        if (a.vec && base + v < E) {
           store8(out + base + v, o);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (base + v + i < E) out[base + v + i] = from_f32<TL>(f[v + i]);
+            if (base + v + i < E) out[base + v + i] = from_f32<TL>(o[i]);
         }
       }
     }
@@ -845,21 +907,25 @@ int64_t gate_parts(int64_t T, int E) {
 
 template <typename TL, int VPL, int LPR>
 int gate_launch(const GateArgs& a, const DeviceInfo* dev, cudaStream_t s) {
-  auto kern = moe_gate_kernel<TL, VPL, LPR>;
-  const size_t smem = gate_smem<LPR>(a.E, a.topk);
+  // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs
+  // as are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38), one
+  // of 32 warps an SM where the registers allow it and there are rows for all of them (fewer partial sums: 65536 x 256
+  // fp32 47 us, with four CTAs of 8 warps 51; bf16 38 with either).
+  constexpr int kLarge = VPL == 8 ? 32 : kGateWarps;
+  const int64_t G = 32 / LPR;
+  const bool few = gate_few(a.T, a.E), large = !few && a.T >= dev->sm_count * kLarge * G;
+  const int warps = large ? kLarge : kGateWarps;
+  const int cluster = a.T <= 2 * kGateWarps * G || !few ? 1 : kGateCluster;
+  const int64_t ctas = few ? cluster
+                           : std::min({gate_parts(a.T, a.E), (a.T + warps * G - 1) / (warps * G),
+                                       int64_t{gate_per_sm(VPL)} * kGateWarps / warps * dev->sm_count});
+  const size_t smem = gate_smem<LPR>(a.E, a.topk, warps);
+  auto kern = large ? moe_gate_kernel<TL, VPL, LPR, kLarge> : moe_gate_kernel<TL, VPL, LPR, kGateWarps>;
   const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), smem);
   if (st != FP8G_OK) return st;
-  // A CTA or a cluster of them for few rows: it finishes the counts and the loss itself.  More rows go to as many CTAs
-  // as are resident at once (in clusters of 8, which do not fill every SM, 65536 x 256 took 54 us instead of 38).
-  const int64_t at_once = kGateWarps * (32 / LPR);
-  const bool few = gate_few(a.T, a.E);
-  const int cluster = a.T <= 2 * at_once || !few ? 1 : kGateCluster;
-  const int64_t ctas = few ? cluster
-                           : std::min<int64_t>(gate_parts(a.T, a.E),
-                                               static_cast<int64_t>(gate_per_sm(VPL)) * dev->sm_count);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kGateThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
