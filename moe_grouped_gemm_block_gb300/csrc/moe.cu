@@ -166,7 +166,7 @@ struct Pick {
   uint32_t key;
   int id;
 };
-constexpr int kListWords = 12;  // eight keys and two for the end; lanes 12 words apart write 16 bytes without bank conflicts
+constexpr int kListWords = 12;  // eight keys, two for the end; lanes 12 words apart write 16 bytes without conflicts
 template <typename TL, int VPL, int LPR>
 struct Ranking {
   static_assert(LPR == 32, "rows of a whole warp");

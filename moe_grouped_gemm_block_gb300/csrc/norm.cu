@@ -193,6 +193,7 @@ constexpr int kRingThreads = 32 * 24, kRingGradThreads = 32 * 20;
 
 struct RingShared {
   uint64_t full[kRingMaxStages], ready[kRingMaxStages], empty[kRingMaxStages];
+  uint64_t peer[kRingMaxStages];   // a cluster's: the other CTA has read its slot
   float4 slot[kRingMaxStages][2];  // a row's sums from each CTA of the cluster
   int dead;
 };
@@ -220,8 +221,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// Written to a CTA of the cluster; its barrier `bar` counts the 16 bytes when they are there.
+__device__ __forceinline__ void st_async4(uint32_t addr, float4 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   addr),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
                : "memory");
 }
 
@@ -286,25 +290,28 @@ __device__ __forceinline__ void ring_init(RingShared& sm, int stages, int column
     sm.dead = 0;
     for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
-      mbar_init(smem_u32(&sm.ready[s]), CL);
-      mbar_init(smem_u32(&sm.empty[s]), CL * column_warps);
+      mbar_init(smem_u32(&sm.ready[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), column_warps);
+      mbar_init(smem_u32(&sm.peer[s]), 1);
     }
     fence_mbar_init();
   }
 }
 
 // The copying thread: row after row into the ring, each stage once it is empty.  `load` copies row i into stage s and
-// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.
-template <typename Load>
-__device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, bool cluster, long long budget,
+// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.  In a
+// cluster it tells the other CTA that the stage's slot has been read, too: the column warps have stores on their way,
+// which an arrival of theirs at the other CTA would have to wait for (4096 x 12288 bf16 backward took 93 us so, and 76 now).
+template <int CL, typename Load>
+__device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, int rank, long long budget,
                                             unsigned int* status, Load load) {
   int s = 0, i = 0;
   uint32_t parity = 1;  // the first round of `empty` counts as complete
   for (; i < rows; ++i) {
     if (i >= stages) {
-      if (cluster) ring_wait<true>(&sm.empty[s], parity, budget, status, &sm.dead);
-      else ring_wait<false>(&sm.empty[s], parity, budget, status, &sm.dead);
+      ring_wait(&sm.empty[s], parity, budget, status, &sm.dead);
       if (*const_cast<volatile int*>(&sm.dead)) break;
+      if constexpr (CL > 1) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.peer[s]), rank ^ 1));
     }
     load(i, s);
     if (++s == stages) {
@@ -319,30 +326,27 @@ __device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages
     }
 }
 
-// A sum warp hands its row on: the sums to every CTA of the cluster, then the arrival.
+// A sum warp hands its row, of the ring's round `round`, on: its sums to every CTA of the cluster.
 template <int CL>
-__device__ __forceinline__ void ring_ready(RingShared& sm, int s, int rank, float4 v) {
+__device__ __forceinline__ void ring_ready(RingShared& sm, int s, int round, int rank, float4 v, long long budget,
+                                           unsigned int* status) {
   const int lane = threadIdx.x & 31;
   if constexpr (CL == 1) {
     if (lane == 0) {
       sm.slot[s][0] = v;
       mbar_arrive(smem_u32(&sm.ready[s]));
     }
-  } else if (lane < CL) {
-    st_cluster4(mapa_shared(smem_u32(&sm.slot[s][rank]), lane), v);
-    mbar_arrive_cluster(mapa_shared(smem_u32(&sm.ready[s]), lane));
+  } else {
+    if (lane == 0) mbar_arrive_expect_tx(true, smem_u32(&sm.ready[s]), CL * 16);
+    if (round > 0) ring_wait<true>(&sm.peer[s], (round - 1) & 1, budget, status, &sm.dead);
+    if (lane < CL)
+      st_async4(mapa_shared(smem_u32(&sm.slot[s][rank]), lane), v, mapa_shared(smem_u32(&sm.ready[s]), lane));
   }
 }
 // A column warp has read the stage and the slot.
-template <int CL>
 __device__ __forceinline__ void ring_empty(RingShared& sm, int s) {
-  const int lane = threadIdx.x & 31;
   __syncwarp();
-  if constexpr (CL == 1) {
-    if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
-  } else {
-    if (lane < CL) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.empty[s]), lane));
-  }
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.empty[s]));
 }
 
 // ---------------------------------------------------------------- forward
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
   else cluster_sync();  // every CTA of the cluster runs before it is written to
   if (warp == column_warps + sum_warps) {
     if (lane == 0)
-      ring_copies(sm, rows, stages, CL > 1, a.budget, a.status, [&](int i, int s) {
+      ring_copies<CL>(sm, rows, stages, rank, a.budget, a.status, [&](int i, int s) {
         const int64_t m = first + static_cast<int64_t>(i) * P;
         const uint32_t bar = smem_u32(&sm.full[s]);
         const uint32_t bytes = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8 * sizeof(TX);
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
           if (a.rstd) a.rstd[m] = st.y;
         }
       }
-      ring_ready<CL>(sm, s, rank, st);
+      ring_ready<CL>(sm, s, it.round, rank, st, a.budget, a.status);
     }
   } else {
     TY* y = static_cast<TY*>(a.y) + shape.col(share.first);
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       for (int v = 0; v < NV; ++v) {
         Raw8<TX> raw;
         if (mask[v]) stage_vector<SHIFT>(raw, stage, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
-        if (v == NV - 1) ring_empty<CL>(sm, s);
+        if (v == NV - 1) ring_empty(sm, s);
         if (!mask[v]) continue;
         float2 f[4];
         raw.get(f);
@@ -901,7 +905,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
   const float inv_n = 1.0f / static_cast<float>(a.N);
   if (warp == column_warps + sum_warps) {
     if (lane == 0)
-      ring_copies(sm, rows, stages, CL > 1, a.budget, a.status, [&](int i, int s) {
+      ring_copies<CL>(sm, rows, stages, rank, a.budget, a.status, [&](int i, int s) {
         const int64_t m = first + static_cast<int64_t>(i) * P;
         const uint32_t bar = smem_u32(&sm.full[s]), dst = smem_u32(ring) + s * stage_bytes;
         const uint32_t n = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8;
@@ -986,7 +990,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
       s2[0] = __fadd2_rn(s2[0], s2[1]);
       const float c1 = warp_sum(s1[0].x + s1[0].y) * inv_n * r;
       const float c2 = warp_sum(s2[0].x + s2[0].y) * inv_n * r * r;
-      ring_ready<CL>(sm, s, rank, make_float4(mu, r, c1, c2));
+      ring_ready<CL>(sm, s, round, rank, make_float4(mu, r, c1, c2), a.budget, a.status);
     }
   } else {
     TX* out = static_cast<TX*>(a.dx) + shape.col(share.first);
@@ -1022,7 +1026,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
           stage_vector<SHIFT>(rx, xs, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
           stage_vector<SHIFT>(ry, ys, v * columns + tid, mask[v], m + 1 == a.M, dy + m * a.lddy);
         }
-        if (v == NV - 1) ring_empty<CL>(sm, s);
+        if (v == NV - 1) ring_empty(sm, s);
         if (!mask[v]) continue;
         float2 xf[4], yf[4], h[4], g[4], f[4];
         rx.get(xf);
@@ -1203,7 +1207,7 @@ constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice th
 constexpr int64_t kCtaMaxN = 32768;      // cta form: up to 4 vectors a thread
 constexpr int64_t kScalarMaxN = 16384;   // scalar form: up to 16 values a thread, forward ...
 constexpr int64_t kGradScalarMaxN = 8192;  // ... and backward
-constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM's stages, at most
+constexpr int kRingBytes = 225 * 1024;   // shared memory of an SM's stages, at most
 constexpr int64_t kNormMaxParts = 608;
 
 // Rows of partial sums that the workspace has room for: the largest grid of any backward form.
