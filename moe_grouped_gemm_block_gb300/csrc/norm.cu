@@ -301,7 +301,7 @@ __device__ __forceinline__ void ring_init(RingShared& sm, int stages, int column
 // The copying thread: row after row into the ring, each stage once it is empty.  `load` copies row i into stage s and
 // returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.  In a
 // cluster it tells the other CTA that the stage's slot has been read, too: the column warps have stores on their way,
-// which an arrival of theirs at the other CTA would have to wait for (4096 x 12288 bf16 backward took 93 us so, and 76 now).
+// which an arrival of theirs at the other CTA would have to wait for (4096 x 12288 bf16 backward: 93 us instead of 76).
 template <int CL, typename Load>
 __device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, int rank, long long budget,
                                             unsigned int* status, Load load) {
@@ -1207,8 +1207,10 @@ constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice th
 constexpr int64_t kCtaMaxN = 32768;      // cta form: up to 4 vectors a thread
 constexpr int64_t kScalarMaxN = 16384;   // scalar form: up to 16 values a thread, forward ...
 constexpr int64_t kGradScalarMaxN = 8192;  // ... and backward
-constexpr int kRingBytes = 225 * 1024;   // shared memory of an SM's stages, at most
-constexpr int64_t kNormMaxParts = 608;
+// Shared memory of the stages (and weights) of one of `per_sm` CTAs an SM: its 228 KB but 1 KB a CTA and RingShared.
+constexpr int ring_bytes(int per_sm) { return 228 * 1024 / per_sm - 1024 - 1280; }
+static_assert(sizeof(RingShared) <= 1280 - 128, "with the stages' alignment");
+constexpr int64_t kNormMaxParts = 912;   // rows of partial sums
 
 // Rows of partial sums that the workspace has room for: the largest grid of any backward form.
 int64_t norm_parts(int64_t M) { return std::min<int64_t>(M, kNormMaxParts); }
@@ -1255,11 +1257,11 @@ RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, int max_threads
   p.sum_warps = std::max(2, std::min(warps - 1 - p.column_warps, (p.column_warps + 2) / 2));
   // Short rows take several CTAs an SM.  Backward each of them writes its partial sums: with 16384 rows of 2048 bf16
   // values two are 20% faster than one (48 against 58 us), with 2560 (fp32 rows) 13% slower (84 against 74).
-  int per_sm = std::max(1, std::min(4, warps / (p.column_warps + p.sum_warps + 1)));
+  int per_sm = std::max(1, warps / (p.column_warps + p.sum_warps + 1));
   if (extra && p.column_warps > 4) per_sm = 1;
   p.stage_bytes = p.each * 8 * size;
   p.stages = static_cast<int>(
-      std::min<int64_t>(kRingMaxStages, (kRingBytes / per_sm - static_cast<int64_t>(p.each) * extra) / p.stage_bytes));
+      std::min<int64_t>(kRingMaxStages, (ring_bytes(per_sm) - static_cast<int64_t>(p.each) * extra) / p.stage_bytes));
   p.sum_warps = std::min(p.sum_warps, p.stages);  // (a sum warp has stages of its own)
   p.threads = 32 * (p.column_warps + p.sum_warps + 1);
   p.rows_at_once = std::min<int64_t>(static_cast<int64_t>(sms) * per_sm / p.cluster, kNormMaxParts);
@@ -1269,7 +1271,7 @@ RingPlan ring_plan(int64_t M, int64_t vecs, int size, int extra, int max_threads
 }
 template <typename Kernel, typename... Args>
 int ring_launch(Kernel kern, const RingPlan& p, int64_t smem, cudaStream_t s, Args... args) {
-  const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), kRingBytes);
+  const int st = allow_shared_memory(reinterpret_cast<const void*>(kern), ring_bytes(1));
   if (st != FP8G_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows_at_once * p.cluster));
