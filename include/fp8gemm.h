@@ -413,8 +413,9 @@ typedef enum { FP8G_BF16 = 0, FP8G_F32 = 1 } fp8g_dtype;
  *   weight, bias  [N], both of type w_dtype; either may be null (1 and 0)
  *   y       [M, N], row stride ldy elements (ldy >= N); may be x itself when the types are the same
  *   mean, rstd  fp32 [M], for the backward call; either may be null
- *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31, eps >= 0.  Pointers aligned to their element; rows that are
- *   16-byte aligned (base and stride) and N a multiple of 8 take the faster paths.
+ *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31, eps >= 0.  Pointers aligned to their element.  Matrices
+ *   whose bases are 16-byte aligned and whose strides are equal modulo 8 take the faster paths, the fastest where
+ *   the strides and N are multiples of 8.
  */
 int fp8g_layer_norm(const void* x, int32_t x_dtype, int64_t M, int64_t N, int64_t ldx, const void* weight,
                     const void* bias, int32_t w_dtype, float eps, void* y, int32_t y_dtype, int64_t ldy,

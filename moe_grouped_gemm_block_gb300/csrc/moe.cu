@@ -20,8 +20,12 @@ namespace {
 //
 // A row is held by LPR lanes of a warp, VPL consecutive logits each (a warp works on 32 / LPR rows at once, 32 for 8
 // experts), so the whole of it stays in registers.  The k best are taken by merging the lanes' sorted lists: each
-// round finds the largest head, whose lane goes on to its next one.  The kernels are bound by their instructions,
-// not by memory.
+// round finds the largest head, whose lane goes on to its next one.
+//
+// The kernels are bound by their instructions, not by memory: 362 of a warp for a bf16 row of 256 with 8 picks, most
+// of them on the ALU, which takes one every second cycle (the sort's minima and maxima, the keys, the picks).
+// 65536 x 256, 8 picks: forward bf16 38 us, fp32 47 (15% and 22% of the copy rate), of which the joined sums take 5;
+// backward bf16 27 us (39%).  Few tokens (64 x 32): 7 us, a launch.
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateMaxExperts = 2048;  // the routed layout's limit
@@ -753,7 +757,9 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
 
 // ---------------------------------------------------------------- combine
 //     out_t = residual_t + sum_j w_tj D[row_tj]
-// Both directions are bound by memory: 16-byte loads, the rows of several entries in flight per thread.
+// Both directions are bound by memory: 16-byte loads, the rows of several entries in flight per thread.  4096 tokens
+// of 2 x 4096, fp32 with a residual: 35 us (85% of the copy rate); 8192 of 8 x 2048, bf16: 56 us (88%); backward
+// 4001 of 4 x 7168: 91 us (92%), 8192 of 8 x 2048: 101 us (93%).
 constexpr int kCombineThreads = 128;
 constexpr int kCombineSpan = kCombineThreads * 8;  // columns a CTA takes at once
 
