@@ -278,6 +278,18 @@ def test_gate_and_gradient(T, E, topk, xd, renorm, masked):
     assert all(torch.equal(p, q) for p, q in zip(a, b))  # the same bits again
 
 
+# more tokens than the GPU's warps take at once, ragged at the end
+@pytest.mark.parametrize("T,E,topk", [(5001, 256, 8), (6007, 130, 32), (9999, 100, 3), (20011, 64, 6), (39001, 32, 32),
+                                      (78003, 16, 4), (156007, 8, 2), (160001, 3, 1), (3001, 300, 8), (2003, 700, 5)])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+def test_gate_many_tokens(T, E, topk, xd):
+    logits = _draw((T, E), xd, T, 1.5)
+    mask = torch.arange(T, device="cuda") % 5 != 1
+    a = _check_gate(logits, topk, True, mask)
+    b = g.moe_gate(logits, topk, renormalize=True, loss_coef=0.05, token_mask=mask)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 @pytest.mark.parametrize("E", [5, 8, 32, 64, 200])
 def test_gate_ties_and_ruled_out_experts(E):
     T = 12
