@@ -224,6 +224,11 @@ __device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity, long l
     }
   }
 }
+// Whether a wait has run out, the same answer in all of a warp.  The sum warps leave then: no barrier is told twice in a
+// phase what to expect.
+__device__ __forceinline__ bool ring_dead(const RingShared& sm) {
+  return __any_sync(0xffffffffu, *const_cast<const volatile int*>(&sm.dead));
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -538,6 +543,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       const int s = it.stage;
       const int64_t m = first + it.row() * P;
       ring_wait(&sm.full[s], it.round & 1, a.budget, a.status, &sm.dead);
+      if (ring_dead(sm)) break;
       const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const Inner<SHIFT> in(share);
       float2 f[4], d1 = both(0.0f), d2 = both(0.0f), e1 = both(0.0f), e2 = both(0.0f);
@@ -947,6 +953,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
       it.next();
       stats();
       ring_wait(&sm.full[s], round & 1, a.budget, a.status, &sm.dead);
+      if (ring_dead(sm)) break;
       const TX* xs = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const TY* ys = reinterpret_cast<const TY*>(ring + s * stage_bytes + x_bytes);
       const Inner<SHIFT> in(share);
