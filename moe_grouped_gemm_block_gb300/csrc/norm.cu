@@ -189,10 +189,11 @@ __device__ __forceinline__ float value_sum(const Raw8<T> (&raw)[NV]) {
 // ---------------------------------------------------------------- the ring of row stages
 // Roles of a CTA's warps: column warps own kRingVecs vectors a thread of every row, sum warps take whole rows in
 // turn and form their sums, one thread of the last warp issues the copies.  A row's stage goes full (its copies have
-// landed) -> ready (its sums are in `slot`) -> empty (every column warp has read it); nothing else orders the warps,
-// so the latencies of one row's sums lie under the columns' work on others.  (With all warps of the CTA taking
-// a row together, sums through a barrier, a row cost about 2000 cycles of latency: 4096 x 7168 bf16 rows took 42 us
-// forward and 43 us backward, and 29 and 36 us with two to four rows at a time.)
+// landed) -> ready (its sums are in `slot`; the column warps wait for this alone, as a sum warp of their CTA gave it
+// after it had seen the stage full: a second wait made 16384 x 4096 bf16 7% slower) -> empty (every column warp has
+// read it); nothing else orders the warps, so the latencies of one row's sums lie under the columns' work on others.
+// (With all warps of the CTA taking a row together, sums through a barrier, a row cost about 2000 cycles of latency:
+// 4096 x 7168 bf16 rows took 42 us forward and 43 us backward, and 29 and 36 us with two to four rows at a time.)
 constexpr int kRingMaxStages = 16;
 constexpr int kRingVecs = 2;
 constexpr int kRingMaxColumnWarps = 16;
@@ -616,7 +617,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
     uint32_t parity = 0;
     for (int i = 0; i < rows; ++i) {
       const int64_t m = first + static_cast<int64_t>(i) * P;
-      ring_wait(&sm.full[s], parity, a.budget, a.status, &sm.dead);
       ring_wait<(CL > 1)>(&sm.ready[s], parity, a.budget, a.status, &sm.dead);
       const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const float4 st = sm.slot[s][0];
@@ -1023,7 +1023,6 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
     uint32_t parity = 0;
     for (int i = 0; i < rows; ++i) {
       const int64_t m = first + static_cast<int64_t>(i) * P;
-      ring_wait(&sm.full[s], parity, a.budget, a.status, &sm.dead);
       ring_wait<(CL > 1)>(&sm.ready[s], parity, a.budget, a.status, &sm.dead);
       const TX* xs = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const TY* ys = reinterpret_cast<const TY*>(ring + s * stage_bytes + x_bytes);
