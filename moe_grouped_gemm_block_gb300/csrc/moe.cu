@@ -32,7 +32,6 @@ constexpr int kGateMaxExperts = 2048;  // the routed layout's limit
 constexpr int kGateMaxTopk = 32;
 constexpr int kGateCluster = 8;        // CTAs of a small call, which finish it together
 constexpr int kGateMaxParts = 608;     // CTAs, and partial sums, of a larger one
-constexpr int kGateBackwardCtas = 608;
 
 // 2^x (relative error 2^-22; results below the normal range are 0).
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -140,12 +139,12 @@ __device__ __forceinline__ void sort8(Exchange ex) {
 template <typename TL, int VPL>
 struct Logits {
   Raw8<TL> raw[VPL / 8];
-  // vec: the row's groups of 8 lie on 16-byte boundaries and E is a multiple of 8
+  // vec: the row's groups of 8 lie on 16-byte boundaries
   __device__ __forceinline__ void load(const TL* row, int base, int E, bool vec) {
 #pragma unroll
     for (int v = 0; v < VPL / 8; ++v) {
       const int c = base + 8 * v;
-      if (vec && c < E) {
+      if (vec && c + 8 <= E) {
         raw[v].load(row + c);
       } else {
         TL f[8];
@@ -632,8 +631,13 @@ struct GateGrad {
   float coef;
 };
 
+// CTAs that are resident on an SM at once: all that are launched (65536 x 64 fp32: 12.4 us, with 4 an SM 14.4).
+__host__ __device__ constexpr int gate_grad_per_sm(int vpl, int lpr) {
+  return vpl == 64 ? 1 : vpl == 16 || (lpr > 1 && lpr < 16) ? 3 : 4;
+}
 template <typename TL, int VPL, int LPR>
-__global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const GateGrad a) {
+__global__ void __launch_bounds__(kGateThreads, gate_grad_per_sm(VPL, LPR))
+    moe_gate_backward_kernel(const GateGrad a) {
   constexpr int G = 32 / LPR;
   // a lane's selected experts, at most
   constexpr int kPicks = LPR >= kGateMaxTopk ? 1 : LPR * 8 >= kGateMaxTopk ? kGateMaxTopk / LPR : 8;
@@ -733,7 +737,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_backward_kernel(const G
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = i & 1 ? f[(v + i) / 2].y : f[(v + i) / 2].x;
-        if (a.vec && base + v < E) {
+        if (a.vec && base + v + 8 <= E) {
           store8(out + base + v, o);
         } else {
 #pragma unroll
@@ -963,10 +967,10 @@ int gate_launch(const GateArgs& a, const DeviceInfo* dev, cudaStream_t s) {
 }
 
 template <typename TL, int VPL, int LPR>
-int gate_backward_launch(const GateGrad& a, cudaStream_t s) {
+int gate_backward_launch(const GateGrad& a, const DeviceInfo* dev, cudaStream_t s) {
   auto kern = moe_gate_backward_kernel<TL, VPL, LPR>;
   const int64_t at_once = kGateWarps * (32 / LPR);
-  const int64_t ctas = std::min<int64_t>((a.T + at_once - 1) / at_once, kGateBackwardCtas);
+  const int64_t ctas = std::min<int64_t>((a.T + at_once - 1) / at_once, gate_grad_per_sm(VPL, LPR) * dev->sm_count);
   kern<<<static_cast<unsigned>(ctas), kGateThreads, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
@@ -994,9 +998,9 @@ auto gate_backward_form(int E) {
          : E <= 512 ? gate_backward_launch<TL, 16, 32>
                     : gate_backward_launch<TL, 64, 32>;
 }
-// Whether rows of E logits can be taken eight at a time.
-bool logit_vectors(const void* p, int64_t ld, int32_t E, int32_t dtype) {
-  return E % 8 == 0 && aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
+// Whether rows of logits can be taken eight at a time.
+bool logit_vectors(const void* p, int64_t ld, int32_t dtype) {
+  return aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
 }
 
 template <typename TO>
@@ -1063,7 +1067,7 @@ extern "C" int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32
   a.part_p = static_cast<float*>(workspace);
   a.part_c = reinterpret_cast<int32_t*>(a.part_p + gate_parts(T, E) * E);
   a.T = T, a.ldl = ldl, a.E = E, a.topk = topk, a.renorm = renormalize, a.coef = loss_coef;
-  a.vec = logit_vectors(logits, ldl, E, dtype);
+  a.vec = logit_vectors(logits, ldl, dtype);
   return (dtype == FP8G_F32 ? gate_form<float>(E) : gate_form<__nv_bfloat16>(E))(a, dev, s);
 }
 
@@ -1088,9 +1092,9 @@ extern "C" int fp8g_moe_gate_backward(const void* logits, int32_t dtype, int64_t
   a.logits = logits, a.mask = token_mask, a.ids = topk_ids, a.counts = counts, a.dweights = dweights, a.dloss = dloss;
   a.dlogits = dlogits, a.T = T, a.ldl = ldl, a.ldd = ldd;
   a.E = E, a.topk = topk, a.renorm = renormalize, a.coef = loss_coef;
-  a.vec = logit_vectors(logits, ldl, E, dtype) && logit_vectors(dlogits, ldd, E, dtype);
+  a.vec = logit_vectors(logits, ldl, dtype) && logit_vectors(dlogits, ldd, dtype);
   return (dtype == FP8G_F32 ? gate_backward_form<float>(E) : gate_backward_form<__nv_bfloat16>(E))(
-      a, static_cast<cudaStream_t>(stream));
+      a, dev, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fp8g_moe_combine(const void* D, int64_t M, int64_t N, int64_t ldd, const int32_t* entry_row,

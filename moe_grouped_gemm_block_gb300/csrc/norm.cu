@@ -25,7 +25,7 @@
 //   ring     16384 x 8192 fp32 rows, bf16 y: forward 135 us (88%), backward 219 (90%)
 //            4096 x 7168 bf16: forward 25 us (69%), backward 42 (62%)
 //            4096 x 12288 bf16, clusters: forward 53 us (56%), backward 76 (59%)
-//   warp     16384 x 512 bf16: forward 12.4 us (40%), backward 17.6 (42%)
+//   warp     16384 x 512 bf16: forward 10.4 us (48%), backward 17.6 (42%)
 //   scalar and any are there for every other row, not for speed
 
 #include <algorithm>
@@ -225,8 +225,8 @@ __device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity, long l
     }
   }
 }
-// Whether a wait has run out, the same answer in all of a warp.  The sum warps leave then: no barrier is told twice in a
-// phase what to expect.
+// Whether a wait has run out, the same answer in all of a warp.  The sum warps leave then: no barrier is told twice in
+// a phase what to expect.
 __device__ __forceinline__ bool ring_dead(const RingShared& sm) {
   return __any_sync(0xffffffffu, *const_cast<const volatile int*>(&sm.dead));
 }
@@ -1316,7 +1316,8 @@ int layer_norm_vectors(const NormArgs& a, Grid grid, const DeviceInfo* dev, cuda
               : vecs <= 32 ? layer_norm_warp_kernel<TX, TY, 32, 1, SHIFT>
                            : layer_norm_warp_kernel<TX, TY, 32, 2, false>;
     const int64_t per = kNormThreads / (vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32);
-    const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 8 * static_cast<int64_t>(sms));
+    // three CTAs an SM, with several rows to a warp: 16384 x 512 bf16 10.4 us, x 128 6.7; with eight 12.4 and 8.2
+    const int64_t ctas = std::min<int64_t>((M + per - 1) / per, 3 * static_cast<int64_t>(sms));
     go<<<static_cast<unsigned>(ctas), kNormThreads, 0, s>>>(a);
   } else if (vecs * 8 <= 2 * kRingMaxN) {
     const RingPlan p = ring_plan(M, vecs, sizeof(TX), 0, kRingThreads, grid, sms);
