@@ -25,7 +25,7 @@
 //   ring     16384 x 8192 fp32 rows, bf16 y: forward 135 us (88%), backward 219 (90%)
 //            4096 x 7168 bf16: forward 25 us (69%), backward 42 (62%)
 //            4096 x 12288 bf16, clusters: forward 53 us (56%), backward 76 (59%)
-//   warp     16384 x 512 bf16: forward 10.4 us (48%), backward 17.6 (42%)
+//   warp     16384 x 512 bf16: forward 10.4 us (48%), backward 16.4 (45%)
 //   scalar and any are there for every other row, not for speed
 
 #include <algorithm>
