@@ -261,15 +261,16 @@ __device__ __forceinline__ int copied(const RowShape<SHIFT>& shape, const Share&
   const bool past = SHIFT && last_row && (shape.N + shape.q) % 8 != 0 && sh.first + sh.count == shape.vectors();
   return sh.count - (past ? 1 : 0);
 }
-// Vector v of the share from its stage; the values that do not exist are zero.
-template <bool SHIFT, typename T>
+// Vector v of the share from its stage.  The values that do not exist are zero (ZERO), or anything: those of the
+// neighbouring rows, which the column warps leave out of all that they store.
+template <bool SHIFT, bool ZERO, typename T>
 __device__ __forceinline__ void stage_vector(Raw8<T>& r, const T* stage, int v, uint32_t mask, bool last_row,
                                              const T* row) {
   if (SHIFT && mask != 0xFFu && last_row) {
     r.gather(row + v * 8, mask);  // row: the share's first vector in memory
   } else {
     r.load(stage + v * 8);
-    if (SHIFT && mask != 0xFFu) r.keep(mask);
+    if (SHIFT && ZERO && mask != 0xFFu) r.keep(mask);
   }
 }
 
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       if (SHIFT && lane < 2) {  // the first and the last vector
         v = lane == 0 ? 0 : share.count - 1;
         const uint32_t mask = shape.mask(share.first + v);
-        stage_vector<SHIFT>(r[0], stage, v, mask, m + 1 == a.M, x + m * a.ldx);
+        stage_vector<SHIFT, true>(r[0], stage, v, mask, m + 1 == a.M, x + m * a.ldx);
         r[0].get(f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         Raw8<TX> raw;
-        if (mask[v]) stage_vector<SHIFT>(raw, stage, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
+        if (mask[v]) stage_vector<SHIFT, false>(raw, stage, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
         if (v == NV - 1) ring_empty(sm, s);
         if (!mask[v]) continue;
         float2 f[4];
@@ -997,8 +998,8 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
       if (SHIFT && lane < 2) {  // the first and the last vector; dy is zero where they do not exist
         v = lane == 0 ? 0 : share.count - 1;
         const uint32_t mask = shape.mask(share.first + v);
-        stage_vector<SHIFT>(rx, xs, v, mask, m + 1 == a.M, x + m * a.ldx);
-        stage_vector<SHIFT>(ry, ys, v, mask, m + 1 == a.M, dy + m * a.lddy);
+        stage_vector<SHIFT, true>(rx, xs, v, mask, m + 1 == a.M, x + m * a.ldx);
+        stage_vector<SHIFT, true>(ry, ys, v, mask, m + 1 == a.M, dy + m * a.lddy);
         add(rx, ry, ws[v], ws[share.count + v]);
       }
       s1[0] = __fadd2_rn(s1[0], s1[1]);
@@ -1037,8 +1038,8 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
         Raw8<TX> rx;
         Raw8<TY> ry;
         if (mask[v]) {
-          stage_vector<SHIFT>(rx, xs, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
-          stage_vector<SHIFT>(ry, ys, v * columns + tid, mask[v], m + 1 == a.M, dy + m * a.lddy);
+          stage_vector<SHIFT, false>(rx, xs, v * columns + tid, mask[v], m + 1 == a.M, x + m * a.ldx);
+          stage_vector<SHIFT, false>(ry, ys, v * columns + tid, mask[v], m + 1 == a.M, dy + m * a.lddy);
         }
         if (v == NV - 1) ring_empty(sm, s);
         if (!mask[v]) continue;
