@@ -1217,7 +1217,7 @@ int dtype_size(int32_t d) { return d == FP8G_F32 ? 4 : 2; }
 // ---------------------------------------------------------------- launches
 // The warp form's vectors a row, at most, on the 16-byte grid and off it.  Beyond them a lane's registers (weights,
 // next row, backward the sums) leave too few warps an SM: 16384 x 1000 bf16 forward 30 us against 21 in the ring,
-// backward 29 against 33; 16384 x 501 forward 30 against 25, backward 41 against 38.
+// backward 29 against 33; 16384 x 501 forward 30 against 21, backward 41 against 31.
 constexpr int64_t kWarpVectors = 64, kWarpGradVectors = 128, kWarpShiftVectors = 32;
 constexpr int64_t kRingMaxN = 8192;      // ring form: a CTA's columns; twice that in clusters of two
 constexpr int64_t kCtaMaxN = 32768;      // cta form: up to 4 vectors a thread
