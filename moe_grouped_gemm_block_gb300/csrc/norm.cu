@@ -120,11 +120,22 @@ __device__ __forceinline__ void weights8(const void* w, int32_t w_kind, int n, u
     r.v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + n));
     r.get(f);
   } else {
+    // eight loads at once, without branches: where a value does not exist, of one that does
+    float t[8];
+    const int some = n + __ffs(mask) - 1;
+    if ((w_kind & ~kWeightVectors) == FP8G_F32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (mask >> (2 * i) & 1u) f[i].x = load_any(w, w_kind, n + 2 * i);
-      if (mask >> (2 * i + 1) & 1u) f[i].y = load_any(w, w_kind, n + 2 * i + 1);
+      for (int j = 0; j < 8; ++j) t[j] = __ldg(static_cast<const float*>(w) + (mask >> j & 1u ? n + j : some));
+    } else {
+      unsigned short h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = __ldg(static_cast<const unsigned short*>(w) + (mask >> j & 1u ? n + j : some));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = __uint_as_float(static_cast<uint32_t>(h[j]) << 16);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (mask >> j & 1u) (j & 1 ? f[j / 2].y : f[j / 2].x) = t[j];
   }
 }
 
