@@ -24,7 +24,7 @@
 // about 8 us of a ring, 11 backward with the joined sums).  Device times, and the share of the copy rate:
 //   ring     16384 x 8192 fp32 rows, bf16 y: forward 135 us (88%), backward 219 (90%)
 //            4096 x 7168 bf16: forward 25 us (69%), backward 42 (62%)
-//            4096 x 12288 bf16, clusters: forward 53 us (56%), backward 76 (59%)
+//            4096 x 12288 bf16, clusters: forward 44 us (67%), backward 75 (59%)
 //   warp     16384 x 512 bf16: forward 10.4 us (48%), backward 16.4 (45%)
 //   scalar and any are there for every other row, not for speed
 
@@ -324,10 +324,18 @@ __device__ __forceinline__ void ring_init(RingShared& sm, int stages, int column
   }
 }
 
+// In a cluster: tells the other CTA that its last row's sums have been read from this CTA's slot s.  Who does is a
+// matter of time, as an arrival at another CTA waits for what its warp has on its way.  The column warps have stores
+// (4096 x 12288 bf16 backward took 93 us).  The copying thread knows first, but then copies late: it does where the
+// stages are few (16384 fp32 columns backward, 3 stages: 274 us, by the sum warps 352).  Else a sum warp does when it
+// finds its stage full again (12288 bf16 columns forward, 16 stages: 44 us, by the copying thread 52).
+constexpr int kRingFewStages = 4;
+__device__ __forceinline__ void ring_tell(RingShared& sm, int s, int rank) {
+  mbar_arrive_cluster(mapa_shared(smem_u32(&sm.peer[s]), rank ^ 1));
+}
+
 // The copying thread: row after row into the ring, each stage once it is empty.  `load` copies row i into stage s and
-// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.  In a
-// cluster it tells the other CTA that the stage's slot has been read, too: the column warps have stores on their way,
-// which an arrival of theirs at the other CTA would have to wait for (4096 x 12288 bf16 backward: 93 us instead of 76).
+// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.
 template <int CL, typename Load>
 __device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, int rank, long long budget,
                                             unsigned int* status, Load load) {
@@ -337,7 +345,7 @@ __device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages
     if (i >= stages) {
       ring_wait(&sm.empty[s], parity, budget, status, &sm.dead);
       if (*const_cast<volatile int*>(&sm.dead)) break;
-      if constexpr (CL > 1) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.peer[s]), rank ^ 1));
+      if (CL > 1 && stages <= kRingFewStages) ring_tell(sm, s, rank);
     }
     load(i, s);
     if (++s == stages) {
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       const int64_t m = first + it.row() * P;
       ring_wait(&sm.full[s], it.round & 1, a.budget, a.status, &sm.dead);
       if (ring_dead(sm)) break;
+      if (CL > 1 && it.round > 0 && lane == 0 && stages > kRingFewStages) ring_tell(sm, s, rank);
       const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const Inner<SHIFT> in(share);
       float2 f[4], d1 = both(0.0f), d2 = both(0.0f), e1 = both(0.0f), e2 = both(0.0f);
@@ -968,6 +977,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
       stats();
       ring_wait(&sm.full[s], round & 1, a.budget, a.status, &sm.dead);
       if (ring_dead(sm)) break;
+      if (CL > 1 && round > 0 && lane == 0 && stages > kRingFewStages) ring_tell(sm, s, rank);
       const TX* xs = reinterpret_cast<const TX*>(ring + s * stage_bytes);
       const TY* ys = reinterpret_cast<const TY*>(ring + s * stage_bytes + x_bytes);
       const Inner<SHIFT> in(share);
