@@ -24,7 +24,7 @@ namespace {
 //
 // The kernels are bound by their instructions, not by memory: 362 of a warp for a bf16 row of 256 with 8 picks, most
 // of them on the ALU, which takes one every second cycle (the sort's minima and maxima, the keys, the picks).
-// 65536 x 256, 8 picks: forward bf16 37 us, fp32 47 (15% and 22% of the copy rate), of which the joined sums take 5;
+// 65536 x 256, 8 picks: forward bf16 38 us, fp32 47 (15% and 22% of the copy rate), of which the joined sums take 5;
 // backward bf16 26 us (40%).  Few tokens (64 x 32): 7 us, a launch.
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;

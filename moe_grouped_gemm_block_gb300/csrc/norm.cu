@@ -22,8 +22,8 @@
 //
 // Bound by memory, and below some tens of MB by a call's fixed part (launch, weights, first rows, the last stores:
 // about 8 us of a ring, 11 backward with the joined sums).  Device times, and the share of the copy rate:
-//   ring     16384 x 8192 fp32 rows, bf16 y: forward 135 us (88%), backward 219 (90%)
-//            4096 x 7168 bf16: forward 25 us (69%), backward 42 (62%)
+//   ring     16384 x 8192 fp32 rows, bf16 y: forward 135 us (88%), backward 212 (93%)
+//            4096 x 7168 bf16: forward 25 us (69%), backward 41 (63%)
 //            4096 x 12288 bf16, clusters: forward 44 us (67%), backward 75 (59%)
 //   warp     16384 x 512 bf16: forward 10.4 us (48%), backward 16.4 (45%)
 //   scalar and any are there for every other row, not for speed
