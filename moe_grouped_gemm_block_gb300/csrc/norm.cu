@@ -34,6 +34,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 #include "vec.cuh"
 
 namespace fp8g {
@@ -52,29 +53,6 @@ __device__ __forceinline__ void store_pairs(float* p, const float2 (&f)[4]) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// How a row falls into vectors of 8.  Where every row starts on the grid of its matrix's 8-value groups (SHIFT
-// false), vector v holds columns 8 v .. 8 v + 7.  Else row m starts q = (m ld) mod 8 values after a group's start and
-// vector v holds columns 8 v - q ..: its first and last vectors reach into the neighbouring rows, whose values are
-// left out.  q repeats every 8 rows, so a thread that steps by multiples of 8 rows keeps its columns, and with
-// them its weights and its sums of the weight gradients.  Every matrix of a call has the same q (the host checks).
-template <bool SHIFT>
-struct RowShape {
-  int N, q;
-  __device__ __forceinline__ RowShape(int n, int64_t m, int64_t ld)
-      : N(n), q(SHIFT ? static_cast<int>((m & 7) * (ld & 7)) & 7 : 0) {}
-  __device__ __forceinline__ int vectors() const { return (N + q + 7) >> 3; }
-  __device__ __forceinline__ int col(int v) const { return 8 * v - q; }
-  // The columns of vector v that exist, a bit each.
-  __device__ __forceinline__ uint32_t mask(int v) const {
-    const int c = col(v);
-    if (!SHIFT) return c < N ? 0xFFu : 0u;
-    uint32_t k = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) k |= (c + j >= 0 && c + j < N ? 1u : 0u) << j;
-    return k;
-  }
-};
-
 // The values of a vector that the mask has.
 template <bool SHIFT, typename T>
 __device__ __forceinline__ void store_masked(T* p, const float2 (&f)[4], uint32_t mask) {
@@ -87,8 +65,8 @@ __device__ __forceinline__ void store_masked(T* p, const float2 (&f)[4], uint32_
     if (mask >> j & 1u) p[j] = from_f32<T>(j & 1 ? f[j / 2].y : f[j / 2].x);
 }
 
-// A vector of a row, read once: 16-byte loads where all of it may be read (`inside`: it lies within its matrix,
-// neighbouring rows included), value by value where it would reach past the matrix's end.
+// A vector of a row, read once: 16-byte loads where all of it may be read (`inside`, see vector_inside), value by value
+// where it would reach past the matrix's end.
 template <bool SHIFT, typename T>
 __device__ __forceinline__ void load_vector(Raw8<T>& r, const T* p, uint32_t mask, bool inside) {
   if constexpr (!SHIFT) {  // a vector is there or not
@@ -254,24 +232,6 @@ __device__ __forceinline__ void st_async4(uint32_t addr, float4 v, uint32_t bar)
                : "memory");
 }
 
-// This CTA's share of every row: the vectors first .. first + count - 1 of the row's.
-struct Share {
-  int first, count;
-  template <bool SHIFT>
-  __device__ __forceinline__ Share(const RowShape<SHIFT>& shape, int rank, int ranks) {
-    const int all = shape.vectors(), each = (all + ranks - 1) / ranks;
-    first = rank * each;
-    count = min(each, all - first);
-  }
-};
-
-// The vectors of the share that a stage's copy holds: a last row's last vector may reach past the matrix, and is left
-// out (the threads that need it read its values themselves).
-template <bool SHIFT>
-__device__ __forceinline__ int copied(const RowShape<SHIFT>& shape, const Share& sh, bool last_row) {
-  const bool past = SHIFT && last_row && (shape.N + shape.q) % 8 != 0 && sh.first + sh.count == shape.vectors();
-  return sh.count - (past ? 1 : 0);
-}
 // Vector v of the share from its stage.  The values that do not exist are zero (ZERO), or anything: those of the
 // neighbouring rows, which the column warps leave out of all that they store.
 template <bool SHIFT, bool ZERO, typename T>
@@ -285,13 +245,6 @@ __device__ __forceinline__ void stage_vector(Raw8<T>& r, const T* stage, int v, 
   }
 }
 
-// The vectors of a share that are whole in every row; off the grid its first and last one may not be.  (A ring's rows
-// have more than 33 vectors a share.)
-template <bool SHIFT>
-struct Inner {
-  int lo, hi;
-  __device__ __forceinline__ Inner(const Share& sh) : lo(SHIFT ? 1 : 0), hi(sh.count - (SHIFT ? 1 : 0)) {}
-};
 constexpr int kSumUnroll = 4;  // vectors in flight per lane of a sum warp
 
 // The rows of sum warp w: those in the stages w, w + warps, ... in every round, so that it sees each round of its
@@ -430,8 +383,10 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_warp_kernel(const Nor
   Raw8<TX> next[NV];
   auto fetch = [&](int64_t m) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      load_vector<SHIFT>(next[v], x + m * a.ldx + shape.col(v * LPR + sub), m < a.M ? mask[v] : 0u, m + 1 < a.M);
+    for (int v = 0; v < NV; ++v) {
+      const int c = shape.col(v * LPR + sub);
+      load_vector<SHIFT>(next[v], x + m * a.ldx + c, m < a.M ? mask[v] : 0u, vector_inside(m, a.M, a.ldx, a.N, c));
+    }
   };
   fetch(m0 + off);
   for (; m0 < a.M; m0 += stride) {
@@ -497,7 +452,8 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
   for (int v = 0; v < NV; ++v) {
     const int i = v * threads + static_cast<int>(threadIdx.x);
     mask[v] = shape.mask(i);
-    load_vector<SHIFT>(raw[v], static_cast<const TX*>(a.x) + m * a.ldx + shape.col(i), mask[v], m + 1 < a.M);
+    load_vector<SHIFT>(raw[v], static_cast<const TX*>(a.x) + m * a.ldx + shape.col(i), mask[v],
+                       vector_inside(m, a.M, a.ldx, a.N, shape.col(i)));
   }
   const int n = warp_count(mask);
   const float2 own = warp_moments<SHIFT>(raw, mask, n ? 1.0f / static_cast<float>(n) : 0.0f);
@@ -837,8 +793,9 @@ __global__ void __launch_bounds__(32 * grad_warps<TX, TY, NV, SHIFT>(), 1)
     nr = in ? a.rstd[m] : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      load_vector<SHIFT>(nx[v], x + m * a.ldx + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
-      load_vector<SHIFT>(ny[v], dy + m * a.lddy + shape.col(v * LPR + sub), in ? mask[v] : 0u, m + 1 < a.M);
+      const int c = shape.col(v * LPR + sub);
+      load_vector<SHIFT>(nx[v], x + m * a.ldx + c, in ? mask[v] : 0u, vector_inside(m, a.M, a.ldx, a.N, c));
+      load_vector<SHIFT>(ny[v], dy + m * a.lddy + c, in ? mask[v] : 0u, vector_inside(m, a.M, a.lddy, a.N, c));
     }
   };
   fetch(m0 + off);
