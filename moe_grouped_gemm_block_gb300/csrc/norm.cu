@@ -483,9 +483,10 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
   }
 }
 
-// ring form.  A sum warp takes the differences from K, the mean of 256 values at the row's start (of its CTA's share):
-// variance = mean (x - K)^2 - (mean (x - K))^2 then loses little to cancellation, as (K - mean)^2 is at most N / 256
-// variances whatever the values.
+// ring form.  A sum warp takes the differences from K, the mean of the row's first whole vectors (of its CTA's share; 32,
+// or 30 at the least): variance = mean (x - K)^2 - (mean (x - K))^2 then loses little to cancellation, as (K - mean)^2 is
+// at most N / 240 variances whatever the values.  Nothing but the row's own values may enter K: a neighbour's could be
+// anything.
 template <typename TX, typename TY, int CL, bool SHIFT>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const NormArgs a, int32_t stages,
                                                                              int32_t stage_bytes, int32_t column_warps,
@@ -516,6 +517,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
     // the values that the share holds
     const int held = min(a.N, shape.col(share.first + share.count)) - max(0, shape.col(share.first));
     const float n = static_cast<float>(held), inv_n = 1.0f / n;
+    const Inner<SHIFT> in(share);
+    const int heads = in.heads();
+    const float inv_heads = 1.0f / static_cast<float>(8 * heads);
     for (SumRows it(warp - column_warps, sum_warps, stages); it.row() < rows; it.next()) {
       const int s = it.stage;
       const int64_t m = first + it.row() * P;
@@ -523,13 +527,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       if (ring_dead(sm)) break;
       if (CL > 1 && it.round > 0 && lane == 0 && stages > kRingFewStages) ring_tell(sm, s, rank);
       const TX* stage = reinterpret_cast<const TX*>(ring + s * stage_bytes);
-      const Inner<SHIFT> in(share);
       float2 f[4], d1 = both(0.0f), d2 = both(0.0f), e1 = both(0.0f), e2 = both(0.0f);
       Raw8<TX> r[kSumUnroll];
-      r[0].load(stage + (in.lo + lane) * 8);
+      if (lane < heads) r[0].load(stage + (in.lo + lane) * 8);
+      else r[0].zero();
       r[0].get(f);
       const float2 t = __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3]));
-      const float K = warp_sum(t.x + t.y) * (1.0f / 256.0f);
+      const float K = warp_sum(t.x + t.y) * inv_heads;
       auto add = [&](const Raw8<TX>& raw) {
         raw.get(f);
 #pragma unroll

@@ -54,12 +54,13 @@ __host__ __device__ __forceinline__ int copied(const RowShape<SHIFT>& shape, con
   const bool past = SHIFT && last_row && (shape.N + shape.q) % 8 != 0 && sh.first + sh.count == shape.vectors();
   return sh.count - (past ? 1 : 0);
 }
-// The vectors of a share that are whole in every row; off the grid its first and last one may not be.  (A ring's rows
-// have more than 33 vectors a share.)
+// The vectors of a share that are whole in every row; off the grid its first and last one may not be.
 template <bool SHIFT>
 struct Inner {
   int lo, hi;
   __host__ __device__ __forceinline__ Inner(const Share& sh) : lo(SHIFT ? 1 : 0), hi(sh.count - (SHIFT ? 1 : 0)) {}
+  // How many of them a warp sees at once: a short row off the grid has fewer than 32 (a ring's at least 30).
+  __host__ __device__ __forceinline__ int heads() const { return SHIFT && hi - lo < 32 ? hi - lo : 32; }
 };
 
 }  // namespace fp8g

@@ -1,5 +1,6 @@
 """How the layer norm's rows fall into 16-byte vectors (csrc/rows.cuh), walked over on the host: what the kernels load as
-a whole vector lies within the matrix, and every column of a row is in one vector.  No GPU needed."""
+a whole vector lies within the matrix, every column of a row is in one vector, and what a ring's sum warps take as a
+row's own whole vectors is that.  No GPU needed."""
 
 import subprocess
 
@@ -38,12 +39,40 @@ static void walk(int64_t M, int N, int64_t ld) {
   }
 }
 
+// A ring's copies and the vectors that its sum warps take as whole ones, for every row and each CTA of a cluster.
+template <bool SHIFT>
+static void walk_ring(int64_t M, int N, int64_t ld, int ranks) {
+  for (int64_t m = 0; m < M; ++m) {
+    const RowShape<SHIFT> shape(N, m, ld);
+    int taken = 0;
+    for (int rank = 0; rank < ranks; ++rank) {
+      const Share sh(shape, rank, ranks);
+      const int n = copied(shape, sh, m + 1 == M);
+      const int64_t at = m * ld + shape.col(sh.first);
+      if (n && (at < 0 || at + 8 * n > (M - 1) * ld + N)) fault("copied from outside", M, N, ld, m, rank);
+      const Inner<SHIFT> in(sh);
+      if (in.heads() < 30 || in.heads() > 32) fault("heads", M, N, ld, m, in.heads());
+      for (int v = in.lo; v < in.hi; ++v)
+        if (shape.mask(sh.first + v) != 0xFFu || v >= n) fault("not whole", M, N, ld, m, v);
+      if (in.lo + in.heads() > in.hi) fault("heads past the whole vectors", M, N, ld, m, in.heads());
+      taken += sh.count;
+    }
+    if (taken != shape.vectors()) fault("shares", M, N, ld, m, taken);
+  }
+}
+
 int main() {
   for (int64_t M = 1; M <= 20; ++M)
     for (int N = 1; N <= 16; ++N)
       for (int64_t ld = N; ld <= N + 9; ++ld) walk(M, N, ld);
   for (int N : {17, 57, 58, 249, 250, 264, 8185, 16370})
     for (int64_t ld = N; ld <= N + 9; ++ld) walk(9, N, ld);
+  for (int N = 250; N <= 300; ++N)  // the shortest rows that the ring takes off the grid
+    for (int64_t ld = N; ld <= N + 9; ++ld)
+      for (int64_t M : {1, 2, 9, 20}) walk_ring<true>(M, N, ld, 1);
+  for (int N : {520, 8184, 8192}) walk_ring<false>(9, N, N, 1);
+  for (int N = 8180; N <= 8200; ++N) walk_ring<true>(9, N, N, N <= 8185 ? 1 : 2);
+  for (int N = 16360; N <= 16377; ++N) walk_ring<true>(9, N, N + 1, 2);
   printf("faults %d\n", faults);
   return faults != 0;
 }
