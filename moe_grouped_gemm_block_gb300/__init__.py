@@ -25,7 +25,7 @@ The training operators around the grouped GEMMs, on bf16 and fp32 tensors (``blo
 ``clip_grad_norm``.
 
 e4m3 tensors may be torch.uint8 or torch.float8_e4m3fn.  Work is enqueued on the
-current CUDA stream of the tensors' device.  A non-zero status raises Fp8GemmError.
+current CUDA stream of the tensors' device, which has to be the current device.  A non-zero status raises Fp8GemmError.
 Convenience wrappers (``quantize_1x128``, ``quantize_128x128``, ``gemm_nt``) allocate
 their outputs with torch and call the above.
 """
@@ -132,7 +132,18 @@ def _check(code: int, what: str):
         raise Fp8GemmError(code, what)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _need_current(dev: int) -> None:
+    """The library launches its kernels on the current device: operands of another GPU are refused."""
+    if dev != _current_device():
+        raise ValueError(f"operands: on GPU {dev}, which is not the current device (see torch.cuda.device)")
+
+
 def _stream(t: torch.Tensor) -> int:
+    """The current stream of the tensor's device, which is the current one."""
+    _need_current(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 

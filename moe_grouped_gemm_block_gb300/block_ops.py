@@ -13,7 +13,8 @@ into the caller's tensors; the ones without the prefix allocate their results wi
     norm = clip_grad_norm(grads, max_norm)
     norm = grad_norm(grads)
 
-Work is enqueued on the current CUDA stream of the tensors' device; nothing synchronises.
+Work is enqueued on the current CUDA stream of the tensors' device, which has to be the current device; nothing
+synchronises.
 """
 
 from __future__ import annotations
@@ -23,7 +24,7 @@ import functools
 
 import torch
 
-from . import Fp8GemmError, _check, _need, _stream, lib
+from . import Fp8GemmError, _check, _need, _need_current, _stream, lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _F32 = torch.float32
@@ -79,7 +80,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _on(t: torch.Tensor, dev: int) -> int:
-    """The current stream of the tensor's device."""
+    """The current stream of the tensor's device, which is the current one."""
+    _need_current(dev)
     return _raw_stream(dev) if _raw_stream is not None else _stream(t)
 
 

@@ -215,3 +215,60 @@ def test_binding_clip():
         g.clip_grad_norm([_f32(8)], 1.0)
     with pytest.raises(ValueError, match="a tensor for each"):
         g.GradList([_f32(8)], [])
+
+
+# ---- tensors of a GPU that is not the current one: the library launches on the current one
+
+class _Elsewhere(torch.Tensor):
+    """A host tensor that says it lies on GPU 1."""
+
+    def get_device(self):
+        return 1
+
+
+def _there(t):
+    return t.as_subclass(_Elsewhere)
+
+
+class _NeverCalled:
+    """Stands for the library: its size queries answer, a launch fails the test."""
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace"):
+            return lambda *a: 0
+        return lambda *a: pytest.fail(f"{name} was launched")
+
+
+def _calls_elsewhere():
+    x, v, m, ids = _there(_f32(4, 8)), _there(_f32(8)), _there(_f32(4)), _there(_i32(4, 2))
+    D, w, tok = _there(_bf16(128, 8)), _there(_f32(4, 2)), _there(_i32(128))
+    return {
+        "fp8g_layer_norm": lambda: g.fp8g_layer_norm(x, v, v, x, m, m),
+        "layer_norm": lambda: g.layer_norm(x, v, v),
+        "fp8g_layer_norm_backward": lambda: g.fp8g_layer_norm_backward(x, x, v, m, m, x, v, v),
+        "layer_norm_backward": lambda: g.layer_norm_backward(x, x, v, m, m),
+        "fp8g_moe_gate": lambda: g.fp8g_moe_gate(x, 2, ids, w, _there(_i32(8))),
+        "moe_gate": lambda: g.moe_gate(x, 2),
+        "fp8g_moe_gate_backward": lambda: g.fp8g_moe_gate_backward(x, ids, _there(_i32(8)), w, None, x),
+        "moe_gate_backward": lambda: g.moe_gate_backward(x, ids, _there(_i32(8)), w),
+        "fp8g_moe_combine": lambda: g.fp8g_moe_combine(D, ids, w, x),
+        "moe_combine": lambda: g.moe_combine(D, ids, w),
+        "fp8g_moe_combine_backward": lambda: g.fp8g_moe_combine_backward(x, D, ids, tok, w, D, w),
+        "fp8g_grad_norm": lambda: g.fp8g_grad_norm(g.GradList([x]), _there(_f32(1)),
+                                                   _there(torch.zeros(8, dtype=torch.uint8))),
+        "fp8g_clip_grad_norm": lambda: g.fp8g_clip_grad_norm(g.GradList([x]), 1.0, _there(_f32(1)), 1e-6,
+                                                             _there(torch.zeros(8, dtype=torch.uint8))),
+        "quantize_1x128": lambda: g._stream(x),  # what every GEMM and quantiser call takes its stream from
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls_elsewhere()))
+def test_tensors_of_another_gpu_than_the_current_one(name, monkeypatch):
+    from moe_grouped_gemm_block_gb300 import block_ops as bo
+    monkeypatch.setattr(g, "_current_device", lambda: 0)
+    monkeypatch.setattr(bo, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: type("S", (), {"cuda_stream": 0}))
+    monkeypatch.setattr(bo, "lib", _NeverCalled)
+    monkeypatch.setattr(bo, "_workspace_bytes", lambda *a: 0)
+    with pytest.raises(ValueError, match="current device"):
+        _calls_elsewhere()[name]()
