@@ -399,7 +399,9 @@ def moe_combine_backward(dout, D, entry_row, row_token, weights=None):
 
 class GradList:
     """The gradients of a program (and, for clipping out of place, the tensors that take the results), checked and
-    listed once.  It holds the tensors, so their memory stays; a program whose gradients move makes a new one."""
+    listed once.  It holds the tensors and the memory they had, so nothing else comes to lie there.  A call refuses a
+    list whose tensors have been given other memory since (``t.data = ...``, a ``resize_`` that grows): a program whose
+    gradients move makes a new one."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -416,8 +418,11 @@ class GradList:
                 _refuse("out: each gradient's shape and type, contiguous")
             if dev < 0 or t.get_device() != dev or o.get_device() != dev:
                 _refuse("grads: CUDA tensors on one device")
-        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
-        self.out_ptrs = self.ptrs if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
+        held = self.grads if out is None else self.grads + self.out
+        self.memory = [t.untyped_storage() for t in held]
+        self.tensors, self.places, self.indices = held, [t.data_ptr() for t in held], list(range(len(held)))
+        self.ptrs = (ctypes.c_void_p * n)(*self.places[:n])
+        self.out_ptrs = self.ptrs if out is None else (ctypes.c_void_p * n)(*self.places[n:])
         self.numels = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
         self.dtypes = (ctypes.c_int32 * n)(*[_DTYPES[t.dtype] for t in self.grads])
         b = ctypes.c_int64()
@@ -427,31 +432,58 @@ class GradList:
     def __len__(self):
         return self.n
 
+    def check_places(self) -> None:
+        """Every tensor where it was when it was listed."""
+        if not _all_at(self.tensors, self.places, self.indices):
+            i = next(i for i, t in enumerate(self.tensors) if t.data_ptr() != self.places[i]) % self.n
+            _refuse(f"grads: tensor {i} has moved since it was listed")
 
-def _norm_buffers(g: GradList, norm, workspace):
+
+# Whether tensors[i].data_ptr() == places[i] for all indices i: on every call, so in one step where torch has it (300
+# tensors 10 us, one by one 28).
+_all_at = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal",
+                  lambda tensors, places, indices: [t.data_ptr() for t in tensors] == places)
+
+
+def _norm_buffers(g: GradList, norm, workspace) -> None:
     _vector(norm, 1, _F32, "norm")
-    if workspace is None:
-        workspace = _empty(g.workspace_bytes, dtype=_U8, device=g.device)
-    else:
+    if workspace is not None:
         _scratch(workspace)
     _one_device(g.device_index, norm, workspace)
-    return workspace
+
+
+def _workspace_of(g: GradList, workspace):
+    return _empty(g.workspace_bytes, dtype=_U8, device=g.device) if workspace is None else workspace
 
 
 def fp8g_grad_norm(grads: GradList, norm, workspace=None) -> None:
     """norm f32 [1] = the 2-norm of all gradients together."""
-    ws = _norm_buffers(grads, norm, workspace)
-    st = lib().fp8g_grad_norm(grads.ptrs, grads.numels, grads.dtypes, grads.n, norm.data_ptr(), ws.data_ptr(),
-                              ws.numel(), _on(norm, grads.device_index))
+    _norm_buffers(grads, norm, workspace)
+    _norm_of(grads, norm, workspace)
+
+
+def _norm_of(g: GradList, norm, workspace) -> None:
+    """The list's check and the call."""
+    g.check_places()
+    ws = _workspace_of(g, workspace)
+    st = lib().fp8g_grad_norm(g.ptrs, g.numels, g.dtypes, g.n, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                              _on(norm, g.device_index))
     if st:
         _raise(st, "fp8g_grad_norm")
 
 
 def fp8g_clip_grad_norm(grads: GradList, max_norm: float, norm, eps: float = 1e-6, workspace=None) -> None:
     """norm f32 [1] as fp8g_grad_norm; every gradient times min(1, max_norm / (norm + eps)), into grads.out."""
-    ws = _norm_buffers(grads, norm, workspace)
-    st = lib().fp8g_clip_grad_norm(grads.ptrs, grads.out_ptrs, grads.numels, grads.dtypes, grads.n, max_norm, eps,
-                                   norm.data_ptr(), ws.data_ptr(), ws.numel(), _on(norm, grads.device_index))
+    _norm_buffers(grads, norm, workspace)
+    _clip(grads, max_norm, norm, eps, workspace)
+
+
+def _clip(g: GradList, max_norm: float, norm, eps: float, workspace) -> None:
+    """The list's check and the call."""
+    g.check_places()
+    ws = _workspace_of(g, workspace)
+    st = lib().fp8g_clip_grad_norm(g.ptrs, g.out_ptrs, g.numels, g.dtypes, g.n, max_norm, eps, norm.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), _on(norm, g.device_index))
     if st:
         _raise(st, "fp8g_clip_grad_norm")
 
@@ -464,7 +496,7 @@ def grad_norm(grads) -> torch.Tensor:
     """grads: a GradList or a sequence of tensors -> their 2-norm, f32 [1] on the device."""
     g = _grad_list(grads)
     norm = _empty(1, dtype=_F32, device=g.device)
-    fp8g_grad_norm(g, norm)
+    _norm_of(g, norm, None)
     return norm
 
 
@@ -473,5 +505,5 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     -> the norm before clipping, f32 [1] on the device."""
     g = _grad_list(grads)
     norm = _empty(1, dtype=_F32, device=g.device)
-    fp8g_clip_grad_norm(g, max_norm, norm, eps)
+    _clip(g, max_norm, norm, eps, None)
     return norm

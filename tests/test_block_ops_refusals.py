@@ -272,3 +272,44 @@ def test_tensors_of_another_gpu_than_the_current_one(name, monkeypatch):
     monkeypatch.setattr(bo, "_workspace_bytes", lambda *a: 0)
     with pytest.raises(ValueError, match="current device"):
         _calls_elsewhere()[name]()
+
+
+# ---- gradients whose storage has been replaced since they were listed
+
+class _Here(torch.Tensor):
+    """A host tensor that says it lies on GPU 0."""
+
+    def get_device(self):
+        return 0
+
+
+def _move_data(t):
+    t.data = t.data.clone()
+
+
+def _grow(t):
+    t.resize_(1 << 20)
+
+
+@pytest.mark.parametrize("move", [_move_data, _grow])
+@pytest.mark.parametrize("which", ["gradient", "result"])
+@pytest.mark.parametrize("call", ["norm", "clip"])
+def test_a_listed_gradient_that_has_moved(move, which, call, monkeypatch):
+    from moe_grouped_gemm_block_gb300 import block_ops as bo
+    monkeypatch.setattr(g, "_current_device", lambda: 0)
+    monkeypatch.setattr(bo, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(bo, "lib", _NeverCalled)
+    grads = [_f32(8).as_subclass(_Here), _bf16(5, 3).as_subclass(_Here)]
+    out = [t.clone() for t in grads]
+    lst = g.GradList(grads, out)
+    move(grads[1] if which == "gradient" or call == "norm" else out[1])
+    one = [_f32(1).as_subclass(_Here), torch.zeros(8, dtype=torch.uint8).as_subclass(_Here)]
+    with pytest.raises(ValueError, match="tensor 1 has moved"):
+        g.fp8g_grad_norm(lst, *one) if call == "norm" else g.fp8g_clip_grad_norm(lst, 1.0, one[0], 1e-6, one[1])
+
+
+def test_a_list_keeps_the_memory_that_it_names():
+    t = torch.zeros(64, 4).as_subclass(_Here)
+    lst, address = g.GradList([t]), t.data_ptr()
+    t.data = torch.zeros(64, 4)
+    assert [m.data_ptr() for m in lst.memory] == [address] != [t.data_ptr()]  # no later tensor can lie there
