@@ -535,7 +535,8 @@ int fp8g_grad_norm(const void* const* grads, const int64_t* numels, const int32_
  * fp8g_clip_grad_norm -- norm as fp8g_grad_norm, and out = grad * min(1, max_norm / (norm + eps)) for every tensor.
  *
  *   outs    HOST array of n device addresses, each of its gradient's size and type: either the gradient itself (in
- *           place, where nothing is written if nothing needs scaling) or memory that overlaps no gradient
+ *           place, where nothing is written if nothing needs scaling) or memory that overlaps no gradient.  No result
+ *           overlaps another one, so a gradient that is clipped in place is listed once.
  *   max_norm >= 0, eps >= 0.  A NaN norm makes every output NaN, an infinite one makes finite values 0.
  */
 int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,

@@ -428,6 +428,7 @@ class GradList:
         b = ctypes.c_int64()
         _check(lib().fp8g_grad_norm_workspace(n, ctypes.byref(b)), "fp8g_grad_norm_workspace")
         self.workspace_bytes = b.value
+        self.disjoint = False  # whether the results are known to be (see check_results)
 
     def __len__(self):
         return self.n
@@ -437,6 +438,25 @@ class GradList:
         if not _all_at(self.tensors, self.places, self.indices):
             i = next(i for i, t in enumerate(self.tensors) if t.data_ptr() != self.places[i]) % self.n
             _refuse(f"grads: tensor {i} has moved since it was listed")
+
+    def check_results(self) -> None:
+        """No result overlaps another one, or a gradient that is not its own: it would be scaled twice, or read while it
+        is written.  The places stay, so once is enough."""
+        spans = []
+        for t, at, to in zip(self.grads, self.ptrs, self.out_ptrs):
+            size = t.numel() * t.element_size()
+            if size:
+                spans.append((to, to + size, True))
+                if at != to:
+                    spans.append((at, at + size, False))
+        written = known = 0  # the ends of the results, and of all tensors, so far
+        for at, end, result in sorted(spans):
+            if at < (known if result else written):
+                _refuse("grads: a result overlaps another tensor of the list")
+            known = max(known, end)
+            if result:
+                written = max(written, end)
+        self.disjoint = True
 
 
 # Whether tensors[i].data_ptr() == places[i] for all indices i: on every call, so in one step where torch has it (300
@@ -479,8 +499,10 @@ def fp8g_clip_grad_norm(grads: GradList, max_norm: float, norm, eps: float = 1e-
 
 
 def _clip(g: GradList, max_norm: float, norm, eps: float, workspace) -> None:
-    """The list's check and the call."""
+    """The list's checks and the call."""
     g.check_places()
+    if not g.disjoint:
+        g.check_results()
     ws = _workspace_of(g, workspace)
     st = lib().fp8g_clip_grad_norm(g.ptrs, g.out_ptrs, g.numels, g.dtypes, g.n, max_norm, eps, norm.data_ptr(),
                                    ws.data_ptr(), ws.numel(), _on(norm, g.device_index))

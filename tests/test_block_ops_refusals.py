@@ -313,3 +313,47 @@ def test_a_list_keeps_the_memory_that_it_names():
     lst, address = g.GradList([t]), t.data_ptr()
     t.data = torch.zeros(64, 4)
     assert [m.data_ptr() for m in lst.memory] == [address] != [t.data_ptr()]  # no later tensor can lie there
+
+
+# ---- results that overlap another tensor of the list: scaled twice, or read while they are written
+
+def _overlap_lists():
+    a, b = _f32(64), _f32(64)
+    return {
+        "the same gradient twice, in place": ([a, a], None, True),
+        "views that share values, in place": ([a[:40], a[39:]], None, True),
+        "neighbouring views, in place": ([a[:40], a[40:]], None, False),
+        "a gradient twice, results apart": ([a, a], [b[:64], _f32(64)], False),
+        "one result for two gradients": ([a[:32], a[32:]], [b[:32], b[:32]], True),
+        "a result over another gradient": ([a[:32], a[32:]], [b[:32], a[:32]], True),
+        "a result over a part of its own gradient": ([a[:32]], [a[4:36]], True),
+        "in place beside apart": ([a[:32], a[32:]], [a[:32], b[:32]], False),
+        "an empty tensor anywhere": ([a, a[5:5]], None, False),
+    }
+
+
+@pytest.mark.parametrize("name", list(_overlap_lists()))
+def test_overlapping_results(name, monkeypatch):
+    from moe_grouped_gemm_block_gb300 import block_ops as bo
+    grads, out, refused = _overlap_lists()[name]
+    launched = []
+
+    class Lib:
+        def __getattr__(self, fn):
+            return lambda *a: launched.append(fn) or 0
+
+    monkeypatch.setattr(g, "_current_device", lambda: 0)
+    monkeypatch.setattr(bo, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(bo, "lib", Lib)
+    here = lambda ts: None if ts is None else [t.as_subclass(_Here) for t in ts]
+    lst = g.GradList(here(grads), here(out))
+    one = [_f32(1).as_subclass(_Here), torch.zeros(8, dtype=torch.uint8).as_subclass(_Here)]
+    g.fp8g_grad_norm(lst, *one)  # the norm alone writes to none of them
+    assert launched[-1] == "fp8g_grad_norm"
+    if refused:
+        with pytest.raises(ValueError, match="overlaps"):
+            g.fp8g_clip_grad_norm(lst, 1.0, one[0], 1e-6, one[1])
+    else:
+        g.fp8g_clip_grad_norm(lst, 1.0, one[0], 1e-6, one[1])
+        g.fp8g_clip_grad_norm(lst, 1.0, one[0], 1e-6, one[1])
+    assert ("fp8g_clip_grad_norm" in launched) is not refused
