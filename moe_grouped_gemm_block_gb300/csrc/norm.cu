@@ -16,9 +16,11 @@
 //   cta      forward, rows longer than the ring takes: a CTA per row, the row in registers
 //   scalar   rows that share no grid: a CTA per row (backward: resident), value by value in registers
 //   any      rows longer than those hold
-// The form follows from N, the types and the alignment alone, never from M: a row's result does not depend on how
-// many rows the call has.  (A CTA per row with all its threads on the sums, for few rows, would save less than a
-// microsecond of the kernel: 64 x 7168 bf16.)
+// The form follows from N, the types, the alignment and the strides, not from M, but that a single row has no stride.  So
+// on the 16-byte grid (N and the strides multiples of 8) a row's bits do not depend on how many rows the call has; off
+// it they also follow from where the row starts, (m ld) mod 8, and a row alone may take another form than among others.
+// (A CTA per row with all its threads on the sums, for few rows, would save less than a microsecond of the kernel:
+// 64 x 7168 bf16.)
 //
 // Bound by memory, and below some tens of MB by a call's fixed part (launch, weights, first rows, the last stores:
 // about 8 us of a ring, 11 backward with the joined sums).  Device times, and the share of the copy rate:

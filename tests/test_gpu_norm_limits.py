@@ -1,8 +1,8 @@
-"""Layer norm at the lengths next to its forms' limits, on the 16-byte grid and off it, contiguous and strided, where what
-lies beside a row (padding, the rows before and after it, what earlier kernels left in shared memory) is not finite.
+"""Layer norm at the lengths next to its forms' limits, on the 16-byte grid and off it, contiguous and strided, where
+what lies beside a row (padding, the rows before and after it, what earlier kernels left in shared memory) is not finite.
 
-The bounds are those of test_gpu_block_ops.py: k = (N / 256 + 16) u covers a sum's additions, and the variance's relative
-error is 2 k times the mean square of |x| + |mean| over the variance.
+The bounds are those of test_gpu_block_ops.py: k = (N / 256 + 16) u covers a sum's additions, and the variance's
+relative error is 2 k times the mean square of |x| + |mean| over the variance.
 """
 
 import numpy as np
@@ -112,9 +112,9 @@ def test_many_rows_and_in_place(M, N, xd):
     check_status()
 
 
-# The ring takes differences from K, the mean of a row's first n = 240 to 256 values, so (K - mean)^2 <= N / n variances:
-# the sums of squares are (1 + N / n) times the variance's own, and their roundings (k each, three of them: the squares'
-# sum and twice the first sum's) weigh as much more.
+# The ring takes differences from K, the mean of a row's first n = 240 to 256 values, so (K - mean)^2 <= N / n
+# variances: the sums of squares are (1 + N / n) times the variance's own, and their roundings (k each, three of them:
+# the squares' sum and twice the first sum's) weigh as much more.
 @pytest.mark.parametrize("N", [264, 1000, 1003, 4096, 4099, 8192, 12288, 16384])
 @pytest.mark.parametrize("xd", ["bf16", "f32"])
 @pytest.mark.parametrize("far", [50.0, -3000.0])
@@ -128,5 +128,22 @@ def test_rows_that_start_far_from_their_mean(N, xd, far):
     var_err = 3 * k * (1 + N / 240)
     _within(mean, rmean, k * np.abs(xn).mean(1) + 2 * k / rrstd * (1 + N / 240) ** 0.5, "f32", "mean")
     _within(rstd, rrstd, (k + var_err) * rrstd, "f32", "rstd")
-    _within(y, ry, _norm_bounds(xn, None, None, rmean, rrstd, N) + (2 * k * (1 + N / 240) ** 0.5) + np.abs(ry) * var_err,
-            xd, "y")
+    bound = _norm_bounds(xn, None, None, rmean, rrstd, N) + 2 * k * (1 + N / 240) ** 0.5
+    _within(y, ry, bound + np.abs(ry) * var_err, xd, "y")
+
+
+# on the 16-byte grid a row's bits do not depend on how many rows the call has (off it they may: a single row starts on
+# the grid whatever its stride)
+@pytest.mark.parametrize("N", [8, 64, 512, 520, 1024, 1032, 4096, 8192, 8200, 16384, 20000])
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("xd,yd", [("bf16", "bf16"), ("f32", "bf16")])
+def test_a_row_on_the_grid_alone_has_the_same_bits(N, pad, xd, yd):
+    x, _ = _strided((400, N), xd, pad, 0, 5, std=2.0, mean=0.5)
+    dy, _ = _strided((400, N), yd, pad, 0, 7, std=0.1)
+    w = _draw((N,), "f32", 2, 0.3, 1.0)
+    y, mean, rstd = g.layer_norm(x, w, out_dtype=DT[yd])
+    dx = g.layer_norm_backward(dy, x, w, mean, rstd)[0]
+    for M in (1, 2, 9):
+        some = g.layer_norm(x[:M], w, out_dtype=DT[yd])
+        assert all(torch.equal(a, b[:M]) for a, b in zip(some, (y, mean, rstd)))
+        assert torch.equal(g.layer_norm_backward(dy[:M], x[:M], w, mean[:M], rstd[:M])[0], dx[:M])
