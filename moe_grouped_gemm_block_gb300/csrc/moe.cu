@@ -44,7 +44,11 @@ __device__ __forceinline__ float recip_approx(float x) {  // 1 / x to one unit i
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// e^(v - mx) for v <= mx; the difference first, which cannot overflow to anything but -inf.
+// e^(v - mx) for v <= mx; the difference d first, which cannot overflow to anything but -inf.  The exponent d log2(e) is
+// rounded, so the result's relative error grows with the distance from the row's largest: (1.3 |d| + 4) 2^-24, beside
+// the |d| 2^-24 that the difference's own rounding is worth where the logits are fp32.  A choice for speed: with the
+// product's remainder multiplied in again (two fused multiply-adds, and a clamp of d so that -inf leaves no NaN) the
+// error stays near 4 2^-24, but 65536 x 256 takes 39.1 us instead of 37.7 (bf16) and 49.2 instead of 47.2 (fp32).
 __device__ __forceinline__ float exp_below(float v, float mx) { return exp2_approx((v - mx) * 1.4426950408889634f); }
 // The same for all of f, in place, and their sum.
 template <int H>

@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(1024) layer_norm_cta_kernel(const NormArgs a) 
 // ring form.  A sum warp takes the differences from K, the mean of the row's first whole vectors (of its CTA's share; 32,
 // or 30 at the least): variance = mean (x - K)^2 - (mean (x - K))^2 then loses little to cancellation, as (K - mean)^2 is
 // at most N / 240 variances whatever the values.  Nothing but the row's own values may enter K: a neighbour's could be
-// anything.
+// anything.  The root is rsqrtf's, two units in the last place at most, which is less than the sums' own roundings (with
+// IEEE roots 8000 x 12001 bf16 takes 88 us instead of 84).
 template <typename TX, typename TY, int CL, bool SHIFT>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const NormArgs a, int32_t stages,
                                                                              int32_t stage_bytes, int32_t column_warps,
