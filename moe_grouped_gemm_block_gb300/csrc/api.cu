@@ -120,6 +120,11 @@ long long wait_budget_cycles() {
   return budget;
 }
 
+int test_skip_stage() {
+  const char* e = std::getenv("FP8G_TEST_SKIP_STAGE");
+  return e ? std::atoi(e) : -1;
+}
+
 }  // namespace fp8g
 
 extern "C" int fp8g_get_status(void* stream) {

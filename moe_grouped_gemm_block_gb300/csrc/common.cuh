@@ -33,6 +33,9 @@ int allow_shared_memory(const void* kernel, size_t bytes);
 
 // Cycle budget of every device-side wait (clock64 ticks).  FP8G_WAIT_BUDGET_CYCLES overrides.
 long long wait_budget_cycles();
+// FP8G_TEST_SKIP_STAGE=<n> (tests only, read on every call; -1 without): every CTA's producer leaves its stage n
+// unfilled, so that the waits for it run out (see GemmArgs::test_skip_stage, and NormArgs::skip for the layer norm's).
+int test_skip_stage();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1581,13 +1581,6 @@ bool sk_workspace(int dev, int sm_count, cudaStream_t stream, float4** part, uin
   return true;
 }
 
-// FP8G_TEST_SKIP_STAGE=<n> (tests only, read on every call): the producer of every CTA leaves its
-// stage n unfilled, so the issuer's wait for it runs out (see GemmArgs::test_skip_stage).
-int env_test_skip_stage() {
-  const char* e = std::getenv("FP8G_TEST_SKIP_STAGE");
-  return e ? std::atoi(e) : -1;
-}
-
 // Raster band height (m-blocks).  Tiles run m-block fastest within a band of m-blocks and n-block
 // by n-block, so the CTAs in flight share the band's A rows and a few B column blocks in L2.
 //   Dense: when all of A fits well inside L2 (<= 48 MB) the band is all of M, so each B column
@@ -1775,7 +1768,7 @@ int run_gemm(const Operands& o, cudaStream_t stream, bool no_alloc = false) {
   a.sb_step = o.sb_step;
   a.idesc_fmt = o.idesc_fmt;
   a.ld_sb = o.ld_sb;
-  a.test_skip_stage = env_test_skip_stage();
+  a.test_skip_stage = test_skip_stage();
   a.band_m = band_rows(a.num_m, o.K, MODE == kDenseSmallM ? kDense : MODE);
   if (MODE == kKGrouped) a.num_tiles = static_cast<int32_t>(o.E) * a.num_m * a.num_n;
   if (swap) {

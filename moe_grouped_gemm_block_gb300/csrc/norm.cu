@@ -199,22 +199,24 @@ struct RingShared {
 };
 
 // Waits for a barrier's phase, at most `budget` cycles; past that it records the status and nobody in the CTA waits
-// any more (the results are void, the kernel ends).  CLUSTER: what the other CTA wrote before it arrived is seen too.
+// any more (the results are void, the kernel ends).  False: the phase is not complete.  CLUSTER: what the other CTA wrote
+// before it arrived is seen too.
 template <bool CLUSTER = false>
-__device__ __forceinline__ void ring_wait(uint64_t* bar, uint32_t parity, long long budget, unsigned int* status,
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, long long budget, unsigned int* status,
                                           volatile int* dead) {
   const uint32_t b = smem_u32(bar);
   auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity); };
-  if (done()) return;
+  if (done()) return true;
   const long long t0 = clock64();
   while (!done()) {
-    if (*dead) return;
+    if (*dead) return false;
     if (clock64() - t0 > budget) {
       *dead = 1;
       record_status(status, FP8G_ERR_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 // Whether a wait has run out, the same answer in all of a warp.  The sum warps leave then: no barrier is told twice in
 // a phase what to expect.
@@ -290,9 +292,10 @@ __device__ __forceinline__ void ring_tell(RingShared& sm, int s, int rank) {
 }
 
 // The copying thread: row after row into the ring, each stage once it is empty.  `load` copies row i into stage s and
-// returns nothing; after a wait that ran out it stops, and waits once more (as long) for copies on their way.
+// returns nothing.  In the end, and where a wait has run out, it waits (with the same limit) for the copies on their way:
+// none may land once the CTA has left.  `skip`: see NormArgs.
 template <int CL, typename Load>
-__device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, int rank, long long budget,
+__device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages, int rank, int skip, long long budget,
                                             unsigned int* status, Load load) {
   int s = 0, i = 0;
   uint32_t parity = 1;  // the first round of `empty` counts as complete
@@ -302,17 +305,27 @@ __device__ __forceinline__ void ring_copies(RingShared& sm, int rows, int stages
       if (*const_cast<volatile int*>(&sm.dead)) break;
       if (CL > 1 && stages <= kRingFewStages) ring_tell(sm, s, rank);
     }
-    load(i, s);
+    if (i != skip) load(i, s);
     if (++s == stages) {
       s = 0;
       parity ^= 1u;
     }
   }
-  if (!*const_cast<volatile int*>(&sm.dead)) return;
   const long long t0 = clock64();
   for (int k = max(0, i - stages); k < i; ++k)
     while (!mbar_try_wait(smem_u32(&sm.full[k % stages]), (k / stages) & 1) && clock64() - t0 <= budget) {
     }
+}
+// The end of a cluster's CTA: neither leaves while the other may still write to it.  Where a wait has run out, sums may be
+// on their way that nobody waits for (their arrival can be seen by their receiver alone): they get 2^17 cycles, some 60
+// us, to land.
+__device__ __forceinline__ void ring_leave_cluster(const RingShared& sm) {
+  if (ring_dead(sm)) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1 << 17)) {
+    }
+  }
+  cluster_sync();
 }
 
 // A sum warp hands its row, of the ring's round `round`, on: its sums to every CTA of the cluster.
@@ -327,12 +340,16 @@ __device__ __forceinline__ void ring_ready(RingShared& sm, int s, int round, int
     }
   } else {
     if (lane == 0) mbar_arrive_expect_tx(true, smem_u32(&sm.ready[s]), CL * 16);
-    if (round > 0) ring_wait<true>(&sm.peer[s], (round - 1) & 1, budget, status, &sm.dead);
+    if (round > 0 && !__all_sync(0xffffffffu, ring_wait<true>(&sm.peer[s], (round - 1) & 1, budget, status, &sm.dead)))
+      return;
     if (lane < CL)
       st_async4(mapa_shared(smem_u32(&sm.slot[s][rank]), lane), v, mapa_shared(smem_u32(&sm.ready[s]), lane));
   }
 }
-// A column warp has read the stage and the slot.
+// A column warp has read the stage and the slot.  (Where a wait has run out the column warps go through their remaining
+// rows, whose values are void, without waiting: leaving the loop would take an answer that a whole warp agrees on in every
+// row, and that holds up the lanes that have done with their last row for those that still store its ragged vectors:
+// 8000 x 12001 bf16 forward 84 us, 88 so.)
 __device__ __forceinline__ void ring_empty(RingShared& sm, int s) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.empty[s]));
@@ -350,6 +367,8 @@ struct NormArgs {
   int64_t M, ldx, ldy;
   int32_t N, w_kind;
   float eps;
+  // Test hook, -1 normally: the ring's copying thread leaves out its row number `skip`, so that the waits for it run out.
+  int32_t skip;
   unsigned int* status;
   long long budget;
 };
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
   else cluster_sync();  // every CTA of the cluster runs before it is written to
   if (warp == column_warps + sum_warps) {
     if (lane == 0)
-      ring_copies<CL>(sm, rows, stages, rank, a.budget, a.status, [&](int i, int s) {
+      ring_copies<CL>(sm, rows, stages, rank, a.skip, a.budget, a.status, [&](int i, int s) {
         const int64_t m = first + static_cast<int64_t>(i) * P;
         const uint32_t bar = smem_u32(&sm.full[s]);
         const uint32_t bytes = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8 * sizeof(TX);
@@ -632,7 +651,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_ring_kernel(const 
       }
     }
   }
-  if constexpr (CL > 1) cluster_sync();  // nobody leaves while another CTA may still write to it
+  if constexpr (CL > 1) ring_leave_cluster(sm);
 }
 
 // scalar form: thread t holds the values t, t + blockDim.x, ...
@@ -716,6 +735,7 @@ struct NormGrad {  // arguments of every backward form
   float* parts;  // each CTA's or cluster's sums of dy h and of dy (see Parts); null where none are wanted
   int64_t M, lddy, ldx, lddx;
   int32_t N, w_kind;
+  int32_t skip;  // see NormArgs
   unsigned int* status;
   long long budget;
 };
@@ -906,7 +926,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
   const float inv_n = 1.0f / static_cast<float>(a.N);
   if (warp == column_warps + sum_warps) {
     if (lane == 0)
-      ring_copies<CL>(sm, rows, stages, rank, a.budget, a.status, [&](int i, int s) {
+      ring_copies<CL>(sm, rows, stages, rank, a.skip, a.budget, a.status, [&](int i, int s) {
         const int64_t m = first + static_cast<int64_t>(i) * P;
         const uint32_t bar = smem_u32(&sm.full[s]), dst = smem_u32(ring) + s * stage_bytes;
         const uint32_t n = static_cast<uint32_t>(copied(shape, share, m + 1 == a.M)) * 8;
@@ -1058,7 +1078,7 @@ __global__ void __launch_bounds__(kRingGradThreads, 1) layer_norm_grad_ring_kern
       }
     }
   }
-  if constexpr (CL > 1) cluster_sync();  // nobody leaves while another CTA may still write to it
+  if constexpr (CL > 1) ring_leave_cluster(sm);
 }
 
 // scalar form: resident CTAs, thread t holds the columns t, t + blockDim.x, ...
@@ -1455,7 +1475,7 @@ extern "C" int fp8g_layer_norm(const void* x, int32_t x_dtype, int64_t M, int64_
   a.x = x, a.y = y, a.w = weight, a.b = bias, a.mean = mean, a.rstd = rstd;
   a.M = M, a.ldx = ldx, a.ldy = ldy;
   a.N = static_cast<int32_t>(N), a.w_kind = w_dtype, a.eps = eps;
-  a.status = dev->status, a.budget = wait_budget_cycles();
+  a.status = dev->status, a.budget = wait_budget_cycles(), a.skip = test_skip_stage();
   return go(a, dev, static_cast<cudaStream_t>(stream));
 }
 
@@ -1503,6 +1523,6 @@ extern "C" int fp8g_layer_norm_backward(const void* dy, int32_t dy_dtype, int64_
   a.parts = dweight || dbias ? static_cast<float*>(workspace) : nullptr;
   a.M = M, a.lddy = lddy, a.ldx = ldx, a.lddx = lddx;
   a.N = static_cast<int32_t>(N), a.w_kind = w_dtype;
-  a.status = dev->status, a.budget = wait_budget_cycles();
+  a.status = dev->status, a.budget = wait_budget_cycles(), a.skip = test_skip_stage();
   return go(a, dweight, dbias, dev, s);
 }
