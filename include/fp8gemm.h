@@ -474,7 +474,8 @@ int fp8g_moe_gate(const void* logits, int32_t dtype, int64_t T, int32_t E, int64
  *     if renormalize;   dlogits[t, e] = p[t, e] * (G[t, e] - sum_e' G[t, e'] * p[t, e'])
  *
  *   logits, dtype, T, E, ldl, topk, renormalize, token_mask, loss_coef, topk_ids, counts  as in the forward call
- *   (Tv is the sum of counts over topk).  Masked tokens get zeros.  Ids outside [0, E) have no gradient.
+ *   (Tv is the sum of counts over topk; a row's ids are distinct).  Masked tokens get zeros.  Ids outside [0, E) have no
+ *   gradient.
  *   dweights  fp32 [T, topk] or null (0);  dloss  fp32 [1], device memory, or null (0)
  *   dlogits   [T, E] (dtype), row stride ldd >= E; may be logits itself
  */
