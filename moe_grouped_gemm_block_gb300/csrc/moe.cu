@@ -44,13 +44,21 @@ __device__ __forceinline__ float recip_approx(float x) {  // 1 / x to one unit i
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// e^(v - mx) for v <= mx; the difference d first, which cannot overflow to anything but -inf.  The exponent d log2(e) is
-// rounded, so the result's relative error grows with the distance from the row's largest: (1.3 |d| + 4) 2^-24, beside
-// the |d| 2^-24 that the difference's own rounding is worth where the logits are fp32.  A choice for speed: with the
-// product's remainder multiplied in again (two fused multiply-adds, and a clamp of d so that -inf leaves no NaN) the
-// error stays near 4 2^-24, but 65536 x 256 takes 39.1 us instead of 37.7 (bf16) and 49.2 instead of 47.2 (fp32).
-__device__ __forceinline__ float exp_below(float v, float mx) { return exp2_approx((v - mx) * 1.4426950408889634f); }
-// The same for all of f, in place, and their sum.
+// e^(v - mx) for v <= mx, for a row's selected experts; the difference d first, which cannot overflow to anything but -inf.
+// The exponent d log2(e) is rounded, to t: what e^d differs from 2^t by, e^(d - t ln 2), is multiplied in again, so the
+// relative error stays near the 2^-22 of exp2_approx however far v lies below mx (65536 x 256 bf16: 37.9 us, without it
+// 37.5).  d is held above -200, where the result is 0 anyway, so that the remainder of -inf is finite; a NaN stays one.
+__device__ __forceinline__ float exp_below(float v, float mx) {
+  constexpr float kLn2 = 0.693147182464599609375f, kLn2Rest = -1.9046542e-9f;  // their sum is ln 2
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v - mx), "f"(-200.0f));
+  const float t = d * 1.4426950408889634f, y = exp2_approx(t);
+  return fmaf(y, fmaf(-t, kLn2Rest, fmaf(-t, kLn2, d)), y);
+}
+// The same for all of f, in place, and their sum, without the remainder: a result's relative error grows with the distance
+// from the row's largest, (1.3 |d| + 4) 2^-24, which the sum, weighted by the results themselves, does not feel.  A choice
+// for speed: with the remainder (two fused multiply-adds, and the clamp) 65536 x 256 forward takes 39.1 us instead of
+// 37.7 (bf16) and 49.2 instead of 47.2 (fp32).
 template <int H>
 __device__ __forceinline__ float exp_below(float2 (&f)[H], float mx) {
   const float2 m = make_float2(-mx, -mx), k = make_float2(1.4426950408889634f, 1.4426950408889634f);
