@@ -20,7 +20,10 @@
  *                  fp8_grouped_gemm_wgrad
  *   training operators around the grouped GEMMs (bf16 / fp32)
  *                  fp8g_layer_norm, fp8g_layer_norm_backward, fp8g_moe_gate, fp8g_moe_gate_backward,
- *                  fp8g_moe_combine, fp8g_moe_combine_backward, fp8g_grad_norm, fp8g_clip_grad_norm
+ *                  fp8g_moe_combine, fp8g_moe_combine_backward, fp8g_grad_norm, fp8g_clip_grad_norm,
+ *                  fp8g_moe_route, fp8g_moe_route_backward, fp8g_residual_rms_norm,
+ *                  fp8g_residual_rms_norm_backward, fp8_swiglu_quantize_1x128, fp8_swiglu_quantize_1x128_masked,
+ *                  fp8g_swiglu_backward, fp8g_adamw
  *   status         fp8g_get_status, fp8g_status_string, fp8g_selftest_bounded_waits, fp8g_last_config,
  *                  fp8g_last_split, fp8g_last_swap_ab, fp8g_last_cluster_k
  *
@@ -543,6 +546,178 @@ int fp8g_grad_norm(const void* const* grads, const int64_t* numels, const int32_
 int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes,
                         int32_t n, float max_norm, float eps, float* norm, void* workspace,
                         int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8g_moe_route -- the router with a choice of scores, a bias for balance and expert groups.
+ *     s[t] = sigmoid(logits[t]) (score 0) or softmax(logits[t]) (score 1);  c[t, e] = s[t, e] + bias[e]
+ *     The experts lie in `groups` equal groups, one after another; a group's score is the sum of its two largest c (its
+ *     one, where it has one).  The topk_groups best groups stay, ties to the lower group.
+ *     topk_ids[t] = the topk largest c among their experts, in descending order, ties to the lower index.  Without a bias
+ *     experts are ordered by their logits, as their scores are.
+ *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where it is 0)
+ *     counts[e] = how many (t, j) of the unmasked tokens chose e
+ * The choice is that of scores in 64 bits.  The bias takes part in the choice alone; a program balances its experts by
+ * moving it after each step, up where counts lie below their mean and down where above.
+ *
+ *   logits      [T, E] (dtype), row stride ldl elements (ldl >= E).  -inf rules an expert out whatever its bias, and so
+ *               does a bias of -inf: it adds nothing to its group's score (a group of nothing else scores -inf) and is
+ *               taken, with weight 0, only where the groups that stay have fewer than topk others.  A NaN ranks first, so
+ *               the ids stay in range; its weight is NaN.
+ *   bias        fp32 [E] or null (0)
+ *   token_mask  bytes [T] or null: 0 = a padding token, which gets ids like any other and weights 0, and is not counted
+ *   topk_ids    int32 [T, topk], topk_weights fp32 [T, topk], counts int32 [E]
+ *   0 <= T < 2^31 (T == 0: counts are zeros), 1 <= E <= 2048, 1 <= groups <= 32 dividing E, 1 <= topk_groups <= groups,
+ *   1 <= topk <= min(32, topk_groups * E / groups), T * topk < 2^31, renormalize 0 or 1, scale not NaN.  Pointers aligned to
+ *   their element.
+ */
+int fp8g_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl, int32_t topk,
+                   const float* bias, int32_t score, int32_t groups, int32_t topk_groups, int32_t renormalize,
+                   float scale, const uint8_t* token_mask, int32_t* topk_ids, float* topk_weights,
+                   int32_t* counts, void* stream);
+
+/*
+ * fp8g_moe_route_backward -- the gradient of topk_weights with respect to the logits, the choice held fixed:
+ *     d[t, j] = scale * dweights[t, j];  if renormalize, with S = sum_i s[t, topk_ids[t, i]]:
+ *     d[t, j] = (d[t, j] - sum_i d[t, i] s[t, topk_ids[t, i]] / S) / S  (0 where S is 0)
+ *     G[t, e] = sum_j [topk_ids[t, j] == e] d[t, j]
+ *     dlogits[t, e] = G s (1 - s) (sigmoid), or s[t, e] (G[t, e] - sum_e' G[t, e'] s[t, e']) (softmax)
+ *
+ *   logits ... token_mask, topk_ids as in the forward call.  Masked tokens get zeros.  Ids outside [0, E) have no
+ *   gradient and no part in S.  (An expert that a bias of -inf ruled out and that was taken for want of others is
+ *   differentiated as if it had been chosen.)
+ *   dweights  fp32 [T, topk];  dlogits  [T, E] (dtype), row stride ldd >= E; may be logits itself (with the same stride)
+ */
+int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl, int32_t topk,
+                            int32_t score, int32_t renormalize, float scale, const uint8_t* token_mask,
+                            const int32_t* topk_ids, const float* dweights, void* dlogits, int64_t ldd,
+                            void* stream);
+
+/*
+ * fp8g_residual_rms_norm -- the norms after a block and before the next one, with the residual between them:
+ *     u = f * rstd_f * post_weight,  rstd_f[m] = 1 / sqrt(sum_n f^2 / N + eps)   (post_norm 1), or u = f (post_norm 0)
+ *     h = x + scale * gate * u
+ *     y = h * rstd * weight,  rstd[m] = 1 / sqrt(sum_n h^2 / N + eps)
+ *
+ *   x, h     [M, N] (stream_dtype): the residual stream before and after the block, row strides ldx, ldh; h may be x
+ *            itself, or null
+ *   f, y     [M, N] (block_dtype): what the block gave and what the next one takes, row strides ldf, ldy.  f null: there
+ *            is no block, h = x (and no post_norm, gate or h is given).  y null: h alone is wanted.
+ *   weight, post_weight, gate  [N], all of type w_dtype, each may be null (1); post_weight only with post_norm
+ *   rstd_f, rstd  fp32 [M], for the backward call; either may be null
+ *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31 - 15, eps >= 0.  Strides are in elements and at least N, pointers aligned to
+ *   their element; rows on the 16-byte grid (bases, strides and N multiples of 8 values) take the faster paths.
+ *   Squares are summed in fp32: beyond values of about 1e19 a row's rstd is 0.
+ */
+int fp8g_residual_rms_norm(const void* x, int64_t ldx, const void* f, int64_t ldf, int32_t stream_dtype,
+                           int32_t block_dtype, int64_t M, int64_t N, int32_t post_norm,
+                           const void* post_weight, const void* gate, float scale, const void* weight,
+                           int32_t w_dtype, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
+                           float* rstd_f, float* rstd, void* stream);
+
+/* fp8g_residual_rms_norm_backward_workspace -- scratch bytes of the backward call with dweight, dgate or dpost. */
+int fp8g_residual_rms_norm_backward_workspace(int64_t M, int64_t N, int64_t* bytes);
+
+/*
+ * fp8g_residual_rms_norm_backward -- with e = h * rstd, g = dy * weight, k = f * rstd_f (or f without post_norm):
+ *     dx = dh + rstd * (g - e * sum_n (g * e) / N),  q = dx * scale * gate * post_weight
+ *     df = rstd_f * (q - k * sum_n (q * k) / N)  (or q without post_norm)
+ *     dweight = sum_m dy * e,  dgate = scale * post_weight * sum_m dx * k,  dpost = scale * gate * sum_m dx * k
+ *
+ *   dy       [M, N] (block_dtype): the gradient of y, or null (0; then h, rstd and dweight are not used or given)
+ *   dh       [M, N] (stream_dtype): what reaches h on other ways, or null (0); not both null
+ *   h, f, rstd_f, rstd, weights  as the forward call had and wrote them.  f may be null where there was none, or where
+ *            neither post_norm nor dgate needs it.
+ *   dx       [M, N] (stream_dtype), may be dh itself; df  [M, N] (block_dtype), or null where there was no f
+ *   dweight, dgate, dpost  fp32 [N], overwritten (M == 0: zeros), each may be null; dgate and dpost only with a gate and a
+ *            post_weight.  Where all are null no workspace is needed and it may be null.
+ *   Sizes and alignment as in the forward call.
+ */
+int fp8g_residual_rms_norm_backward(
+    const void* dy, int64_t lddy, const void* dh, int64_t lddh, const void* h, int64_t ldh, const void* f,
+    int64_t ldf, int32_t stream_dtype, int32_t block_dtype, int64_t M, int64_t N, int32_t post_norm,
+    const void* post_weight, const void* gate, float scale, const void* weight, int32_t w_dtype,
+    const float* rstd_f, const float* rstd, void* dx, int64_t lddx, void* df, int64_t lddf, float* dweight,
+    float* dgate, float* dpost, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8_swiglu_quantize_1x128 -- the gated activation between an expert's two matrix products, quantised for the second:
+ *     h[m, n] = g s(g) u,  g = gu[m, n],  u = gu[m, F + n],  s(g) = 1 / (1 + e^-g)  (0 where below 2^-126)
+ *     codes and scales of h in 1x128 blocks as fp8_quantize_1x128 writes them, formed from the fp32 h; h itself in bf16
+ *
+ *   gu    bf16 [M, 2F], row stride ldgu elements (>= 2F, % 8): a product whose first F columns are the gates
+ *   q     e4m3 [M, F], row stride ldq bytes (>= F, % 16), or null;  sA  fp32 [F/128][ld_sa] (ld_sa >= M, % 4)
+ *   h     bf16 [M, F], row stride ldh (>= F, % 8), or null; not both null
+ *   M >= 0 (M == 0: no-op), F % 128 == 0 (without q: F % 8 == 0), M * ceil(F/128) < 2^31.  Pointers 16-byte aligned.
+ */
+int fp8_swiglu_quantize_1x128(const void* gu, int64_t M, int64_t F, int64_t ldgu, void* q, int64_t ldq,
+                              float* sA, int64_t ld_sa, void* h, int64_t ldh, void* stream);
+
+/*
+ * fp8_swiglu_quantize_1x128_masked -- the same for the masked layout: gu [E, cap, 2F] and q [E, cap, F] contiguous, only
+ * rows m < masked_m[e] of each expert (int32 [E], DEVICE memory, clamped to [0, cap]); the others of q and their
+ * scales are left as they are.  sA  fp32 [F/128][ld_sa] with row index e*cap + m (ld_sa >= E*cap, % 4).
+ *   1 <= E <= 65535, cap >= 0 (cap == 0: no-op), F % 128 == 0, E*cap*(F/128) < 2^31.  gu, q, sA 16-byte aligned.
+ */
+int fp8_swiglu_quantize_1x128_masked(const void* gu, int32_t E, int64_t cap, int64_t F, const int32_t* masked_m,
+                                     void* q, float* sA, int64_t ld_sa, void* stream);
+
+/*
+ * fp8g_swiglu_backward -- dgu[m, n] = dh u s(g) (1 + g (1 - s(g))),  dgu[m, F + n] = dh g s(g);  h again, for the second
+ * product's weight gradient.
+ *
+ *   dh    bf16 [M, F], row stride lddh;  gu  bf16 [M, 2F], row stride ldgu
+ *   dgu   bf16 [M, 2F], row stride lddgu; may be gu itself (with the same stride);  h  bf16 [M, F], row stride ldh, or
+ *         null
+ *   M >= 0 (M == 0: no-op), F % 8 == 0, M * F / 8 < 2^31.  Pointers 16-byte aligned, strides multiples of 8.
+ */
+int fp8g_swiglu_backward(const void* dh, int64_t lddh, const void* gu, int64_t M, int64_t F, int64_t ldgu, void* dgu,
+                         int64_t lddgu, void* h, int64_t ldh, void* stream);
+
+/* A tensor of fp8g_adamw: DEVICE addresses of `numel` contiguous values each. */
+typedef struct {
+  void* param;        /* param_dtype */
+  const void* grad;   /* grad_dtype */
+  void* m;            /* fp32, or e4m3 codes (state_bits 8) */
+  void* v;            /* fp32 second moments, or e4m3 codes of their roots */
+  float* m_scale;     /* state_bits 8: fp32 [ceil(numel / 128)]; else ignored */
+  float* v_scale;
+  float* master;      /* fp32 copy of a bf16 param, or null */
+  int64_t numel;
+  float weight_decay; /* >= 0 */
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t reserved;
+} fp8g_adamw_tensor;
+
+#define FP8G_ADAMW_WORKSPACE 64 /* bytes of fp8g_adamw's workspace */
+
+/*
+ * fp8g_adamw -- one AdamW step over n tensors.  With t = step[0] + 1, which step[0] becomes:
+ *     coef = min(1, max_norm / (norm[0] + norm_eps)), or 1 without norm;  g = coef * grad
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p - lr * (weight_decay * p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * in fp32; p is the param, or its master copy, of which the param then is the rounding.
+ * Where norm is given and is not finite the step is left out: nothing changes, step[0] neither.
+ *
+ * state_bits 8: m and the root of v are held as e4m3 codes with one scale, amax * (1 / 448), for each 128 values (a
+ * tensor's blocks start at its first value; scale 0 and codes of 0 where amax < 2^-60).  The step uses the unrounded new
+ * states; they are then taken to one of the two codes next to them: with y = |x| * (448 * (1 / amax)) between the codes a <= y < b of
+ * value i of its tensor, up where (y - a) / (b - a) + u >= 1, u = floor(((i * 0xC13FA9A9 + t * 0x91E10DA5 + z) mod 2^32) /
+ * 2^12) / 2^20, z = 0 (m) or 2^31 (the root), which is right on the average of the steps; a root > 0 becomes at least
+ * the lowest code.
+ *
+ *   tensors   HOST array, read during the call only; the addresses travel as kernel arguments, so a captured graph keeps
+ *             them.  Empty tensors (numel 0) may hold nulls.  No written tensor overlaps another one of the list.
+ *   lr        >= 0; lr_dev  fp32 [1], device memory, read instead where it is not null
+ *   step      int64 [1], device memory: the steps taken so far (>= 0).  A replayed graph counts on.
+ *   norm      fp32 [1], device memory, as fp8g_grad_norm wrote it, or null (max_norm and norm_eps are then ignored)
+ *   workspace FP8G_ADAMW_WORKSPACE bytes, 16-byte aligned, of calls that do not overlap in time
+ *   0 <= beta1, beta2 < 1, eps >= 1e-30, max_norm, norm_eps >= 0, n <= 2^20, at most 2^40 values.  Pointers aligned to their
+ *   element; tensors on 16-byte boundaries (codes: 8) take the faster path.  Gradients are finite, or norm is given.
+ */
+int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t state_bits, double lr, const float* lr_dev,
+               double beta1, double beta2, double eps, int64_t* step, const float* norm, float max_norm,
+               float norm_eps, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * fp8g_get_status -- synchronise `stream`, then return and clear the current

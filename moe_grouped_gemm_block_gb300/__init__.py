@@ -22,7 +22,8 @@ functions here carry the same names and take torch tensors:
 
 The training operators around the grouped GEMMs, on bf16 and fp32 tensors (``block_ops.py``): ``layer_norm``,
 ``moe_gate`` (top-k, counts and balance loss), ``moe_combine``, their ``_backward`` calls, ``grad_norm`` and
-``clip_grad_norm``.
+``clip_grad_norm``; and those of whole MoE blocks (``train_ops.py``): ``moe_route`` (bias and expert groups),
+``residual_rms_norm``, ``swiglu_quantize_1x128``, their ``_backward`` calls, and ``adamw_step`` over an ``AdamWList``.
 
 e4m3 tensors may be torch.uint8 or torch.float8_e4m3fn.  Work is enqueued on the
 current CUDA stream of the tensors' device, which has to be the current device.  A non-zero status raises Fp8GemmError.
@@ -58,6 +59,7 @@ class Fp8GemmError(RuntimeError):
 _lib = None
 
 _I64, _I32, _P, _FP, _F32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float
+_F64 = ctypes.c_double
 _SIGNATURES = {
     "fp8_quantize_1x128": [_P, _I64, _I64, _I64, _P, _I64, _FP, _I64, _P],
     "fp8_quantize_128x128": [_P, _I64, _I64, _I64, _P, _FP, _P],
@@ -89,6 +91,17 @@ _SIGNATURES = {
     "fp8g_grad_norm_workspace": [_I32, ctypes.POINTER(ctypes.c_int64)],
     "fp8g_grad_norm": [_P, _P, _P, _I32, _FP, _P, _I64, _P],
     "fp8g_clip_grad_norm": [_P, _P, _P, _P, _I32, _F32, _F32, _FP, _P, _I64, _P],
+    "fp8g_moe_route": [_P, _I32, _I64, _I32, _I64, _I32, _FP, _I32, _I32, _I32, _I32, _F32, _P, _P, _FP, _P, _P],
+    "fp8g_moe_route_backward": [_P, _I32, _I64, _I32, _I64, _I32, _I32, _I32, _F32, _P, _P, _FP, _P, _I64, _P],
+    "fp8g_residual_rms_norm": [_P, _I64, _P, _I64, _I32, _I32, _I64, _I64, _I32, _P, _P, _F32, _P, _I32, _F32, _P, _I64,
+                               _P, _I64, _FP, _FP, _P],
+    "fp8g_residual_rms_norm_backward_workspace": [_I64, _I64, ctypes.POINTER(ctypes.c_int64)],
+    "fp8g_residual_rms_norm_backward": [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I64, _I64, _I32, _P, _P, _F32,
+                                        _P, _I32, _FP, _FP, _P, _I64, _P, _I64, _FP, _FP, _FP, _P, _I64, _P],
+    "fp8_swiglu_quantize_1x128": [_P, _I64, _I64, _I64, _P, _I64, _FP, _I64, _P, _I64, _P],
+    "fp8_swiglu_quantize_1x128_masked": [_P, _I32, _I64, _I64, _P, _P, _FP, _I64, _P],
+    "fp8g_swiglu_backward": [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P],
+    "fp8g_adamw": [_P, _I32, _I32, _F64, _FP, _F64, _F64, _F64, _P, _FP, _F32, _F32, _P, _I64, _P],
     "fp8g_selftest_bounded_waits": [_I64, _P, _P],
     "fp8g_get_status": [_P],
     "fp8g_last_config": [ctypes.POINTER(ctypes.c_int)] * 3,
@@ -563,3 +576,7 @@ from .block_ops import (  # noqa: E402 -- they use the helpers above
     GradList, clip_grad_norm, fp8g_clip_grad_norm, fp8g_grad_norm, fp8g_layer_norm, fp8g_layer_norm_backward,
     fp8g_moe_combine, fp8g_moe_combine_backward, fp8g_moe_gate, fp8g_moe_gate_backward, grad_norm, layer_norm,
     layer_norm_backward, moe_combine, moe_combine_backward, moe_gate, moe_gate_backward)
+from .train_ops import (  # noqa: E402
+    AdamWList, adamw_step, fp8_swiglu_quantize_1x128, fp8_swiglu_quantize_1x128_masked, fp8g_adamw, fp8g_moe_route,
+    fp8g_moe_route_backward, fp8g_residual_rms_norm, fp8g_residual_rms_norm_backward, fp8g_swiglu_backward, moe_route,
+    moe_route_backward, residual_rms_norm, residual_rms_norm_backward, swiglu, swiglu_backward, swiglu_quantize_1x128)

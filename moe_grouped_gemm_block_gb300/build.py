@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfp8gemm.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "noalloc.cu", "norm.cu", "moe.cu", "clip.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "noalloc.cu", "norm.cu", "moe.cu", "clip.cu", "route.cu",
+           "resnorm.cu", "swiglu.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,351 @@
+// adamw.cu -- one AdamW step over many tensors, with states in 32 or in 8 bits.
+//
+//     g = coef grad,   coef = min(1, max_norm / (norm + norm_eps))  (1 without a norm)
+//     m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,   c1 = 1 - b1^t,   c2 = 1 - b2^t
+//     p = p - lr (decay p + (m / c1) / (sqrt(v / c2) + eps))
+//
+// in fp32 whatever the types; p is the tensor itself or its fp32 master copy, whose rounding the tensor then gets.
+//
+// States in 8 bits are e4m3 codes with one fp32 scale, amax (1 / 448), for each 128 consecutive values, as the quantisers
+// of the GEMMs' operands have them: m itself, and the root of v (e4m3's range, 2^17, is then that of the gradients and
+// not of their squares).  The step itself uses the new m and v before they are rounded.  Two things differ from a GEMM
+// operand's rounding.  To the nearest, a state that changes by less than half a step (3 to 6% of itself) at a time would
+// never change: with b2 = 0.999 a root follows no fall of its gradients.  So a value goes up where its place between
+// two codes and a number in [0, 1) are 1 or more together; the numbers run through an evenly spread sequence in the
+// steps and the places of the tensor, (place A + step B) mod 2^32, so that a state is right on the average of a few
+// steps and a call is repeatable.  And a root that is not 0 keeps the lowest code where it would round to 0: it is then
+// too large, which makes a step too small, never too large.  A block whose largest is below 2^-60 becomes 0.
+//
+// Bound by memory.
+
+#include <algorithm>
+#include <cmath>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace fp8g {
+namespace {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamPass = kAdamThreads * 8;  // values a CTA takes at once: 16 lanes a block of 128, 8 values each
+constexpr int32_t kAdamMaxTensors = 1 << 20;
+constexpr int64_t kAdamMaxValues = int64_t{1} << 40;
+constexpr uint32_t kPlaceStep = 0xC13FA9A9u, kTimeStep = 0x91E10DA5u;  // 2^32 / r and 2^32 / r^2, r^3 = r + 1
+constexpr uint32_t kRootShift = 0x80000000u;
+
+enum : uint32_t { kParamF32 = 1, kGradF32 = 2, kMaster = 4, kVectors = 8 };
+
+struct AdamTensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int64_t numel;
+  float decay;
+  uint32_t kind;
+};
+template <int CAP>
+struct AdamTable {
+  AdamTensor t[CAP];
+  uint32_t end[CAP];  // chunks of the tensors up to and with this one
+  int32_t n, passes;  // passes a chunk
+};
+constexpr int kAdamCap = 384;
+static_assert(sizeof(AdamTable<kAdamCap>) <= 32000, "kernel arguments hold 32764 bytes");
+
+struct AdamHyper {
+  float b1, nb1, b2, nb2, eps;  // nb = 1 - b, rounded once
+};
+// What every CTA needs of the step, made by one thread (the powers in 64 bits).
+struct AdamStep {
+  float coef, lr, lr1, root2;  // lr, lr / c1, 1 / sqrt(c2)
+  uint32_t time, skip;
+};
+static_assert(sizeof(AdamStep) <= 32, "");
+
+__global__ void adamw_step_kernel(const float* lr_dev, double lr, double b1, double b2, int64_t* step, const float* norm,
+                                  float max_norm, float norm_eps, AdamStep* out) {
+  griddep_launch_dependents();
+  AdamStep s{};
+  s.coef = 1.0f;
+  if (norm) {
+    const float n = *norm;
+    s.skip = isfinite(n) ? 0u : 1u;
+    s.coef = fminf(1.0f, __fmul_rn(max_norm, __frcp_rn(n + norm_eps)));
+  }
+  if (!s.skip) {
+    const int64_t t = *step + 1;
+    *step = t;
+    s.time = static_cast<uint32_t>(t);
+    if (lr_dev) lr = *lr_dev;
+    s.lr = static_cast<float>(lr);
+    s.lr1 = static_cast<float>(lr / (1.0 - pow(b1, static_cast<double>(t))));
+    s.root2 = static_cast<float>(1.0 / sqrt(1.0 - pow(b2, static_cast<double>(t))));
+  }
+  *out = s;
+}
+
+// Values j = 0 .. 7 of a thread: eight in a row (`full`), or single ones with a step between them.
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, int64_t at, int step, int64_t n, bool full, float (&f)[8]) {
+  if (full) {
+    load8(p + at, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = at + j * step < n ? to_f32(p[at + j * step]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put8(T* p, int64_t at, int step, int64_t n, bool full, const float (&f)[8]) {
+  if (full) {
+    store8(p + at, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j * step < n) p[at + j * step] = from_f32<T>(f[j]);
+  }
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ void get_codes(const uint8_t* p, int64_t at, int step, int64_t n, bool full, float scale,
+                                          float (&f)[8]) {
+  uint32_t w[2] = {0u, 0u};
+  if (full) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p + at);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j * step < n) w[j / 4] |= static_cast<uint32_t>(p[at + j * step]) << (8 * (j & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = e4m3x2_to_f32(w[j / 2] >> (16 * (j & 1)));
+    f[2 * j] = __fmul_rn(d.x, scale);
+    f[2 * j + 1] = __fmul_rn(d.y, scale);
+  }
+}
+// The codes of a block that 16 lanes hold, and its scale (see above).  ROOT: what is not 0 gets no 0.
+template <bool ROOT>
+__device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, int step, int64_t n, bool full,
+                                          uint32_t time, const float (&f)[8]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+  const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, off));
+  const bool live = top >= 0x1p-60f;
+  const float inv = live ? __fmul_rn(448.0f, __frcp_rn(top)) : 0.0f;
+  if ((threadIdx.x & 15) == 0) *scale = live ? __fmul_rn(top, 1.0f / 448.0f) : 0.0f;
+  const uint32_t shift = time * kTimeStep + (ROOT ? kRootShift : 0u);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * j + k;
+      const float y = __fmul_rn(fabsf(f[i]), inv);
+      // A code has 3 bits after the point, y 20 more: their sum with u carries into the code's or does not.  Below 2^-6
+      // the codes are 2^-9 apart, as they are from 2^-6 to 2^-5: the sum with 2^-6 (what it cuts off is less than u's
+      // last bit) has them at the same bits.
+      const float low = y < 0x1p-6f ? 0x1p-6f : 0.0f;
+      const uint32_t u = (static_cast<uint32_t>(at + i * step) * kPlaceStep + shift) >> 12;
+      float r = __uint_as_float((__float_as_uint(__fadd_rz(y, low)) + u) & 0xFFF00000u) - low;
+      if (ROOT && live && f[i] > 0.0f) r = fmaxf(r, 0x1p-9f);
+      c[k] = copysignf(r, f[i]);
+    }
+    w[j / 2] |= static_cast<uint32_t>(cvt_e4m3x2(c[1], c[0])) << (16 * (j & 1));
+  }
+  if (full) {
+    *reinterpret_cast<uint2*>(p + at) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (at + j * step < n) p[at + j * step] = static_cast<uint8_t>(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+
+// One block of 128 values of tensor t, from `block` on.
+template <int BITS, typename TP, typename TG, bool MASTER>
+__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
+  const int lane = threadIdx.x & 15;
+  const int64_t n = t.numel;
+  const bool vec = t.kind & kVectors;
+  const int64_t at = block + (vec ? 8 * lane : lane);
+  const int step = vec ? 1 : 16;
+  const bool full = vec && at + 8 <= n;
+  float p[8], g[8], m[8], v[8];
+  get8(static_cast<const TG*>(t.grad), at, step, n, full, g);
+  if constexpr (MASTER) get8(t.master, at, step, n, full, p);
+  else get8(static_cast<const TP*>(t.param), at, step, n, full, p);
+  if constexpr (BITS == 32) {
+    get8(static_cast<const float*>(t.m), at, step, n, full, m);
+    get8(static_cast<const float*>(t.v), at, step, n, full, v);
+  } else {
+    get_codes(static_cast<const uint8_t*>(t.m), at, step, n, full, t.m_scale[block >> 7], m);
+    get_codes(static_cast<const uint8_t*>(t.v), at, step, n, full, t.v_scale[block >> 7], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // (products and sums rounded one by one: the codes' rounding then is that of the formulas as they stand)
+    const float gj = __fmul_rn(g[j], s.coef);
+    m[j] = __fadd_rn(__fmul_rn(h.b1, m[j]), __fmul_rn(h.nb1, gj));
+    v[j] = __fadd_rn(__fmul_rn(h.b2, v[j]), __fmul_rn(__fmul_rn(h.nb2, gj), gj));
+    const float root = __fsqrt_rn(v[j]);
+    const float to = __fdiv_rn(m[j], fmaf(root, s.root2, h.eps));
+    p[j] = p[j] - fmaf(s.lr1, to, s.lr * t.decay * p[j]);
+    if (BITS == 8) v[j] = root;
+  }
+  put8(static_cast<TP*>(t.param), at, step, n, full, p);
+  if constexpr (MASTER) put8(t.master, at, step, n, full, p);
+  if constexpr (BITS == 32) {
+    put8(static_cast<float*>(t.m), at, step, n, full, m);
+    put8(static_cast<float*>(t.v), at, step, n, full, v);
+  } else {
+    put_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + (block >> 7), at, step, n, full, s.time, m);
+    put_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + (block >> 7), at, step, n, full, s.time, v);
+  }
+}
+
+template <int CAP, int BITS>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
+                                                             const AdamHyper h, const AdamStep* __restrict__ step) {
+  int lo = 0, hi = tab.n - 1;
+  const uint32_t c = blockIdx.x;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < tab.end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  const AdamTensor& t = tab.t[lo];
+  const int64_t first = static_cast<int64_t>(c - (lo ? tab.end[lo - 1] : 0u)) * (tab.passes * kAdamPass);
+  griddep_wait();
+  AdamStep s;
+  s.coef = __ldcg(&step->coef), s.lr = __ldcg(&step->lr), s.lr1 = __ldcg(&step->lr1), s.root2 = __ldcg(&step->root2);
+  s.time = __ldcg(&step->time), s.skip = __ldcg(&step->skip);
+  if (s.skip) return;
+  for (int i = 0; i < tab.passes; ++i) {
+    const int64_t block = first + static_cast<int64_t>(i) * kAdamPass + (threadIdx.x >> 4) * 128;
+    if (block >= t.numel) return;
+    switch (t.kind & (kParamF32 | kGradF32 | kMaster)) {
+      case 0: adam_block<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block); break;
+      case kGradF32: adam_block<BITS, __nv_bfloat16, float, false>(t, h, s, block); break;
+      case kMaster: adam_block<BITS, __nv_bfloat16, __nv_bfloat16, true>(t, h, s, block); break;
+      case kMaster | kGradF32: adam_block<BITS, __nv_bfloat16, float, true>(t, h, s, block); break;
+      case kParamF32: adam_block<BITS, float, __nv_bfloat16, false>(t, h, s, block); break;
+      default: adam_block<BITS, float, float, false>(t, h, s, block); break;
+    }
+  }
+}
+
+int check_adam(const fp8g_adamw_tensor* ts, int32_t n, int32_t bits) {
+  if (n < 0 || n > kAdamMaxTensors || (n > 0 && !ts) || (bits != 8 && bits != 32)) return FP8G_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const fp8g_adamw_tensor& t = ts[i];
+    if (t.numel < 0 || t.numel > kAdamMaxValues || !(t.weight_decay >= 0.0f) ||
+        (t.param_dtype != FP8G_BF16 && t.param_dtype != FP8G_F32) ||
+        (t.grad_dtype != FP8G_BF16 && t.grad_dtype != FP8G_F32) || (t.master && t.param_dtype != FP8G_BF16))
+      return FP8G_ERR_INVALID_ARG;
+    total += t.numel;
+    if (total > kAdamMaxValues) return FP8G_ERR_INVALID_ARG;
+    if (t.numel == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || (bits == 8 && (!t.m_scale || !t.v_scale))) return FP8G_ERR_INVALID_ARG;
+    const uintptr_t state = bits == 32 ? 4 : 1;
+    if (!aligned_to(t.param, t.param_dtype == FP8G_F32 ? 4 : 2) || !aligned_to(t.grad, t.grad_dtype == FP8G_F32 ? 4 : 2) ||
+        !aligned_to(t.m, state) || !aligned_to(t.v, state) || !aligned_to(t.master, 4) ||
+        (bits == 8 && (!aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4))))
+      return FP8G_ERR_ALIGNMENT;
+  }
+  return FP8G_OK;
+}
+
+template <int CAP, int BITS>
+int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, int32_t passes, const AdamHyper& h, const AdamStep* step,
+                 cudaStream_t s) {
+  AdamTable<CAP> tab;
+  const uintptr_t state = BITS == 32 ? 16 : 8;
+  bool first = true;
+  for (int32_t i = 0; i < n;) {
+    tab.n = 0;
+    tab.passes = passes;
+    uint64_t chunks = 0;
+    for (; i < n && tab.n < CAP; ++i) {
+      const fp8g_adamw_tensor& t = ts[i];
+      if (t.numel == 0) continue;
+      const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) && aligned_to(t.m, state) &&
+                       aligned_to(t.v, state);
+      tab.t[tab.n] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.numel, t.weight_decay,
+                      (t.param_dtype == FP8G_F32 ? kParamF32 : 0u) | (t.grad_dtype == FP8G_F32 ? kGradF32 : 0u) |
+                          (t.master ? kMaster : 0u) | (vec ? kVectors : 0u)};
+      chunks += static_cast<uint64_t>((t.numel + passes * kAdamPass - 1) / (passes * kAdamPass));
+      tab.end[tab.n++] = static_cast<uint32_t>(chunks);
+    }
+    if (tab.n == 0) break;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(chunks));
+    cfg.blockDim = dim3(kAdamThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = first ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    first = false;
+    if (cudaLaunchKernelEx(&cfg, adamw_kernel<CAP, BITS>, tab, h, step) != cudaSuccess) {
+      cudaGetLastError();
+      return FP8G_ERR_CUDA;
+    }
+  }
+  return FP8G_OK;
+}
+
+}  // namespace
+}  // namespace fp8g
+
+using namespace fp8g;
+
+extern "C" int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t state_bits, double lr, const float* lr_dev,
+                          double beta1, double beta2, double eps, int64_t* step, const float* norm, float max_norm,
+                          float norm_eps, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = check_adam(tensors, n, state_bits);
+  if (st != FP8G_OK) return st;
+  if (!(lr >= 0.0) || !std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+      !(eps >= 1e-30) || !std::isfinite(eps) || !step || (norm && (!(max_norm >= 0.0f) || !(norm_eps >= 0.0f))) || !workspace ||
+      workspace_bytes < FP8G_ADAMW_WORKSPACE)
+    return FP8G_ERR_INVALID_ARG;
+  if (!aligned_to(step, 8) || !aligned_to(norm, 4) || !aligned_to(lr_dev, 4) || !aligned16(workspace))
+    return FP8G_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  st = current_device(&dev);
+  if (st != FP8G_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AdamStep* out = static_cast<AdamStep*>(workspace);
+  adamw_step_kernel<<<1, 1, 0, s>>>(lr_dev, lr, beta1, beta2, step, norm, max_norm, norm_eps, out);
+  if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) total += tensors[i].numel;
+  const AdamHyper h{static_cast<float>(beta1), static_cast<float>(1.0 - beta1), static_cast<float>(beta2),
+                    static_cast<float>(1.0 - beta2), static_cast<float>(eps)};
+  int64_t passes = total < (int64_t{1} << 24) ? 1 : 4;
+  while (total / (passes * kAdamPass) + n >= (int64_t{1} << 31)) passes *= 2;  // a grid has fewer than 2^31 CTAs
+  const int32_t p = static_cast<int32_t>(passes);
+  if (state_bits == 32)
+    return n <= 64 ? adamw_launch<64, 32>(tensors, n, p, h, out, s) : adamw_launch<kAdamCap, 32>(tensors, n, p, h, out, s);
+  return n <= 64 ? adamw_launch<64, 8>(tensors, n, p, h, out, s) : adamw_launch<kAdamCap, 8>(tensors, n, p, h, out, s);
+}

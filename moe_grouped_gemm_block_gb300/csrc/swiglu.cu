@@ -1,0 +1,192 @@
+// swiglu.cu -- the gated activation between an expert's two matrix products, quantised for the second one, and its
+// gradient.
+//
+//     h = g s(g) u,  s(g) = 1 / (1 + e^-g)        (a row of the first product is g [F], then u [F])
+//     e4m3 of h in 1 x 128 blocks: scale = amax / 448, code = e4m3(h / scale), as the quantisers' of unfused rows
+//     dg = dh u s (1 + g (1 - s)),  du = dh g s
+//
+// Everything is fp32 until the one rounding of a result.  Bound by memory: forward 4 bytes read and 1 written a value
+// (3 with h in bf16), backward 6 read and 4 written (6).
+
+#include <algorithm>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace fp8g {
+namespace {
+
+constexpr int kGluThreads = 256;
+constexpr int kGluGroups = kGluThreads / 16;  // 16 lanes take a block of 128 values, 8 each
+
+struct GluArgs {
+  const __nv_bfloat16* gu;
+  const __nv_bfloat16* dh;
+  __nv_bfloat16* h;
+  __nv_bfloat16* dgu;
+  uint8_t* q;
+  float* sA;
+  const int32_t* counts;
+  int64_t ldgu, lddh, ldh, lddgu, ldq, ld_sa;
+  uint32_t M, KB, cap;
+  int32_t F;
+};
+
+// s(g).  e^-g as a power of two of a rounded exponent and the reciprocal are off by (4 + |g|) 2^-24 of themselves
+// together, far below the results' own rounding.  s below 2^-126 (g < -87) is 0.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
+template <bool MASKED>
+__global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+  uint32_t M = a.M;
+  int64_t row0 = 0;
+  if (MASKED) {
+    const int32_t c = __ldg(a.counts + blockIdx.y);
+    M = c < 0 ? 0u : min(static_cast<uint32_t>(c), a.cap);
+    row0 = static_cast<int64_t>(blockIdx.y) * a.cap;
+  }
+  const uint32_t items = M * a.KB;
+  for (uint32_t i = blockIdx.x * kGluGroups + group; i < items; i += gridDim.x * kGluGroups) {
+    const int64_t m = row0 + i / a.KB;
+    const uint32_t kb = i % a.KB;
+    const int col = static_cast<int>(kb) * 128 + lane * 8;
+    float h[8] = {};
+    if (col < a.F) {
+      float g[8], u[8];
+      load8(a.gu + m * a.ldgu + col, g);
+      load8(a.gu + m * a.ldgu + a.F + col, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
+      if (a.h) store8(a.h + m * a.ldh + col, h);
+    }
+    if (!a.q) continue;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[j]));
+    const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, off));
+    const float s = __fdiv_rn(top, 448.0f);
+    // 1 / s of a tiny scale is beyond fp32: such a block is taken 2^64 times larger
+    const float big = s < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s * big);
+    uint16_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(h[2 * j + 1] * big * inv, h[2 * j] * big * inv);
+    *reinterpret_cast<uint2*>(a.q + m * a.ldq + col) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (lane == 0) a.sA[kb * a.ld_sa + m] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kGluThreads) swiglu_backward_kernel(const GluArgs a) {
+  const uint32_t C = static_cast<uint32_t>(a.F) / 8;
+  const uint32_t items = a.M * C;
+  for (uint32_t i = blockIdx.x * kGluThreads + threadIdx.x; i < items; i += gridDim.x * kGluThreads) {
+    const int64_t m = i / C;
+    const int col = static_cast<int>(i % C) * 8;
+    float g[8], u[8], d[8];
+    load8(a.gu + m * a.ldgu + col, g);
+    load8(a.gu + m * a.ldgu + a.F + col, u);
+    load8(a.dh + m * a.lddh + col, d);
+    float h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = sigmoid(g[j]), act = g[j] * s;
+      h[j] = act * u[j];
+      const float dg = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+      u[j] = d[j] * act;
+      g[j] = dg;
+    }
+    store8(a.dgu + m * a.lddgu + col, g);
+    store8(a.dgu + m * a.lddgu + a.F + col, u);
+    if (a.h) store8(a.h + m * a.ldh + col, h);
+  }
+}
+
+unsigned ctas(int64_t work, int64_t per, const DeviceInfo* dev, int per_sm) {
+  return static_cast<unsigned>(std::min<int64_t>((work + per - 1) / per, int64_t{1} * dev->sm_count * per_sm));
+}
+
+bool bad_rows(const void* p, int64_t ld) { return !aligned16(p) || ld % 8 != 0; }
+
+}  // namespace
+}  // namespace fp8g
+
+using namespace fp8g;
+
+extern "C" int fp8_swiglu_quantize_1x128(const void* gu, int64_t M, int64_t F, int64_t ldgu, void* q, int64_t ldq,
+                                         float* sA, int64_t ld_sa, void* h, int64_t ldh, void* stream) {
+  if (M < 0 || F <= 0 || F % 8 != 0 || F > (1 << 29) || M > 0x7FFFFFFF || ldgu < 2 * F || (q && M && !sA) ||
+      (q && (F % 128 != 0 || ldq < F || ld_sa < M)) || (h && ldh < F) || M * ((F + 127) / 128) >= (int64_t{1} << 31))
+    return FP8G_ERR_INVALID_ARG;
+  if (M == 0) return FP8G_OK;
+  if (!gu || (!q && !h)) return FP8G_ERR_INVALID_ARG;
+  if (bad_rows(gu, ldgu) || (h && bad_rows(h, ldh)) || (q && (!aligned16(q) || !aligned16(sA) || ldq % 16 || ld_sa % 4)))
+    return FP8G_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != FP8G_OK) return st;
+  GluArgs a{};
+  a.gu = static_cast<const __nv_bfloat16*>(gu), a.ldgu = ldgu;
+  a.h = static_cast<__nv_bfloat16*>(h), a.ldh = ldh;
+  a.q = static_cast<uint8_t*>(q), a.ldq = ldq, a.sA = sA, a.ld_sa = ld_sa;
+  a.M = static_cast<uint32_t>(M), a.KB = static_cast<uint32_t>((F + 127) / 128), a.F = static_cast<int32_t>(F);
+  swiglu_kernel<false><<<ctas(M * a.KB, kGluGroups, dev, 8), kGluThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+extern "C" int fp8_swiglu_quantize_1x128_masked(const void* gu, int32_t E, int64_t cap, int64_t F,
+                                                const int32_t* masked_m, void* q, float* sA, int64_t ld_sa,
+                                                void* stream) {
+  if (E < 1 || E > 65535 || cap < 0 || cap > 0x7FFFFFFF || F <= 0 || F % 128 != 0 || F > (1 << 29) ||
+      ld_sa < static_cast<int64_t>(E) * cap || static_cast<int64_t>(E) * cap > 0x7FFFFFFF ||
+      static_cast<int64_t>(E) * cap * (F / 128) >= (int64_t{1} << 31))
+    return FP8G_ERR_INVALID_ARG;
+  if (cap == 0) return FP8G_OK;
+  if (!gu || !q || !sA || !masked_m) return FP8G_ERR_INVALID_ARG;
+  if (!aligned16(gu) || !aligned16(q) || !aligned16(sA) || ld_sa % 4 != 0 || !aligned_to(masked_m, 4))
+    return FP8G_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != FP8G_OK) return st;
+  GluArgs a{};
+  a.gu = static_cast<const __nv_bfloat16*>(gu), a.ldgu = 2 * F;
+  a.q = static_cast<uint8_t*>(q), a.ldq = F, a.sA = sA, a.ld_sa = ld_sa;
+  a.counts = masked_m;
+  a.cap = static_cast<uint32_t>(cap), a.KB = static_cast<uint32_t>(F / 128), a.F = static_cast<int32_t>(F);
+  const unsigned bx = std::max(1u, std::min(ctas(cap * a.KB, kGluGroups, dev, 8),
+                                            static_cast<unsigned>((16 * dev->sm_count + E - 1) / E)));
+  swiglu_kernel<true><<<dim3(bx, static_cast<unsigned>(E)), kGluThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+
+extern "C" int fp8g_swiglu_backward(const void* dh, int64_t lddh, const void* gu, int64_t M, int64_t F, int64_t ldgu,
+                                    void* dgu, int64_t lddgu, void* h, int64_t ldh, void* stream) {
+  if (M < 0 || F <= 0 || F % 8 != 0 || F > (1 << 29) || M > 0x7FFFFFFF || M * (F / 8) >= (int64_t{1} << 31) ||
+      lddh < F || ldgu < 2 * F || lddgu < 2 * F || (h && ldh < F))
+    return FP8G_ERR_INVALID_ARG;
+  if (M == 0) return FP8G_OK;
+  if (!dh || !gu || !dgu) return FP8G_ERR_INVALID_ARG;
+  if (bad_rows(dh, lddh) || bad_rows(gu, ldgu) || bad_rows(dgu, lddgu) || (h && bad_rows(h, ldh)))
+    return FP8G_ERR_ALIGNMENT;
+  DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st != FP8G_OK) return st;
+  GluArgs a{};
+  a.dh = static_cast<const __nv_bfloat16*>(dh), a.lddh = lddh;
+  a.gu = static_cast<const __nv_bfloat16*>(gu), a.ldgu = ldgu;
+  a.dgu = static_cast<__nv_bfloat16*>(dgu), a.lddgu = lddgu;
+  a.h = static_cast<__nv_bfloat16*>(h), a.ldh = ldh;
+  a.M = static_cast<uint32_t>(M), a.F = static_cast<int32_t>(F);
+  swiglu_backward_kernel<<<ctas(M * (F / 8), kGluThreads, dev, 8), kGluThreads, 0,
+                           static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}

@@ -23,6 +23,8 @@ Modules:
                K-grouped weight-gradient GEMM of a grouped MoE layer
   block_ops -- layer norm, the MoE gate with its balance loss, the combine, their gradients and
                gradient clipping, in float64
+  train_ops -- the router with bias and expert groups, the RMS norms around a block, the gated
+               activation, their gradients and AdamW, in float64
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 invariants, brute force on tiny inputs and library routines; none is "parity
 unpinned".
