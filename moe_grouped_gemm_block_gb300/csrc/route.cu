@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "topk.cuh"
 #include "vec.cuh"
 
 namespace fp8g {
@@ -32,7 +33,7 @@ struct RouteArgs {
   const float* dweights;
   void* dlogits;
   int64_t T, ldl, ldd;
-  int32_t E, topk, groups, kept, softmax, renorm, vec;
+  int32_t E, topk, groups, kept, log_groups, softmax, renorm, vec;
   float scale;
 };
 
@@ -109,8 +110,8 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, double* c,
       const int i = __shfl_xor_sync(0xffffffffu, at, off);
       if (v > best || (v == best && i < at) || (best != best && v == v)) best = v, at = i;
     }
-    if (lane == j) pick = at;
-    if ((at & 31) == lane) c[at] = nan;
+    if (lane == j) pick = min(at, E - 1);
+    if ((at & 31) == lane && at < E) c[at] = nan;
     __syncwarp();
   }
   weight = 0.0f;
@@ -121,22 +122,401 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, double* c,
   __syncwarp();
 }
 
+// A row's result, as lane j < topk has its j-th choice.
+__device__ __forceinline__ void put_row(const RouteArgs& a, int64_t t, int id, float w, int32_t* counts) {
+  const int lane = threadIdx.x & 31;
+  const bool real = !a.mask || a.mask[t];
+  const float sum = warp_sum(w);
+  if (a.renorm) w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+  if (lane < a.topk) {
+    a.ids[t * a.topk + lane] = id;
+    a.weights[t * a.topk + lane] = real ? w * a.scale : 0.0f;
+    if (real) atomicAdd(counts + id, 1);  // whole numbers: the order does not matter
+  }
+}
+
+// The general form: every row in 64 bits (2.7 ms for 65536 x 256).
 template <typename TL>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs a) {
-  extern __shared__ double choice[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ __align__(16) double choice[];
+  const int warp = threadIdx.x >> 5;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += gridDim.x * kRouteWarps) {
     int id;
     float w;
     route_row<TL>(a, t, choice + warp * a.E, id, w);
-    const bool real = !a.mask || a.mask[t];
-    const float sum = warp_sum(w);
-    if (a.renorm) w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
-    if (lane < a.topk) {
-      a.ids[t * a.topk + lane] = id;
-      a.weights[t * a.topk + lane] = real ? w * a.scale : 0.0f;
-      if (real) atomicAdd(a.counts + id, 1);  // whole numbers: the order does not matter
+    put_row(a, t, id, w, a.counts);
+  }
+}
+
+// The fast form.  A row is held by LPR lanes of a warp, each expert group by L = LPR / (groups rounded up to a power
+// of 2) of them, VPL experts a lane.  A choice score becomes a place on a grid of 2^23 steps over the range that the
+// scores can have with these biases, t = 2^23 + 32 + (c - lowest bias) K: a key of 32 bits holds its 23 bits and, below
+// them, the expert's slot (ties: the lower one), so that a sorting network of unsigned minima and maxima and one
+// maximum over the row a pick choose the experts.  (bf16 logits without a bias need no grid: their own 16 bits order
+// them exactly.)
+//
+// What the grid cannot tell apart is found and decided in 64 bits: a row goes to route_row if two neighbours in the order
+// of its picks, or a group that stays and one that does not, lie within `near` steps.  Two experts with the same logit
+// and the same bias are the exception, as their order is that of their indices in any precision (a router with a bias
+// of zeros and bf16 logits has them in every tenth row).  How far t can be off, in steps (of at least 2^-23, R their
+// range, R >= 1): s by 4.3 2^-24 (sigmoid: 1/4 (2^-22 of ex2) + 0.28 2^-24 for the exponent's rounding, one
+// unit of the reciprocal and half a unit of the sum) or 36 2^-24 (softmax: ex2, the exponents' roundings weighted by the
+// scores, at most log E, the sum's 13), 2.2 or 18 steps; the bias' part 1.5, the sum 0.5.  So two are within 2 x 4.2 or
+// 2 x 20.5 steps of their true distance, sums of two within twice that.
+//
+// Rows with a logit that is NaN or +inf, with fewer experts left than are to be chosen, or with a group that has a single
+// one left, go there too.  65536 x 256 normal logits: one row in 2000.
+constexpr int kRouteFastWarps = 32;
+constexpr float kGrid = 8388608.0f;  // 2^23
+// Shared memory, every part a multiple of 16 bytes: a row of doubles a warp, the CTA's counts, then a warp's lists of
+// keys, its rows' picks and their scores.
+__host__ __device__ constexpr int route_doubles(int E) { return (E + 1) / 2 * 2; }
+template <typename TL, int VPL, int LPR>
+__host__ __device__ constexpr int route_warp_words(int topk) {
+  return (VPL == 8 ? 32 * 12 : 0) + ((32 / LPR) * (2 * topk + 1) + 3) / 4 * 4;
+}
+
+// The lane's keys by rank, as the row's lanes take them: `next` gives the row's largest that is left (0: none).
+template <int VPL, int LPR>
+struct KeyList;
+template <int LPR>
+struct KeyList<8, LPR> {
+  uint32_t head, second;
+  const uint32_t* at;
+  __device__ __forceinline__ void init(uint32_t (&key)[8], uint32_t* list) {
+    sort8([&](int a, int b) {
+      const uint32_t hi = max(key[a], key[b]), lo = min(key[a], key[b]);
+      key[a] = hi;
+      key[b] = lo;
+    });
+    head = key[0];
+    second = key[1];
+    at = list + 1;
+    reinterpret_cast<uint4*>(list)[0] = make_uint4(key[0], key[1], key[2], key[3]);
+    reinterpret_cast<uint4*>(list)[1] = make_uint4(key[4], key[5], key[6], key[7]);  // (words 8 and 9 are 0)
+  }
+  __device__ __forceinline__ uint32_t next() {
+    const uint32_t top = row_max<LPR>(head);
+    if (head == top && top != 0u) {
+      head = second;
+      second = *++at;
     }
+    return top;
+  }
+};
+template <int LPR>
+struct KeyList<16, LPR> {  // unsorted: what is below the last pick, anew each time
+  uint32_t key[16];
+  uint32_t last;
+  __device__ __forceinline__ void init(uint32_t (&k)[16], uint32_t*) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) key[i] = k[i];
+    last = 0xffffffffu;
+  }
+  __device__ __forceinline__ uint32_t next() {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, key[i] < last ? key[i] : 0u);
+    last = row_max<LPR>(m);
+    return last;
+  }
+};
+
+template <typename TL, int VPL, int LPR, bool KEYS16>
+__global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr int G = 32 / LPR;  // rows a warp at once
+  extern __shared__ __align__(16) double smem64[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int sub = lane % LPR, grp = lane / LPR;
+  const uint32_t row_lanes = (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u) << (lane & ~(LPR - 1));
+  const int E = a.E, topk = a.topk, per = E / a.groups, L = LPR >> a.log_groups, log_l = 31 - __clz(L);
+  const int group = sub >> log_l, base = group * per + (sub & (L - 1)) * VPL;
+  const int end = group < a.groups ? group * per + per : 0;
+  double* choice = smem64 + warp * route_doubles(E);
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem64 + warps * route_doubles(E));
+  int32_t* cnt = reinterpret_cast<int32_t*>(words);
+  uint32_t* mine = words + (E + 3) / 4 * 4 + warp * route_warp_words<TL, VPL, LPR>(topk);
+  uint32_t* list = mine + lane * 12;
+  uint32_t* pick = mine + (VPL == 8 ? 32 * 12 : 0) + grp * (topk + 1);
+  float* pick_w = reinterpret_cast<float*>(mine + (VPL == 8 ? 32 * 12 : 0) + G * (topk + 1)) + grp * topk;
+  if constexpr (VPL == 8) list[8] = list[9] = 0u;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
+  __syncthreads();
+  const TL* logits = static_cast<const TL*>(a.logits);
+  const bool scored = !KEYS16 || a.groups > 1;  // whether the choice needs the scores
+
+  // the grid, and the biases' places on it (-inf: no expert there)
+  float low = INFINITY, high = -INFINITY;
+  bool all_exact = false;
+  if (a.bias) {
+    for (int e = lane; e < E; e += 32) {
+      const float b = a.bias[e];
+      if (!(b < INFINITY)) all_exact = true;
+      else if (b > -INFINITY) low = fminf(low, b), high = fmaxf(high, b);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+      high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, off));
+    }
+    all_exact = __any_sync(0xffffffffu, all_exact);
+  }
+  if (!(low <= high)) low = high = 0.0f;
+  const float range = 1.0f + (high - low);
+  all_exact |= !(range < INFINITY);
+  const float K = __fdiv_rn(kGrid - 64.0f, range);
+  const float near = a.softmax ? 48.0f : 12.0f;
+  float place[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float b = base + i < end ? (a.bias ? a.bias[base + i] : 0.0f) : -INFINITY;
+    place[i] = kGrid + 32.0f + (b - low) * K;
+  }
+
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * warps * G;
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * warps + warp) * G;
+  Raw8<TL> next[VPL / 8];
+  auto fetch = [&](int64_t at) {
+    const TL* row = logits + (at + grp < a.T ? at + grp : a.T - 1) * a.ldl;
+#pragma unroll
+    for (int v = 0; v < VPL / 8; ++v) {
+      const int c = base + 8 * v;
+      if (a.vec && c + 8 <= end) {
+        next[v].load(row + c);
+      } else {
+        TL f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < end ? row[c + i] : from_f32<TL>(0.0f);
+        next[v].set(f);
+      }
+    }
+  };
+  if (t0 < a.T) fetch(t0);
+  for (; t0 < a.T; t0 += stride) {
+    const int64_t t = t0 + grp;
+    const bool there = t < a.T;
+    const TL* row = logits + (there ? t : a.T - 1) * a.ldl;
+    float f[VPL];
+    uint32_t key[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL / 8; ++v) next[v].get(reinterpret_cast<float2(&)[4]>(f[8 * v]));
+    if constexpr (KEYS16) {
+#pragma unroll
+      for (int v = 0; v < VPL / 8; ++v) {
+        const uint32_t* w = &next[v].v.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k = order_key2(w[i]), c = 0xFFFFu - static_cast<uint32_t>(sub * VPL + 8 * v + 2 * i);
+          key[8 * v + 2 * i] = __byte_perm(k, c, 0x1054);          // the low key over the slot
+          key[8 * v + 2 * i + 1] = __byte_perm(k, c - 1u, 0x3254);  // the high one
+        }
+      }
+      if (base + VPL > end) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = base + i < end ? key[i] : 0u;
+      }
+    }
+    if (t0 + stride < a.T) fetch(t0 + stride);
+    float odd = 0.0f;  // NaN where a logit is not finite
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) odd = fmaf(f[i], 0.0f, odd);
+    const bool some_odd = __any_sync(0xffffffffu, odd != 0.0f);
+    bool exact = all_exact;
+    if (some_odd) {
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) bad |= !(f[i] < INFINITY);
+      exact |= (__ballot_sync(0xffffffffu, bad) & row_lanes) != 0u;
+    }
+    float mx = 0.0f, inv = 1.0f;
+    float c[VPL];  // the choice scores' places
+    if (a.softmax) {
+      if (base + VPL > end) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) f[i] = base + i < end ? f[i] : -INFINITY;
+      }
+      mx = f[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, f[i]);
+      mx = row_max<LPR>(mx);
+      if (mx == -INFINITY) mx = 0.0f;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        c[i] = exp2_approx((f[i] - mx) * 1.4426950408889634f);
+        s += c[i];
+      }
+      s = row_sum<LPR>(s);
+      inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
+      const float by = K * inv;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = fmaf(c[i], by, place[i]);
+    } else if (scored) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        c[i] = fmaf(recip_approx(1.0f + exp2_approx(f[i] * -1.4426950408889634f)), K, place[i]);
+    }
+    if (some_odd && scored) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = f[i] == -INFINITY ? -INFINITY : c[i];
+    }
+    if (KEYS16 && some_odd) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = f[i] == -INFINITY ? 0u : key[i];
+    }
+    if constexpr (!KEYS16) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = __float_as_uint(c[i]) * 512u + (511u - static_cast<uint32_t>(sub * VPL + i));
+    }
+    if (a.groups > 1) {
+      float first = c[0], second = -INFINITY;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) {
+        second = fmaxf(second, fminf(first, c[i]));
+        first = fmaxf(first, c[i]);
+      }
+      for (int off = 1; off < L; off <<= 1) {
+        const float o1 = __shfl_xor_sync(0xffffffffu, first, off), o2 = __shfl_xor_sync(0xffffffffu, second, off);
+        second = fmaxf(fmaxf(second, o2), fminf(first, o1));
+        first = fmaxf(first, o1);
+      }
+      const float sum = per == 1 ? first - kGrid : (first - kGrid) + (second - kGrid);
+      const float above = sum + 2.0f * near, below = sum - 2.0f * near;
+      int surely = 0, maybe = -1;  // groups that are better than this lane's (itself left out)
+      for (int g = 0; g < a.groups; ++g) {
+        const float other = __shfl_sync(0xffffffffu, sum, (lane & ~(LPR - 1)) + g * L);
+        surely += other > above ? 1 : 0;
+        maybe += other > below ? 1 : 0;
+      }
+      const bool stays = maybe < a.kept;
+      const bool unsure = group < a.groups && (stays != (surely < a.kept) || !(sum > -INFINITY));
+      exact |= (__ballot_sync(0xffffffffu, unsure) & row_lanes) != 0u;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = stays ? key[i] : 0u;
+    }
+    KeyList<VPL, LPR> keys;
+    keys.init(key, list);
+    for (int j = 0; j < topk + (KEYS16 ? 0 : 1); ++j) {
+      const uint32_t top = keys.next();
+      if (sub == 0) pick[j] = top;
+    }
+    __syncwarp();
+    auto expert = [&](uint32_t k) {
+      const int slot = KEYS16 ? 0xFFFF - static_cast<int>(k & 0xFFFFu) : 511 - static_cast<int>(k & 511u);
+      const int l = slot / VPL;
+      return min((l >> log_l) * per + (l & (L - 1)) * VPL + slot % VPL, E - 1);  // (a void key's slot is no expert's)
+    };
+    const uint32_t least = KEYS16 ? 1u : 512u;  // keys below stand for no expert
+    // whether two neighbours in the order may stand the other way round: 0 no, 1 yes, 2 they are alike
+    auto doubt = [&](uint32_t hi, uint32_t lo) {
+      if (lo < least || (hi >> 9) - (lo >> 9) > static_cast<uint32_t>(near)) return 0;
+      const int x = expert(hi), y = expert(lo);
+      return to_f32(row[x]) == to_f32(row[y]) && (!a.bias || a.bias[x] == a.bias[y]) ? 2 : 1;
+    };
+    bool unsure = false, open = false;
+    float picked = 0.0f;
+    for (int j = sub; j < topk; j += LPR) {
+      const uint32_t k = pick[j];
+      const float l = to_f32(row[expert(k)]);
+      float s;
+      if (a.softmax) s = expf(l - mx) * inv;
+      else s = __fdiv_rn(1.0f, 1.0f + expf(-l));
+      unsure |= k < least;
+      if constexpr (!KEYS16) {
+        const int d = doubt(k, pick[j + 1]);
+        unsure |= d == 1;
+        open |= d == 2 && j == topk - 1;  // the last one that is taken and the first that is not
+      }
+      pick_w[j] = s;
+      picked += s;
+    }
+    if constexpr (!KEYS16) {
+      uint32_t before = pick[topk];
+      while (__any_sync(0xffffffffu, open)) {  // those that are alike, down to one that lies further off
+        const uint32_t k = keys.next();
+        const int d = open ? doubt(before, k) : 0;
+        unsure |= d == 1;
+        open = d == 2;
+        before = k;
+      }
+    }
+    exact |= (__ballot_sync(0xffffffffu, unsure) & row_lanes) != 0u;
+    picked = row_sum<LPR>(picked);
+    const bool real = there && (!a.mask || a.mask[t]);
+    if (there && !exact) {
+      for (int j = sub; j < topk; j += LPR) {
+        const int id = expert(pick[j]);
+        float w = pick_w[j];
+        if (a.renorm) w = picked == 0.0f ? 0.0f : __fdiv_rn(w, picked);
+        a.ids[t * topk + j] = id;
+        a.weights[t * topk + j] = real ? w * a.scale : 0.0f;
+        if (real) atomicAdd(cnt + id, 1);  // whole numbers: the order does not matter
+      }
+    }
+    uint32_t rest = __ballot_sync(0xffffffffu, there && exact && sub == 0);
+    while (rest) {
+      const int64_t at = t0 + (__ffs(rest) - 1) / LPR;
+      rest &= rest - 1;
+      int id;
+      float w;
+      route_row<TL>(a, at, choice, id, w);
+      put_row(a, at, id, w, cnt);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    if (gridDim.x == 1) a.counts[e] = cnt[e];
+    else if (cnt[e]) atomicAdd(a.counts + e, cnt[e]);
+  }
+}
+
+// How a row falls into lanes: VPL experts a lane (8 or 16; 0: the general form), LPR lanes a row.
+struct RouteForm {
+  int vpl, lpr, log_groups;
+};
+int ceil_log2(int v) {
+  int k = 0;
+  while (1 << k < v) ++k;
+  return k;
+}
+RouteForm route_form(int E, int groups) {
+  const int per = E / groups, g = ceil_log2(groups);
+  for (int vpl = 8; vpl <= 16; vpl *= 2) {
+    const int lpr = g + ceil_log2((per + vpl - 1) / vpl);
+    if (lpr <= 5) return {vpl, vpl == 16 ? 32 : std::max(4, 1 << lpr), g};
+  }
+  return {0, 32, g};
+}
+
+template <typename TL, int VPL, int LPR, bool KEYS16>
+int route_launch(const RouteArgs& a, const DeviceInfo* dev, cudaStream_t s) {
+  constexpr int G = 32 / LPR;
+  const int64_t groups = (a.T + G - 1) / G;
+  // one CTA where its 32 warps take no more than two rounds: it writes the counts itself
+  const int64_t ctas = groups <= 2 * kRouteFastWarps
+                           ? 1 : std::min<int64_t>((groups + kRouteFastWarps - 1) / kRouteFastWarps, dev->sm_count);
+  const int warps = static_cast<int>(std::min<int64_t>(kRouteFastWarps, groups));
+  if (ctas > 1 && cudaMemsetAsync(a.counts, 0, static_cast<size_t>(a.E) * 4, s) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  const size_t smem = static_cast<size_t>(warps) * (8 * route_doubles(a.E) + 4 * route_warp_words<TL, VPL, LPR>(a.topk)) +
+                      static_cast<size_t>((a.E + 3) / 4 * 4) * 4;
+  auto kernel = moe_route_kernel<TL, VPL, LPR, KEYS16>;
+  const int st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
+  if (st != FP8G_OK) return st;
+  kernel<<<static_cast<unsigned>(ctas), 32 * warps, smem, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+}
+template <typename TL, bool KEYS16>
+int route_any_lanes(const RouteArgs& a, const RouteForm& f, const DeviceInfo* dev, cudaStream_t s) {
+  if (f.vpl == 16) return route_launch<TL, 16, 32, KEYS16>(a, dev, s);
+  switch (f.lpr) {
+    case 4: return route_launch<TL, 8, 4, KEYS16>(a, dev, s);
+    case 8: return route_launch<TL, 8, 8, KEYS16>(a, dev, s);
+    case 16: return route_launch<TL, 8, 16, KEYS16>(a, dev, s);
+    default: return route_launch<TL, 8, 32, KEYS16>(a, dev, s);
   }
 }
 
@@ -232,17 +612,24 @@ extern "C" int fp8g_moe_route(const void* logits, int32_t dtype, int64_t T, int3
   st = current_device(&dev);
   if (st != FP8G_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  RouteArgs a{};
+  a.logits = logits, a.bias = bias, a.mask = token_mask, a.ids = topk_ids, a.weights = topk_weights, a.counts = counts;
+  a.T = T, a.ldl = ldl, a.E = E, a.topk = topk, a.groups = groups, a.kept = topk_groups, a.softmax = score;
+  a.renorm = renormalize, a.scale = scale;
+  const RouteForm f = route_form(E, groups);
+  a.log_groups = f.log_groups;
+  a.vec = aligned16(logits) && (T == 1 || ldl % 8 == 0) && E / groups % 8 == 0;
+  if (f.vpl && T > 0) {
+    if (dtype == FP8G_F32) return route_any_lanes<float, false>(a, f, dev, s);
+    return bias ? route_any_lanes<__nv_bfloat16, false>(a, f, dev, s) : route_any_lanes<__nv_bfloat16, true>(a, f, dev, s);
+  }
   if (cudaMemsetAsync(counts, 0, static_cast<size_t>(E) * 4, s) != cudaSuccess) {
     cudaGetLastError();
     return FP8G_ERR_CUDA;
   }
   if (T == 0) return FP8G_OK;
-  RouteArgs a{};
-  a.logits = logits, a.bias = bias, a.mask = token_mask, a.ids = topk_ids, a.weights = topk_weights, a.counts = counts;
-  a.T = T, a.ldl = ldl, a.E = E, a.topk = topk, a.groups = groups, a.kept = topk_groups, a.softmax = score;
-  a.renorm = renormalize, a.scale = scale;
   const size_t smem = sizeof(double) * kRouteWarps * static_cast<size_t>(E);
-  auto kernel = dtype == FP8G_F32 ? moe_route_kernel<float> : moe_route_kernel<__nv_bfloat16>;
+  auto kernel = dtype == FP8G_F32 ? moe_route_any_kernel<float> : moe_route_any_kernel<__nv_bfloat16>;
   st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (st != FP8G_OK) return st;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>((T + kRouteWarps - 1) / kRouteWarps, 8 * dev->sm_count));
