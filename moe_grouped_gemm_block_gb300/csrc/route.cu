@@ -33,7 +33,7 @@ struct RouteArgs {
   const float* dweights;
   void* dlogits;
   int64_t T, ldl, ldd;
-  int32_t E, topk, groups, kept, log_groups, softmax, renorm, vec;
+  int32_t E, topk, groups, kept, log_groups, softmax, renorm, vec, single;
   float scale;
 };
 
@@ -48,13 +48,24 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// One row by a warp, in 64 bits.  `c`: E doubles of the warp's own.  A place that holds NaN is not to be had (a score
-// that is not a number ranks first: it stands as infinity).
+// The order of doubles as an unsigned integer (this GPU compares those many times faster): what is not a number stands as
+// infinity, and so ranks first; 0 is below every value's key.
+__device__ __forceinline__ uint64_t order_key(double v) {
+  if (!(v == v)) v = INFINITY;
+  const int64_t u = __double_as_longlong(v + 0.0);
+  return static_cast<uint64_t>(u) ^ (static_cast<uint64_t>(u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_value(uint64_t key) {
+  return __longlong_as_double(static_cast<int64_t>(key & 0x8000000000000000ull ? key ^ 0x8000000000000000ull : ~key));
+}
+constexpr uint64_t kRuledOut = 0x000FFFFFFFFFFFFFull;  // the key of -inf
+
+// One row by a warp, in 64 bits.  `key`: E words of the warp's own, the experts' keys (0: not to be had).
 template <typename TL>
-__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, double* c, int& pick, float& weight) {
+__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
   const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups;
   const TL* row = static_cast<const TL*>(a.logits) + t * a.ldl;
-  const double nan = __longlong_as_double(0x7FF8000000000000LL), inf = INFINITY;
+  const double inf = INFINITY;
   double mx = 0.0, inv = 1.0;
   if (a.softmax) {
     mx = -inf;
@@ -67,57 +78,65 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, double* c,
     inv = s == 0.0 ? 0.0 : 1.0 / s;
   }
   auto score = [&](double l) { return a.softmax ? exp(l - mx) * inv : 1.0 / (1.0 + exp(-l)); };
+  const bool scored = a.bias || a.groups > 1;
   for (int e = lane; e < E; e += 32) {
-    const double l = to_f32(row[e]), b = a.bias ? static_cast<double>(a.bias[e]) : 0.0;
-    const double v = l == -inf || b == -inf ? -inf : score(l) + b;
-    c[e] = v == v ? v : inf;
+    const float l = to_f32(row[e]), b = a.bias ? a.bias[e] : 0.0f;
+    if (l == -INFINITY || b == -INFINITY) key[e] = kRuledOut;
+    else if (scored) key[e] = order_key(score(l) + static_cast<double>(b));
   }
   __syncwarp();
   uint32_t open = 0xffffffffu;
+  const int log_l = 5 - a.log_groups, L = 1 << log_l, group = lane >> log_l;
   if (a.groups > 1) {
-    double first = -inf, second = -inf;
-    if (lane < a.groups)
-      for (int i = 0; i < per; ++i) {
-        const double v = c[lane * per + i];
-        if (v > first) second = first, first = v;
-        else if (v > second) second = v;
+    uint64_t first = 0, second = 0;
+    if (group < a.groups)
+      for (int i = lane & (L - 1); i < per; i += L) {
+        const uint64_t v = key[group * per + i];
+        second = max(second, min(first, v));
+        first = max(first, v);
       }
-    const double mine = second == -inf ? first : first + second;
+    for (int off = 1; off < L; off <<= 1) {
+      const uint64_t o1 = __shfl_xor_sync(0xffffffffu, first, off), o2 = __shfl_xor_sync(0xffffffffu, second, off);
+      second = max(max(second, o2), min(first, o1));
+      first = max(first, o1);
+    }
+    const uint64_t mine = second <= kRuledOut ? first : order_key(key_value(first) + key_value(second));
     int better = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const double other = __shfl_sync(0xffffffffu, mine, g);
-      better += other > mine || (other == mine && g < lane) ? 1 : 0;
+      const uint64_t other = __shfl_sync(0xffffffffu, mine, g << log_l);
+      better += other > mine || (other == mine && g < group) ? 1 : 0;
     }
-    open = __ballot_sync(0xffffffffu, lane < a.groups && better < a.kept);
+    open = __ballot_sync(0xffffffffu, group < a.groups && better < a.kept);
   }
+  uint64_t best = 0;
+  int at = kRouteMaxExperts;
   for (int e = lane; e < E; e += 32) {
-    double v = c[e];
-    if (!a.bias && v != -inf) {  // the scores order as the logits do
-      v = to_f32(row[e]);
-      v = v == v ? v : inf;
-    }
-    c[e] = open >> (e / per) & 1u ? v : nan;
+    uint64_t v = scored ? key[e] : 0;
+    if (!a.bias) v = order_key(static_cast<double>(to_f32(row[e])));  // the scores order as the logits do
+    v = open >> (e / per << log_l) & 1u ? v : 0;
+    key[e] = v;
+    if (v > best) best = v, at = e;
   }
   pick = 0;
   for (int j = 0; j < a.topk; ++j) {
-    double best = nan;
-    int at = kRouteMaxExperts;
-    for (int e = lane; e < E; e += 32)
-      if (c[e] > best || (best != best && c[e] == c[e])) best = c[e], at = e;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double v = __shfl_xor_sync(0xffffffffu, best, off);
-      const int i = __shfl_xor_sync(0xffffffffu, at, off);
-      if (v > best || (v == best && i < at) || (best != best && v == v)) best = v, at = i;
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = hi == top ? static_cast<uint32_t>(best) : 0u, low = __reduce_max_sync(0xffffffffu, lo);
+    const uint32_t e = hi == top && lo == low ? static_cast<uint32_t>(at) : kRouteMaxExperts;
+    const int one = static_cast<int>(__reduce_min_sync(0xffffffffu, e));
+    if (lane == j) pick = min(one, E - 1);
+    if (one == at && one < E) {  // its lane looks for its next one
+      key[one] = 0;
+      best = 0;
+      at = kRouteMaxExperts;
+      for (int i = lane; i < E; i += 32)
+        if (key[i] > best) best = key[i], at = i;
     }
-    if (lane == j) pick = min(at, E - 1);
-    if ((at & 31) == lane && at < E) c[at] = nan;
     __syncwarp();
   }
   weight = 0.0f;
   if (lane < a.topk) {
-    const double l = to_f32(row[pick]);
-    weight = l == -inf || (a.bias && a.bias[pick] == -INFINITY) ? 0.0f : static_cast<float>(score(l));
+    const float l = to_f32(row[pick]);
+    if (!(l == -INFINITY || (a.bias && a.bias[pick] == -INFINITY))) weight = static_cast<float>(score(l));
   }
   __syncwarp();
 }
@@ -138,7 +157,7 @@ __device__ __forceinline__ void put_row(const RouteArgs& a, int64_t t, int id, f
 // The general form: every row in 64 bits (2.7 ms for 65536 x 256).
 template <typename TL>
 __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const __grid_constant__ RouteArgs a) {
-  extern __shared__ __align__(16) double choice[];
+  extern __shared__ __align__(16) uint64_t choice[];
   const int warp = threadIdx.x >> 5;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += gridDim.x * kRouteWarps) {
     int id;
@@ -167,13 +186,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
 // Rows with a logit that is NaN or +inf, with fewer experts left than are to be chosen, or with a group that has a single
 // one left, go there too.  65536 x 256 normal logits: one row in 2000.
 constexpr int kRouteFastWarps = 32;
+constexpr int kRouteCluster = 8;
 constexpr float kGrid = 8388608.0f;  // 2^23
-// Shared memory, every part a multiple of 16 bytes: a row of doubles a warp, the CTA's counts, then a warp's lists of
+// Shared memory, every part a multiple of 16 bytes: a row of 64-bit keys a warp, the CTA's counts, then a warp's lists of
 // keys, its rows' picks and their scores.
-__host__ __device__ constexpr int route_doubles(int E) { return (E + 1) / 2 * 2; }
+__host__ __device__ constexpr int route_keys(int E) { return (E + 1) / 2 * 2; }
 template <typename TL, int VPL, int LPR>
 __host__ __device__ constexpr int route_warp_words(int topk) {
   return (VPL == 8 ? 32 * 12 : 0) + ((32 / LPR) * (2 * topk + 1) + 3) / 4 * 4;
+}
+
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // The lane's keys by rank, as the row's lanes take them: `next` gives the row's largest that is left (0: none).
@@ -225,15 +251,15 @@ struct KeyList<16, LPR> {  // unsorted: what is below the last pick, anew each t
 template <typename TL, int VPL, int LPR, bool KEYS16>
 __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(const __grid_constant__ RouteArgs a) {
   constexpr int G = 32 / LPR;  // rows a warp at once
-  extern __shared__ __align__(16) double smem64[];
+  extern __shared__ __align__(16) uint64_t smem64[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int sub = lane % LPR, grp = lane / LPR;
   const uint32_t row_lanes = (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u) << (lane & ~(LPR - 1));
   const int E = a.E, topk = a.topk, per = E / a.groups, L = LPR >> a.log_groups, log_l = 31 - __clz(L);
   const int group = sub >> log_l, base = group * per + (sub & (L - 1)) * VPL;
   const int end = group < a.groups ? group * per + per : 0;
-  double* choice = smem64 + warp * route_doubles(E);
-  uint32_t* words = reinterpret_cast<uint32_t*>(smem64 + warps * route_doubles(E));
+  uint64_t* choice = smem64 + warp * route_keys(E);
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem64 + warps * route_keys(E));
   int32_t* cnt = reinterpret_cast<int32_t*>(words);
   uint32_t* mine = words + (E + 3) / 4 * 4 + warp * route_warp_words<TL, VPL, LPR>(topk);
   uint32_t* list = mine + lane * 12;
@@ -465,10 +491,25 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
     __syncwarp();
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    if (gridDim.x == 1) a.counts[e] = cnt[e];
-    else if (cnt[e]) atomicAdd(a.counts + e, cnt[e]);
+  if (a.single) {  // one cluster: each CTA joins a share of the counts
+    cluster_sync();
+    const int ranks = static_cast<int>(gridDim.x), each = (E + ranks - 1) / ranks, lo = blockIdx.x * each;
+    for (int e = lo + static_cast<int>(threadIdx.x); e < min(E, lo + each); e += blockDim.x) {
+      int32_t n = 0;
+      for (int r = 0; r < ranks; ++r) n += ld_cluster_s32(mapa_shared(smem_u32(cnt + e), r));
+      a.counts[e] = n;
+    }
+    cluster_sync();  // (nobody leaves while its counts may still be read)
+    return;
   }
+  griddep_wait();  // the counts are zero
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    if (cnt[e]) atomicAdd(a.counts + e, cnt[e]);
+}
+
+__global__ void moe_route_zero_kernel(int32_t* counts, int32_t E) {
+  griddep_launch_dependents();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) counts[e] = 0;
 }
 
 // How a row falls into lanes: VPL experts a lane (8 or 16; 0: the general form), LPR lanes a row.
@@ -493,21 +534,40 @@ template <typename TL, int VPL, int LPR, bool KEYS16>
 int route_launch(const RouteArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   constexpr int G = 32 / LPR;
   const int64_t groups = (a.T + G - 1) / G;
-  // one CTA where its 32 warps take no more than two rounds: it writes the counts itself
-  const int64_t ctas = groups <= 2 * kRouteFastWarps
-                           ? 1 : std::min<int64_t>((groups + kRouteFastWarps - 1) / kRouteFastWarps, dev->sm_count);
-  const int warps = static_cast<int>(std::min<int64_t>(kRouteFastWarps, groups));
-  if (ctas > 1 && cudaMemsetAsync(a.counts, 0, static_cast<size_t>(a.E) * 4, s) != cudaSuccess) {
-    cudaGetLastError();
-    return FP8G_ERR_CUDA;
-  }
-  const size_t smem = static_cast<size_t>(warps) * (8 * route_doubles(a.E) + 4 * route_warp_words<TL, VPL, LPR>(a.topk)) +
+  // Few rows: one cluster, which joins the counts itself.  More: the counts are zeroed by a launch before, under whose
+  // end this one starts, and added up.
+  const bool single = groups <= kRouteCluster * 16;
+  const int64_t ctas = single ? std::min<int64_t>(kRouteCluster, groups) : std::min<int64_t>((groups + 3) / 4, dev->sm_count);
+  const int warps = static_cast<int>(std::min<int64_t>(kRouteFastWarps, (groups + ctas - 1) / ctas));
+  const size_t smem = static_cast<size_t>(warps) * (8 * route_keys(a.E) + 4 * route_warp_words<TL, VPL, LPR>(a.topk)) +
                       static_cast<size_t>((a.E + 3) / 4 * 4) * 4;
   auto kernel = moe_route_kernel<TL, VPL, LPR, KEYS16>;
   const int st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (st != FP8G_OK) return st;
-  kernel<<<static_cast<unsigned>(ctas), 32 * warps, smem, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  if (!single) moe_route_zero_kernel<<<1, 256, 0, s>>>(a.counts, a.E);
+  RouteArgs args = a;
+  args.single = single ? 1 : 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (single) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return FP8G_ERR_CUDA;
+  }
+  return FP8G_OK;
 }
 template <typename TL, bool KEYS16>
 int route_any_lanes(const RouteArgs& a, const RouteForm& f, const DeviceInfo* dev, cudaStream_t s) {
@@ -628,7 +688,7 @@ extern "C" int fp8g_moe_route(const void* logits, int32_t dtype, int64_t T, int3
     return FP8G_ERR_CUDA;
   }
   if (T == 0) return FP8G_OK;
-  const size_t smem = sizeof(double) * kRouteWarps * static_cast<size_t>(E);
+  const size_t smem = sizeof(uint64_t) * kRouteWarps * static_cast<size_t>(E);
   auto kernel = dtype == FP8G_F32 ? moe_route_any_kernel<float> : moe_route_any_kernel<__nv_bfloat16>;
   st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (st != FP8G_OK) return st;
