@@ -60,6 +60,20 @@ __device__ __forceinline__ double key_value(uint64_t key) {
 }
 constexpr uint64_t kRuledOut = 0x000FFFFFFFFFFFFFull;  // the key of -inf
 
+// e^x for x <= 0, in 64 bits without a branch (0 below 2^-1022): 2^n e^r with |r| <= ln 2 / 2, the series of e^r up to
+// r^13 / 13! (the next term is below 2^-57).  ln 2 in two parts, the first with zeros at its end, so that n times it is exact.
+__device__ __forceinline__ double exp_series(double x) {
+  const double n = rint(x * 1.4426950408889634);
+  const double r = fma(n, -1.90821492927058770002e-10, fma(n, -6.93147180369123816490e-01, x));
+  double p = 1.0 / 6227020800.0;
+  constexpr double c[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                            1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
+#pragma unroll
+  for (int i = 0; i < 13; ++i) p = fma(p, r, c[i]);
+  const int k = static_cast<int>(fmax(n, -1023.0));
+  return x < -708.0 ? 0.0 : p * __longlong_as_double(static_cast<int64_t>(k + 1023) << 52);
+}
+
 // One row by a warp, in 64 bits.  `key`: E words of the warp's own, the experts' keys (0: not to be had).
 template <typename TL>
 __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
@@ -73,16 +87,21 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* 
     mx = warp_max(mx);
     if (mx == -inf) mx = 0.0;
     double s = 0.0;
-    for (int e = lane; e < E; e += 32) s += exp(static_cast<double>(to_f32(row[e])) - mx);
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) s += exp_series(static_cast<double>(to_f32(row[e])) - mx);
     s = warp_sum(s);
     inv = s == 0.0 ? 0.0 : 1.0 / s;
   }
-  auto score = [&](double l) { return a.softmax ? exp(l - mx) * inv : 1.0 / (1.0 + exp(-l)); };
+  auto score = [&](float l) {
+    const double x = exp_series(a.softmax ? static_cast<double>(l) - mx : -fabs(static_cast<double>(l)));
+    return a.softmax ? x * inv : (l < 0.0f ? x : 1.0) * __drcp_rn(1.0 + x);
+  };
   const bool scored = a.bias || a.groups > 1;
+#pragma unroll 4
   for (int e = lane; e < E; e += 32) {
     const float l = to_f32(row[e]), b = a.bias ? a.bias[e] : 0.0f;
-    if (l == -INFINITY || b == -INFINITY) key[e] = kRuledOut;
-    else if (scored) key[e] = order_key(score(l) + static_cast<double>(b));
+    const uint64_t k = scored ? order_key(score(l) + static_cast<double>(b)) : 0;
+    key[e] = l == -INFINITY || b == -INFINITY ? kRuledOut : k;
   }
   __syncwarp();
   uint32_t open = 0xffffffffu;
@@ -191,9 +210,10 @@ constexpr float kGrid = 8388608.0f;  // 2^23
 // Shared memory, every part a multiple of 16 bytes: a row of 64-bit keys a warp, the CTA's counts, then a warp's lists of
 // keys, its rows' picks and their scores.
 __host__ __device__ constexpr int route_keys(int E) { return (E + 1) / 2 * 2; }
-template <typename TL, int VPL, int LPR>
+constexpr int kRouteBatch = 8;  // rows whose picks are worked on at once, at most
+template <int VPL>
 __host__ __device__ constexpr int route_warp_words(int topk) {
-  return (VPL == 8 ? 32 * 12 : 0) + ((32 / LPR) * (2 * topk + 1) + 3) / 4 * 4;
+  return (VPL == 8 ? 32 * 12 : 0) + (kRouteBatch * (topk + 2) + 3) / 4 * 4;
 }
 
 __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
@@ -261,10 +281,10 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
   uint64_t* choice = smem64 + warp * route_keys(E);
   uint32_t* words = reinterpret_cast<uint32_t*>(smem64 + warps * route_keys(E));
   int32_t* cnt = reinterpret_cast<int32_t*>(words);
-  uint32_t* mine = words + (E + 3) / 4 * 4 + warp * route_warp_words<TL, VPL, LPR>(topk);
+  uint32_t* mine = words + (E + 3) / 4 * 4 + warp * route_warp_words<VPL>(topk);
   uint32_t* list = mine + lane * 12;
-  uint32_t* pick = mine + (VPL == 8 ? 32 * 12 : 0) + grp * (topk + 1);
-  float* pick_w = reinterpret_cast<float*>(mine + (VPL == 8 ? 32 * 12 : 0) + G * (topk + 1)) + grp * topk;
+  uint32_t* picks = mine + (VPL == 8 ? 32 * 12 : 0);  // [rows][topk]
+  float2* info = reinterpret_cast<float2*>(picks + (kRouteBatch * topk + 1) / 2 * 2);  // a softmax's maximum and 1 / sum
   if constexpr (VPL == 8) list[8] = list[9] = 0u;
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
@@ -291,7 +311,7 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
   const float range = 1.0f + (high - low);
   all_exact |= !(range < INFINITY);
   const float K = __fdiv_rn(kGrid - 64.0f, range);
-  const float near = a.softmax ? 48.0f : 12.0f;
+  const float near = a.softmax ? 48.0f : 12.0f;  // steps (see above)
   float place[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -317,11 +337,29 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
       }
     }
   };
+  // Picks, scores and results take a lane each, `seg` lanes a row: a whole warp's row waits for others to be worked on
+  // together (65536 x 256, 8 picks: one at a time took a third more instructions).
+  const int log_seg = topk == 1 ? 0 : 32 - __clz(topk - 1), per_pass = 32 >> log_seg;
+  const int batch = LPR == 32 ? min(per_pass, kRouteBatch) : G;
+  const uint32_t least = KEYS16 ? 1u : 512u;  // keys below stand for no expert
+  auto expert = [&](uint32_t k) {
+    const int slot = KEYS16 ? 0xFFFF - static_cast<int>(k & 0xFFFFu) : 511 - static_cast<int>(k & 511u);
+    const int l = slot / VPL;
+    return min((l >> log_l) * per + (l & (L - 1)) * VPL + slot % VPL, E - 1);  // (a void key's slot is no expert's)
+  };
+  // whether two experts have the same logit and the same bias
+  auto alike = [&](const TL* row, uint32_t p, uint32_t q) {
+    const int x = expert(p), y = expert(q);
+    return to_f32(row[x]) == to_f32(row[y]) && (!a.bias || a.bias[x] == a.bias[y]);
+  };
+  auto close = [&](uint32_t hi, uint32_t lo) { return lo >= least && (hi >> 9) - (lo >> 9) <= static_cast<uint32_t>(near); };
+  int waiting = 0;
+  uint32_t exact_rows = 0;  // of those that wait, a bit each
+  int64_t tb = t0;          // the first of them
   if (t0 < a.T) fetch(t0);
   for (; t0 < a.T; t0 += stride) {
-    const int64_t t = t0 + grp;
-    const bool there = t < a.T;
-    const TL* row = logits + (there ? t : a.T - 1) * a.ldl;
+    const TL* row = logits + (t0 + grp < a.T ? t0 + grp : a.T - 1) * a.ldl;
+    uint32_t* pick = picks + (LPR == 32 ? waiting : grp) * topk;
     float f[VPL];
     uint32_t key[VPL];
 #pragma unroll
@@ -343,10 +381,11 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
       }
     }
     if (t0 + stride < a.T) fetch(t0 + stride);
-    float odd = 0.0f;  // NaN where a logit is not finite
+    float2 odds = make_float2(0.0f, 0.0f);  // NaN where a logit is not finite
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) odd = fmaf(f[i], 0.0f, odd);
-    const bool some_odd = __any_sync(0xffffffffu, odd != 0.0f);
+    for (int i = 0; i < VPL / 2; ++i)
+      odds = __ffma2_rn(make_float2(f[2 * i], f[2 * i + 1]), make_float2(0.0f, 0.0f), odds);
+    const bool some_odd = __any_sync(0xffffffffu, odds.x + odds.y != 0.0f);
     bool exact = all_exact;
     if (some_odd) {
       bool bad = false;
@@ -379,8 +418,13 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
       for (int i = 0; i < VPL; ++i) c[i] = fmaf(c[i], by, place[i]);
     } else if (scored) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        c[i] = fmaf(recip_approx(1.0f + exp2_approx(f[i] * -1.4426950408889634f)), K, place[i]);
+      for (int i = 0; i < VPL; i += 2) {
+        float2 v = __fmul2_rn(make_float2(f[i], f[i + 1]), make_float2(-1.4426950408889634f, -1.4426950408889634f));
+        v = __fadd2_rn(make_float2(exp2_approx(v.x), exp2_approx(v.y)), make_float2(1.0f, 1.0f));
+        v = __ffma2_rn(make_float2(recip_approx(v.x), recip_approx(v.y)), make_float2(K, K),
+                       make_float2(place[i], place[i + 1]));
+        c[i] = v.x, c[i + 1] = v.y;
+      }
     }
     if (some_odd && scored) {
 #pragma unroll
@@ -407,88 +451,103 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
         first = fmaxf(first, o1);
       }
       const float sum = per == 1 ? first - kGrid : (first - kGrid) + (second - kGrid);
-      const float above = sum + 2.0f * near, below = sum - 2.0f * near;
-      int surely = 0, maybe = -1;  // groups that are better than this lane's (itself left out)
-      for (int g = 0; g < a.groups; ++g) {
-        const float other = __shfl_sync(0xffffffffu, sum, (lane & ~(LPR - 1)) + g * L);
-        surely += other > above ? 1 : 0;
-        maybe += other > below ? 1 : 0;
+      // the best groups one after the other (a group's lanes have the same key); ties and what lies near a tie at the
+      // border go to route_row
+      uint32_t g = group < a.groups && sum > -INFINITY ? (static_cast<uint32_t>(sum) << 5) + 31u - group : 0u;
+      exact |= (__ballot_sync(0xffffffffu, group < a.groups && g == 0u) & row_lanes) != 0u;
+      uint32_t worst = 0u;
+      bool stays = false;
+      for (int i = 0; i < a.kept; ++i) {
+        worst = row_max<LPR>(g);
+        stays |= g == worst;
+        g = g == worst ? 0u : g;
       }
-      const bool stays = maybe < a.kept;
-      const bool unsure = group < a.groups && (stays != (surely < a.kept) || !(sum > -INFINITY));
-      exact |= (__ballot_sync(0xffffffffu, unsure) & row_lanes) != 0u;
+      const uint32_t out = row_max<LPR>(g);
+      exact |= out != 0u && (worst >> 5) - (out >> 5) <= 2u * static_cast<uint32_t>(near);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = stays ? key[i] : 0u;
     }
     KeyList<VPL, LPR> keys;
     keys.init(key, list);
-    for (int j = 0; j < topk + (KEYS16 ? 0 : 1); ++j) {
-      const uint32_t top = keys.next();
-      if (sub == 0) pick[j] = top;
+    uint32_t last = 0u;
+#pragma unroll 2
+    for (int j = 0; j < topk; ++j) {
+      last = keys.next();
+      if (sub == 0) pick[j] = last;
+    }
+    exact |= last < least;
+    if constexpr (!KEYS16) {  // the last one that is taken and the first that is not
+      uint32_t after = keys.next();
+      bool open = close(last, after);
+      while (__any_sync(0xffffffffu, open)) {  // those that are alike, down to one that lies further off
+        const bool same = open && alike(row, last, after);
+        exact |= open && !same;
+        last = after;
+        after = keys.next();
+        open = same && close(last, after);
+      }
+    }
+    if (sub == 0) info[LPR == 32 ? waiting : grp] = make_float2(mx, inv);
+    if constexpr (LPR == 32) {
+      exact_rows |= exact ? 1u << waiting : 0u;
+      if (++waiting < batch && t0 + stride < a.T) continue;
+    } else {
+      const uint32_t e = __ballot_sync(0xffffffffu, exact);
+      exact_rows = __ballot_sync(0xffffffffu, lane < G && (e >> (lane * LPR & 31) & 1u));
+      waiting = static_cast<int>(min(static_cast<int64_t>(G), a.T - t0));
+      tb = t0;
     }
     __syncwarp();
-    auto expert = [&](uint32_t k) {
-      const int slot = KEYS16 ? 0xFFFF - static_cast<int>(k & 0xFFFFu) : 511 - static_cast<int>(k & 511u);
-      const int l = slot / VPL;
-      return min((l >> log_l) * per + (l & (L - 1)) * VPL + slot % VPL, E - 1);  // (a void key's slot is no expert's)
-    };
-    const uint32_t least = KEYS16 ? 1u : 512u;  // keys below stand for no expert
-    // whether two neighbours in the order may stand the other way round: 0 no, 1 yes, 2 they are alike
-    auto doubt = [&](uint32_t hi, uint32_t lo) {
-      if (lo < least || (hi >> 9) - (lo >> 9) > static_cast<uint32_t>(near)) return 0;
-      const int x = expert(hi), y = expert(lo);
-      return to_f32(row[x]) == to_f32(row[y]) && (!a.bias || a.bias[x] == a.bias[y]) ? 2 : 1;
-    };
-    bool unsure = false, open = false;
-    float picked = 0.0f;
-    for (int j = sub; j < topk; j += LPR) {
-      const uint32_t k = pick[j];
-      const float l = to_f32(row[expert(k)]);
-      float s;
-      if (a.softmax) s = expf(l - mx) * inv;
-      else s = __fdiv_rn(1.0f, 1.0f + expf(-l));
-      unsure |= k < least;
-      if constexpr (!KEYS16) {
-        const int d = doubt(k, pick[j + 1]);
-        unsure |= d == 1;
-        open |= d == 2 && j == topk - 1;  // the last one that is taken and the first that is not
+    const int64_t step = LPR == 32 ? stride : 1;
+    for (int r0 = 0; r0 < waiting; r0 += per_pass) {
+      const int r = r0 + (lane >> log_seg), j = lane & ((1 << log_seg) - 1);
+      const bool has = r < waiting && j < topk;
+      const int64_t t = tb + (r < waiting ? r : 0) * step;
+      int id = 0;
+      float w = 0.0f;
+      bool unsure = false;
+      if (has) {
+        const TL* at = logits + t * a.ldl;
+        const uint32_t k = picks[r * topk + j];
+        id = expert(k);
+        const float l = to_f32(at[id]);
+        if (a.softmax) w = exp_below(l, info[r].x) * info[r].y;
+        else {
+          const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
+          w = l < 0.0f ? x * y : y;
+        }
+        if (!KEYS16 && j + 1 < topk) {
+          const uint32_t q = picks[r * topk + j + 1];
+          unsure = close(k, q) && !alike(at, k, q);
+        }
       }
-      pick_w[j] = s;
-      picked += s;
-    }
-    if constexpr (!KEYS16) {
-      uint32_t before = pick[topk];
-      while (__any_sync(0xffffffffu, open)) {  // those that are alike, down to one that lies further off
-        const uint32_t k = keys.next();
-        const int d = open ? doubt(before, k) : 0;
-        unsure |= d == 1;
-        open = d == 2;
-        before = k;
+      const uint32_t u = __ballot_sync(0xffffffffu, unsure);
+      if (u) {
+        const uint32_t seg = log_seg == 5 ? 0xffffffffu : (1u << (1 << log_seg)) - 1u;
+        exact_rows |= __ballot_sync(0xffffffffu, lane < per_pass && (u >> (lane << log_seg & 31) & seg)) << r0;
       }
-    }
-    exact |= (__ballot_sync(0xffffffffu, unsure) & row_lanes) != 0u;
-    picked = row_sum<LPR>(picked);
-    const bool real = there && (!a.mask || a.mask[t]);
-    if (there && !exact) {
-      for (int j = sub; j < topk; j += LPR) {
-        const int id = expert(pick[j]);
-        float w = pick_w[j];
-        if (a.renorm) w = picked == 0.0f ? 0.0f : __fdiv_rn(w, picked);
+      float all = w;
+      for (int off = 1; off < 1 << log_seg; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+      if (has && !(exact_rows >> r & 1u)) {
+        const bool real = !a.mask || a.mask[t];
+        if (a.renorm) w *= all == 0.0f ? 0.0f : recip_approx(all);
         a.ids[t * topk + j] = id;
         a.weights[t * topk + j] = real ? w * a.scale : 0.0f;
         if (real) atomicAdd(cnt + id, 1);  // whole numbers: the order does not matter
       }
     }
-    uint32_t rest = __ballot_sync(0xffffffffu, there && exact && sub == 0);
-    while (rest) {
-      const int64_t at = t0 + (__ffs(rest) - 1) / LPR;
-      rest &= rest - 1;
+    exact_rows &= (1u << waiting) - 1u;  // (waiting <= 8)
+    while (exact_rows) {
+      const int64_t at = tb + (__ffs(exact_rows) - 1) * step;
+      exact_rows &= exact_rows - 1;
       int id;
       float w;
       route_row<TL>(a, at, choice, id, w);
       put_row(a, at, id, w, cnt);
     }
     __syncwarp();
+    waiting = 0;
+    tb = t0 + stride;
   }
   __syncthreads();
   if (a.single) {  // one cluster: each CTA joins a share of the counts
@@ -539,7 +598,7 @@ int route_launch(const RouteArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   const bool single = groups <= kRouteCluster * 16;
   const int64_t ctas = single ? std::min<int64_t>(kRouteCluster, groups) : std::min<int64_t>((groups + 3) / 4, dev->sm_count);
   const int warps = static_cast<int>(std::min<int64_t>(kRouteFastWarps, (groups + ctas - 1) / ctas));
-  const size_t smem = static_cast<size_t>(warps) * (8 * route_keys(a.E) + 4 * route_warp_words<TL, VPL, LPR>(a.topk)) +
+  const size_t smem = static_cast<size_t>(warps) * (8 * route_keys(a.E) + 4 * route_warp_words<VPL>(a.topk)) +
                       static_cast<size_t>((a.E + 3) / 4 * 4) * 4;
   auto kernel = moe_route_kernel<TL, VPL, LPR, KEYS16>;
   const int st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
