@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libfp8gemm.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "noalloc.cu", "norm.cu", "moe.cu", "clip.cu", "route.cu",
-           "resnorm.cu", "swiglu.cu", "adamw.cu"]
+           "resnorm.cu", "resnorm_grad.cu", "swiglu.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
