@@ -19,57 +19,60 @@
 namespace fp8g {
 namespace {
 
-template <typename TS, typename TB, int LPR, int V, bool VEC>
-__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, V == 4 || !VEC ? 1 : 2) residual_norm_kernel(const ResArgs a) {
+template <typename TS, typename TB, int LPR, int V, int MODE>
+__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE == kAligned ? 2 : 1)
+    residual_norm_kernel(const ResArgs a) {
   __shared__ __align__(16) float red[2][32];
-  extern __shared__ __align__(16) unsigned char stage_memory[];
-  using Cols = Columns<VEC, V>;
-  constexpr int kRows = LPR ? 256 / (LPR ? LPR : 1) : 1;
-  const int mine = LPR ? static_cast<int>(threadIdx.x) / (LPR ? LPR : 1) : 0;
-  const Cols col{LPR ? static_cast<int>(threadIdx.x) % (LPR ? LPR : 1) : static_cast<int>(threadIdx.x),
-                 LPR ? LPR : static_cast<int>(blockDim.x), a.N,
-                 VEC && a.M > 1 ? static_cast<int>((blockIdx.x * kRows + mine) % 8 * (a.ldx & 7)) & 7 : 0};
-  if (!LPR) res_sum_init(red);
-  const uint32_t slots = smem_u32(stage_memory), f_at = blockDim.x * Cols::template slot_bytes<TS>();
-  const uint32_t stage = f_at + (a.f ? blockDim.x * Cols::template slot_bytes<TB>() : 0u);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  const TS* x_rows = static_cast<const TS*>(a.x);
-  const TB* f_rows = static_cast<const TB*>(a.f);
-  // the weights of y, and of f: post gate scale
-  float* kept = reinterpret_cast<float*>(stage_memory + a.stages * stage);
-  float *kept_w = nullptr, *kept_f = nullptr;
-  const bool f_weights = a.post || a.gate;
-  if (a.keep) {
-    if (a.w) col.keep_weights(kept_w = kept, a.w, nullptr, a.w_kind, 1.0f);
-    if (f_weights) col.keep_weights(kept_f = kept + (a.w ? blockDim.x * Cols::weight_bytes() / 4 : 0), a.post, a.gate, a.w_kind, a.scale);
-  }
-  auto bring = [&](int64_t m, int s) {
-    if (m < a.M) {
-      col.copy(slots + s * stage, x_rows + m * a.ldx);
-      if (f_rows) col.copy(slots + s * stage + f_at, f_rows + m * a.ldf);
+  extern __shared__ __align__(16) unsigned char shared[];
+  using Cols = Columns<MODE, V>;
+  using SX = Source<TS, MODE, V>;
+  using SF = Source<TB, MODE, V>;
+  FP8G_RES_ROWS(a.ldx)
+  if (!LPR) res_sum_init(red, a.ranks);
+  // the weights of y, and of f: post gate scale; the stages
+  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * V * blockDim.x;
+  col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
+  if (a.f) col.keep_weights(f_at, a.post, a.gate, a.w_kind, a.scale);
+  const uint32_t stages = smem_u32(a.f ? f_at + 2 * V * blockDim.x : f_at);
+  const uint32_t x_bytes = blockDim.x * SX::thread_bytes(), stage = x_bytes + (a.f ? blockDim.x * SF::thread_bytes() : 0u);
+  SX sx{};
+  SF sf{};
+  int64_t ahead = m_first + mine;  // the row that is copied next
+  sx.init(a.x, ahead, a.ldx, step, stages, stage, a.stages, col);
+  if (a.f) sf.init(a.f, ahead, a.ldf, step, stages + x_bytes, stage, a.stages, col);
+  auto bring = [&](int s) {
+    if (ahead < a.M) {
+      sx.copy(s, col);
+      if (a.f) sf.copy(s, col);
     }
+    if (SX::kStaged) sx.row += sx.step;
+    if (SF::kStaged) sf.row += sf.step;
+    ahead += step;
     cp_async_commit();
   };
   int phase = 0, s = 0;
-  int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  for (int i = 0; i < a.stages; ++i) bring(m0 + mine + i * step, i);
-  for (; m0 < a.M; m0 += step) {
+  for (int i = 0; i < a.stages; ++i) bring(i);
+  for (int64_t m0 = m_first; m0 < a.M; m0 += step) {
     const int64_t m = m0 + mine;
-    const bool real = m < a.M;
+    const bool real = LPR == 0 || m < a.M;
     Raw8<TB> rf[V];
     float2 x[V][4];
     cp_async_wait(a.stages - 1);
+    if (!SX::kStaged && !real) sx.row = nullptr;
+    if (!SF::kStaged && !real) sf.row = nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Raw8<TS> r;
-      col.load(r, slots + s * stage, x_rows + m * a.ldx, v, real);
+      sx.load(r, s, v, col);
       r.get(x[v]);
-      if (f_rows) col.load(rf[v], slots + s * stage + f_at, f_rows + m * a.ldf, v, real);
+      if (a.f) sf.load(rf[v], s, v, col);
     }
-    bring(m + a.stages * step, s);
+    if (!SX::kStaged) sx.row += sx.step;
+    if (!SF::kStaged) sf.row += sf.step;
+    bring(s);
     if (++s == a.stages) s = 0;
-    if (f_rows) {
-      float by = f_weights ? 1.0f : a.scale;
+    if (a.f) {
+      float by = 1.0f;
       if (a.norm_f) {
         float2 sq = both(0.0f);
 #pragma unroll
@@ -79,19 +82,20 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, V == 4 || !VEC ? 1
 #pragma unroll
           for (int j = 0; j < 4; ++j) sq = __ffma2_rn(f[j], f[j], sq);
         }
-        float q = sq.x + sq.y;
-        q = root_inverse(res_sum<LPR>(q, red, phase) * a.inv_n, a.eps);
-        if (col.t == 0 && real && a.rstd_f) a.rstd_f[m] = q;
-        by *= q;
+        by = root_inverse(res_sum<LPR>(sq.x + sq.y, red, phase, a.ranks) * a.inv_n, a.eps);
+        if (col.t == 0 && rank == 0 && real && a.rstd_f) a.rstd_f[m] = by;
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float2 f[4];
         rf[v].get(f);
-        if (f_weights) col.times(kept_f, a.post, a.gate, a.w_kind, a.scale, v, f);
+        col.times(f_at, v, f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[v][j] = __ffma2_rn(both(by), f[j], x[v][j]);
-        if (real && a.h) col.store(static_cast<TS*>(a.h) + m * a.ldh, v, x[v]);
+      }
+      if (real && a.h) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) col.store(static_cast<TS*>(a.h) + m * a.ldh, v, x[v]);
       }
     }
     if (!a.y) continue;
@@ -100,24 +104,24 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, V == 4 || !VEC ? 1
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sq = __ffma2_rn(x[v][j], x[v][j], sq);
-    float q = sq.x + sq.y;
-    q = root_inverse(res_sum<LPR>(q, red, phase) * a.inv_n, a.eps);
-    if (col.t == 0 && real && a.rstd) a.rstd[m] = q;
+    const float r = root_inverse(res_sum<LPR>(sq.x + sq.y, red, phase, a.ranks) * a.inv_n, a.eps);
+    if (col.t == 0 && rank == 0 && real && a.rstd) a.rstd[m] = r;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[v][j] = __fmul2_rn(x[v][j], both(q));
-      if (a.w) col.times(kept_w, a.w, nullptr, a.w_kind, 1.0f, v, x[v]);
+      for (int j = 0; j < 4; ++j) x[v][j] = __fmul2_rn(x[v][j], both(r));
+      col.times(w_at, v, x[v]);
       if (real) col.store(static_cast<TB*>(a.y) + m * a.ldy, v, x[v]);
     }
   }
+  if (!LPR && a.ranks > 1) cluster_sync();  // (nobody leaves while it may still be written to)
 }
 
 // Rows of any length: a CTA a row, which reads it again for each step.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const ResArgs a) {
   __shared__ __align__(16) float red[2][32];
-  res_sum_init(red);
+  res_sum_init(red, 1);
   int phase = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const TS* x = static_cast<const TS*>(a.x) + m * a.ldx;
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const
     if (f && a.norm_f) {
       float s = 0.0f;
       for (int n = threadIdx.x; n < a.N; n += kResMaxThreads) s = fmaf(to_f32(f[n]), to_f32(f[n]), s);
-      s = root_inverse(res_sum<0>(s, red, phase) * a.inv_n, a.eps);
+      s = root_inverse(res_sum<0>(s, red, phase, 1) * a.inv_n, a.eps);
       if (threadIdx.x == 0 && a.rstd_f) a.rstd_f[m] = s;
       by *= s;
     }
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const
         const float v = value(n);
         s = fmaf(v, v, s);
       }
-      s = root_inverse(res_sum<0>(s, red, phase) * a.inv_n, a.eps);
+      s = root_inverse(res_sum<0>(s, red, phase, 1) * a.inv_n, a.eps);
       if (threadIdx.x == 0 && a.rstd) a.rstd[m] = s;
     }
     for (int n = threadIdx.x; n < a.N; n += kResMaxThreads) {  // (h may be x: a value is read before it is written)
@@ -157,35 +161,29 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const
   }
 }
 
-template <typename TS, typename TB, bool VEC>
-int res_forward(ResArgs a, bool shifted, const DeviceInfo* dev, cudaStream_t s) {
-  const ResForm f = res_form(a.N, shifted, false);
-  auto go = f.lpr == 8    ? residual_norm_kernel<TS, TB, VEC ? 8 : 32, 1, VEC>
-            : f.lpr == 16 ? residual_norm_kernel<TS, TB, VEC ? 16 : 32, 1, VEC>
-            : f.lpr == 32 ? (f.v == 1 ? residual_norm_kernel<TS, TB, 32, 1, VEC> : residual_norm_kernel<TS, TB, 32, 2, VEC>)
-            : f.v == 1    ? residual_norm_kernel<TS, TB, 0, 1, VEC>
-            : f.v == 2    ? residual_norm_kernel<TS, TB, 0, 2, VEC>
-                          : residual_norm_kernel<TS, TB, 0, 4, VEC>;
-  const int rows = f.lpr > 0 && !VEC ? 8 : f.rows;
-  const int per_sm = f.v == 4 || f.lpr < 0 ? 1 : std::max(2, 1024 / f.threads);
+template <typename TS, typename TB, int MODE>
+int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
+  constexpr ResMode kMode = static_cast<ResMode>(MODE);
+  const ResForm f = res_form(a.N, kMode, false);
+  const int per_sm = f.ranks > 1 || f.lpr < 0 ? 1 : std::max(2, 1024 / f.threads);
   const int64_t values = static_cast<int64_t>(f.threads) * f.v * 8;
-  const ResShared sh = res_shared(values * ((VEC || sizeof(TS) == 4 ? sizeof(TS) : 0) +
-                                            (a.f && (VEC || sizeof(TB) == 4) ? sizeof(TB) : 0)),
-                                  values * 4 * ((a.w ? 1 : 0) + (a.post || a.gate ? 1 : 0)), per_sm);
-  const bool any = f.lpr < 0 || sh.stages == 0;
-  if (any) {
+  const ResShared sh = res_shared(f.threads * (res_thread_bytes(kMode, f.v, sizeof(TS)) + (a.f ? res_thread_bytes(kMode, f.v, sizeof(TB)) : 0)),
+                                  values * 4 * (a.f ? 2 : 1), 0, per_sm);
+  if (f.lpr < 0 || sh.stages == 0) {
     residual_norm_any_kernel<TS, TB><<<static_cast<unsigned>(std::min<int64_t>(a.M, 2 * dev->sm_count)), kResMaxThreads, 0,
                                        s>>>(a);
-  } else {
-    a.stages = sh.stages;
-    const int st = allow_shared_memory(reinterpret_cast<const void*>(go), sh.bytes + 1024);  // (and what is static)
-    if (st != FP8G_OK) return st;
-    // (a multiple of 8 where a CTA takes more than one row: see Columns)
-    const int64_t ctas = std::min<int64_t>((a.M + rows - 1) / rows, int64_t{1} * dev->sm_count / 8 * 8 * per_sm);
-    a.keep = sh.weights && a.M > 4 * rows * ctas;  // (few rows a CTA: not worth it)
-    go<<<static_cast<unsigned>(ctas), f.threads, static_cast<size_t>(sh.bytes), s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
+  constexpr int kSmall = MODE == kSingle ? 32 : 8, kSome = MODE == kSingle ? 32 : 16;
+  auto go = f.lpr == 8    ? residual_norm_kernel<TS, TB, kSmall, 1, MODE>
+            : f.lpr == 16 ? residual_norm_kernel<TS, TB, kSome, 1, MODE>
+            : f.lpr == 32 ? (f.v == 1 ? residual_norm_kernel<TS, TB, 32, 1, MODE> : residual_norm_kernel<TS, TB, 32, 2, MODE>)
+            : f.v == 1    ? residual_norm_kernel<TS, TB, 0, 1, MODE>
+                          : residual_norm_kernel<TS, TB, 0, 2, MODE>;
+  a.stages = sh.stages, a.ranks = f.ranks;
+  // (row blocks: a multiple of 8 where a CTA takes more than one, see Columns)
+  const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count / f.ranks / 8 * 8 * per_sm);
+  return res_launch(go, blocks * f.ranks, f.threads, sh.bytes, f.ranks, a, s);
 }
 
 }  // namespace
@@ -216,13 +214,17 @@ extern "C" int fp8g_residual_rms_norm(const void* x, int64_t ldx, const void* f,
   a.h = h, a.ldh = ldh, a.y = y, a.ldy = ldy, a.rstd = rstd, a.rstd_f = rstd_f;
   a.M = M, a.N = static_cast<int32_t>(N), a.w_kind = w_dtype, a.norm_f = post_norm;
   a.scale = scale, a.eps = eps, a.inv_n = 1.0f / static_cast<float>(N);
-  const ResGrid grid = res_grid(M, N, {{x, ldx}, {f, ldf}, {h, ldh}, {y, ldy}});
-  const bool vec = grid != ResGrid::kNone;
+  const ResMode mode = res_mode(M, N, {{x, ldx}, {f, ldf}, {h, ldh}, {y, ldy}});
   using B = __nv_bfloat16;
+  auto pick = [mode](auto aligned, auto shifted, auto single) {
+    return mode == kAligned ? aligned : mode == kShifted ? shifted : single;
+  };
   auto go = stream_dtype == FP8G_F32
-                ? (block_dtype == FP8G_F32 ? (vec ? res_forward<float, float, true> : res_forward<float, float, false>)
-                                           : (vec ? res_forward<float, B, true> : res_forward<float, B, false>))
-                : (block_dtype == FP8G_F32 ? (vec ? res_forward<B, float, true> : res_forward<B, float, false>)
-                                           : (vec ? res_forward<B, B, true> : res_forward<B, B, false>));
-  return go(a, grid == ResGrid::kShifted, dev, static_cast<cudaStream_t>(stream));
+                ? (block_dtype == FP8G_F32
+                       ? pick(res_forward<float, float, kAligned>, res_forward<float, float, kShifted>, res_forward<float, float, kSingle>)
+                       : pick(res_forward<float, B, kAligned>, res_forward<float, B, kShifted>, res_forward<float, B, kSingle>))
+                : (block_dtype == FP8G_F32
+                       ? pick(res_forward<B, float, kAligned>, res_forward<B, float, kShifted>, res_forward<B, float, kSingle>)
+                       : pick(res_forward<B, B, kAligned>, res_forward<B, B, kShifted>, res_forward<B, B, kSingle>));
+  return go(a, dev, static_cast<cudaStream_t>(stream));
 }

@@ -8,173 +8,149 @@
 namespace fp8g {
 namespace {
 
-// (V 4: a row's values are read again from their stage for the second step, instead of held in registers.)
-template <typename TS, typename TB, int LPR, int V, bool VEC>
-__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1)
-    residual_norm_backward_kernel(const ResArgs a) {
+template <typename TS, typename TB, int LPR, int V, int MODE>
+__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) residual_norm_backward_kernel(const ResArgs a) {
   __shared__ __align__(16) float red[2][32];
-  extern __shared__ __align__(16) unsigned char stage_memory[];  // (in the end, LPR: [2][N] sums)
-  using Cols = Columns<VEC, V>;
-  constexpr bool kAgain = V == 4;
+  extern __shared__ __align__(16) unsigned char shared[];  // (in the end, LPR: [2][N] sums)
+  using Cols = Columns<MODE, V>;
+  using SS = Source<TS, MODE, V>;
+  using SB = Source<TB, MODE, V>;
   griddep_launch_dependents();
-  constexpr int kRows = LPR ? 256 / (LPR ? LPR : 1) : 1;
-  const int mine = LPR ? static_cast<int>(threadIdx.x) / (LPR ? LPR : 1) : 0;
-  const Cols col{LPR ? static_cast<int>(threadIdx.x) % (LPR ? LPR : 1) : static_cast<int>(threadIdx.x),
-                 LPR ? LPR : static_cast<int>(blockDim.x), a.N,
-                 VEC && a.M > 1 ? static_cast<int>((blockIdx.x * kRows + mine) % 8 * (a.lddx & 7)) & 7 : 0};
-  if (!LPR) res_sum_init(red);
-  const uint32_t slots = smem_u32(stage_memory);
-  const uint32_t one_s = blockDim.x * Cols::template slot_bytes<TS>(), one_b = blockDim.x * Cols::template slot_bytes<TB>();
-  const uint32_t y_at = one_s, dh_at = a.dy ? one_s + one_b : 0u, f_at = dh_at + (a.dh ? one_s : 0u);
-  const uint32_t stage = f_at + (a.f ? one_b : 0u);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  const TS *h_rows = static_cast<const TS*>(a.x), *dh_rows = static_cast<const TS*>(a.dh);
-  const TB *dy_rows = static_cast<const TB*>(a.dy), *f_rows = static_cast<const TB*>(a.f);
-  // the weights of dy, and of dx: post gate scale
-  float* kept = reinterpret_cast<float*>(stage_memory + a.stages * stage);
-  float *kept_w = nullptr, *kept_f = nullptr;
-  const bool w_weights = a.dy && a.w, f_weights = a.df && (a.post || a.gate);
-  if (a.keep) {
-    if (w_weights) col.keep_weights(kept_w = kept, a.w, nullptr, a.w_kind, 1.0f);
-    if (f_weights) col.keep_weights(kept_f = kept + (w_weights ? blockDim.x * Cols::weight_bytes() / 4 : 0), a.post, a.gate, a.w_kind, a.scale);
-  }
-  auto bring = [&](int64_t m, int s) {
-    if (m < a.M) {
-      const uint32_t to = slots + s * stage;
-      if (dy_rows) {
-        col.copy(to, h_rows + m * a.ldx);
-        col.copy(to + y_at, dy_rows + m * a.lddy);
-      }
-      if (dh_rows) col.copy(to + dh_at, dh_rows + m * a.lddh);
-      if (f_rows) col.copy(to + f_at, f_rows + m * a.ldf);
+  FP8G_RES_ROWS(a.lddx)
+  if (!LPR) res_sum_init(red, a.ranks);
+  // the weights of dy, and of dx: post gate scale; zeros for a matrix that is not there; the stages
+  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * V * blockDim.x;
+  col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
+  col.keep_weights(f_at, a.post, a.gate, a.w_kind, a.scale);
+  const uint32_t one_s = blockDim.x * SS::thread_bytes(), one_b = blockDim.x * SB::thread_bytes();
+  const uint32_t zeros = smem_u32(f_at + 2 * V * blockDim.x);
+  const bool missing = !a.dy || !a.dh || !a.f;
+  const uint32_t h_at = zeros + (missing ? max(one_s, one_b) : 0u), dy_at = h_at + (a.dy ? one_s : 0u);
+  const uint32_t dh_at = dy_at + (a.dy ? one_b : 0u), k_at = dh_at + (a.dh ? one_s : 0u);
+  const uint32_t stage = k_at + (a.f ? one_b : 0u) - h_at;
+  SS sh, sd;
+  SB sy, sf;
+  int64_t ahead = m_first + mine;  // the row that is copied next
+  sh.init(a.dy ? a.x : nullptr, ahead, a.ldx, step, a.dy ? h_at : zeros, stage, a.stages, col);
+  sy.init(a.dy, ahead, a.lddy, step, a.dy ? dy_at : zeros, stage, a.stages, col);
+  sd.init(a.dh, ahead, a.lddh, step, a.dh ? dh_at : zeros, stage, a.stages, col);
+  sf.init(a.f, ahead, a.ldf, step, a.f ? k_at : zeros, stage, a.stages, col);
+  auto advance = [&] {
+    if (a.dy) sh.row += sh.step, sy.row += sy.step;
+    if (a.dh) sd.row += sd.step;
+    if (a.f) sf.row += sf.step;
+  };
+  auto bring = [&](int s) {
+    if (ahead < a.M) {
+      sh.copy(s, col);
+      sy.copy(s, col);
+      sd.copy(s, col);
+      sf.copy(s, col);
     }
+    ahead += step;
     cp_async_commit();
   };
+  // the rows' statistics, a row ahead
+  float next_r = 0.0f, next_rf = 1.0f;
+  auto statistics = [&](int64_t m) {
+    if (m < a.M) {
+      if (a.dy) next_r = a.rstd[m];
+      if (a.norm_f) next_rf = a.rstd_f[m];
+    }
+  };
+  statistics(ahead);
   int phase = 0, st = 0;
   float2 dw[V][4], df_sum[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[v][j] = df_sum[v][j] = both(0.0f);
-  int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  for (int i = 0; i < a.stages; ++i) bring(m0 + mine + i * step, i);
-  // the rows' statistics, a row ahead
-  float next_r = 0.0f, next_rf = 1.0f;
-  auto statistics = [&](int64_t m) {
-    if (m < a.M) {
-      if (dy_rows) next_r = a.rstd[m];
-      if (a.norm_f) next_rf = a.rstd_f[m];
-    }
-  };
-  statistics(m0 + mine);
-  for (; m0 < a.M; m0 += step) {
+  // (where a matrix is not staged but loaded at its row's turn, all keep to one stage)
+  constexpr bool kAhead = SS::kStaged && SB::kStaged;
+  for (int i = 0; i < a.stages; ++i) {
+    bring(i);
+    if (kAhead) advance();
+  }
+  for (int64_t m0 = m_first; m0 < a.M; m0 += step) {
     const int64_t m = m0 + mine;
-    const bool real = m < a.M;
-    const uint32_t from = slots + st * stage;
-    Raw8<TS> rh[V], rd[V];
-    Raw8<TB> ry[V], rf[V];
-    auto load_first = [&](int v) {
-      col.load(rh[v], from, h_rows + m * a.ldx, v, real);
-      col.load(ry[v], from + y_at, dy_rows + m * a.lddy, v, real);
-    };
-    auto load_second = [&](int v) {
-      if (dh_rows) col.load(rd[v], from + dh_at, dh_rows + m * a.lddh, v, real);
-      else rd[v].zero();
-      if (f_rows) col.load(rf[v], from + f_at, f_rows + m * a.ldf, v, real);
-    };
-    const float r = next_r, rf_ = next_rf;
+    const bool real = LPR == 0 || m < a.M;
+    const float r = next_r, rf = next_rf;
     statistics(m + step);
-    cp_async_wait(a.stages - 1);
-    float s = 0.0f;
-    if constexpr (!kAgain) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (dy_rows) load_first(v);
-        load_second(v);
-      }
-      bring(m + a.stages * step, st);
-    }
-    if (dy_rows) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if constexpr (kAgain) load_first(v);
-        float2 g[4], e[4];
-        ry[v].get(g);
-        rh[v].get(e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[j] = __fmul2_rn(e[j], both(r));
-          dw[v][j] = __ffma2_rn(g[j], e[j], dw[v][j]);
-        }
-        if (w_weights) col.times(kept_w, a.w, nullptr, a.w_kind, 1.0f, v, g);
-        float2 sum = both(0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum = __ffma2_rn(g[j], e[j], sum);
-        s += sum.x + sum.y;
-      }
-      s = res_sum<LPR>(s, red, phase) * a.inv_n * r;  // e once more is h r
-    }
-    float2 dx[V][4];
-    float q = 0.0f;
+    Raw8<TS> rh[V], rd[V];
+    Raw8<TB> ry[V], rk[V];
+    cp_async_wait(kAhead ? a.stages - 1 : 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (kAgain) {
-        if (dy_rows) load_first(v);
-        load_second(v);
-      }
-      rd[v].get(dx[v]);
-      if (dy_rows) {
-        float2 g[4], e[4];
-        ry[v].get(g);
-        rh[v].get(e);
-        if (w_weights) col.times(kept_w, a.w, nullptr, a.w_kind, 1.0f, v, g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dx[v][j] = __ffma2_rn(both(r), __ffma2_rn(e[j], both(-s), g[j]), dx[v][j]);
-      }
-      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx[v]);
-      if (!a.df) continue;
-      float2 k[4];
-      if (f_rows) {
-        rf[v].get(k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          k[j] = __fmul2_rn(k[j], both(rf_));
-          df_sum[v][j] = __ffma2_rn(dx[v][j], k[j], df_sum[v][j]);
-        }
-      }
-      if (f_weights) {
-        col.times(kept_f, a.post, a.gate, a.w_kind, a.scale, v, dx[v]);
+      if (real) {
+        sh.load(rh[v], st, v, col);
+        sy.load(ry[v], st, v, col);
+        sd.load(rd[v], st, v, col);
+        sf.load(rk[v], st, v, col);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dx[v][j] = __fmul2_rn(dx[v][j], both(a.scale));
-      }
-      if (a.norm_f) {
-        float2 sum = both(0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum = __ffma2_rn(dx[v][j], k[j], sum);
-        q += sum.x + sum.y;
+        rh[v].zero(), ry[v].zero(), rd[v].zero(), rk[v].zero();
       }
     }
-    if (a.df) {
-      if (a.norm_f) q = res_sum<LPR>(q, red, phase) * a.inv_n;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (a.norm_f) {
-          float2 k[4];
-          if constexpr (kAgain) col.load(rf[v], from + f_at, f_rows + m * a.ldf, v, real);
-          rf[v].get(k);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dx[v][j] = __fmul2_rn(both(rf_), __ffma2_rn(k[j], both(-q * rf_), dx[v][j]));
-        }
-        if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
-      }
-    }
-    if constexpr (kAgain) bring(m + a.stages * step, st);
+    if (!kAhead) advance();
+    bring(st);
+    if (kAhead) advance();
     if (++st == a.stages) st = 0;
+    float2 sum = both(0.0f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float2 g[4], e[4];
+      ry[v].get(g);
+      rh[v].get(e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        e[j] = __fmul2_rn(e[j], both(r));
+        dw[v][j] = __ffma2_rn(g[j], e[j], dw[v][j]);
+      }
+      col.times(w_at, v, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(g[j], e[j], sum);
+    }
+    float s = 0.0f;
+    if (a.dy) s = res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * r;  // e once more is h r
+    float2 dx[V][4];
+    sum = both(0.0f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float2 g[4], e[4], k[4];
+      rd[v].get(dx[v]);
+      ry[v].get(g);
+      rh[v].get(e);
+      rk[v].get(k);
+      col.times(w_at, v, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dx[v][j] = __ffma2_rn(both(r), __ffma2_rn(e[j], both(-s), g[j]), dx[v][j]);
+      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx[v]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        k[j] = __fmul2_rn(k[j], both(rf));
+        df_sum[v][j] = __ffma2_rn(dx[v][j], k[j], df_sum[v][j]);
+      }
+      col.times(f_at, v, dx[v]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(dx[v][j], k[j], sum);
+    }
+    if (!a.df) continue;
+    float by = 1.0f, c = 0.0f;
+    if (a.norm_f) {
+      by = rf;
+      c = -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * rf;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float2 k[4];
+      rk[v].get(k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dx[v][j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[v][j]));
+      if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
+    }
   }
+  if (!LPR && a.ranks > 1) cluster_sync();  // (nobody leaves while it may still be written to)
   if (!a.parts) return;
-  float* out = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  float* out = a.parts + block * 2 * a.N;
   if constexpr (LPR == 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -186,19 +162,19 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1)
         }
   } else {
     // the CTA's rows one after the other (their columns may lie shifted)
-    float* sums = reinterpret_cast<float*>(stage_memory);
+    float* sums = reinterpret_cast<float*>(shared);
     cp_async_wait(0);
-    __syncthreads();  // nobody's stage is in use any more
-    for (int r = 0; r < kRows; ++r) {
-      if (mine == r) {
+    __syncthreads();  // nobody's places are in use any more
+    for (int q = 0; q < kRows; ++q) {
+      if (mine == q) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (col.has(v, j)) {
               float* p = sums + col.at(v, j);
-              p[0] = (r ? p[0] : 0.0f) + (j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x);
-              p[a.N] = (r ? p[a.N] : 0.0f) + (j & 1 ? df_sum[v][j / 2].y : df_sum[v][j / 2].x);
+              p[0] = (q ? p[0] : 0.0f) + (j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x);
+              p[a.N] = (q ? p[a.N] : 0.0f) + (j & 1 ? df_sum[v][j / 2].y : df_sum[v][j / 2].x);
             }
       }
       __syncthreads();
@@ -213,7 +189,7 @@ template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_kernel(const ResArgs a) {
   __shared__ __align__(16) float red[2][32];
   griddep_launch_dependents();
-  res_sum_init(red);
+  res_sum_init(red, 1);
   int phase = 0;
   float* out = a.parts ? a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.N : nullptr;
   if (out)
@@ -228,7 +204,7 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_ker
     float s = 0.0f, s2 = 0.0f;
     if (dy) {
       for (int n = threadIdx.x; n < a.N; n += kResMaxThreads) s = fmaf(grad_y(n), to_f32(h[n]), s);
-      s = res_sum<0>(s, red, phase) * a.inv_n * r * r;
+      s = res_sum<0>(s, red, phase, 1) * a.inv_n * r * r;
     }
     auto grad_x = [&](int n) {
       const float d = dh ? to_f32(dh[n]) : 0.0f;
@@ -242,7 +218,7 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_ker
     };
     if (a.df && a.norm_f) {
       for (int n = threadIdx.x; n < a.N; n += kResMaxThreads) s2 = fmaf(grad_u(grad_x(n), n), to_f32(f[n]), s2);
-      s2 = res_sum<0>(s2, red, phase) * a.inv_n * rf * rf;
+      s2 = res_sum<0>(s2, red, phase, 1) * a.inv_n * rf * rf;
     }
     for (int n = threadIdx.x; n < a.N; n += kResMaxThreads) {  // (dx may be dh: read before it is written)
       const float dx = grad_x(n);
@@ -292,49 +268,49 @@ __global__ void __launch_bounds__(256) residual_norm_join_kernel(const ResJoin a
 
 // CTAs that are resident on an SM: 512 threads of 128 registers.
 int res_grad_per_sm(const ResForm& f) { return f.lpr > 0 ? 2 : f.lpr < 0 ? 1 : std::min(4, std::max(1, 512 / f.threads)); }
-// CTAs of a call: rows have to stay with their CTA for the column sums, so no more than are resident.
-int64_t res_grad_ctas(const ResForm& f, int64_t M) {
-  return std::min<int64_t>((M + f.rows - 1) / f.rows, 152 * res_grad_per_sm(f));
+// Blocks of rows, and partial sums, of a call: rows stay with their CTAs for the column sums, so no more than are resident
+// (and, where a block takes several rows, a multiple of 8 of them, see Columns).
+int64_t res_grad_blocks(const ResForm& f, int64_t M) {
+  return std::min<int64_t>((M + f.rows - 1) / f.rows, f.ranks > 1 ? 72 : 152 * res_grad_per_sm(f));
 }
 
-template <typename TS, typename TB, bool VEC>
-int res_backward(ResArgs a, const ResJoin& j, bool shifted, cudaStream_t s) {
-  const ResForm f = res_form(a.N, shifted, true);
-  unsigned ctas = static_cast<unsigned>(res_grad_ctas(f, a.M));
-  auto go = f.lpr == 8    ? residual_norm_backward_kernel<TS, TB, VEC ? 8 : 32, 1, VEC>
-            : f.lpr == 16 ? residual_norm_backward_kernel<TS, TB, VEC ? 16 : 32, 1, VEC>
-            : f.lpr == 32 ? (f.v == 1 ? residual_norm_backward_kernel<TS, TB, 32, 1, VEC>
-                                      : residual_norm_backward_kernel<TS, TB, 32, 2, VEC>)
-            : f.v == 2    ? residual_norm_backward_kernel<TS, TB, 0, 2, VEC>
-                          : residual_norm_backward_kernel<TS, TB, 0, 4, VEC>;
-  if (ctas) {
-    const int64_t ts = VEC || sizeof(TS) == 4 ? sizeof(TS) : 0, tb = VEC || sizeof(TB) == 4 ? sizeof(TB) : 0;
-    const int64_t values = static_cast<int64_t>(f.threads) * f.v * 8;
-    const ResShared sh = res_shared(values * ((a.dy ? ts + tb : 0) + (a.dh ? ts : 0) + (a.f ? tb : 0)),
-                                    values * 4 * ((a.dy && a.w ? 1 : 0) + (a.df && (a.post || a.gate) ? 1 : 0)),
-                                    res_grad_per_sm(f));
+template <typename TS, typename TB, int MODE>
+int res_backward(ResArgs a, const ResJoin& j, cudaStream_t s) {
+  constexpr ResMode kMode = static_cast<ResMode>(MODE);
+  const ResForm f = res_form(a.N, kMode, true);
+  const unsigned blocks = static_cast<unsigned>(res_grad_blocks(f, a.M));
+  if (blocks) {
+    const int64_t one_s = f.threads * res_thread_bytes(kMode, f.v, sizeof(TS)), one_b = f.threads * res_thread_bytes(kMode, f.v, sizeof(TB));
+    const ResShared sh = res_shared((a.dy ? one_s + one_b : 0) + (a.dh ? one_s : 0) + (a.f ? one_b : 0),
+                                    static_cast<int64_t>(f.threads) * f.v * 64,
+                                    a.dy && a.dh && a.f ? 0 : std::max(one_s, one_b), res_grad_per_sm(f));
     if (f.lpr < 0 || sh.stages == 0) {
-      residual_norm_backward_any_kernel<TS, TB><<<ctas, kResMaxThreads, 0, s>>>(a);
+      residual_norm_backward_any_kernel<TS, TB><<<blocks, kResMaxThreads, 0, s>>>(a);
+      if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
     } else {
-      a.stages = sh.stages;
-      a.keep = sh.weights && a.M > int64_t{4} * f.rows * ctas;  // (few rows a CTA: not worth it)
-      const size_t smem = static_cast<size_t>(std::max<int64_t>(sh.bytes, f.lpr > 0 ? 8 * a.N : 0));
-      const int st = allow_shared_memory(reinterpret_cast<const void*>(go), smem + 1024);  // (and what is static)
+      constexpr int kSmall = MODE == kSingle ? 32 : 8, kSome = MODE == kSingle ? 32 : 16;
+      auto go = f.lpr == 8    ? residual_norm_backward_kernel<TS, TB, kSmall, 1, MODE>
+                : f.lpr == 16 ? residual_norm_backward_kernel<TS, TB, kSome, 1, MODE>
+                : f.lpr == 32 ? (f.v == 1 ? residual_norm_backward_kernel<TS, TB, 32, 1, MODE>
+                                          : residual_norm_backward_kernel<TS, TB, 32, 2, MODE>)
+                              : residual_norm_backward_kernel<TS, TB, 0, 2, MODE>;
+      a.stages = MODE == kSingle && sizeof(TS) + sizeof(TB) < 8 ? 1 : sh.stages;  // (see kAhead)
+      a.ranks = f.ranks;
+      const int st = res_launch(go, int64_t{1} * blocks * f.ranks, f.threads, std::max<int64_t>(sh.bytes, f.lpr > 0 ? 8 * a.N : 0),
+                                f.ranks, a, s);
       if (st != FP8G_OK) return st;
-      go<<<ctas, f.threads, smem, s>>>(a);
     }
-    if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
   }
   if (!a.parts) return FP8G_OK;
   ResJoin join = j;
-  join.P = static_cast<int32_t>(ctas);
+  join.P = static_cast<int32_t>(blocks);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((a.N + 31) / 32));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = ctas ? 1 : 0;
+  attr[0].val.programmaticStreamSerializationAllowed = blocks ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, residual_norm_join_kernel, join) != cudaSuccess) {
@@ -351,7 +327,9 @@ using namespace fp8g;
 
 extern "C" int fp8g_residual_rms_norm_backward_workspace(int64_t M, int64_t N, int64_t* bytes) {
   if (M < 0 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFF0 || !bytes) return FP8G_ERR_INVALID_ARG;
-  *bytes = std::max<int64_t>(16, std::max(res_grad_ctas(res_form(N, false, true), M), res_grad_ctas(res_form(N, true, true), M)) * 2 * N * 4);
+  int64_t P = 0;
+  for (const ResMode mode : {kAligned, kShifted, kSingle}) P = std::max(P, res_grad_blocks(res_form(N, mode, true), M));
+  *bytes = std::max<int64_t>(16, P * 2 * N * 4);
   return FP8G_OK;
 }
 
@@ -389,14 +367,18 @@ extern "C" int fp8g_residual_rms_norm_backward(
   a.parts = sums ? static_cast<float*>(workspace) : nullptr;
   a.M = M, a.N = static_cast<int32_t>(N), a.w_kind = w_dtype, a.norm_f = post_norm;
   a.scale = scale, a.inv_n = 1.0f / static_cast<float>(N);
-  const ResGrid grid = res_grid(M, N, {{a.x, ldh}, {f, ldf}, {dy, lddy}, {dh, lddh}, {dx, lddx}, {df, lddf}});
-  const bool vec = grid != ResGrid::kNone;
+  const ResMode mode = res_mode(M, N, {{a.x, ldh}, {f, ldf}, {dy, lddy}, {dh, lddh}, {dx, lddx}, {df, lddf}});
   const ResJoin j{a.parts, post_weight, gate, dweight, dgate, dpost, 0, a.N, w_dtype, scale};
   using B = __nv_bfloat16;
+  auto pick = [mode](auto aligned, auto shifted, auto single) {
+    return mode == kAligned ? aligned : mode == kShifted ? shifted : single;
+  };
   auto go = stream_dtype == FP8G_F32
-                ? (block_dtype == FP8G_F32 ? (vec ? res_backward<float, float, true> : res_backward<float, float, false>)
-                                           : (vec ? res_backward<float, B, true> : res_backward<float, B, false>))
-                : (block_dtype == FP8G_F32 ? (vec ? res_backward<B, float, true> : res_backward<B, float, false>)
-                                           : (vec ? res_backward<B, B, true> : res_backward<B, B, false>));
-  return go(a, j, grid == ResGrid::kShifted, static_cast<cudaStream_t>(stream));
+                ? (block_dtype == FP8G_F32
+                       ? pick(res_backward<float, float, kAligned>, res_backward<float, float, kShifted>, res_backward<float, float, kSingle>)
+                       : pick(res_backward<float, B, kAligned>, res_backward<float, B, kShifted>, res_backward<float, B, kSingle>))
+                : (block_dtype == FP8G_F32
+                       ? pick(res_backward<B, float, kAligned>, res_backward<B, float, kShifted>, res_backward<B, float, kSingle>)
+                       : pick(res_backward<B, B, kAligned>, res_backward<B, B, kShifted>, res_backward<B, B, kSingle>));
+  return go(a, j, static_cast<cudaStream_t>(stream));
 }
