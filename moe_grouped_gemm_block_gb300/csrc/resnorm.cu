@@ -19,79 +19,90 @@
 namespace fp8g {
 namespace {
 
-template <typename TS, typename TB, int LPR, int V, int MODE>
+template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
 __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE == kAligned ? 2 : 1)
     residual_norm_kernel(const ResArgs a) {
-  __shared__ __align__(16) float red[2][32];
+  __shared__ float red[2][1][32];
   extern __shared__ __align__(16) unsigned char shared[];
-  using Cols = Columns<MODE, V>;
-  using SX = Source<TS, MODE, V>;
-  using SF = Source<TB, MODE, V>;
+  constexpr int G = res_unit<TS, TB>(), V = EIGHTS * 8 / G, H = G / 2;
+  using Cols = Columns<MODE, G, V>;
+  using SX = Source<TS, MODE, G, V>;
+  using SF = Source<TB, MODE, G, V>;
   FP8G_RES_ROWS(a.ldx)
-  if (!LPR) res_sum_init(red, a.ranks);
+  if (!LPR) res_sum_init<1>(red, a.ranks);
   // the weights of y, and of f: post gate scale; the stages
-  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * V * blockDim.x;
+  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * EIGHTS * blockDim.x;
   col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
   if (a.f) col.keep_weights(f_at, a.post, a.gate, a.w_kind, a.scale);
-  const uint32_t stages = smem_u32(a.f ? f_at + 2 * V * blockDim.x : f_at);
-  const uint32_t x_bytes = blockDim.x * SX::thread_bytes(), stage = x_bytes + (a.f ? blockDim.x * SF::thread_bytes() : 0u);
+  const uint32_t stages = smem_u32(a.f ? f_at + 2 * EIGHTS * blockDim.x : f_at);
+  const uint32_t x_bytes = blockDim.x * SX::thread_bytes(), f_bytes = blockDim.x * SF::thread_bytes();
   SX sx{};
   SF sf{};
   int64_t ahead = m_first + mine;  // the row that is copied next
-  sx.init(a.x, ahead, a.ldx, step, stages, stage, a.stages, col);
-  if (a.f) sf.init(a.f, ahead, a.ldf, step, stages + x_bytes, stage, a.stages, col);
-  auto bring = [&](int s) {
-    if (ahead < a.M) {
-      sx.copy(s, col);
-      if (a.f) sf.copy(s, col);
-    }
-    if (SX::kStaged) sx.row += sx.step;
+  sx.init(a.x, ahead, a.ldx, step, stages, x_bytes, a.stages, col);
+  if (a.f) sf.init(a.f, ahead, a.ldf, step, stages + a.stages * x_bytes, f_bytes, a.stages_f, col);
+  // f's row, which may lie one behind the others', is a group of its own before theirs
+  int64_t ahead_f = ahead;
+  auto bring_f = [&](int s) {
+    if (a.f && ahead_f < a.M) sf.copy(s, col);
     if (SF::kStaged) sf.row += sf.step;
+    ahead_f += step;
+    cp_async_commit();
+  };
+  auto bring = [&](int s) {
+    if (ahead < a.M) sx.copy(s, col);
+    if (SX::kStaged) sx.row += sx.step;
     ahead += step;
     cp_async_commit();
   };
-  int phase = 0, s = 0;
-  for (int i = 0; i < a.stages; ++i) bring(i);
+  const int later = a.stages == a.stages_f ? 2 * a.stages - 2 : 2 * a.stages_f - 1;
+  int phase = 0, s = 0, s_f = 0;
+  for (int i = 0; i < a.stages; ++i) {
+    if (i >= a.stages - a.stages_f) bring_f(i - (a.stages - a.stages_f));
+    bring(i);
+  }
   for (int64_t m0 = m_first; m0 < a.M; m0 += step) {
     const int64_t m = m0 + mine;
     const bool real = LPR == 0 || m < a.M;
-    Raw8<TB> rf[V];
-    float2 x[V][4];
-    cp_async_wait(a.stages - 1);
+    Unit<TB, G> rf[V];
+    float2 x[V][H];
+    cp_async_wait(later);
     if (!SX::kStaged && !real) sx.row = nullptr;
     if (!SF::kStaged && !real) sf.row = nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      Raw8<TS> r;
+      Unit<TS, G> r;
       sx.load(r, s, v, col);
       r.get(x[v]);
-      if (a.f) sf.load(rf[v], s, v, col);
+      if (a.f) sf.load(rf[v], s_f, v, col);
     }
     if (!SX::kStaged) sx.row += sx.step;
     if (!SF::kStaged) sf.row += sf.step;
+    bring_f(s_f);
     bring(s);
     if (++s == a.stages) s = 0;
+    if (++s_f == a.stages_f) s_f = 0;
     if (a.f) {
       float by = 1.0f;
       if (a.norm_f) {
         float2 sq = both(0.0f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          float2 f[4];
+          float2 f[H];
           rf[v].get(f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sq = __ffma2_rn(f[j], f[j], sq);
+          for (int j = 0; j < H; ++j) sq = __ffma2_rn(f[j], f[j], sq);
         }
         by = root_inverse(res_sum<LPR>(sq.x + sq.y, red, phase, a.ranks) * a.inv_n, a.eps);
         if (col.t == 0 && rank == 0 && real && a.rstd_f) a.rstd_f[m] = by;
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float2 f[4];
+        float2 f[H];
         rf[v].get(f);
         col.times(f_at, v, f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[v][j] = __ffma2_rn(both(by), f[j], x[v][j]);
+        for (int j = 0; j < H; ++j) x[v][j] = __ffma2_rn(both(by), f[j], x[v][j]);
       }
       if (real && a.h) {
 #pragma unroll
@@ -103,13 +114,13 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE == kAl
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sq = __ffma2_rn(x[v][j], x[v][j], sq);
+      for (int j = 0; j < H; ++j) sq = __ffma2_rn(x[v][j], x[v][j], sq);
     const float r = root_inverse(res_sum<LPR>(sq.x + sq.y, red, phase, a.ranks) * a.inv_n, a.eps);
     if (col.t == 0 && rank == 0 && real && a.rstd) a.rstd[m] = r;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[v][j] = __fmul2_rn(x[v][j], both(r));
+      for (int j = 0; j < H; ++j) x[v][j] = __fmul2_rn(x[v][j], both(r));
       col.times(w_at, v, x[v]);
       if (real) col.store(static_cast<TB*>(a.y) + m * a.ldy, v, x[v]);
     }
@@ -120,8 +131,8 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE == kAl
 // Rows of any length: a CTA a row, which reads it again for each step.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const ResArgs a) {
-  __shared__ __align__(16) float red[2][32];
-  res_sum_init(red, 1);
+  __shared__ float red[2][1][32];
+  res_sum_init<1>(red, 1);
   int phase = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const TS* x = static_cast<const TS*>(a.x) + m * a.ldx;
@@ -167,8 +178,9 @@ int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
   const ResForm f = res_form(a.N, kMode, false);
   const int per_sm = f.ranks > 1 || f.lpr < 0 ? 1 : std::max(2, 1024 / f.threads);
   const int64_t values = static_cast<int64_t>(f.threads) * f.v * 8;
-  const ResShared sh = res_shared(f.threads * (res_thread_bytes(kMode, f.v, sizeof(TS)) + (a.f ? res_thread_bytes(kMode, f.v, sizeof(TB)) : 0)),
-                                  values * 4 * (a.f ? 2 : 1), 0, per_sm);
+  const ResShared sh = res_shared(f.threads * res_thread_bytes(kMode, f.v, sizeof(TS)),
+                                  a.f ? f.threads * res_thread_bytes(kMode, f.v, sizeof(TB)) : 0, values * 4 * (a.f ? 2 : 1),
+                                  per_sm);
   if (f.lpr < 0 || sh.stages == 0) {
     residual_norm_any_kernel<TS, TB><<<static_cast<unsigned>(std::min<int64_t>(a.M, 2 * dev->sm_count)), kResMaxThreads, 0,
                                        s>>>(a);
@@ -180,7 +192,7 @@ int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
             : f.lpr == 32 ? (f.v == 1 ? residual_norm_kernel<TS, TB, 32, 1, MODE> : residual_norm_kernel<TS, TB, 32, 2, MODE>)
             : f.v == 1    ? residual_norm_kernel<TS, TB, 0, 1, MODE>
                           : residual_norm_kernel<TS, TB, 0, 2, MODE>;
-  a.stages = sh.stages, a.ranks = f.ranks;
+  a.stages = sh.stages, a.stages_f = sh.stages_f, a.ranks = f.ranks;
   // (row blocks: a multiple of 8 where a CTA takes more than one, see Columns)
   const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count / f.ranks / 8 * 8 * per_sm);
   return res_launch(go, blocks * f.ranks, f.threads, sh.bytes, f.ranks, a, s);

@@ -25,7 +25,7 @@ struct ResArgs {
   float *rstd, *rstd_f;  // results of the forward, inputs of the backward call
   float* parts;          // [rows at once][2][N]
   int64_t M, ldx, ldf, ldh, ldy, lddy, lddh, lddx, lddf;
-  int32_t N, w_kind, norm_f, stages, ranks;  // ranks: CTAs a row
+  int32_t N, w_kind, norm_f, stages, stages_f, ranks;  // stages_f: of f, stages or one less; ranks: CTAs a row
   float scale, eps, inv_n;
 };
 
@@ -37,16 +37,19 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, int b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All of this thread's groups of copies but the last `later` (0 .. kResMaxStages - 1) have landed.
+// All of this thread's groups of copies but the last `later` (at most 4) have landed.
 __device__ __forceinline__ void cp_async_wait(int later) {
   if (later == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
   else if (later == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (later == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (later == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else asm volatile("cp.async.wait_group 4;" ::: "memory");
 }
 
 
-// How a row falls to its threads: R threads of a CTA, which has the columns [lo, end) of it, take eight values at a time, V
-// times.
+// How a row falls to its threads: R threads of a CTA, which has the columns [lo, end) of it, take G values at a time, V
+// times.  G is 8 where all matrices are bf16 and 4 where one is fp32, so that a warp's 16-byte accesses to the wider type
+// lie side by side.
 //   kAligned  in vectors; every row lies on the 16-byte grid
 //   kShifted  in vectors on the grid, but row m starts q = (m ld) mod 8 values after a vector's start, in all matrices
 //             alike (the host checks): its first and last vectors reach into what lies beside it, which is read and left
@@ -59,178 +62,278 @@ __device__ __forceinline__ void cp_async_wait(int later) {
 // those of a matrix that is not there, hold zeros from the start, so that no row asks what there is.  (bf16 value by value
 // is too narrow for such copies: it is loaded when it is needed.)
 enum ResMode { kAligned, kShifted, kSingle };
-template <int MODE, int V>
+template <typename TS, typename TB>
+__host__ __device__ constexpr int res_unit() { return sizeof(TS) == 4 || sizeof(TB) == 4 ? 4 : 8; }
+// G values as they lie in memory.
+template <typename T, int G>
+struct Unit {
+  static constexpr int kWords = G * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void get(float2 (&f)[G / 2]) const {
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i)
+      f[i] = sizeof(T) == 4 ? make_float2(__uint_as_float(w[2 * i % kWords]), __uint_as_float(w[(2 * i + 1) % kWords]))
+                            : make_float2(__uint_as_float(w[i % kWords] << 16), __uint_as_float(w[i % kWords] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void set(int j, T v) {  // value j, of zeros
+    if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(v);
+    else w[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(v)) << (16 * (j & 1));
+  }
+  __device__ __forceinline__ void keep(int j, bool yes) {
+    if constexpr (sizeof(T) == 4) w[j] = yes ? w[j] : 0u;
+    else w[j / 2] &= yes ? 0xFFFFFFFFu : (j & 1 ? 0xFFFFu : 0xFFFF0000u);
+  }
+};
+template <int MODE, int G, int V>
 struct Columns {
   int t, R, lo, end;
   __device__ __forceinline__ int at(int v, int j) const {
-    return MODE == kSingle ? lo + t + (8 * v + j) * R : lo + 8 * (t + v * R) + j;
+    return MODE == kSingle ? lo + t + (G * v + j) * R : lo + G * (t + v * R) + j;
   }
   __device__ __forceinline__ bool has(int v, int j) const { return at(v, j) < end && (MODE != kShifted || at(v, j) >= 0); }
   __device__ __forceinline__ bool whole(int v) const {
-    return MODE == kAligned ? at(v, 0) < end : at(v, 0) >= 0 && at(v, 7) < end;
+    return MODE == kAligned ? at(v, 0) < end : at(v, 0) >= 0 && at(v, G - 1) < end;
   }
-  // 8 V float32 weights, the product of two vectors (null: 1) and a factor, in places of 16 bytes a thread
+  // G V fp32 weights, the product of two vectors (null: 1) and a factor, in places of 16 bytes a thread
   __device__ __forceinline__ void keep_weights(float4* to, const void* a, const void* b, int kind, float by) const {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 f[4] = {make_float2(by, by), make_float2(by, by), make_float2(by, by), make_float2(by, by)};
+      float f[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) f[j] = by;
       if (a) from_memory(a, kind, v, f);
       if (b) from_memory(b, kind, v, f);
-      to[2 * v * blockDim.x + threadIdx.x] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      to[(2 * v + 1) * blockDim.x + threadIdx.x] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+#pragma unroll
+      for (int c = 0; c < G / 4; ++c)
+        to[(v * (G / 4) + c) * blockDim.x + threadIdx.x] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
     }
   }
-  __device__ __forceinline__ void times(const float4* w, int v, float2 (&f)[4]) const {
-    const float4 x = w[2 * v * blockDim.x + threadIdx.x], y = w[(2 * v + 1) * blockDim.x + threadIdx.x];
-    f[0] = __fmul2_rn(f[0], make_float2(x.x, x.y));
-    f[1] = __fmul2_rn(f[1], make_float2(x.z, x.w));
-    f[2] = __fmul2_rn(f[2], make_float2(y.x, y.y));
-    f[3] = __fmul2_rn(f[3], make_float2(y.z, y.w));
-  }
-  __device__ __forceinline__ void from_memory(const void* w, int kind, int v, float2 (&f)[4]) const {
-    float g[8];
+  __device__ __forceinline__ void from_memory(const void* w, int kind, int v, float (&f)[G]) const {
     if (MODE == kAligned && (reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
       if (!whole(v)) return;
-      if (kind == FP8G_F32) load8(static_cast<const float*>(w) + at(v, 0), g);
-      else load8(static_cast<const __nv_bfloat16*>(w) + at(v, 0), g);
+      float2 g[G / 2];
+      if (kind == FP8G_F32) {
+#pragma unroll
+        for (int c = 0; c < G / 4; ++c) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at(v, 4 * c)));
+          g[2 * c] = make_float2(x.x, x.y), g[2 * c + 1] = make_float2(x.z, x.w);
+        }
+      } else {
+        Unit<__nv_bfloat16, G> u;
+#pragma unroll
+        for (int c = 0; c < G / 4; ++c) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + at(v, 4 * c)));
+          u.w[2 * c] = x.x, u.w[2 * c + 1] = x.y;
+        }
+        u.get(g);
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) f[j] *= j & 1 ? g[j / 2].y : g[j / 2].x;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = has(v, j) ? load_any(w, kind, at(v, j)) : 0.0f;
+      for (int j = 0; j < G; ++j) f[j] *= has(v, j) ? load_any(w, kind, at(v, j)) : 0.0f;
     }
+  }
+  // the weights of unit v
+  __device__ __forceinline__ void weights(const float4* w, int v, float2 (&f)[G / 2]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(f[i], make_float2(g[2 * i], g[2 * i + 1]));
+    for (int c = 0; c < G / 4; ++c) {
+      const float4 x = w[(v * (G / 4) + c) * blockDim.x + threadIdx.x];
+      f[2 * c] = make_float2(x.x, x.y), f[2 * c + 1] = make_float2(x.z, x.w);
+    }
+  }
+  __device__ __forceinline__ void times(const float4* w, int v, float2 (&f)[G / 2]) const {
+    float2 g[G / 2];
+    weights(w, v, g);
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) f[i] = __fmul2_rn(f[i], g[i]);
   }
   template <typename T>
-  __device__ __forceinline__ void store(T* row, int v, const float2 (&f)[4]) const {
+  __device__ __forceinline__ void store(T* row, int v, const float2 (&f)[G / 2]) const {
     if (MODE != kSingle && whole(v)) {
-      store8_stream(row + at(v, 0), {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y});
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int c = 0; c < G / 4; ++c)
+          __stcs(reinterpret_cast<float4*>(row + at(v, 4 * c)), make_float4(f[2 * c].x, f[2 * c].y, f[2 * c + 1].x, f[2 * c + 1].y));
+      } else if constexpr (G == 8) {
+        __stcs(reinterpret_cast<uint4*>(row + at(v, 0)),
+               make_uint4(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y), pack2(f[2].x, f[2].y), pack2(f[3].x, f[3].y)));
+      } else {
+        __stcs(reinterpret_cast<uint2*>(row + at(v, 0)), make_uint2(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y)));
+      }
     } else if (MODE != kAligned) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < G; ++j)
         if (has(v, j)) row[at(v, j)] = from_f32<T>(j & 1 ? f[j / 2].y : f[j / 2].x);
     }
   }
 };
 
 // A thread's places of one matrix: stage s at slot + s stride.
-template <typename T, int MODE, int V>
+template <typename T, int MODE, int G, int V>
 struct Source {
+  using Cols = Columns<MODE, G, V>;
   static constexpr bool kStaged = MODE != kSingle || sizeof(T) == 4;
-  static constexpr int kPlace = MODE == kSingle ? 4 : 16;  // bytes of a copy
-  static constexpr int kCopies = kStaged ? V * 8 * static_cast<int>(sizeof(T)) / kPlace : 0;
+  static constexpr int kUnit = G * static_cast<int>(sizeof(T));                         // bytes of G values
+  static constexpr int kPlace = MODE == kSingle ? 4 : kUnit < 16 ? kUnit : 16;          // bytes of a copy
+  static constexpr int kCopies = kStaged ? V * kUnit / kPlace : 0, kChunks = kUnit / kPlace, kPer = G / kChunks;
   static __host__ __device__ constexpr int thread_bytes() { return kCopies * kPlace; }
   const T* row;   // the row to be copied next (loaded next, where it is not staged)
   int64_t step;   // elements to the one after it
   uint32_t slot, stride;
+  static __device__ __forceinline__ void copy_place(uint32_t to, const T* from, int bytes) {
+    if constexpr (kPlace == 16) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    } else if constexpr (kPlace == 8) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    } else {
+      cp_async_4(to, from);
+    }
+  }
+  static __device__ __forceinline__ void copy_place(uint32_t to, const T* from) {
+    if constexpr (kPlace == 16) cp_async_16(to, from);
+    else if constexpr (kPlace == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+    else cp_async_4(to, from);
+  }
+  static __device__ __forceinline__ void zero_place(uint32_t to) {
+#pragma unroll
+    for (int b = 0; b < kPlace; b += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + b), "r"(0u) : "memory");
+  }
   // `matrix` null: the places at `slot` of one stage hold zeros
   __device__ __forceinline__ void init(const void* matrix, int64_t m, int64_t ld, int64_t rows, uint32_t at, uint32_t stage,
-                                       int stages, const Columns<MODE, V>& col) {
+                                       int stages, const Cols& col) {
     row = matrix ? static_cast<const T*>(matrix) + m * ld : nullptr;
     step = rows * ld;
     slot = at + threadIdx.x * kPlace;
     stride = matrix ? stage : 0u;
     for (int s = 0; s < (matrix ? stages : 1); ++s)
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const uint32_t to = slot + s * stride + i * blockDim.x * kPlace;
-        if constexpr (MODE == kSingle) {
-          if (!matrix || !col.has(i / 8, i % 8)) asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0u) : "memory");
-        } else {
-          constexpr int kChunks = sizeof(T) / 2;
-          if (!matrix || !col.whole(i / kChunks)) st_shared_v4(to, 0u, 0u, 0u, 0u);
-        }
-      }
+      for (int i = 0; i < kCopies; ++i)
+        if (!matrix || !(MODE == kSingle ? col.has(i / G, i % G) : col.whole(i / kChunks)))
+          zero_place(slot + s * stride + i * blockDim.x * kPlace);
   }
-  __device__ __forceinline__ void copy(int s, const Columns<MODE, V>& col) const {
+  __device__ __forceinline__ void copy(int s, const Cols& col) const {
     if constexpr (!kStaged) return;
     if (!row) return;
     const uint32_t to = slot + s * stride, next = blockDim.x * kPlace;
     if constexpr (MODE == kSingle) {
 #pragma unroll
-      for (int i = 0; i < 8 * V; ++i)
-        if (col.has(i / 8, i % 8)) cp_async_4(to + i * next, row + col.at(i / 8, i % 8));
+      for (int i = 0; i < G * V; ++i)
+        if (col.has(i / G, i % G)) copy_place(to + i * next, row + col.at(i / G, i % G));
     } else {
-      constexpr int kChunks = sizeof(T) / 2, kPer = 8 / kChunks;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (MODE == kAligned ? col.whole(v) : col.at(v, 7) < col.end) {
+        if (MODE == kAligned ? col.whole(v) : col.at(v, G - 1) < col.end) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) cp_async_16(to + (v * kChunks + c) * next, row + col.at(v, c * kPer));
+          for (int c = 0; c < kChunks; ++c) copy_place(to + (v * kChunks + c) * next, row + col.at(v, c * kPer));
         } else if (MODE == kShifted) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             const int n = min(kPer, col.end - col.at(v, c * kPer));
-            if (n > 0) cp_async_16(to + (v * kChunks + c) * next, row + col.at(v, c * kPer), n * static_cast<int>(sizeof(T)));
+            if (n > 0) copy_place(to + (v * kChunks + c) * next, row + col.at(v, c * kPer), n * static_cast<int>(sizeof(T)));
           }
         }
       }
     }
   }
-  // Eight values of stage s; 0 where there are none.
-  __device__ __forceinline__ void load(Raw8<T>& r, int s, int v, const Columns<MODE, V>& col) const {
+  // Unit v of stage s; 0 where there is nothing.
+  __device__ __forceinline__ void load(Unit<T, G>& u, int s, int v, const Cols& col) const {
     const uint32_t from = slot + s * stride, next = blockDim.x * kPlace;
     if constexpr (MODE != kSingle) {
-      if constexpr (sizeof(T) == 2) {
-        const float4 a = ld_shared_v4f(from + v * next);
-        r.v = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w));
-      } else {
-        r.a = ld_shared_v4f(from + 2 * v * next);
-        r.b = ld_shared_v4f(from + (2 * v + 1) * next);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const uint32_t p = from + (v * kChunks + c) * next;
+        if constexpr (kPlace == 16)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(u.w[4 * c % u.kWords]), "=r"(u.w[(4 * c + 1) % u.kWords]), "=r"(u.w[(4 * c + 2) % u.kWords]), "=r"(u.w[(4 * c + 3) % u.kWords])
+                       : "r"(p) : "memory");
+        else
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.w[0]), "=r"(u.w[1]) : "r"(p) : "memory");
       }
       if (MODE == kShifted && !col.whole(v)) {
-        uint32_t mask = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mask |= (col.has(v, j) ? 1u : 0u) << j;
-        r.keep(mask);
+        for (int j = 0; j < G; ++j) u.keep(j, col.has(v, j));
       }
     } else {
-      T f[8];
+      u.zero();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (kStaged) f[j] = ld_shared_f32(from + (8 * v + j) * next);
-        else f[j] = row && col.has(v, j) ? row[col.at(v, j)] : from_f32<T>(0.0f);
+      for (int j = 0; j < G; ++j) {
+        if constexpr (kStaged) u.set(j, ld_shared_f32(from + (G * v + j) * next));
+        else if (row && col.has(v, j)) u.set(j, row[col.at(v, j)]);
       }
-      r.set(f);
     }
   }
 };
 
-// The sum over the threads of a row: LPR lanes of a warp, or (LPR 0) the CTAs of a cluster, of which each warp tells all
-// its sum; entries of `red` past the warps are 0.
-template <int LPR>
-__device__ __forceinline__ float res_sum(float v, float (*red)[32], int& phase, int ranks) {
+// Sums of NV values over the threads of a row: LPR lanes of a warp, or (LPR 0) the CTAs of a cluster, of which each warp
+// tells all its sums; entries of `red` past the warps are 0.
+template <int LPR, int NV>
+__device__ __forceinline__ void res_sum(float (&v)[NV], float (*red)[NV][32], int& phase, int ranks) {
   if constexpr (LPR > 0) {
 #pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+    for (int off = LPR / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
   } else {
-    v = warp_sum(v);
-    float* r = red[phase & 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (NV == 4) {  // each half of the lanes goes on with two of the sums, each quarter with one
+      const bool half = lane & 16, quarter = lane & 8;
+      const float a = (half ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, half ? v[0] : v[2], 16);
+      const float b = (half ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, half ? v[1] : v[3], 16);
+      v[0] = (quarter ? b : a) + __shfl_xor_sync(0xffffffffu, quarter ? a : b, 8);
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
+    }
+    float(*r)[32] = red[phase & 1];
     ++phase;
-    const int warp = threadIdx.x >> 5;
+    const int each = 32 / NV;  // lane i each has sum i
+    const float mine = NV == 4 ? v[0] : v[lane / each % NV];
     if (ranks == 1) {
-      if ((threadIdx.x & 31) == 0) r[warp] = v;
+      if (lane % each == 0) r[lane / each][warp] = mine;
       __syncthreads();
     } else {
-      if ((threadIdx.x & 31) < ranks) {
-        const uint32_t to = mapa_shared(smem_u32(r + static_cast<int>(cluster_ctarank()) * 16 + warp), threadIdx.x & 31);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+      if (lane % each < ranks) {
+        const uint32_t to = mapa_shared(smem_u32(&r[lane / each][static_cast<int>(cluster_ctarank()) * 16 + warp]), lane % each);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(mine) : "memory");
       }
       cluster_sync();
     }
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int quads = ranks == 1 ? 4 : 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= quads) break;
-      const float4 q = *reinterpret_cast<const float4*>(r + 4 * i);
-      s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+    for (int i = 0; i < NV; ++i) {  // (32 entries, a lane each: the same order in every warp)
+      const float s = r[i][lane];
+      v[i] = s;
     }
-    return (s.x + s.y) + (s.z + s.w);
+    if constexpr (NV == 4) {
+      const bool half = lane & 16, quarter = lane & 8;
+      const float a = (half ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, half ? v[0] : v[2], 16);
+      const float b = (half ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, half ? v[1] : v[3], 16);
+      float c = (quarter ? b : a) + __shfl_xor_sync(0xffffffffu, quarter ? a : b, 8);
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
+    }
   }
 }
-__device__ __forceinline__ void res_sum_init(float (*red)[32], int ranks) {
-  for (int i = threadIdx.x; i < 64; i += blockDim.x) (&red[0][0])[i] = 0.0f;
+template <int LPR>
+__device__ __forceinline__ float res_sum(float v, float (*red)[1][32], int& phase, int ranks) {
+  float one[1] = {v};
+  res_sum<LPR, 1>(one, red, phase, ranks);
+  return one[0];
+}
+template <int NV>
+__device__ __forceinline__ void res_sum_init(float (*red)[NV][32], int ranks) {
+  for (int i = threadIdx.x; i < 64 * NV; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
   __syncthreads();
   if (ranks > 1) cluster_sync();
 }
@@ -239,7 +342,8 @@ __device__ __forceinline__ float root_inverse(float mean_square, float eps) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The form of a row's length: LPR lanes of a warp (0: CTAs), V eights a thread, `ranks` CTAs a row; lpr -1: any length.
+// The form of a row's length: LPR lanes of a warp (0: CTAs), V eights (of two units where G is 4) a thread, `ranks` CTAs a
+// row; lpr -1: any length.
 struct ResForm {
   int lpr, v, threads, rows, ranks;  // rows a CTA at once
 };
@@ -255,16 +359,20 @@ inline ResForm res_form(int64_t N, ResMode mode, bool backward) {
   const int v = mine <= kResMaxThreads && !backward && ranks == 1 ? 1 : 2;
   return {0, v, static_cast<int>(((mine + v - 1) / v + 31) / 32 * 32), 1, ranks};
 }
-// Shared memory of a CTA, where `per_sm` of them are to be resident: `weights` bytes of weights, `zeros` bytes of zeros, and
-// up to kResMaxStages stages of `stage` bytes.  stages 0: not even one fits (such rows are taken as rows of any length).
+// Shared memory of a CTA, where `per_sm` of them are to be resident: `fixed` bytes (weights, zeros) and up to kResMaxStages
+// stages of `stage` bytes and of `f` bytes, the latter one less where that lets another stage of the others in: a row that
+// is worked on leaves memory idle for its latency unless more than one is on its way.  stages 0: not even one fits (such
+// rows are taken as rows of any length).
 struct ResShared {
   int64_t bytes;
-  int32_t stages;
+  int32_t stages, stages_f;
 };
-inline ResShared res_shared(int64_t stage, int64_t weights, int64_t zeros, int per_sm) {
-  const int64_t each = 224 * 1024 / per_sm - 1024, left = each - weights - zeros;
-  const int64_t n = left < 0 ? 0 : std::min<int64_t>(kResMaxStages, stage ? left / stage : 1);
-  return {n * stage + weights + zeros, static_cast<int32_t>(n)};
+inline ResShared res_shared(int64_t stage, int64_t f, int64_t fixed, int per_sm) {
+  const int64_t left = 224 * 1024 / per_sm - 1024 - fixed;
+  for (int n = kResMaxStages; n > 0; --n)
+    for (int k = n; k >= std::max(1, n - 1); --k)
+      if (n * stage + k * f <= left) return {n * stage + k * f + fixed, n, k};
+  return {0, 0, 0};
 }
 
 inline bool bad_type(int32_t t) { return t != FP8G_BF16 && t != FP8G_F32; }

@@ -1,6 +1,6 @@
 // resnorm_grad.cu -- the gradient of the norms around a block (the formulas: resnorm.cu).
 //
-// A row takes two sums, one after the other, and gives two results; a column's sums over the rows stay in the registers
+// A row takes two means, of which the second needs the first's result, and gives two results; a column's sums over the rows stay in the registers
 // of the threads that have the column, and leave a partial sum a CTA that a second, dependent launch joins in order.
 
 #include "resnorm.cuh"
@@ -8,47 +8,56 @@
 namespace fp8g {
 namespace {
 
-template <typename TS, typename TB, int LPR, int V, int MODE>
+template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
 __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) residual_norm_backward_kernel(const ResArgs a) {
-  __shared__ __align__(16) float red[2][32];
+  __shared__ float red[2][4][32];
   extern __shared__ __align__(16) unsigned char shared[];  // (in the end, LPR: [2][N] sums)
-  using Cols = Columns<MODE, V>;
-  using SS = Source<TS, MODE, V>;
-  using SB = Source<TB, MODE, V>;
+  constexpr int G = res_unit<TS, TB>(), V = EIGHTS * 8 / G, H = G / 2;
+  using Cols = Columns<MODE, G, V>;
+  using SS = Source<TS, MODE, G, V>;
+  using SB = Source<TB, MODE, G, V>;
   griddep_launch_dependents();
   FP8G_RES_ROWS(a.lddx)
-  if (!LPR) res_sum_init(red, a.ranks);
+  if (!LPR) res_sum_init<4>(red, a.ranks);
   // the weights of dy, and of dx: post gate scale; zeros for a matrix that is not there; the stages
-  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * V * blockDim.x;
+  float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * EIGHTS * blockDim.x;
   col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
   col.keep_weights(f_at, a.post, a.gate, a.w_kind, a.scale);
   const uint32_t one_s = blockDim.x * SS::thread_bytes(), one_b = blockDim.x * SB::thread_bytes();
-  const uint32_t zeros = smem_u32(f_at + 2 * V * blockDim.x);
+  const uint32_t zeros = smem_u32(f_at + 2 * EIGHTS * blockDim.x);
   const bool missing = !a.dy || !a.dh || !a.f;
   const uint32_t h_at = zeros + (missing ? max(one_s, one_b) : 0u), dy_at = h_at + (a.dy ? one_s : 0u);
-  const uint32_t dh_at = dy_at + (a.dy ? one_b : 0u), k_at = dh_at + (a.dh ? one_s : 0u);
-  const uint32_t stage = k_at + (a.f ? one_b : 0u) - h_at;
+  const uint32_t dh_at = dy_at + (a.dy ? one_b : 0u), stage = dh_at + (a.dh ? one_s : 0u) - h_at;
+  const uint32_t k_at = h_at + a.stages * stage;
   SS sh, sd;
   SB sy, sf;
   int64_t ahead = m_first + mine;  // the row that is copied next
   sh.init(a.dy ? a.x : nullptr, ahead, a.ldx, step, a.dy ? h_at : zeros, stage, a.stages, col);
   sy.init(a.dy, ahead, a.lddy, step, a.dy ? dy_at : zeros, stage, a.stages, col);
   sd.init(a.dh, ahead, a.lddh, step, a.dh ? dh_at : zeros, stage, a.stages, col);
-  sf.init(a.f, ahead, a.ldf, step, a.f ? k_at : zeros, stage, a.stages, col);
-  auto advance = [&] {
-    if (a.dy) sh.row += sh.step, sy.row += sy.step;
-    if (a.dh) sd.row += sd.step;
-    if (a.f) sf.row += sf.step;
+  sf.init(a.f, ahead, a.ldf, step, a.f ? k_at : zeros, one_b, a.stages_f, col);
+  // f's row, which may lie one behind the others', is a group of its own before theirs
+  int64_t ahead_f = ahead;
+  auto bring_f = [&](int s) {
+    if (ahead_f < a.M) sf.copy(s, col);
+    ahead_f += step;
+    cp_async_commit();
   };
   auto bring = [&](int s) {
     if (ahead < a.M) {
       sh.copy(s, col);
       sy.copy(s, col);
       sd.copy(s, col);
-      sf.copy(s, col);
     }
     ahead += step;
     cp_async_commit();
+  };
+  auto advance = [&] {
+    if (a.dy) sh.row += sh.step, sy.row += sy.step;
+    if (a.dh) sd.row += sd.step;
+  };
+  auto advance_f = [&] {
+    if (a.f) sf.row += sf.step;
   };
   // the rows' statistics, a row ahead
   float next_r = 0.0f, next_rf = 1.0f;
@@ -59,15 +68,20 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
     }
   };
   statistics(ahead);
-  int phase = 0, st = 0;
-  float2 dw[V][4], df_sum[V][4];
+  int phase = 0, st = 0, st_f = 0;
+  float2 dw[V][H], df_sum[V][H];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dw[v][j] = df_sum[v][j] = both(0.0f);
+    for (int j = 0; j < H; ++j) dw[v][j] = df_sum[v][j] = both(0.0f);
   // (where a matrix is not staged but loaded at its row's turn, all keep to one stage)
   constexpr bool kAhead = SS::kStaged && SB::kStaged;
+  const int later = !kAhead ? 0 : a.stages == a.stages_f ? 2 * a.stages - 2 : 2 * a.stages_f - 1;
   for (int i = 0; i < a.stages; ++i) {
+    if (i >= a.stages - a.stages_f) {
+      bring_f(i - (a.stages - a.stages_f));
+      if (kAhead) advance_f();
+    }
     bring(i);
     if (kAhead) advance();
   }
@@ -76,76 +90,77 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
     const bool real = LPR == 0 || m < a.M;
     const float r = next_r, rf = next_rf;
     statistics(m + step);
-    Raw8<TS> rh[V], rd[V];
-    Raw8<TB> ry[V], rk[V];
-    cp_async_wait(kAhead ? a.stages - 1 : 0);
+    Unit<TS, G> rh[V], rd[V];
+    Unit<TB, G> ry[V], rk[V];
+    cp_async_wait(later);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (real) {
         sh.load(rh[v], st, v, col);
         sy.load(ry[v], st, v, col);
         sd.load(rd[v], st, v, col);
-        sf.load(rk[v], st, v, col);
+        sf.load(rk[v], st_f, v, col);
       } else {
         rh[v].zero(), ry[v].zero(), rd[v].zero(), rk[v].zero();
       }
     }
-    if (!kAhead) advance();
+    if (!kAhead) advance(), advance_f();
+    bring_f(st_f);
     bring(st);
-    if (kAhead) advance();
+    if (kAhead) advance(), advance_f();
     if (++st == a.stages) st = 0;
-    float2 sum = both(0.0f);
+    if (++st_f == a.stages_f) st_f = 0;
+    // With p = post gate scale, p dx = p dh + r (p g - p e s) and so sum p dx k = sum p dh k + r (sum p g k - s sum p e k):
+    // one sum over the row for both means (two of them, one after the other, took a third longer).
+    float2 ge = both(0.0f), pdk = ge, pgk = ge, pek = ge;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 g[4], e[4];
+      float2 g[H], e[H], d[H], k[H], w[H];
       ry[v].get(g);
       rh[v].get(e);
+      rd[v].get(d);
+      rk[v].get(k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < H; ++j) {
         e[j] = __fmul2_rn(e[j], both(r));
         dw[v][j] = __ffma2_rn(g[j], e[j], dw[v][j]);
       }
       col.times(w_at, v, g);
+      col.weights(f_at, v, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(g[j], e[j], sum);
+      for (int j = 0; j < H; ++j) {
+        ge = __ffma2_rn(g[j], e[j], ge);
+        const float2 pk = __fmul2_rn(w[j], __fmul2_rn(k[j], both(rf)));
+        pdk = __ffma2_rn(pk, d[j], pdk);
+        pgk = __ffma2_rn(pk, g[j], pgk);
+        pek = __ffma2_rn(pk, e[j], pek);
+      }
     }
-    float s = 0.0f;
-    if (a.dy) s = res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * r;  // e once more is h r
-    float2 dx[V][4];
-    sum = both(0.0f);
+    float sums[4] = {ge.x + ge.y, pdk.x + pdk.y, pgk.x + pgk.y, pek.x + pek.y};
+    res_sum<LPR, 4>(sums, red, phase, a.ranks);
+    const float s = sums[0] * a.inv_n;                                          // mean (g e)
+    const float by = a.norm_f ? rf : 1.0f;
+    const float c = a.norm_f ? -fmaf(r, sums[2] - s * sums[3], sums[1]) * a.inv_n * rf : 0.0f;  // - r_f mean (q k)
+    const float sr = -s * r;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 g[4], e[4], k[4];
-      rd[v].get(dx[v]);
+      float2 g[H], h[H], k[H], dx[H];
+      rd[v].get(dx);
       ry[v].get(g);
-      rh[v].get(e);
+      rh[v].get(h);
       rk[v].get(k);
       col.times(w_at, v, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dx[v][j] = __ffma2_rn(both(r), __ffma2_rn(e[j], both(-s), g[j]), dx[v][j]);
-      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx[v]);
+      for (int j = 0; j < H; ++j) dx[j] = __ffma2_rn(both(r), __ffma2_rn(h[j], both(sr), g[j]), dx[j]);
+      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        k[j] = __fmul2_rn(k[j], both(rf));
-        df_sum[v][j] = __ffma2_rn(dx[v][j], k[j], df_sum[v][j]);
+      for (int j = 0; j < H; ++j) df_sum[v][j] = __ffma2_rn(dx[j], __fmul2_rn(k[j], both(rf)), df_sum[v][j]);
+      if (a.df) {
+        col.times(f_at, v, dx);
+#pragma unroll
+        for (int j = 0; j < H; ++j) dx[j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[j]));
+        if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx);
       }
-      col.times(f_at, v, dx[v]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum = __ffma2_rn(dx[v][j], k[j], sum);
-    }
-    if (!a.df) continue;
-    float by = 1.0f, c = 0.0f;
-    if (a.norm_f) {
-      by = rf;
-      c = -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * rf;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float2 k[4];
-      rk[v].get(k);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dx[v][j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[v][j]));
-      if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
     }
   }
   if (!LPR && a.ranks > 1) cluster_sync();  // (nobody leaves while it may still be written to)
@@ -155,7 +170,7 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < G; ++j)
         if (col.has(v, j)) {
           out[col.at(v, j)] = j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x;
           out[a.N + col.at(v, j)] = j & 1 ? df_sum[v][j / 2].y : df_sum[v][j / 2].x;
@@ -170,7 +185,7 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < G; ++j)
             if (col.has(v, j)) {
               float* p = sums + col.at(v, j);
               p[0] = (q ? p[0] : 0.0f) + (j & 1 ? dw[v][j / 2].y : dw[v][j / 2].x);
@@ -187,9 +202,9 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
 // workspace.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_kernel(const ResArgs a) {
-  __shared__ __align__(16) float red[2][32];
+  __shared__ float red[2][1][32];
   griddep_launch_dependents();
-  res_sum_init(red, 1);
+  res_sum_init<1>(red, 1);
   int phase = 0;
   float* out = a.parts ? a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.N : nullptr;
   if (out)
@@ -281,9 +296,9 @@ int res_backward(ResArgs a, const ResJoin& j, cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>(res_grad_blocks(f, a.M));
   if (blocks) {
     const int64_t one_s = f.threads * res_thread_bytes(kMode, f.v, sizeof(TS)), one_b = f.threads * res_thread_bytes(kMode, f.v, sizeof(TB));
-    const ResShared sh = res_shared((a.dy ? one_s + one_b : 0) + (a.dh ? one_s : 0) + (a.f ? one_b : 0),
-                                    static_cast<int64_t>(f.threads) * f.v * 64,
-                                    a.dy && a.dh && a.f ? 0 : std::max(one_s, one_b), res_grad_per_sm(f));
+    const ResShared sh = res_shared((a.dy ? one_s + one_b : 0) + (a.dh ? one_s : 0), a.f ? one_b : 0,
+                                    static_cast<int64_t>(f.threads) * f.v * 64 +
+                                        (a.dy && a.dh && a.f ? 0 : std::max(one_s, one_b)), res_grad_per_sm(f));
     if (f.lpr < 0 || sh.stages == 0) {
       residual_norm_backward_any_kernel<TS, TB><<<blocks, kResMaxThreads, 0, s>>>(a);
       if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
@@ -294,7 +309,8 @@ int res_backward(ResArgs a, const ResJoin& j, cudaStream_t s) {
                 : f.lpr == 32 ? (f.v == 1 ? residual_norm_backward_kernel<TS, TB, 32, 1, MODE>
                                           : residual_norm_backward_kernel<TS, TB, 32, 2, MODE>)
                               : residual_norm_backward_kernel<TS, TB, 0, 2, MODE>;
-      a.stages = MODE == kSingle && sizeof(TS) + sizeof(TB) < 8 ? 1 : sh.stages;  // (see kAhead)
+      a.stages = sh.stages, a.stages_f = sh.stages_f;
+      if (MODE == kSingle && sizeof(TS) + sizeof(TB) < 8) a.stages = a.stages_f = 1;  // (see kAhead)
       a.ranks = f.ranks;
       const int st = res_launch(go, int64_t{1} * blocks * f.ranks, f.threads, std::max<int64_t>(sh.bytes, f.lpr > 0 ? 8 * a.N : 0),
                                 f.ranks, a, s);
