@@ -10,7 +10,7 @@ namespace {
 
 template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
 __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) residual_norm_backward_kernel(const ResArgs a) {
-  __shared__ float red[2][4][32];
+  __shared__ float red[2][1][32];
   extern __shared__ __align__(16) unsigned char shared[];  // (in the end, LPR: [2][N] sums)
   constexpr int G = res_unit<TS, TB>(), V = EIGHTS * 8 / G, H = G / 2;
   using Cols = Columns<MODE, G, V>;
@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
   using SB = Source<TB, MODE, G, V>;
   griddep_launch_dependents();
   FP8G_RES_ROWS(a.lddx)
-  if (!LPR) res_sum_init<4>(red, a.ranks);
+  if (!LPR) res_sum_init<1>(red, a.ranks);
   // the weights of dy, and of dx: post gate scale; zeros for a matrix that is not there; the stages
   float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * EIGHTS * blockDim.x;
   col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
@@ -110,57 +110,57 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
     if (kAhead) advance(), advance_f();
     if (++st == a.stages) st = 0;
     if (++st_f == a.stages_f) st_f = 0;
-    // With p = post gate scale, p dx = p dh + r (p g - p e s) and so sum p dx k = sum p dh k + r (sum p g k - s sum p e k):
-    // one sum over the row for both means (two of them, one after the other, took a third longer).
-    float2 ge = both(0.0f), pdk = ge, pgk = ge, pek = ge;
+    float2 sum = both(0.0f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 g[H], e[H], d[H], k[H], w[H];
+      float2 g[H], e[H];
       ry[v].get(g);
       rh[v].get(e);
-      rd[v].get(d);
-      rk[v].get(k);
 #pragma unroll
       for (int j = 0; j < H; ++j) {
         e[j] = __fmul2_rn(e[j], both(r));
         dw[v][j] = __ffma2_rn(g[j], e[j], dw[v][j]);
       }
       col.times(w_at, v, g);
-      col.weights(f_at, v, w);
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        ge = __ffma2_rn(g[j], e[j], ge);
-        const float2 pk = __fmul2_rn(w[j], __fmul2_rn(k[j], both(rf)));
-        pdk = __ffma2_rn(pk, d[j], pdk);
-        pgk = __ffma2_rn(pk, g[j], pgk);
-        pek = __ffma2_rn(pk, e[j], pek);
-      }
+      for (int j = 0; j < H; ++j) sum = __ffma2_rn(g[j], e[j], sum);
     }
-    float sums[4] = {ge.x + ge.y, pdk.x + pdk.y, pgk.x + pgk.y, pek.x + pek.y};
-    res_sum<LPR, 4>(sums, red, phase, a.ranks);
-    const float s = sums[0] * a.inv_n;                                          // mean (g e)
-    const float by = a.norm_f ? rf : 1.0f;
-    const float c = a.norm_f ? -fmaf(r, sums[2] - s * sums[3], sums[1]) * a.inv_n * rf : 0.0f;  // - r_f mean (q k)
-    const float sr = -s * r;
+    const float s = a.dy ? -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * r : 0.0f;  // (e once more is h r)
+    float2 dx[V][H];
+    sum = both(0.0f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float2 g[H], h[H], k[H], dx[H];
-      rd[v].get(dx);
+      float2 g[H], h[H], k[H];
+      rd[v].get(dx[v]);
       ry[v].get(g);
       rh[v].get(h);
       rk[v].get(k);
       col.times(w_at, v, g);
 #pragma unroll
-      for (int j = 0; j < H; ++j) dx[j] = __ffma2_rn(both(r), __ffma2_rn(h[j], both(sr), g[j]), dx[j]);
-      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx);
+      for (int j = 0; j < H; ++j) dx[v][j] = __ffma2_rn(both(r), __ffma2_rn(h[j], both(s), g[j]), dx[v][j]);
+      if (real) col.store(static_cast<TS*>(a.dx) + m * a.lddx, v, dx[v]);
 #pragma unroll
-      for (int j = 0; j < H; ++j) df_sum[v][j] = __ffma2_rn(dx[j], __fmul2_rn(k[j], both(rf)), df_sum[v][j]);
-      if (a.df) {
-        col.times(f_at, v, dx);
-#pragma unroll
-        for (int j = 0; j < H; ++j) dx[j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[j]));
-        if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx);
+      for (int j = 0; j < H; ++j) {
+        k[j] = __fmul2_rn(k[j], both(rf));
+        df_sum[v][j] = __ffma2_rn(dx[v][j], k[j], df_sum[v][j]);
       }
+      col.times(f_at, v, dx[v]);
+#pragma unroll
+      for (int j = 0; j < H; ++j) sum = __ffma2_rn(dx[v][j], k[j], sum);
+    }
+    if (!a.df) continue;
+    float by = 1.0f, c = 0.0f;
+    if (a.norm_f) {
+      by = rf;
+      c = -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * rf;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float2 k[H];
+      rk[v].get(k);
+#pragma unroll
+      for (int j = 0; j < H; ++j) dx[v][j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[v][j]));
+      if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
     }
   }
   if (!LPR && a.ranks > 1) cluster_sync();  // (nobody leaves while it may still be written to)
@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_ker
   }
 }
 
-// The columns' sums from the CTAs' partial ones, in their order: 32 columns a CTA, 8 threads a column.
+// The columns' sums from the CTAs' partial ones, in a fixed order: 32 columns a CTA, 32 threads a column with four loads of
+// each kind on their way (with 8 threads and one, 16384 x 64 took 24 us instead of 13).
 struct ResJoin {
   const float* parts;
   const void *post, *gate;
@@ -257,36 +258,40 @@ struct ResJoin {
   int32_t P, N, w_kind;
   float scale;
 };
-__global__ void __launch_bounds__(256) residual_norm_join_kernel(const ResJoin a) {
-  __shared__ float s[2][8][33];
+constexpr int kJoinSlices = 32;
+__global__ void __launch_bounds__(32 * kJoinSlices) residual_norm_join_kernel(const ResJoin a) {
+  __shared__ float s[2][kJoinSlices][33];
   griddep_wait();
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockIdx.x * 32 + c;
   float w = 0.0f, f = 0.0f;
-  if (n < a.N)
-    for (int p = k; p < a.P; p += 8) {
-      w += __ldcg(a.parts + static_cast<int64_t>(p) * 2 * a.N + n);
-      f += __ldcg(a.parts + (static_cast<int64_t>(p) * 2 + 1) * a.N + n);
+  if (n < a.N) {
+    const float* p = a.parts + n;
+    const int64_t row = 2 * static_cast<int64_t>(a.N);
+#pragma unroll 4
+    for (int i = k; i < a.P; i += kJoinSlices) {
+      w += __ldcg(p + i * row);
+      f += __ldcg(p + i * row + a.N);
     }
+  }
   s[0][k][c] = w;
   s[1][k][c] = f;
   __syncthreads();
-  if (k > 0 || n >= a.N) return;
-  w = f = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w += s[0][i][c], f += s[1][i][c];
-  f *= a.scale;
-  if (a.dw) a.dw[n] = w;
-  if (a.dgate) a.dgate[n] = f * (a.post ? load_any(a.post, a.w_kind, n) : 1.0f);
-  if (a.dpost) a.dpost[n] = f * (a.gate ? load_any(a.gate, a.w_kind, n) : 1.0f);
+  // warp k has column k of the CTA's: a lane a slice
+  const int col = blockIdx.x * 32 + k;
+  w = warp_sum(s[0][c][k]);
+  f = warp_sum(s[1][c][k]) * a.scale;
+  if (c > 0 || col >= a.N) return;
+  if (a.dw) a.dw[col] = w;
+  if (a.dgate) a.dgate[col] = f * (a.post ? load_any(a.post, a.w_kind, col) : 1.0f);
+  if (a.dpost) a.dpost[col] = f * (a.gate ? load_any(a.gate, a.w_kind, col) : 1.0f);
 }
-
 
 // CTAs that are resident on an SM: 512 threads of 128 registers.
 int res_grad_per_sm(const ResForm& f) { return f.lpr > 0 ? 2 : f.lpr < 0 ? 1 : std::min(4, std::max(1, 512 / f.threads)); }
 // Blocks of rows, and partial sums, of a call: rows stay with their CTAs for the column sums, so no more than are resident
 // (and, where a block takes several rows, a multiple of 8 of them, see Columns).
 int64_t res_grad_blocks(const ResForm& f, int64_t M) {
-  return std::min<int64_t>((M + f.rows - 1) / f.rows, f.ranks > 1 ? 72 : 152 * res_grad_per_sm(f));
+  return std::min<int64_t>((M + f.rows - 1) / f.rows, 152 * res_grad_per_sm(f) / f.ranks / 8 * 8);
 }
 
 template <typename TS, typename TB, int MODE>
@@ -322,7 +327,7 @@ int res_backward(ResArgs a, const ResJoin& j, cudaStream_t s) {
   join.P = static_cast<int32_t>(blocks);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((a.N + 31) / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kJoinSlices);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
