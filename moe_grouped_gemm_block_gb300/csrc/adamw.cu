@@ -31,6 +31,7 @@ namespace fp8g {
 namespace {
 
 constexpr int kAdamThreads = 256;
+constexpr int kAdamPerSm = 4;                // resident CTAs an SM
 constexpr int kAdamPass = kAdamThreads * 8;  // values a CTA takes at once: 16 lanes a block of 128, 8 values each
 constexpr int32_t kAdamMaxTensors = 1 << 20;
 constexpr int64_t kAdamMaxValues = int64_t{1} << 40;
@@ -55,7 +56,7 @@ template <int CAP>
 struct AdamTable {
   AdamTensor t[CAP];
   uint32_t end[CAP];  // chunks of the tensors up to and with this one
-  int32_t n, passes;  // passes a chunk
+  int32_t n;
 };
 constexpr int kAdamCap = 384;
 static_assert(sizeof(AdamTable<kAdamCap>) <= 32000, "kernel arguments hold 32764 bytes");
@@ -70,27 +71,45 @@ struct AdamStep {
 };
 static_assert(sizeof(AdamStep) <= 32, "");
 
-__global__ void adamw_step_kernel(const float* lr_dev, double lr, double b1, double b2, int64_t* step, const float* norm,
-                                  float max_norm, float norm_eps, AdamStep* out) {
+// b^t by squaring: off by some t 2^-53 of itself, when it counts (the library's pow takes 6 us on this GPU's fp64).
+__device__ __forceinline__ double power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0 && r > 0.0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+// One warp; lane 0 has beta1's power, lane 1 beta2's.
+__global__ void __launch_bounds__(32) adamw_step_kernel(const float* lr_dev, double lr, double b1, double b2, int64_t* step,
+                                                        const float* norm, float max_norm, float norm_eps, AdamStep* out) {
   griddep_launch_dependents();
   AdamStep s{};
   s.coef = 1.0f;
+  const int64_t t = *step + 1;
+  float rate = static_cast<float>(lr);
+  if (lr_dev) rate = *lr_dev;
   if (norm) {
     const float n = *norm;
     s.skip = isfinite(n) ? 0u : 1u;
     s.coef = fminf(1.0f, __fmul_rn(max_norm, __frcp_rn(n + norm_eps)));
   }
-  if (!s.skip) {
-    const int64_t t = *step + 1;
-    *step = t;
-    s.time = static_cast<uint32_t>(t);
-    if (lr_dev) lr = *lr_dev;
-    s.lr = static_cast<float>(lr);
-    s.lr1 = static_cast<float>(lr / (1.0 - pow(b1, static_cast<double>(t))));
-    s.root2 = static_cast<float>(1.0 / sqrt(1.0 - pow(b2, static_cast<double>(t))));
+  const float c = static_cast<float>(1.0 - power(threadIdx.x ? b2 : b1, t)), c2 = __shfl_sync(0xffffffffu, c, 1);
+  s.time = static_cast<uint32_t>(t);
+  s.lr = rate;
+  s.lr1 = __fdiv_rn(rate, c);
+  s.root2 = __fdiv_rn(1.0f, __fsqrt_rn(c2));
+  if (threadIdx.x == 0) {
+    if (!s.skip) *step = t;
+    *out = s;
   }
-  *out = s;
 }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+// A sum of products that keeps their own roundings (a two-wide sum is joined with the products, whatever it is written as).
+__device__ __forceinline__ float2 add_apart(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
 
 // Values j = 0 .. 7 of a thread: eight in a row (`full`), or single ones with a step between them.
 template <typename T>
@@ -113,6 +132,38 @@ __device__ __forceinline__ void put8(T* p, int64_t at, int step, int64_t n, bool
   }
 }
 
+// The roots of eight values >= 0: an approximate one and a step of Heron's iteration on its residual (Markstein), which is
+// the rounded root but for one value in some 2^20 (whose true root lies so near the middle between two floats); by the
+// compiler's root where one of the eight is below the normal range or not finite.  (With that and its quotient for all,
+// a branch in each, 117M values with 8-bit states took 479 us.)
+__device__ __forceinline__ void square_roots(const float2 (&v)[4], float2 (&root)[4]) {
+  float lo = v[0].x, hi = v[0].x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    lo = fminf(lo, fminf(v[j].x, v[j].y));
+    hi = fmaxf(hi, fmaxf(v[j].x, v[j].y));
+  }
+  if (lo >= 0x1p-126f && hi < INFINITY) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float2 r;
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v[j].x));
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v[j].y));
+      const float2 s = mul2(v[j], r), minus = make_float2(-s.x, -s.y);
+      root[j] = __ffma2_rn(__ffma2_rn(minus, s, v[j]), mul2(r, both(0.5f)), s);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) root[j] = make_float2(__fsqrt_rn(v[j].x), __fsqrt_rn(v[j].y));
+  }
+}
+__device__ __forceinline__ float2 quotient(float2 a, float2 b) {  // two units in the last place; b is normal
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(b.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(b.y));
+  return mul2(a, r);
+}
+
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
@@ -132,8 +183,7 @@ __device__ __forceinline__ void get_codes(const uint8_t* p, int64_t at, int step
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 d = e4m3x2_to_f32(w[j / 2] >> (16 * (j & 1)));
-    f[2 * j] = __fmul_rn(d.x, scale);
-    f[2 * j + 1] = __fmul_rn(d.y, scale);
+    reinterpret_cast<float2(&)[4]>(f)[j] = mul2(d, both(scale));
   }
 }
 // The codes of a block that 16 lanes hold, and its scale (see above).  ROOT: what is not 0 gets no 0.
@@ -149,23 +199,26 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, 
   const bool live = top >= 0x1p-60f;
   const float inv = live ? __fmul_rn(448.0f, __frcp_rn(top)) : 0.0f;
   if ((threadIdx.x & 15) == 0) *scale = live ? __fmul_rn(top, 1.0f / 448.0f) : 0.0f;
-  const uint32_t shift = time * kTimeStep + (ROOT ? kRootShift : 0u);
+  const uint32_t first = static_cast<uint32_t>(at) * kPlaceStep + time * kTimeStep + (ROOT ? kRootShift : 0u);
+  const uint32_t next = static_cast<uint32_t>(step) * kPlaceStep;
+  const float lowest = live ? 0x1p-9f : 0.0f;
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float c[2];
+    // A code has 3 bits after the point, y 20 more: their sum with u carries into the code's or does not.  Below 2^-6
+    // the codes are 2^-9 apart, as they are from 2^-6 to 2^-5: the sum with 2^-6 (what it cuts off is less than u's
+    // last bit) has them at the same bits.
+    const float2 x = make_float2(f[2 * j], f[2 * j + 1]);
+    const float2 y = mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(inv));
+    float c[2] = {y.x, y.y};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int i = 2 * j + k;
-      const float y = __fmul_rn(fabsf(f[i]), inv);
-      // A code has 3 bits after the point, y 20 more: their sum with u carries into the code's or does not.  Below 2^-6
-      // the codes are 2^-9 apart, as they are from 2^-6 to 2^-5: the sum with 2^-6 (what it cuts off is less than u's
-      // last bit) has them at the same bits.
-      const float low = y < 0x1p-6f ? 0x1p-6f : 0.0f;
-      const uint32_t u = (static_cast<uint32_t>(at + i * step) * kPlaceStep + shift) >> 12;
-      float r = __uint_as_float((__float_as_uint(__fadd_rz(y, low)) + u) & 0xFFF00000u) - low;
-      if (ROOT && live && f[i] > 0.0f) r = fmaxf(r, 0x1p-9f);
-      c[k] = copysignf(r, f[i]);
+      const float low = c[k] < 0x1p-6f ? 0x1p-6f : 0.0f;
+      const uint32_t u = (first + (2 * j + k) * next) >> 12;
+      c[k] = __uint_as_float((__float_as_uint(__fadd_rz(c[k], low)) + u) & 0xFFF00000u) - low;
+      const float own = k ? x.y : x.x;
+      if (ROOT) c[k] = fmaxf(c[k], fminf(own * 0x1p100f, lowest));  // (the least root is 2^-75)
+      else c[k] = copysignf(c[k], own);
     }
     w[j / 2] |= static_cast<uint32_t>(cvt_e4m3x2(c[1], c[0])) << (16 * (j & 1));
   }
@@ -197,19 +250,27 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper&
   } else {
     get_codes(static_cast<const uint8_t*>(t.m), at, step, n, full, t.m_scale[block >> 7], m);
     get_codes(static_cast<const uint8_t*>(t.v), at, step, n, full, t.v_scale[block >> 7], v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
   }
+  float2 root[4];
+  auto& p2 = reinterpret_cast<float2(&)[4]>(p);
+  auto& g2 = reinterpret_cast<float2(&)[4]>(g);
+  auto& m2 = reinterpret_cast<float2(&)[4]>(m);
+  auto& v2 = reinterpret_cast<float2(&)[4]>(v);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     // (products and sums rounded one by one: the codes' rounding then is that of the formulas as they stand)
-    const float gj = __fmul_rn(g[j], s.coef);
-    m[j] = __fadd_rn(__fmul_rn(h.b1, m[j]), __fmul_rn(h.nb1, gj));
-    v[j] = __fadd_rn(__fmul_rn(h.b2, v[j]), __fmul_rn(__fmul_rn(h.nb2, gj), gj));
-    const float root = __fsqrt_rn(v[j]);
-    const float to = __fdiv_rn(m[j], fmaf(root, s.root2, h.eps));
-    p[j] = p[j] - fmaf(s.lr1, to, s.lr * t.decay * p[j]);
-    if (BITS == 8) v[j] = root;
+    if (BITS == 8) v2[j] = mul2(v2[j], v2[j]);
+    const float2 gj = mul2(g2[j], both(s.coef));
+    m2[j] = add_apart(mul2(both(h.b1), m2[j]), mul2(both(h.nb1), gj));
+    v2[j] = add_apart(mul2(both(h.b2), v2[j]), mul2(mul2(both(h.nb2), gj), gj));
+  }
+  square_roots(v2, root);
+  const float shrink = -s.lr * t.decay;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 to = quotient(m2[j], __ffma2_rn(root[j], both(s.root2), both(h.eps)));
+    p2[j] = __ffma2_rn(both(-s.lr1), to, __ffma2_rn(both(shrink), p2[j], p2[j]));
+    if (BITS == 8) v2[j] = root[j];
   }
   put8(static_cast<TP*>(t.param), at, step, n, full, p);
   if constexpr (MASTER) put8(t.master, at, step, n, full, p);
@@ -222,26 +283,31 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper&
   }
 }
 
+// Resident CTAs walk over the chunks of 2048 values (a CTA a chunk: 16M values took 100 us, most of it the CTAs' starts).
 template <int CAP, int BITS>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
-                                                             const AdamHyper h, const AdamStep* __restrict__ step) {
-  int lo = 0, hi = tab.n - 1;
-  const uint32_t c = blockIdx.x;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (c < tab.end[mid]) hi = mid;
-    else lo = mid + 1;
-  }
-  const AdamTensor& t = tab.t[lo];
-  const int64_t first = static_cast<int64_t>(c - (lo ? tab.end[lo - 1] : 0u)) * (tab.passes * kAdamPass);
+__global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
+                                                                         const AdamHyper h,
+                                                                         const AdamStep* __restrict__ step) {
+  const uint32_t chunks = tab.end[tab.n - 1];
   griddep_wait();
   AdamStep s;
   s.coef = __ldcg(&step->coef), s.lr = __ldcg(&step->lr), s.lr1 = __ldcg(&step->lr1), s.root2 = __ldcg(&step->root2);
   s.time = __ldcg(&step->time), s.skip = __ldcg(&step->skip);
   if (s.skip) return;
-  for (int i = 0; i < tab.passes; ++i) {
-    const int64_t block = first + static_cast<int64_t>(i) * kAdamPass + (threadIdx.x >> 4) * 128;
-    if (block >= t.numel) return;
+  int i = 0;
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    if (c >= tab.end[i]) {
+      int lo = i + 1, hi = tab.n - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (c < tab.end[mid]) hi = mid;
+        else lo = mid + 1;
+      }
+      i = lo;
+    }
+    const AdamTensor& t = tab.t[i];
+    const int64_t block = static_cast<int64_t>(c - (i ? tab.end[i - 1] : 0u)) * kAdamPass + (threadIdx.x >> 4) * 128;
+    if (block >= t.numel) continue;
     switch (t.kind & (kParamF32 | kGradF32 | kMaster)) {
       case 0: adam_block<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block); break;
       case kGradF32: adam_block<BITS, __nv_bfloat16, float, false>(t, h, s, block); break;
@@ -276,14 +342,13 @@ int check_adam(const fp8g_adamw_tensor* ts, int32_t n, int32_t bits) {
 }
 
 template <int CAP, int BITS>
-int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, int32_t passes, const AdamHyper& h, const AdamStep* step,
-                 cudaStream_t s) {
+int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, const AdamHyper& h, const AdamStep* step,
+                 const DeviceInfo* dev, cudaStream_t s) {
   AdamTable<CAP> tab;
   const uintptr_t state = BITS == 32 ? 16 : 8;
   bool first = true;
   for (int32_t i = 0; i < n;) {
     tab.n = 0;
-    tab.passes = passes;
     uint64_t chunks = 0;
     for (; i < n && tab.n < CAP; ++i) {
       const fp8g_adamw_tensor& t = ts[i];
@@ -293,12 +358,12 @@ int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, int32_t passes, const A
       tab.t[tab.n] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.master, t.numel, t.weight_decay,
                       (t.param_dtype == FP8G_F32 ? kParamF32 : 0u) | (t.grad_dtype == FP8G_F32 ? kGradF32 : 0u) |
                           (t.master ? kMaster : 0u) | (vec ? kVectors : 0u)};
-      chunks += static_cast<uint64_t>((t.numel + passes * kAdamPass - 1) / (passes * kAdamPass));
+      chunks += static_cast<uint64_t>((t.numel + kAdamPass - 1) / kAdamPass);
       tab.end[tab.n++] = static_cast<uint32_t>(chunks);
     }
     if (tab.n == 0) break;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(chunks));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<uint64_t>(chunks, static_cast<uint64_t>(dev->sm_count) * kAdamPerSm)));
     cfg.blockDim = dim3(kAdamThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -336,16 +401,11 @@ extern "C" int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t s
   if (st != FP8G_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   AdamStep* out = static_cast<AdamStep*>(workspace);
-  adamw_step_kernel<<<1, 1, 0, s>>>(lr_dev, lr, beta1, beta2, step, norm, max_norm, norm_eps, out);
+  adamw_step_kernel<<<1, 32, 0, s>>>(lr_dev, lr, beta1, beta2, step, norm, max_norm, norm_eps, out);
   if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
-  int64_t total = 0;
-  for (int32_t i = 0; i < n; ++i) total += tensors[i].numel;
   const AdamHyper h{static_cast<float>(beta1), static_cast<float>(1.0 - beta1), static_cast<float>(beta2),
                     static_cast<float>(1.0 - beta2), static_cast<float>(eps)};
-  int64_t passes = total < (int64_t{1} << 24) ? 1 : 4;
-  while (total / (passes * kAdamPass) + n >= (int64_t{1} << 31)) passes *= 2;  // a grid has fewer than 2^31 CTAs
-  const int32_t p = static_cast<int32_t>(passes);
   if (state_bits == 32)
-    return n <= 64 ? adamw_launch<64, 32>(tensors, n, p, h, out, s) : adamw_launch<kAdamCap, 32>(tensors, n, p, h, out, s);
-  return n <= 64 ? adamw_launch<64, 8>(tensors, n, p, h, out, s) : adamw_launch<kAdamCap, 8>(tensors, n, p, h, out, s);
+    return n <= 64 ? adamw_launch<64, 32>(tensors, n, h, out, dev, s) : adamw_launch<kAdamCap, 32>(tensors, n, h, out, dev, s);
+  return n <= 64 ? adamw_launch<64, 8>(tensors, n, h, out, dev, s) : adamw_launch<kAdamCap, 8>(tensors, n, h, out, dev, s);
 }
