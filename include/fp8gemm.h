@@ -713,7 +713,7 @@ typedef struct {
  *   norm      fp32 [1], device memory, as fp8g_grad_norm wrote it, or null (max_norm and norm_eps are then ignored)
  *   workspace FP8G_ADAMW_WORKSPACE bytes, 16-byte aligned, of calls that do not overlap in time
  *   0 <= beta1, beta2 < 1, eps >= 1e-30, max_norm, norm_eps >= 0, n <= 2^20, at most 2^40 values.  Pointers aligned to their
- *   element; tensors on 16-byte boundaries (codes: 8) take the faster path.  Gradients are finite, or norm is given.
+ *   element; tensors on 16-byte boundaries (codes: 4) take the faster path.  Gradients are finite, or norm is given.
  */
 int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t state_bits, double lr, const float* lr_dev,
                double beta1, double beta2, double eps, int64_t* step, const float* norm, float max_norm,

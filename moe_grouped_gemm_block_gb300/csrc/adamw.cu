@@ -31,7 +31,7 @@ namespace fp8g {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamPerSm = 4;                // resident CTAs an SM
+constexpr int adam_per_sm(int bits) { return bits == 32 ? 3 : 4; }  // resident CTAs an SM
 constexpr int kAdamPass = kAdamThreads * 8;  // values a CTA takes at once: 16 lanes a block of 128, 8 values each
 constexpr int32_t kAdamMaxTensors = 1 << 20;
 constexpr int64_t kAdamMaxValues = int64_t{1} << 40;
@@ -111,24 +111,52 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 // A sum of products that keeps their own roundings (a two-wide sum is joined with the products, whatever it is written as).
 __device__ __forceinline__ float2 add_apart(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
 
-// Values j = 0 .. 7 of a thread: eight in a row (`full`), or single ones with a step between them.
-template <typename T>
-__device__ __forceinline__ void get8(const T* p, int64_t at, int step, int64_t n, bool full, float (&f)[8]) {
-  if (full) {
-    load8(p + at, f);
+// How a block of 128 values falls to 16 lanes: two fours a lane, 64 values apart, as vectors (lanes' fp32 accesses then lie
+// side by side); in a block that is not whole, or off the vectors' boundaries, value by value, 16 apart.
+template <bool FULL>
+struct Places {
+  int64_t first;  // of the lane, in the tensor
+  int64_t n;      // values of the tensor
+  __device__ __forceinline__ Places(int64_t block, int64_t numel) : first(block + (FULL ? 4 : 1) * (threadIdx.x & 15)), n(numel) {}
+  static constexpr __device__ __forceinline__ int offset(int j) { return FULL ? (j & 3) + 64 * (j >> 2) : 16 * j; }
+  __device__ __forceinline__ bool has(int j) const { return FULL || first + offset(j) < n; }
+};
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+}
+template <typename T, bool FULL>
+__device__ __forceinline__ void get8(const T* p, const Places<FULL>& at, float (&f)[8]) {
+  p += at.first;
+  if constexpr (FULL) {
+    load4(p, f);
+    load4(p + 64, f + 4);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = at + j * step < n ? to_f32(p[at + j * step]) : 0.0f;
+    for (int j = 0; j < 8; ++j) f[j] = at.has(j) ? to_f32(p[at.offset(j)]) : 0.0f;
   }
 }
-template <typename T>
-__device__ __forceinline__ void put8(T* p, int64_t at, int step, int64_t n, bool full, const float (&f)[8]) {
-  if (full) {
-    store8(p + at, f);
+template <typename T, bool FULL>
+__device__ __forceinline__ void put8(T* p, const Places<FULL>& at, const float (&f)[8]) {
+  p += at.first;
+  if constexpr (FULL) {
+    store4(p, f);
+    store4(p + 64, f + 4);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (at + j * step < n) p[at + j * step] = from_f32<T>(f[j]);
+      if (at.has(j)) p[at.offset(j)] = from_f32<T>(f[j]);
   }
 }
 
@@ -169,16 +197,17 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-__device__ __forceinline__ void get_codes(const uint8_t* p, int64_t at, int step, int64_t n, bool full, float scale,
-                                          float (&f)[8]) {
+template <bool FULL>
+__device__ __forceinline__ void get_codes(const uint8_t* p, const Places<FULL>& at, float scale, float (&f)[8]) {
   uint32_t w[2] = {0u, 0u};
-  if (full) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p + at);
-    w[0] = v.x, w[1] = v.y;
+  p += at.first;
+  if constexpr (FULL) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    w[1] = *reinterpret_cast<const uint32_t*>(p + 64);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (at + j * step < n) w[j / 4] |= static_cast<uint32_t>(p[at + j * step]) << (8 * (j & 3));
+      if (at.has(j)) w[j / 4] |= static_cast<uint32_t>(p[at.offset(j)]) << (8 * (j & 3));
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -187,9 +216,8 @@ __device__ __forceinline__ void get_codes(const uint8_t* p, int64_t at, int step
   }
 }
 // The codes of a block that 16 lanes hold, and its scale (see above).  ROOT: what is not 0 gets no 0.
-template <bool ROOT>
-__device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, int step, int64_t n, bool full,
-                                          uint32_t time, const float (&f)[8]) {
+template <bool ROOT, bool FULL>
+__device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places<FULL>& at, uint32_t time, const float (&f)[8]) {
   float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
@@ -199,8 +227,7 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, 
   const bool live = top >= 0x1p-60f;
   const float inv = live ? __fmul_rn(448.0f, __frcp_rn(top)) : 0.0f;
   if ((threadIdx.x & 15) == 0) *scale = live ? __fmul_rn(top, 1.0f / 448.0f) : 0.0f;
-  const uint32_t first = static_cast<uint32_t>(at) * kPlaceStep + time * kTimeStep + (ROOT ? kRootShift : 0u);
-  const uint32_t next = static_cast<uint32_t>(step) * kPlaceStep;
+  const uint32_t first = static_cast<uint32_t>(at.first) * kPlaceStep + time * kTimeStep + (ROOT ? kRootShift : 0u);
   const float lowest = live ? 0x1p-9f : 0.0f;
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
@@ -214,7 +241,7 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float low = c[k] < 0x1p-6f ? 0x1p-6f : 0.0f;
-      const uint32_t u = (first + (2 * j + k) * next) >> 12;
+      const uint32_t u = (first + static_cast<uint32_t>(at.offset(2 * j + k)) * kPlaceStep) >> 12;
       c[k] = __uint_as_float((__float_as_uint(__fadd_rz(c[k], low)) + u) & 0xFFF00000u) - low;
       const float own = k ? x.y : x.x;
       if (ROOT) c[k] = fmaxf(c[k], fminf(own * 0x1p100f, lowest));  // (the least root is 2^-75)
@@ -222,34 +249,31 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, int64_t at, 
     }
     w[j / 2] |= static_cast<uint32_t>(cvt_e4m3x2(c[1], c[0])) << (16 * (j & 1));
   }
-  if (full) {
-    *reinterpret_cast<uint2*>(p + at) = make_uint2(w[0], w[1]);
+  p += at.first;
+  if constexpr (FULL) {
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+    *reinterpret_cast<uint32_t*>(p + 64) = w[1];
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (at + j * step < n) p[at + j * step] = static_cast<uint8_t>(w[j / 4] >> (8 * (j & 3)));
+      if (at.has(j)) p[at.offset(j)] = static_cast<uint8_t>(w[j / 4] >> (8 * (j & 3)));
   }
 }
 
 // One block of 128 values of tensor t, from `block` on.
-template <int BITS, typename TP, typename TG, bool MASTER>
-__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
-  const int lane = threadIdx.x & 15;
-  const int64_t n = t.numel;
-  const bool vec = t.kind & kVectors;
-  const int64_t at = block + (vec ? 8 * lane : lane);
-  const int step = vec ? 1 : 16;
-  const bool full = vec && at + 8 <= n;
+template <int BITS, typename TP, typename TG, bool MASTER, bool FULL>
+__device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
+  const Places<FULL> at(block, t.numel);
   float p[8], g[8], m[8], v[8];
-  get8(static_cast<const TG*>(t.grad), at, step, n, full, g);
-  if constexpr (MASTER) get8(t.master, at, step, n, full, p);
-  else get8(static_cast<const TP*>(t.param), at, step, n, full, p);
+  get8(static_cast<const TG*>(t.grad), at, g);
+  if constexpr (MASTER) get8(t.master, at, p);
+  else get8(static_cast<const TP*>(t.param), at, p);
   if constexpr (BITS == 32) {
-    get8(static_cast<const float*>(t.m), at, step, n, full, m);
-    get8(static_cast<const float*>(t.v), at, step, n, full, v);
+    get8(static_cast<const float*>(t.m), at, m);
+    get8(static_cast<const float*>(t.v), at, v);
   } else {
-    get_codes(static_cast<const uint8_t*>(t.m), at, step, n, full, t.m_scale[block >> 7], m);
-    get_codes(static_cast<const uint8_t*>(t.v), at, step, n, full, t.v_scale[block >> 7], v);
+    get_codes(static_cast<const uint8_t*>(t.m), at, t.m_scale[block >> 7], m);
+    get_codes(static_cast<const uint8_t*>(t.v), at, t.v_scale[block >> 7], v);
   }
   float2 root[4];
   auto& p2 = reinterpret_cast<float2(&)[4]>(p);
@@ -272,20 +296,26 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper&
     p2[j] = __ffma2_rn(both(-s.lr1), to, __ffma2_rn(both(shrink), p2[j], p2[j]));
     if (BITS == 8) v2[j] = root[j];
   }
-  put8(static_cast<TP*>(t.param), at, step, n, full, p);
-  if constexpr (MASTER) put8(t.master, at, step, n, full, p);
+  put8(static_cast<TP*>(t.param), at, p);
+  if constexpr (MASTER) put8(t.master, at, p);
   if constexpr (BITS == 32) {
-    put8(static_cast<float*>(t.m), at, step, n, full, m);
-    put8(static_cast<float*>(t.v), at, step, n, full, v);
+    put8(static_cast<float*>(t.m), at, m);
+    put8(static_cast<float*>(t.v), at, v);
   } else {
-    put_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + (block >> 7), at, step, n, full, s.time, m);
-    put_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + (block >> 7), at, step, n, full, s.time, v);
+    put_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + (block >> 7), at, s.time, m);
+    put_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + (block >> 7), at, s.time, v);
   }
+}
+
+template <int BITS, typename TP, typename TG, bool MASTER>
+__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
+  if ((t.kind & kVectors) && block + 128 <= t.numel) adam_values<BITS, TP, TG, MASTER, true>(t, h, s, block);
+  else adam_values<BITS, TP, TG, MASTER, false>(t, h, s, block);
 }
 
 // Resident CTAs walk over the chunks of 2048 values (a CTA a chunk: 16M values took 100 us, most of it the CTAs' starts).
 template <int CAP, int BITS>
-__global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
+__global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
                                                                          const AdamHyper h,
                                                                          const AdamStep* __restrict__ step) {
   const uint32_t chunks = tab.end[tab.n - 1];
@@ -345,7 +375,7 @@ template <int CAP, int BITS>
 int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, const AdamHyper& h, const AdamStep* step,
                  const DeviceInfo* dev, cudaStream_t s) {
   AdamTable<CAP> tab;
-  const uintptr_t state = BITS == 32 ? 16 : 8;
+  const uintptr_t state = BITS == 32 ? 16 : 4;
   bool first = true;
   for (int32_t i = 0; i < n;) {
     tab.n = 0;
@@ -363,7 +393,7 @@ int adamw_launch(const fp8g_adamw_tensor* ts, int32_t n, const AdamHyper& h, con
     }
     if (tab.n == 0) break;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<uint64_t>(chunks, static_cast<uint64_t>(dev->sm_count) * kAdamPerSm)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<uint64_t>(chunks, static_cast<uint64_t>(dev->sm_count) * adam_per_sm(BITS))));
     cfg.blockDim = dim3(kAdamThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
