@@ -122,19 +122,19 @@ struct Places {
   __device__ __forceinline__ bool has(int j) const { return FULL || first + offset(j) < n; }
 };
 __device__ __forceinline__ void load4(const float* p, float* f) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
+  const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
   f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
 }
 __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
   f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
   f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
 __device__ __forceinline__ void store4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
 }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* f) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3])));
 }
 template <typename T, bool FULL>
 __device__ __forceinline__ void get8(const T* p, const Places<FULL>& at, float (&f)[8]) {
