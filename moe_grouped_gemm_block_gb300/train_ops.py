@@ -118,14 +118,14 @@ def moe_route_backward(logits, topk_ids, dweights, score: str = "sigmoid", renor
 
 # ------------------------------------------------------------------ norms around a block
 
-def _weights(n: int, *named) -> int:
+def _weights(n: int, weight, post_weight, gate) -> int:
     """The common type of the weights that are there (f32 where none is)."""
     code = None
-    for t, what in named:
+    for t in (weight, post_weight, gate):
         if t is not None:
-            c = _dtype(t, what)
+            c = _dtype(t, "weight, post_weight, gate")
             if t.numel() != n or not t.is_contiguous():
-                _refuse(f"{what}: [{n}], contiguous")
+                _refuse(f"weight, post_weight, gate: [{n}], contiguous")
             if code is not None and c != code:
                 _refuse("weight, post_weight and gate: one type")
             code = c
@@ -143,31 +143,38 @@ def fp8g_residual_rms_norm(x, f, weight, h, y, rstd=None, rstd_f=None, gate=None
                            post_norm: bool = False, post_weight=None, eps: float = 1e-6) -> None:
     """x [M,N] and f [M,N] (or None) -> h [M,N] of x's type (or None), y [M,N] of f's type (or None), rstd and rstd_f
     f32 [M] (or None); weight, gate, post_weight [N] or None.  h may be x."""
-    xd, ldx = _dtype(x, "x"), _rows(x, "x")
-    M, N = shape = x.shape
-    ldf = ldh = ldy = 0
-    block = x.dtype
+    shape, block = x.shape, x.dtype
     if y is not None:
         block = y.dtype
-        ldy = _like(y, shape, block, "y")
+    elif f is not None:
+        block = f.dtype
+    ldy = 0 if y is None else _like(y, shape, block, "y")
+    ldh = 0 if h is None else _like(h, shape, x.dtype, "h")
+    if rstd is not None:
+        _vector(rstd, shape[0], _F32, "rstd")
+    if rstd_f is not None:
+        _vector(rstd_f, shape[0], _F32, "rstd_f")
+    _one_device(x.get_device(), h, y, rstd, rstd_f)
+    _residual(x, f, block, weight, gate, scale, post_norm, post_weight, eps, _opt(h), ldh, _opt(y), ldy, _opt(rstd_f),
+              _opt(rstd))
+
+
+def _residual(x, f, block, weight, gate, scale, post_norm, post_weight, eps, h, ldh, y, ldy, rstd_f, rstd) -> None:
+    """The inputs' checks and the call."""
+    xd, ldx = _dtype(x, "x"), _rows(x, "x")
+    M, N = shape = x.shape
+    ldf, ptr_f = 0, None
     if f is not None:
-        block = f.dtype if y is None else block
-        ldf = _like(f, shape, block, "f")
-    if h is not None:
-        ldh = _like(h, shape, x.dtype, "h")
+        ldf, ptr_f = _like(f, shape, block, "f"), f.data_ptr()
     bd = _DTYPES.get(block)
     if bd is None:
         _refuse("f, y: bf16 or f32")
-    wd = _weights(N, (weight, "weight"), (post_weight, "post_weight"), (gate, "gate"))
-    if rstd is not None:
-        _vector(rstd, M, _F32, "rstd")
-    if rstd_f is not None:
-        _vector(rstd_f, M, _F32, "rstd_f")
+    wd = _weights(N, weight, post_weight, gate)
     dev = x.get_device()
-    _one_device(dev, f, h, y, weight, post_weight, gate, rstd, rstd_f)
-    st = lib().fp8g_residual_rms_norm(x.data_ptr(), ldx, _opt(f), ldf, xd, bd, M, N, 1 if post_norm else 0,
-                                      _opt(post_weight), _opt(gate), scale, _opt(weight), wd, eps, _opt(h), ldh, _opt(y),
-                                      ldy, _opt(rstd_f), _opt(rstd), _on(x, dev))
+    _one_device(dev, f, weight, post_weight, gate)
+    st = lib().fp8g_residual_rms_norm(x.data_ptr(), ldx, ptr_f, ldf, xd, bd, M, N, 1 if post_norm else 0,
+                                      _opt(post_weight), _opt(gate), scale, _opt(weight), wd, eps, h, ldh, y, ldy, rstd_f,
+                                      rstd, _on(x, dev))
     if st:
         _raise(st, "fp8g_residual_rms_norm")
 
@@ -177,14 +184,21 @@ def residual_rms_norm(x, f=None, weight=None, gate=None, scale: float = 1.0, pos
     """x [M,N], f [M,N] or None -> (h [M,N] of x's type, y [M,N] of f's type (without f: out_dtype, or x's), rstd f32 [M],
     rstd_f f32 [M]).  Without f h is x; without post_norm rstd_f is None."""
     dev, shape = x.device, x.shape
-    h = x if f is None else _empty(shape, dtype=x.dtype, device=dev)
-    y = _empty(shape, dtype=f.dtype if f is not None else out_dtype or x.dtype, device=dev)
-    if f is not None and out_dtype not in (None, f.dtype):
-        _refuse("out_dtype: f's type")
+    block = out_dtype or x.dtype
+    h, ptr_h, rstd_f = x, None, None
+    if f is not None:
+        block = f.dtype
+        if out_dtype not in (None, block):
+            _refuse("out_dtype: f's type")
+        h = _empty(shape, dtype=x.dtype, device=dev)
+        ptr_h = h.data_ptr()
+    y = _empty(shape, dtype=block, device=dev)
     rstd = _empty(shape[0], dtype=_F32, device=dev)
-    rstd_f = _empty(shape[0], dtype=_F32, device=dev) if post_norm else None
-    fp8g_residual_rms_norm(x, f, weight, None if f is None else h, y, rstd, rstd_f, gate, scale, post_norm, post_weight,
-                           eps)
+    if post_norm:
+        rstd_f = _empty(shape[0], dtype=_F32, device=dev)
+    N = shape[-1]
+    _residual(x, f, block, weight, gate, scale, post_norm, post_weight, eps, ptr_h, N, y.data_ptr(), N, _opt(rstd_f),
+              rstd.data_ptr())
     return h, y, rstd, rstd_f
 
 
@@ -203,7 +217,7 @@ def fp8g_residual_rms_norm_backward(dy, dh, h, f, rstd, rstd_f, weight, dx, df=N
         _refuse("dy, f, df: bf16 or f32")
     lddy, lddh, ldh, ldf, lddf = (0 if t is None else _like(t, shape, d, what) for t, d, what in (
         (dy, block, "dy"), (dh, dx.dtype, "dh"), (h, dx.dtype, "h"), (f, block, "f"), (df, block, "df")))
-    wd = _weights(N, (weight, "weight"), (post_weight, "post_weight"), (gate, "gate"))
+    wd = _weights(N, weight, post_weight, gate)
     for t, n, what in ((rstd, M, "rstd"), (rstd_f, M, "rstd_f"), (dweight, N, "dweight"), (dgate, N, "dgate"),
                        (dpost, N, "dpost")):
         if t is not None:
