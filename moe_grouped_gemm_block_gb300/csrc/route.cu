@@ -639,9 +639,125 @@ int route_any_lanes(const RouteArgs& a, const RouteForm& f, const DeviceInfo* de
   }
 }
 
+// The gradient.  A row's scores in LPR lanes, 8 V logits each (its chosen ones alone for a sigmoid); its choices in `seg` lanes, a
+// choice each; then every expert's value is written, and over it those of the chosen ones.  Bound by memory.
+// 16383 x 160 fp32, softmax: 10 us (a lane's logits one by one and read three times: 19).
+constexpr int kRouteGradWarps = 8;
+template <typename TL, int V, int LPR>
+__global__ void __launch_bounds__(32 * kRouteGradWarps) moe_route_backward_kernel(const RouteArgs a) {
+  constexpr int G = 32 / LPR, VPL = 8 * V;
+  __shared__ float2 s_info[kRouteGradWarps][G];  // a row's maximum and 1 / sum; then q, and whether it is a real token's
+  __shared__ float s_value[kRouteGradWarps][32 * G];
+  __shared__ int32_t s_id[kRouteGradWarps][32 * G];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
+  const int E = a.E, topk = a.topk;
+  const int log_seg = topk == 1 ? 0 : 32 - __clz(topk - 1), per_pass = 32 >> log_seg;
+  float2* info = s_info[warp];
+  float* value = s_value[warp];
+  int32_t* ids = s_id[warp];
+  const TL* logits = static_cast<const TL*>(a.logits);
+  TL* dlogits = static_cast<TL*>(a.dlogits);
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRouteGradWarps + warp) * G; t0 < a.T;
+       t0 += static_cast<int64_t>(gridDim.x) * kRouteGradWarps * G) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(G), a.T - t0));
+    const int64_t t = t0 + (grp < rows ? grp : 0);
+    float2 f[VPL / 2];
+    if (a.softmax) {
+      Logits<TL, VPL> l;
+      l.load(logits + t * a.ldl, base, E, a.vec);
+      l.get(f);
+      float mx = f[0].x;
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
+      mx = row_max<LPR>(mx);
+      if (mx == -INFINITY) mx = 0.0f;
+      const float sum = row_sum<LPR>(exp_below(f, mx));
+      const float inv = sum == 0.0f ? 0.0f : recip_approx(sum);
+#pragma unroll
+      for (int i = 0; i < VPL / 2; ++i) f[i] = __fmul2_rn(f[i], make_float2(inv, inv));
+      if (sub == 0) info[grp] = make_float2(mx, inv);
+      __syncwarp();
+    }
+    for (int r0 = 0; r0 < rows; r0 += per_pass) {
+      const int r = r0 + (lane >> log_seg), j = lane & ((1 << log_seg) - 1);
+      const bool has = r < rows && j < topk;
+      const int64_t at = t0 + (r < rows ? r : 0);
+      const bool real = r < rows && (!a.mask || a.mask[at]);
+      int id = -1;
+      float d = 0.0f, s = 0.0f, slope = 0.0f;
+      if (has) {
+        id = a.ids[at * topk + j];
+        if (id < 0 || id >= E) id = -1;
+      }
+      if (id >= 0) {
+        d = a.dweights[at * topk + j] * a.scale;
+        const float l = to_f32(logits[at * a.ldl + id]);
+        if (a.softmax) {
+          s = exp_below(l, info[r].x) * info[r].y;
+        } else {
+          const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
+          s = l >= 0.0f ? y : x * y;
+          slope = x * y * y;  // s (1 - s)
+        }
+      }
+      auto seg_sum = [&](float v) {
+        for (int off = 1; off < 1 << log_seg; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        return v;
+      };
+      if (a.renorm) {
+        const float sum = seg_sum(s), inner = seg_sum(d * s);
+        const float by = sum == 0.0f ? 0.0f : recip_approx(sum);
+        d = id < 0 ? 0.0f : (d - inner * by) * by;
+      }
+      const float q = a.softmax ? seg_sum(d * s) : 0.0f;
+      // the same expert twice gets the sum of both
+      const uint32_t same = __match_any_sync(0xffffffffu, id < 0 ? -1 : r * kRouteMaxExperts + id);
+      if (__any_sync(0xffffffffu, id >= 0 && __popc(same) > 1)) {
+        float all = 0.0f;
+        for (int i = 0; i < 32; ++i) {
+          const float v = __shfl_sync(0xffffffffu, d, i);
+          if (same >> i & 1u) all += v;
+        }
+        d = all;
+      }
+      if (has) {
+        ids[r * topk + j] = real ? id : -1;
+        value[r * topk + j] = a.softmax ? s * (d - q) : d * slope;
+      }
+      __syncwarp();
+      if (r < rows && j == 0) info[r] = make_float2(q, real ? 1.0f : 0.0f);
+    }
+    __syncwarp();
+    if (grp < rows) {
+      const float2 row = info[grp];
+      const bool some = a.softmax && row.y != 0.0f;
+      TL* out = dlogits + t * a.ldd;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = base + 8 * v;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = some ? -row.x * (i & 1 ? f[4 * v + i / 2].y : f[4 * v + i / 2].x) : 0.0f;
+        if (a.vec && c + 8 <= E) {
+          store8_stream(out + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < E) out[c + i] = from_f32<TL>(o[i]);
+        }
+      }
+    }
+    __syncwarp();
+    for (int i = lane; i < rows * topk; i += 32)
+      if (ids[i] >= 0) dlogits[(t0 + i / topk) * a.ldd + ids[i]] = from_f32<TL>(value[i]);
+    __syncwarp();
+  }
+}
+
+// The same for more experts than lanes hold.
 // A warp a row; lane j < topk has the row's j-th choice.
 template <typename TL>
-__global__ void __launch_bounds__(256) moe_route_backward_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(256) moe_route_backward_any_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp; t < a.T; t += gridDim.x * 8) {
     const TL* row = static_cast<const TL*>(a.logits) + t * a.ldl;
@@ -775,8 +891,18 @@ extern "C" int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_
   a.logits = logits, a.mask = token_mask, a.ids = const_cast<int32_t*>(topk_ids), a.dweights = dweights;
   a.dlogits = dlogits, a.T = T, a.ldl = ldl, a.ldd = ldd, a.E = E, a.topk = topk, a.softmax = score;
   a.renorm = renormalize, a.scale = scale;
-  auto kernel = dtype == FP8G_F32 ? moe_route_backward_kernel<float> : moe_route_backward_kernel<__nv_bfloat16>;
-  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>((T + 7) / 8, 8 * dev->sm_count));
-  kernel<<<ctas, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.vec = aligned16(logits) && aligned16(dlogits) && (T == 1 || (ldl % 8 == 0 && ldd % 8 == 0));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int lanes = E <= 64 ? 8 : E <= 128 ? 16 : 32;  // a row
+  const int64_t rows = E <= 512 ? kRouteGradWarps * 32 / lanes : 8;
+  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>((T + rows - 1) / rows, 8 * dev->sm_count));
+  using B = __nv_bfloat16;
+  auto pick = [&](auto f32, auto bf16) { return dtype == FP8G_F32 ? f32 : bf16; };
+  auto kernel = E <= 64    ? pick(moe_route_backward_kernel<float, 1, 8>, moe_route_backward_kernel<B, 1, 8>)
+                : E <= 128 ? pick(moe_route_backward_kernel<float, 1, 16>, moe_route_backward_kernel<B, 1, 16>)
+                : E <= 256 ? pick(moe_route_backward_kernel<float, 1, 32>, moe_route_backward_kernel<B, 1, 32>)
+                : E <= 512 ? pick(moe_route_backward_kernel<float, 2, 32>, moe_route_backward_kernel<B, 2, 32>)
+                           : pick(moe_route_backward_any_kernel<float>, moe_route_backward_any_kernel<B>);
+  kernel<<<ctas, 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
