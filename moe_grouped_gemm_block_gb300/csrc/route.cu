@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(32 * kRouteGradWarps) moe_route_backward_kerne
   __shared__ float2 s_info[kRouteGradWarps][G];  // a row's maximum and 1 / sum; then q, and whether it is a real token's
   __shared__ float s_value[kRouteGradWarps][32 * G];
   __shared__ int32_t s_id[kRouteGradWarps][32 * G];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR, base = sub * VPL;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, grp = lane / LPR;
   const int E = a.E, topk = a.topk;
   const int log_seg = topk == 1 ? 0 : 32 - __clz(topk - 1), per_pass = 32 >> log_seg;
   float2* info = s_info[warp];
@@ -663,9 +663,12 @@ __global__ void __launch_bounds__(32 * kRouteGradWarps) moe_route_backward_kerne
     const int64_t t = t0 + (grp < rows ? grp : 0);
     float2 f[VPL / 2];
     if (a.softmax) {
-      Logits<TL, VPL> l;
-      l.load(logits + t * a.ldl, base, E, a.vec);
-      l.get(f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {  // eights of a row go to its lanes in turn
+        Logits<TL, 8> l;
+        l.load(logits + t * a.ldl, 8 * (v * LPR + sub), E, a.vec);
+        l.get(reinterpret_cast<float2(&)[4]>(f[4 * v]));
+      }
       float mx = f[0].x;
 #pragma unroll
       for (int i = 0; i < VPL / 2; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(32 * kRouteGradWarps) moe_route_backward_kerne
       TL* out = dlogits + t * a.ldd;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = base + 8 * v;
+        const int c = 8 * (v * LPR + sub);
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = some ? -row.x * (i & 1 ? f[4 * v + i / 2].y : f[4 * v + i / 2].x) : 0.0f;
@@ -893,15 +896,15 @@ extern "C" int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_
   a.renorm = renormalize, a.scale = scale;
   a.vec = aligned16(logits) && aligned16(dlogits) && (T == 1 || (ldl % 8 == 0 && ldd % 8 == 0));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int lanes = E <= 64 ? 8 : E <= 128 ? 16 : 32;  // a row
+  const int lanes = E <= 256 ? 8 : 16;  // a row
   const int64_t rows = E <= 512 ? kRouteGradWarps * 32 / lanes : 8;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>((T + rows - 1) / rows, 8 * dev->sm_count));
   using B = __nv_bfloat16;
   auto pick = [&](auto f32, auto bf16) { return dtype == FP8G_F32 ? f32 : bf16; };
   auto kernel = E <= 64    ? pick(moe_route_backward_kernel<float, 1, 8>, moe_route_backward_kernel<B, 1, 8>)
-                : E <= 128 ? pick(moe_route_backward_kernel<float, 1, 16>, moe_route_backward_kernel<B, 1, 16>)
-                : E <= 256 ? pick(moe_route_backward_kernel<float, 1, 32>, moe_route_backward_kernel<B, 1, 32>)
-                : E <= 512 ? pick(moe_route_backward_kernel<float, 2, 32>, moe_route_backward_kernel<B, 2, 32>)
+                : E <= 128 ? pick(moe_route_backward_kernel<float, 2, 8>, moe_route_backward_kernel<B, 2, 8>)
+                : E <= 256 ? pick(moe_route_backward_kernel<float, 4, 8>, moe_route_backward_kernel<B, 4, 8>)
+                : E <= 512 ? pick(moe_route_backward_kernel<float, 4, 16>, moe_route_backward_kernel<B, 4, 16>)
                            : pick(moe_route_backward_any_kernel<float>, moe_route_backward_any_kernel<B>);
   kernel<<<ctas, 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
