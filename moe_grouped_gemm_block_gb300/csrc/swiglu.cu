@@ -19,6 +19,7 @@ namespace fp8g {
 namespace {
 
 constexpr int kGluThreads = 256;
+constexpr int kGluPerSm = 8;
 constexpr int kGluGroups = kGluThreads / 16;  // 16 lanes take a block of 128 values, 8 each
 
 struct GluArgs {
@@ -53,19 +54,28 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
     M = c < 0 ? 0u : min(static_cast<uint32_t>(c), a.cap);
     row0 = static_cast<int64_t>(blockIdx.y) * a.cap;
   }
-  const uint32_t items = M * a.KB;
-  for (uint32_t i = blockIdx.x * kGluGroups + group; i < items; i += gridDim.x * kGluGroups) {
-    const int64_t m = row0 + i / a.KB;
-    const uint32_t kb = i % a.KB;
+  // a CTA's groups take the same 128 columns of neighbouring rows, so that their scales lie side by side
+  const uint32_t items = (M + kGluGroups - 1) / kGluGroups * a.KB;
+  for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const uint32_t kb = i % a.KB, m = i / a.KB * kGluGroups + group;
     const int col = static_cast<int>(kb) * 128 + lane * 8;
+    if (m >= M) continue;  // (the same for a group's lanes)
+    const int64_t row = row0 + m;
     float h[8] = {};
     if (col < a.F) {
-      float g[8], u[8];
-      load8(a.gu + m * a.ldgu + col, g);
-      load8(a.gu + m * a.ldgu + a.F + col, u);
+      Raw8<__nv_bfloat16> rg, ru;
+      const __nv_bfloat16* p = a.gu + row * a.ldgu + col;
+      rg.load_stream(p);
+      ru.load_stream(p + a.F);
+      float2 g[4], u[4];
+      rg.get(g);
+      ru.get(u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
-      if (a.h) store8(a.h + m * a.ldh + col, h);
+      for (int j = 0; j < 4; ++j) {
+        h[2 * j] = g[j].x * sigmoid(g[j].x) * u[j].x;
+        h[2 * j + 1] = g[j].y * sigmoid(g[j].y) * u[j].y;
+      }
+      if (a.h) store8_stream(a.h + row * a.ldh + col, h);
     }
     if (!a.q) continue;
     float top = 0.0f;
@@ -81,8 +91,8 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
     uint16_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(h[2 * j + 1] * big * inv, h[2 * j] * big * inv);
-    *reinterpret_cast<uint2*>(a.q + m * a.ldq + col) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    if (lane == 0) a.sA[kb * a.ld_sa + m] = s;
+    *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (lane == 0) a.sA[kb * a.ld_sa + row] = s;
   }
 }
 
@@ -92,22 +102,27 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_backward_kernel(const GluA
   for (uint32_t i = blockIdx.x * kGluThreads + threadIdx.x; i < items; i += gridDim.x * kGluThreads) {
     const int64_t m = i / C;
     const int col = static_cast<int>(i % C) * 8;
-    float g[8], u[8], d[8];
-    load8(a.gu + m * a.ldgu + col, g);
-    load8(a.gu + m * a.ldgu + a.F + col, u);
-    load8(a.dh + m * a.lddh + col, d);
-    float h[8];
+    Raw8<__nv_bfloat16> rg, ru, rd;
+    rg.load_stream(a.gu + m * a.ldgu + col);
+    ru.load_stream(a.gu + m * a.ldgu + a.F + col);
+    rd.load_stream(a.dh + m * a.lddh + col);
+    float2 g2[4], u2[4], d2[4];
+    rg.get(g2);
+    ru.get(u2);
+    rd.get(d2);
+    float dg[8], du[8], h[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float s = sigmoid(g[j]), act = g[j] * s;
-      h[j] = act * u[j];
-      const float dg = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-      u[j] = d[j] * act;
-      g[j] = dg;
+      const float g = j & 1 ? g2[j / 2].y : g2[j / 2].x, u = j & 1 ? u2[j / 2].y : u2[j / 2].x;
+      const float d = j & 1 ? d2[j / 2].y : d2[j / 2].x;
+      const float s = sigmoid(g), act = g * s;
+      h[j] = act * u;
+      dg[j] = d * u * s * (1.0f + g * (1.0f - s));
+      du[j] = d * act;
     }
-    store8(a.dgu + m * a.lddgu + col, g);
-    store8(a.dgu + m * a.lddgu + a.F + col, u);
-    if (a.h) store8(a.h + m * a.ldh + col, h);
+    store8_stream(a.dgu + m * a.lddgu + col, dg);
+    store8_stream(a.dgu + m * a.lddgu + a.F + col, du);
+    if (a.h) store8_stream(a.h + m * a.ldh + col, h);
   }
 }
 
@@ -139,7 +154,7 @@ extern "C" int fp8_swiglu_quantize_1x128(const void* gu, int64_t M, int64_t F, i
   a.h = static_cast<__nv_bfloat16*>(h), a.ldh = ldh;
   a.q = static_cast<uint8_t*>(q), a.ldq = ldq, a.sA = sA, a.ld_sa = ld_sa;
   a.M = static_cast<uint32_t>(M), a.KB = static_cast<uint32_t>((F + 127) / 128), a.F = static_cast<int32_t>(F);
-  swiglu_kernel<false><<<ctas(M * a.KB, kGluGroups, dev, 8), kGluThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  swiglu_kernel<false><<<ctas((M + kGluGroups - 1) / kGluGroups * a.KB, 1, dev, kGluPerSm), kGluThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
 }
 
@@ -162,7 +177,7 @@ extern "C" int fp8_swiglu_quantize_1x128_masked(const void* gu, int32_t E, int64
   a.q = static_cast<uint8_t*>(q), a.ldq = F, a.sA = sA, a.ld_sa = ld_sa;
   a.counts = masked_m;
   a.cap = static_cast<uint32_t>(cap), a.KB = static_cast<uint32_t>(F / 128), a.F = static_cast<int32_t>(F);
-  const unsigned bx = std::max(1u, std::min(ctas(cap * a.KB, kGluGroups, dev, 8),
+  const unsigned bx = std::max(1u, std::min(ctas((cap + kGluGroups - 1) / kGluGroups * a.KB, 1, dev, kGluPerSm),
                                             static_cast<unsigned>((16 * dev->sm_count + E - 1) / E)));
   swiglu_kernel<true><<<dim3(bx, static_cast<unsigned>(E)), kGluThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
