@@ -84,13 +84,22 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, off));
-    const float s = __fdiv_rn(top, 448.0f);
-    // 1 / s of a tiny scale is beyond fp32: such a block is taken 2^64 times larger
-    const float big = s < 0x1p-100f ? 0x1p64f : 1.0f;
-    const float inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s * big);
+    // top / 448, rounded: a product and a step on its exact remainder (Markstein), as an IEEE division where that could
+    // leave the normal range; there 1 / s is beyond fp32, and the block is taken 2^64 times larger
+    float s, inv;
+    if (top >= 0x1p-100f) {
+      s = top * (1.0f / 448.0f);
+      s = fmaf(fmaf(-448.0f, s, top), 1.0f / 448.0f, s);
+    } else {
+      s = __fdiv_rn(top, 448.0f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] *= 0x1p64f;
+    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(top >= 0x1p-100f ? s : s * 0x1p64f));
+    inv = s == 0.0f ? 0.0f : inv;
     uint16_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(h[2 * j + 1] * big * inv, h[2 * j] * big * inv);
+    for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(h[2 * j + 1] * inv, h[2 * j] * inv);
     *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     if (lane == 0) a.sA[kb * a.ld_sa + row] = s;
   }
