@@ -74,36 +74,42 @@ __device__ __forceinline__ double exp_series(double x) {
   return x < -708.0 ? 0.0 : p * __longlong_as_double(static_cast<int64_t>(k + 1023) << 52);
 }
 
-// One row by a warp, in 64 bits.  `key`: E words of the warp's own, the experts' keys (0: not to be had).
+// A row in 64 bits: `parts` warps make the keys of its experts in `key` (E words of shared memory; 0: not to be had), one of
+// them chooses.  The scores of an expert: exponential() of its logit, then key() with the softmax's sum.
 template <typename TL>
-__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
+struct ExactRow {
+  const RouteArgs& a;
+  const TL* row;
+  double mx;
+  __device__ __forceinline__ ExactRow(const RouteArgs& args, int64_t t)
+      : a(args), row(static_cast<const TL*>(args.logits) + t * args.ldl), mx(0.0) {
+    if (!a.softmax) return;
+    float m = -INFINITY;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) m = fmaxf(m, to_f32(row[e]));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    mx = m == -INFINITY ? 0.0 : static_cast<double>(m);
+  }
+  __device__ __forceinline__ bool scored() const { return a.bias || a.groups > 1; }
+  __device__ __forceinline__ double exponential(int e) const {
+    const double l = to_f32(row[e]);
+    return exp_series(a.softmax ? l - mx : -fabs(l));
+  }
+  __device__ __forceinline__ uint64_t key(int e, double x, double inv) const {
+    const float l = to_f32(row[e]), b = a.bias ? a.bias[e] : 0.0f;
+    const double score = a.softmax ? x * inv : (l < 0.0f ? x : 1.0) * __drcp_rn(1.0 + x);
+    return l == -INFINITY || b == -INFINITY ? kRuledOut : order_key(score + static_cast<double>(b));
+  }
+};
+
+// The choice of one warp from the keys: lane j < topk gets the j-th expert and its score.  (Without a bias and groups the keys
+// are not looked at.)
+template <typename TL>
+__device__ __noinline__ void route_choose(const RouteArgs& a, int64_t t, uint64_t* key, double mx, double inv, int& pick,
+                                          float& weight) {
   const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups;
   const TL* row = static_cast<const TL*>(a.logits) + t * a.ldl;
-  const double inf = INFINITY;
-  double mx = 0.0, inv = 1.0;
-  if (a.softmax) {
-    mx = -inf;
-    for (int e = lane; e < E; e += 32) mx = fmax(mx, static_cast<double>(to_f32(row[e])));
-    mx = warp_max(mx);
-    if (mx == -inf) mx = 0.0;
-    double s = 0.0;
-#pragma unroll 4
-    for (int e = lane; e < E; e += 32) s += exp_series(static_cast<double>(to_f32(row[e])) - mx);
-    s = warp_sum(s);
-    inv = s == 0.0 ? 0.0 : 1.0 / s;
-  }
-  auto score = [&](float l) {
-    const double x = exp_series(a.softmax ? static_cast<double>(l) - mx : -fabs(static_cast<double>(l)));
-    return a.softmax ? x * inv : (l < 0.0f ? x : 1.0) * __drcp_rn(1.0 + x);
-  };
   const bool scored = a.bias || a.groups > 1;
-#pragma unroll 4
-  for (int e = lane; e < E; e += 32) {
-    const float l = to_f32(row[e]), b = a.bias ? a.bias[e] : 0.0f;
-    const uint64_t k = scored ? order_key(score(l) + static_cast<double>(b)) : 0;
-    key[e] = l == -INFINITY || b == -INFINITY ? kRuledOut : k;
-  }
-  __syncwarp();
   uint32_t open = 0xffffffffu;
   const int log_l = 5 - a.log_groups, L = 1 << log_l, group = lane >> log_l;
   if (a.groups > 1) {
@@ -155,9 +161,34 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* 
   weight = 0.0f;
   if (lane < a.topk) {
     const float l = to_f32(row[pick]);
-    if (!(l == -INFINITY || (a.bias && a.bias[pick] == -INFINITY))) weight = static_cast<float>(score(l));
+    if (!(l == -INFINITY || (a.bias && a.bias[pick] == -INFINITY))) {
+      if (a.softmax) {
+        weight = exp_below(l, static_cast<float>(mx)) * static_cast<float>(inv);
+      } else {
+        const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
+        weight = l < 0.0f ? x * y : y;
+      }
+    }
   }
   __syncwarp();
+}
+
+// A row by one warp.
+template <typename TL>
+__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
+  const ExactRow<TL> r(a, t);
+  const int lane = threadIdx.x & 31;
+  double inv = 1.0;
+  if (a.softmax) {
+    double s = 0.0;
+    for (int e = lane; e < a.E; e += 32) s += r.exponential(e);
+    s = warp_sum(s);
+    inv = s == 0.0 ? 0.0 : 1.0 / s;
+  }
+  if (r.scored())
+    for (int e = lane; e < a.E; e += 32) key[e] = r.key(e, r.exponential(e), inv);
+  __syncwarp();
+  route_choose<TL>(a, t, key, r.mx, inv, pick, weight);
 }
 
 // A row's result, as lane j < topk has its j-th choice.
@@ -191,13 +222,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
 // scores can have with these biases, t = 2^23 + 32 + (c - lowest bias) K: a key of 32 bits holds its 23 bits and, below
 // them, the expert's slot (ties: the lower one), so that a sorting network of unsigned minima and maxima and one
 // maximum over the row a pick choose the experts.  (bf16 logits without a bias need no grid: their own 16 bits order
-// them exactly.)
+// them exactly.  A softmax's grid is the row's, up to its largest score: most of them are small.)
 //
-// What the grid cannot tell apart is found and decided in 64 bits: a row goes to route_row if two neighbours in the order
+// What the grid cannot tell apart is found and decided in 64 bits, by all of the CTA's warps when their rows are done (a warp
+// alone takes 18 us for a row of 256, most of it this GPU's fp64 exponentials): a row goes there if two neighbours in the order
 // of its picks, or a group that stays and one that does not, lie within `near` steps.  Two experts with the same logit
 // and the same bias are the exception, as their order is that of their indices in any precision (a router with a bias
-// of zeros and bf16 logits has them in every tenth row).  How far t can be off, in steps (of at least 2^-23, R their
-// range, R >= 1): s by 4.3 2^-24 (sigmoid: 1/4 (2^-22 of ex2) + 0.28 2^-24 for the exponent's rounding, one
+// of zeros and bf16 logits has them in every tenth row).  How far t can be off, in steps of R 2^-23, R the grid's
+// range: s by 4.3 2^-24 (sigmoid: 1/4 (2^-22 of ex2) + 0.28 2^-24 for the exponent's rounding, one
 // unit of the reciprocal and half a unit of the sum) or 36 2^-24 (softmax: ex2, the exponents' roundings weighted by the
 // scores, at most log E, the sum's 13), 2.2 or 18 steps; the bias' part 1.5, the sum 0.5.  So two are within 2 x 4.2 or
 // 2 x 20.5 steps of their true distance, sums of two within twice that.
@@ -206,6 +238,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
 // one left, go there too.  65536 x 256 normal logits: one row in 2000.
 constexpr int kRouteFastWarps = 32;
 constexpr int kRouteCluster = 8;
+constexpr int kRouteListed = 64;  // rows that a CTA leaves for its end; more are decided where they are met
 constexpr float kGrid = 8388608.0f;  // 2^23
 // Shared memory, every part a multiple of 16 bytes: a row of 64-bit keys a warp, the CTA's counts, then a warp's lists of
 // keys, its rows' picks and their scores.
@@ -272,6 +305,9 @@ template <typename TL, int VPL, int LPR, bool KEYS16>
 __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(const __grid_constant__ RouteArgs a) {
   constexpr int G = 32 / LPR;  // rows a warp at once
   extern __shared__ __align__(16) uint64_t smem64[];
+  __shared__ int64_t list_of_rows[kRouteListed];  // for the end, see there
+  __shared__ int listed;
+  __shared__ double part_sum[kRouteFastWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int sub = lane % LPR, grp = lane / LPR;
   const uint32_t row_lanes = (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1u) << (lane & ~(LPR - 1));
@@ -287,6 +323,7 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
   float2* info = reinterpret_cast<float2*>(picks + (kRouteBatch * topk + 1) / 2 * 2);  // a softmax's maximum and 1 / sum
   if constexpr (VPL == 8) list[8] = list[9] = 0u;
   for (int e = threadIdx.x; e < E; e += blockDim.x) cnt[e] = 0;
+  if (threadIdx.x == 0) listed = 0;
   __syncthreads();
   const TL* logits = static_cast<const TL*>(a.logits);
   const bool scored = !KEYS16 || a.groups > 1;  // whether the choice needs the scores
@@ -316,7 +353,7 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const float b = base + i < end ? (a.bias ? a.bias[base + i] : 0.0f) : -INFINITY;
-    place[i] = kGrid + 32.0f + (b - low) * K;
+    place[i] = a.softmax ? b - low : kGrid + 32.0f + (b - low) * K;
   }
 
   const int64_t stride = static_cast<int64_t>(gridDim.x) * warps * G;
@@ -413,9 +450,10 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
       }
       s = row_sum<LPR>(s);
       inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
-      const float by = K * inv;
+      // the row's own grid: its largest score is inv
+      const float k_row = (kGrid - 64.0f) * recip_approx(inv + (high - low)), by = k_row * inv;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = fmaf(c[i], by, place[i]);
+      for (int i = 0; i < VPL; ++i) c[i] = fmaf(c[i], by, fmaf(place[i], k_row, kGrid + 32.0f));
     } else if (scored) {
 #pragma unroll
       for (int i = 0; i < VPL; i += 2) {
@@ -540,6 +578,13 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
     while (exact_rows) {
       const int64_t at = tb + (__ffs(exact_rows) - 1) * step;
       exact_rows &= exact_rows - 1;
+      int place = 0;
+      if (lane == 0) place = atomicAdd(&listed, 1);
+      place = __shfl_sync(0xffffffffu, place, 0);
+      if (place < kRouteListed) {
+        if (lane == 0) list_of_rows[place] = at;
+        continue;
+      }
       int id;
       float w;
       route_row<TL>(a, at, choice, id, w);
@@ -550,6 +595,36 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
     tb = t0 + stride;
   }
   __syncthreads();
+  // the listed rows: an expert a lane, so as many warps a row as it has 32 experts, and several rows at once
+  const int parts = min((E + 31) / 32, warps), at_once = warps / parts, slot = warp / parts, part = warp % parts;
+  for (int r0 = 0, n = min(listed, kRouteListed); r0 < n; r0 += at_once) {
+    const bool mine_too = slot < at_once && r0 + slot < n;
+    const int64_t t = list_of_rows[min(r0 + slot, n - 1)];
+    uint64_t* key = smem64 + slot * route_keys(E);
+    const ExactRow<TL> r(a, t);
+    double inv = 1.0;
+    if (a.softmax) {
+      double sum = 0.0;
+      if (mine_too)
+        for (int e = part * 32 + lane; e < E; e += parts * 32) sum += r.exponential(e);
+      sum = warp_sum(sum);
+      if (lane == 0) part_sum[warp] = sum;
+      __syncthreads();
+      sum = 0.0;
+      for (int i = 0; i < parts; ++i) sum += part_sum[warp - part + i];
+      inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+    }
+    if (mine_too && r.scored())
+      for (int e = part * 32 + lane; e < E; e += parts * 32) key[e] = r.key(e, r.exponential(e), inv);
+    __syncthreads();
+    if (mine_too && part == 0) {
+      int id;
+      float w;
+      route_choose<TL>(a, t, key, r.mx, inv, id, w);
+      put_row(a, t, id, w, cnt);
+    }
+    __syncthreads();
+  }
   if (a.single) {  // one cluster: each CTA joins a share of the counts
     cluster_sync();
     const int ranks = static_cast<int>(gridDim.x), each = (E + ranks - 1) / ranks, lo = blockIdx.x * each;
