@@ -176,7 +176,7 @@ template <typename TS, typename TB, int MODE>
 int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
   constexpr ResMode kMode = static_cast<ResMode>(MODE);
   const ResForm f = res_form(a.N, kMode, false);
-  const int per_sm = f.ranks > 1 || f.lpr < 0 ? 1 : std::max(2, 1024 / f.threads);
+  const int per_sm = f.lpr < 0 ? 1 : f.ranks > 1 ? 2 : std::max(2, 1024 / f.threads);
   const int64_t values = static_cast<int64_t>(f.threads) * f.v * 8;
   const ResShared sh = res_shared(f.threads * res_thread_bytes(kMode, f.v, sizeof(TS)),
                                   a.f ? f.threads * res_thread_bytes(kMode, f.v, sizeof(TB)) : 0, values * 4 * (a.f ? 2 : 1),
@@ -194,7 +194,7 @@ int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
                           : residual_norm_kernel<TS, TB, 0, 2, MODE>;
   a.stages = sh.stages, a.stages_f = sh.stages_f, a.ranks = f.ranks;
   // (row blocks: a multiple of 8 where a CTA takes more than one, see Columns)
-  const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count / f.ranks / 8 * 8 * per_sm);
+  const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count * per_sm / f.ranks / 8 * 8);
   return res_launch(go, blocks * f.ranks, f.threads, sh.bytes, f.ranks, a, s);
 }
 

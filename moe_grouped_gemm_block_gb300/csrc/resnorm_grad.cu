@@ -176,12 +176,27 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
           out[a.N + col.at(v, j)] = j & 1 ? df_sum[v][j / 2].y : df_sum[v][j / 2].x;
         }
   } else {
-    // the CTA's rows one after the other (their columns may lie shifted)
+    // the rows of a warp, where they have the same columns, then the warps (else the rows) one after the other
     float* sums = reinterpret_cast<float*>(shared);
     cp_async_wait(0);
     __syncthreads();  // nobody's places are in use any more
-    for (int q = 0; q < kRows; ++q) {
-      if (mine == q) {
+    if constexpr (MODE != kShifted) {
+#pragma unroll
+      for (int off = 16; off >= (LPR ? LPR : 1); off >>= 1)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            dw[v][j].x += __shfl_xor_sync(0xffffffffu, dw[v][j].x, off);
+            dw[v][j].y += __shfl_xor_sync(0xffffffffu, dw[v][j].y, off);
+            df_sum[v][j].x += __shfl_xor_sync(0xffffffffu, df_sum[v][j].x, off);
+            df_sum[v][j].y += __shfl_xor_sync(0xffffffffu, df_sum[v][j].y, off);
+          }
+    }
+    constexpr int kTurns = MODE == kShifted ? kRows : 8;
+    const int turn = MODE == kShifted ? mine : (threadIdx.x & 31) < (LPR ? LPR : 1) ? static_cast<int>(threadIdx.x >> 5) : -1;
+    for (int q = 0; q < kTurns; ++q) {
+      if (turn == q) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
