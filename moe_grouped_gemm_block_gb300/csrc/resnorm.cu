@@ -20,7 +20,7 @@ namespace fp8g {
 namespace {
 
 template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
-__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE == kAligned ? 2 : 1)
+__global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE != kSingle ? 2 : 1)
     residual_norm_kernel(const ResArgs a) {
   __shared__ float red[2][1][32];
   extern __shared__ __align__(16) unsigned char shared[];
