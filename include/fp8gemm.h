@@ -567,8 +567,8 @@ int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64
  *   token_mask  bytes [T] or null: 0 = a padding token, which gets ids like any other and weights 0, and is not counted
  *   topk_ids    int32 [T, topk], topk_weights fp32 [T, topk], counts int32 [E]
  *   0 <= T < 2^31 (T == 0: counts are zeros), 1 <= E <= 2048, 1 <= groups <= 32 dividing E, 1 <= topk_groups <= groups,
- *   1 <= topk <= min(32, topk_groups * E / groups), T * topk < 2^31, renormalize 0 or 1, scale not NaN.  Pointers aligned to
- *   their element.
+ *   1 <= topk <= min(32, topk_groups * E / groups), T * topk < 2^31, renormalize 0 or 1, scale not NaN.  Pointers
+ *   aligned to their element.
  */
 int fp8g_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int64_t ldl, int32_t topk,
                    const float* bias, int32_t score, int32_t groups, int32_t topk_groups, int32_t renormalize,
@@ -604,8 +604,9 @@ int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_
  *            is no block, h = x (and no post_norm, gate or h is given).  y null: h alone is wanted.
  *   weight, post_weight, gate  [N], all of type w_dtype, each may be null (1); post_weight only with post_norm
  *   rstd_f, rstd  fp32 [M], for the backward call; either may be null
- *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31 - 15, eps >= 0.  Strides are in elements and at least N, pointers aligned to
- *   their element; rows on the 16-byte grid (bases, strides and N multiples of 8 values) take the faster paths.
+ *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31 - 15, eps >= 0.  Strides are in elements and at least N, pointers
+ *   aligned to their element.  Matrices whose bases are 16-byte aligned and whose strides are equal modulo 8 take the
+ *   faster paths, the fastest where the strides and N are multiples of 8; so do at most 16384 columns.
  *   Squares are summed in fp32: beyond values of about 1e19 a row's rstd is 0.
  */
 int fp8g_residual_rms_norm(const void* x, int64_t ldx, const void* f, int64_t ldf, int32_t stream_dtype,
@@ -628,8 +629,8 @@ int fp8g_residual_rms_norm_backward_workspace(int64_t M, int64_t N, int64_t* byt
  *   h, f, rstd_f, rstd, weights  as the forward call had and wrote them.  f may be null where there was none, or where
  *            neither post_norm nor dgate needs it.
  *   dx       [M, N] (stream_dtype), may be dh itself; df  [M, N] (block_dtype), or null where there was no f
- *   dweight, dgate, dpost  fp32 [N], overwritten (M == 0: zeros), each may be null; dgate and dpost only with a gate and a
- *            post_weight.  Where all are null no workspace is needed and it may be null.
+ *   dweight, dgate, dpost  fp32 [N], overwritten (M == 0: zeros), each may be null; dgate and dpost only with a gate
+ *            and a post_weight.  Where all are null no workspace is needed and it may be null.
  *   Sizes and alignment as in the forward call.
  */
 int fp8g_residual_rms_norm_backward(
@@ -701,10 +702,10 @@ typedef struct {
  *
  * state_bits 8: m and the root of v are held as e4m3 codes with one scale, amax * (1 / 448), for each 128 values (a
  * tensor's blocks start at its first value; scale 0 and codes of 0 where amax < 2^-60).  The step uses the unrounded new
- * states; they are then taken to one of the two codes next to them: with y = |x| * (448 * (1 / amax)) between the codes a <= y < b of
- * value i of its tensor, up where (y - a) / (b - a) + u >= 1, u = floor(((i * 0xC13FA9A9 + t * 0x91E10DA5 + z) mod 2^32) /
- * 2^12) / 2^20, z = 0 (m) or 2^31 (the root), which is right on the average of the steps; a root > 0 becomes at least
- * the lowest code.
+ * states; they are then taken to one of the two codes next to them: for value i of its tensor with
+ * y = |x| * (448 * (1 / amax)) between the codes a <= y < b, up where (y - a) / (b - a) + u >= 1 with
+ * u = floor(((i * 0xC13FA9A9 + t * 0x91E10DA5 + z) mod 2^32) / 2^12) / 2^20, z = 0 (m) or 2^31 (the root), which is right
+ * on the average of the steps; a root > 0 becomes at least the lowest code.
  *
  *   tensors   HOST array, read during the call only; the addresses travel as kernel arguments, so a captured graph keeps
  *             them.  Empty tensors (numel 0) may hold nulls.  No written tensor overlaps another one of the list.
@@ -712,8 +713,8 @@ typedef struct {
  *   step      int64 [1], device memory: the steps taken so far (>= 0).  A replayed graph counts on.
  *   norm      fp32 [1], device memory, as fp8g_grad_norm wrote it, or null (max_norm and norm_eps are then ignored)
  *   workspace FP8G_ADAMW_WORKSPACE bytes, 16-byte aligned, of calls that do not overlap in time
- *   0 <= beta1, beta2 < 1, eps >= 1e-30, max_norm, norm_eps >= 0, n <= 2^20, at most 2^40 values.  Pointers aligned to their
- *   element; tensors on 16-byte boundaries (codes: 4) take the faster path.  Gradients are finite, or norm is given.
+ *   0 <= beta1, beta2 < 1, eps >= 1e-30, max_norm, norm_eps >= 0, n <= 2^20, at most 2^40 values.  Pointers aligned to
+ *   their element; tensors on 16-byte boundaries (codes: 4) take the faster path.  Gradients are finite, or norm is given.
  */
 int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t state_bits, double lr, const float* lr_dev,
                double beta1, double beta2, double eps, int64_t* step, const float* norm, float max_norm,

@@ -16,8 +16,9 @@
 // steps and a call is repeatable.  And a root that is not 0 keeps the lowest code where it would round to 0: it is then
 // too large, which makes a step too small, never too large.  A block whose largest is below 2^-60 becomes 0.
 //
-// Bound by memory.
-
+// Bound by memory with states in 32 bits, by that and 65 instructions a value in 8.  117M values, device times and the
+// share of the copy rate: 32 bits, fp32 with bf16 gradients 475 to 485 us (93%); 8 bits with masters 337 (83%), without
+// 278 (63%).  1M values: 9 and 11 us, of which the step's launch before is 2.
 #include <algorithm>
 #include <cmath>
 #include <cuda_fp16.h>

@@ -1,7 +1,17 @@
 // resnorm_grad.cu -- the gradient of the norms around a block (the formulas: resnorm.cu).
 //
-// A row takes two means, of which the second needs the first's result, and gives two results; a column's sums over the rows stay in the registers
-// of the threads that have the column, and leave a partial sum a CTA that a second, dependent launch joins in order.
+// A row takes two means, of which the second needs the first's result, and gives two results; a column's sums over the rows
+// stay in the registers of the threads that have the column, and leave a partial sum a CTA that a second, dependent
+// launch joins in order.
+//
+// Bound by memory where a matrix is fp32 and by its instructions' latencies where all are bf16 (an SM holds 16 warps of 128
+// registers; 39 instructions a value, of which the unpacking of bf16, twice, is a fifth):
+//   8192 x 7168, fp32 stream and bf16 block: 192 us (81% of the copy rate);  16384 x 4096: 195 (91%)
+//   4096 x 7168 bf16: 87 (60%);  16384 x 2048 bf16: 84 (71%);  16384 x 64 bf16: 12 (16%)
+// What was slower: fp32 rows in eights a thread (a warp's accesses then touch twice the sectors: 252 us), both means from
+// one sum over the row (sum q k = sum p dh k + r (sum p g k - s sum p e k): as fast with fp32, 103 instead of 90 us with
+// bf16), bulk copies with a barrier a stage (equal, and 222 instead of 194 us at 16384 x 4096), a second stage for three of
+// the four matrices (kept, worth 1%), 32 warps with a unit each (equal).
 
 #include "resnorm.cuh"
 

@@ -6,7 +6,9 @@
 //     dg = dh u s (1 + g (1 - s)),  du = dh g s
 //
 // Everything is fp32 until the one rounding of a result.  Bound by memory: forward 4 bytes read and 1 written a value
-// (3 with h in bf16), backward 6 read and 4 written (6).
+// (3 with h in bf16), backward 6 read and 4 written (6).  Device times, and the share of the copy rate:
+//   33024 x 4096: 113 us (89%), with h 156 (90%), backward with h 248 (96%);  64 rows of 32 experts, masked: 4.0
+// Two or four blocks of 128 a group at once were slower (123 and 157 us without h).
 
 #include <algorithm>
 #include <cuda_runtime.h>
