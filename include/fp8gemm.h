@@ -604,7 +604,7 @@ int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_
  *            is no block, h = x (and no post_norm, gate or h is given).  y null: h alone is wanted.
  *   weight, post_weight, gate  [N], all of type w_dtype, each may be null (1); post_weight only with post_norm
  *   rstd_f, rstd  fp32 [M], for the backward call; either may be null
- *   0 <= M < 2^31 (M == 0: no-op), 1 <= N < 2^31 - 15, eps >= 0.  Strides are in elements and at least N, pointers
+ *   0 <= M < 2^31 (M == 0: no-op), 1 <= N <= 2^29, eps >= 0.  Strides are in elements and at least N, pointers
  *   aligned to their element.  Matrices whose bases are 16-byte aligned and whose strides are equal modulo 8 take the
  *   faster paths, the fastest where the strides and N are multiples of 8; so do at most 16384 columns.
  *   Squares are summed in fp32: beyond values of about 1e19 a row's rstd is 0.

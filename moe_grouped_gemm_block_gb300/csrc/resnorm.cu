@@ -213,7 +213,7 @@ extern "C" int fp8g_residual_rms_norm(const void* x, int64_t ldx, const void* f,
                                       int32_t w_dtype, float eps, void* h, int64_t ldh, void* y, int64_t ldy,
                                       float* rstd_f, float* rstd, void* stream) {
   if (bad_type(stream_dtype) || bad_type(block_dtype) || bad_type(w_dtype) || M < 0 || M > 0x7FFFFFFF || N < 1 ||
-      N > 0x7FFFFFF0 || ldx < N || (f && ldf < N) || (h && ldh < N) || (y && ldy < N) || (post_norm & ~1) ||
+      N > kResMaxCols || ldx < N || (f && ldf < N) || (h && ldh < N) || (y && ldy < N) || (post_norm & ~1) ||
       !(eps >= 0.0f) || (post_weight && !post_norm))
     return FP8G_ERR_INVALID_ARG;
   if (M == 0) return FP8G_OK;  // (no rows: their addresses may all be null)

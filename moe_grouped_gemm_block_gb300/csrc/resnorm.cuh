@@ -376,6 +376,8 @@ inline ResShared res_shared(int64_t stage, int64_t f, int64_t fixed, int per_sm)
   return {0, 0, 0};
 }
 
+// Columns a row may have: the kernels count them, and twice as many, in 32 bits.
+constexpr int64_t kResMaxCols = int64_t{1} << 29;
 inline bool bad_type(int32_t t) { return t != FP8G_BF16 && t != FP8G_F32; }
 inline int64_t type_size(int32_t t) { return t == FP8G_F32 ? 4 : 2; }
 // How the rows of all matrices of a call lie.

@@ -372,7 +372,7 @@ int res_backward(ResArgs a, const ResJoin& j, cudaStream_t s) {
 using namespace fp8g;
 
 extern "C" int fp8g_residual_rms_norm_backward_workspace(int64_t M, int64_t N, int64_t* bytes) {
-  if (M < 0 || M > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFF0 || !bytes) return FP8G_ERR_INVALID_ARG;
+  if (M < 0 || M > 0x7FFFFFFF || N < 1 || N > kResMaxCols || !bytes) return FP8G_ERR_INVALID_ARG;
   int64_t P = 0;
   for (const ResMode mode : {kAligned, kShifted, kSingle}) P = std::max(P, res_grad_blocks(res_form(N, mode, true), M));
   *bytes = std::max<int64_t>(16, P * 2 * N * 4);
@@ -387,7 +387,7 @@ extern "C" int fp8g_residual_rms_norm_backward(
     int64_t workspace_bytes, void* stream) {
   const bool sums = dweight || dgate || dpost;
   if (bad_type(stream_dtype) || bad_type(block_dtype) || bad_type(w_dtype) || M < 0 || M > 0x7FFFFFFF || N < 1 ||
-      N > 0x7FFFFFF0 || lddx < N || (dy && (lddy < N || ldh < N)) || (dh && lddh < N) || (f && ldf < N) ||
+      N > kResMaxCols || lddx < N || (dy && (lddy < N || ldh < N)) || (dh && lddh < N) || (f && ldf < N) ||
       (df && lddf < N) || (post_norm & ~1) || (post_weight && !post_norm) || (dgate && !gate) || (dpost && !post_weight))
     return FP8G_ERR_INVALID_ARG;
   if (M > 0 && (!dx || (!dy && !dh) || (!df && (f || post_norm || dgate || dpost)) || (dy && (!h || !rstd)) || (post_norm && (!f || !rstd_f)) ||
