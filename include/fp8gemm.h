@@ -599,7 +599,7 @@ int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_
  *     y = h * rstd * weight,  rstd[m] = 1 / sqrt(sum_n h^2 / N + eps)
  *
  *   x, h     [M, N] (stream_dtype): the residual stream before and after the block, row strides ldx, ldh; h may be x
- *            itself, or null
+ *            itself (with the same stride), or null
  *   f, y     [M, N] (block_dtype): what the block gave and what the next one takes, row strides ldf, ldy.  f null: there
  *            is no block, h = x (and no post_norm, gate or h is given).  y null: h alone is wanted.
  *   weight, post_weight, gate  [N], all of type w_dtype, each may be null (1); post_weight only with post_norm
@@ -628,7 +628,8 @@ int fp8g_residual_rms_norm_backward_workspace(int64_t M, int64_t N, int64_t* byt
  *   dh       [M, N] (stream_dtype): what reaches h on other ways, or null (0); not both null
  *   h, f, rstd_f, rstd, weights  as the forward call had and wrote them.  f may be null where there was none, or where
  *            neither post_norm nor dgate needs it.
- *   dx       [M, N] (stream_dtype), may be dh itself; df  [M, N] (block_dtype), or null where there was no f
+ *   dx       [M, N] (stream_dtype), may be dh itself (with the same stride);  df  [M, N] (block_dtype), or null where
+ *            there was no f
  *   dweight, dgate, dpost  fp32 [N], overwritten (M == 0: zeros), each may be null; dgate and dpost only with a gate
  *            and a post_weight.  Where all are null no workspace is needed and it may be null.
  *   Sizes and alignment as in the forward call.

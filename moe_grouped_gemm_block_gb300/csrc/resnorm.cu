@@ -217,6 +217,7 @@ extern "C" int fp8g_residual_rms_norm(const void* x, int64_t ldx, const void* f,
       !(eps >= 0.0f) || (post_weight && !post_norm))
     return FP8G_ERR_INVALID_ARG;
   if (M == 0) return FP8G_OK;  // (no rows: their addresses may all be null)
+  if (h == x && h && M > 1 && ldh != ldx) return FP8G_ERR_INVALID_ARG;  // (its rows would lie on others that are still read)
   if (!x || (!h && !y) || (!f && (post_norm || post_weight || gate || h))) return FP8G_ERR_INVALID_ARG;
   const int64_t ss = type_size(stream_dtype), bs = type_size(block_dtype), ws = type_size(w_dtype);
   if (!aligned_to(x, ss) || !aligned_to(h, ss) || !aligned_to(f, bs) || !aligned_to(y, bs) || !aligned_to(weight, ws) ||

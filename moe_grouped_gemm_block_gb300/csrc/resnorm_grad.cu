@@ -393,6 +393,7 @@ extern "C" int fp8g_residual_rms_norm_backward(
   if (M > 0 && (!dx || (!dy && !dh) || (!df && (f || post_norm || dgate || dpost)) || (dy && (!h || !rstd)) || (post_norm && (!f || !rstd_f)) ||
                 ((dgate || dpost) && !f) || (dweight && !dy)))
     return FP8G_ERR_INVALID_ARG;
+  if (dx && dx == dh && M > 1 && lddx != lddh) return FP8G_ERR_INVALID_ARG;
   int64_t need = 0;
   fp8g_residual_rms_norm_backward_workspace(M, N, &need);
   if (sums && (!workspace || workspace_bytes < need)) return FP8G_ERR_INVALID_ARG;

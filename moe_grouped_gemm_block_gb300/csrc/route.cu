@@ -963,7 +963,7 @@ extern "C" int fp8g_moe_route_backward(const void* logits, int32_t dtype, int64_
   if (st != FP8G_OK) return st;
   if (ldd < E || scale != scale) return FP8G_ERR_INVALID_ARG;
   if (T == 0) return FP8G_OK;
-  if (!logits || !topk_ids || !dweights || !dlogits) return FP8G_ERR_INVALID_ARG;
+  if (!logits || !topk_ids || !dweights || !dlogits || (dlogits == logits && T > 1 && ldd != ldl)) return FP8G_ERR_INVALID_ARG;
   const uintptr_t size = dtype == FP8G_F32 ? 4 : 2;
   if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(topk_ids, 4) || !aligned_to(dweights, 4))
     return FP8G_ERR_ALIGNMENT;

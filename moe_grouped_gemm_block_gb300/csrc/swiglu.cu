@@ -200,7 +200,7 @@ extern "C" int fp8g_swiglu_backward(const void* dh, int64_t lddh, const void* gu
       lddh < F || ldgu < 2 * F || lddgu < 2 * F || (h && ldh < F))
     return FP8G_ERR_INVALID_ARG;
   if (M == 0) return FP8G_OK;
-  if (!dh || !gu || !dgu) return FP8G_ERR_INVALID_ARG;
+  if (!dh || !gu || !dgu || (dgu == gu && M > 1 && lddgu != ldgu)) return FP8G_ERR_INVALID_ARG;
   if (bad_rows(dh, lddh) || bad_rows(gu, ldgu) || bad_rows(dgu, lddgu) || (h && bad_rows(h, ldh)))
     return FP8G_ERR_ALIGNMENT;
   DeviceInfo* dev = nullptr;

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from tests.test_train_ops_refusals import INVALID, NORM, NORM_BWD, _args, lib  # noqa: F401
+from tests.test_train_ops_refusals import GLU_BWD, INVALID, NORM, NORM_BWD, ROUTE_BWD, _args, lib  # noqa: F401
 
 P2 = 1 << 29
 
@@ -23,3 +23,10 @@ def test_norm_workspace_of_the_widest_rows(lib):  # noqa: F811
     n = ctypes.c_int64()
     assert lib.fp8g_residual_rms_norm_backward_workspace(1 << 20, P2, ctypes.byref(n)) == 0
     assert n.value >= 2 * P2 * 4 and n.value % (2 * P2 * 4) == 0
+
+
+def test_results_in_place_of_an_input_keep_its_stride(lib):  # noqa: F811
+    assert lib.fp8g_residual_rms_norm(*_args(NORM, dict(ldh=72))) == INVALID
+    assert lib.fp8g_residual_rms_norm_backward(*_args(NORM_BWD, dict(lddx=72))) == INVALID
+    assert lib.fp8g_swiglu_backward(*_args(GLU_BWD, dict(lddgu=264))) == INVALID
+    assert lib.fp8g_moe_route_backward(*_args(ROUTE_BWD, dict(ldd=24))) == INVALID
