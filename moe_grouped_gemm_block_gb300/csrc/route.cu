@@ -61,10 +61,11 @@ __device__ __forceinline__ double key_value(uint64_t key) {
 constexpr uint64_t kRuledOut = 0x000FFFFFFFFFFFFFull;  // the key of -inf
 
 // e^x for x <= 0, in 64 bits without a branch (0 below 2^-1022): 2^n e^r with |r| <= ln 2 / 2, the series of e^r up to
-// r^13 / 13! (the next term is below 2^-57).  ln 2 in two parts, the first with zeros at its end, so that n times it is exact.
+// r^13 / 13! (the next term is below 2^-57).  ln 2 in two parts (Cody and Waite), the first its 42 leading bits, so that n
+// times it, of at most 11 bits, is exact.
 __device__ __forceinline__ double exp_series(double x) {
   const double n = rint(x * 1.4426950408889634);
-  const double r = fma(n, -1.90821492927058770002e-10, fma(n, -6.93147180369123816490e-01, x));
+  const double r = fma(n, -0x1.ef35793c7673p-45, fma(n, -0x1.62e42fefa38p-1, x));
   double p = 1.0 / 6227020800.0;
   constexpr double c[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
                             1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
