@@ -314,12 +314,43 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper&
   else adam_values<BITS, TP, TG, MASTER, false>(t, h, s, block);
 }
 
+// The tensor of chunk c, from the i-th on.
+template <int CAP>
+__device__ __forceinline__ int adam_find(const AdamTable<CAP>& tab, uint32_t c, int i) {
+  if (c < tab.end[i]) return i;
+  int lo = i + 1, hi = tab.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (c < tab.end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+// Brings the CTA's first chunk into L2, a line of 128 bytes a thread and matrix (memory cold: 150 tensors of 10000 values
+// 18.9 -> 16.9 us, 16M values 82.4 -> 80.8).
+template <int BITS, int CAP>
+__device__ __forceinline__ void adam_prefetch(const AdamTable<CAP>& tab) {
+  const int i = adam_find(tab, blockIdx.x, 0);
+  const AdamTensor& t = tab.t[i];
+  const int64_t first = static_cast<int64_t>(blockIdx.x - (i ? tab.end[i - 1] : 0u)) * kAdamPass;
+  const int64_t n = min(t.numel - first, static_cast<int64_t>(kAdamPass));
+  auto bring = [&](const void* p, int size) {
+    const int64_t at = static_cast<int64_t>(threadIdx.x) * 128;
+    if (p && at < n * size) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + first * size + at));
+  };
+  bring(t.grad, t.kind & kGradF32 ? 4 : 2);
+  bring(t.master ? t.master : t.param, t.kind & (kMaster | kParamF32) ? 4 : 2);
+  bring(t.m, BITS / 8);
+  bring(t.v, BITS / 8);
+}
+
 // Resident CTAs walk over the chunks of 2048 values (a CTA a chunk: 16M values took 100 us, most of it the CTAs' starts).
 template <int CAP, int BITS>
 __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
                                                                          const AdamHyper h,
                                                                          const AdamStep* __restrict__ step) {
   const uint32_t chunks = tab.end[tab.n - 1];
+  adam_prefetch<BITS>(tab);  // (under the step's end: what was before that is complete)
   griddep_wait();
   AdamStep s;
   s.coef = __ldcg(&step->coef), s.lr = __ldcg(&step->lr), s.lr1 = __ldcg(&step->lr1), s.root2 = __ldcg(&step->root2);
@@ -327,15 +358,7 @@ __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(
   if (s.skip) return;
   int i = 0;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    if (c >= tab.end[i]) {
-      int lo = i + 1, hi = tab.n - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (c < tab.end[mid]) hi = mid;
-        else lo = mid + 1;
-      }
-      i = lo;
-    }
+    i = adam_find(tab, c, i);
     const AdamTensor& t = tab.t[i];
     const int64_t block = static_cast<int64_t>(c - (i ? tab.end[i - 1] : 0u)) * kAdamPass + (threadIdx.x >> 4) * 128;
     if (block >= t.numel) continue;
