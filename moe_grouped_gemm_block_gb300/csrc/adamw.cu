@@ -308,10 +308,12 @@ __device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper
   }
 }
 
+// The blocks of tensor t from `block` on, `step` values apart.
 template <int BITS, typename TP, typename TG, bool MASTER>
-__device__ __forceinline__ void adam_block(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
-  if ((t.kind & kVectors) && block + 128 <= t.numel) adam_values<BITS, TP, TG, MASTER, true>(t, h, s, block);
-  else adam_values<BITS, TP, TG, MASTER, false>(t, h, s, block);
+__device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block, int64_t step) {
+  const int64_t whole = t.kind & kVectors ? t.numel - 128 : -1;  // the last place where a whole block may start
+  for (; block <= whole; block += step) adam_values<BITS, TP, TG, MASTER, true>(t, h, s, block);
+  for (; block < t.numel; block += step) adam_values<BITS, TP, TG, MASTER, false>(t, h, s, block);
 }
 
 // The tensor of chunk c, from the i-th on.
@@ -357,18 +359,19 @@ __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(
   s.time = __ldcg(&step->time), s.skip = __ldcg(&step->skip);
   if (s.skip) return;
   int i = 0;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  const int64_t step_size = static_cast<int64_t>(gridDim.x) * kAdamPass;
+  for (uint32_t c = blockIdx.x; c < chunks;) {
     i = adam_find(tab, c, i);
     const AdamTensor& t = tab.t[i];
     const int64_t block = static_cast<int64_t>(c - (i ? tab.end[i - 1] : 0u)) * kAdamPass + (threadIdx.x >> 4) * 128;
-    if (block >= t.numel) continue;
+    c += (tab.end[i] - c + gridDim.x - 1) / gridDim.x * gridDim.x;  // the CTA's first chunk past this tensor's
     switch (t.kind & (kParamF32 | kGradF32 | kMaster)) {
-      case 0: adam_block<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block); break;
-      case kGradF32: adam_block<BITS, __nv_bfloat16, float, false>(t, h, s, block); break;
-      case kMaster: adam_block<BITS, __nv_bfloat16, __nv_bfloat16, true>(t, h, s, block); break;
-      case kMaster | kGradF32: adam_block<BITS, __nv_bfloat16, float, true>(t, h, s, block); break;
-      case kParamF32: adam_block<BITS, float, __nv_bfloat16, false>(t, h, s, block); break;
-      default: adam_block<BITS, float, float, false>(t, h, s, block); break;
+      case 0: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block, step_size); break;
+      case kGradF32: adam_blocks<BITS, __nv_bfloat16, float, false>(t, h, s, block, step_size); break;
+      case kMaster: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, true>(t, h, s, block, step_size); break;
+      case kMaster | kGradF32: adam_blocks<BITS, __nv_bfloat16, float, true>(t, h, s, block, step_size); break;
+      case kParamF32: adam_blocks<BITS, float, __nv_bfloat16, false>(t, h, s, block, step_size); break;
+      default: adam_blocks<BITS, float, float, false>(t, h, s, block, step_size); break;
     }
   }
 }
