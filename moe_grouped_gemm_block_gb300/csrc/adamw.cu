@@ -23,6 +23,7 @@
 #include <cmath>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -165,7 +166,8 @@ __device__ __forceinline__ void put8(T* p, const Places<FULL>& at, const float (
 // the rounded root but for one value in some 2^20 (whose true root lies so near the middle between two floats); by the
 // compiler's root where one of the eight is below the normal range or not finite.  (With that and its quotient for all,
 // a branch in each, 117M values with 8-bit states took 479 us.)
-__device__ __forceinline__ void square_roots(const float2 (&v)[4], float2 (&root)[4]) {
+// -> whether all are positive for sure.
+__device__ __forceinline__ bool square_roots(const float2 (&v)[4], float2 (&root)[4]) {
   float lo = v[0].x, hi = v[0].x;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -181,9 +183,11 @@ __device__ __forceinline__ void square_roots(const float2 (&v)[4], float2 (&root
       const float2 s = mul2(v[j], r), minus = make_float2(-s.x, -s.y);
       root[j] = __ffma2_rn(__ffma2_rn(minus, s, v[j]), mul2(r, both(0.5f)), s);
     }
+    return true;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) root[j] = make_float2(__fsqrt_rn(v[j].x), __fsqrt_rn(v[j].y));
+    return false;
   }
 }
 __device__ __forceinline__ float2 quotient(float2 a, float2 b) {  // two units in the last place; b is normal
@@ -198,27 +202,23 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-template <bool FULL>
-__device__ __forceinline__ void get_codes(const uint8_t* p, const Places<FULL>& at, float scale, float (&f)[8]) {
+__device__ __forceinline__ void decode(const uint32_t (&w)[2], float scale, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<float2(&)[4]>(f)[j] = mul2(e4m3x2_to_f32(w[j / 2] >> (16 * (j & 1))), both(scale));
+}
+__device__ __forceinline__ void get_codes(const uint8_t* p, const Places<false>& at, float scale, float (&f)[8]) {
   uint32_t w[2] = {0u, 0u};
   p += at.first;
-  if constexpr (FULL) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-    w[1] = *reinterpret_cast<const uint32_t*>(p + 64);
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at.has(j)) w[j / 4] |= static_cast<uint32_t>(p[at.offset(j)]) << (8 * (j & 3));
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 d = e4m3x2_to_f32(w[j / 2] >> (16 * (j & 1)));
-    reinterpret_cast<float2(&)[4]>(f)[j] = mul2(d, both(scale));
-  }
+  for (int j = 0; j < 8; ++j)
+    if (at.has(j)) w[j / 4] |= static_cast<uint32_t>(p[at.offset(j)]) << (8 * (j & 3));
+  decode(w, scale, f);
 }
-// The codes of a block that 16 lanes hold, and its scale (see above).  ROOT: what is not 0 gets no 0.
+// The codes of a block that 16 lanes hold, and its scale (see above).  ROOT: what is not 0 gets no 0; positive: none is 0.
 template <bool ROOT, bool FULL>
-__device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places<FULL>& at, uint32_t time, const float (&f)[8]) {
+__device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places<FULL>& at, uint32_t time, const float (&f)[8],
+                                          bool positive = false) {
   float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
@@ -237,16 +237,17 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places
     // the codes are 2^-9 apart, as they are from 2^-6 to 2^-5: the sum with 2^-6 (what it cuts off is less than u's
     // last bit) has them at the same bits.
     const float2 x = make_float2(f[2 * j], f[2 * j + 1]);
-    const float2 y = mul2(make_float2(fabsf(x.x), fabsf(x.y)), both(inv));
-    float c[2] = {y.x, y.y};
+    const float2 y = mul2(x, both(inv));
+    float c[2] = {fabsf(y.x), fabsf(y.y)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float low = c[k] < 0x1p-6f ? 0x1p-6f : 0.0f;
+      const float low = c[k] < 0x1p-6f ? 1.0f : 0.0f;
       const uint32_t u = (first + static_cast<uint32_t>(at.offset(2 * j + k)) * kPlaceStep) >> 12;
-      c[k] = __uint_as_float((__float_as_uint(__fadd_rz(c[k], low)) + u) & 0xFFF00000u) - low;
+      c[k] = fmaf(low, -0x1p-6f, __uint_as_float((__float_as_uint(__fmaf_rz(low, 0x1p-6f, c[k])) + u) & 0xFFF00000u));
       const float own = k ? x.y : x.x;
-      if (ROOT) c[k] = fmaxf(c[k], fminf(own * 0x1p100f, lowest));  // (the least root is 2^-75)
+      if (ROOT) c[k] = fmaxf(c[k], lowest);
       else c[k] = copysignf(c[k], own);
+      if (ROOT && !positive) c[k] = own == 0.0f ? 0.0f : c[k];
     }
     w[j / 2] |= static_cast<uint32_t>(cvt_e4m3x2(c[1], c[0])) << (16 * (j & 1));
   }
@@ -261,21 +262,71 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places
   }
 }
 
-// One block of 128 values of tensor t, from `block` on.
-template <int BITS, typename TP, typename TG, bool MASTER, bool FULL>
-__device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
-  const Places<FULL> at(block, t.numel);
-  float p[8], g[8], m[8], v[8];
-  get8(static_cast<const TG*>(t.grad), at, g);
-  if constexpr (MASTER) get8(t.master, at, p);
-  else get8(static_cast<const TP*>(t.param), at, p);
-  if constexpr (BITS == 32) {
-    get8(static_cast<const float*>(t.m), at, m);
-    get8(static_cast<const float*>(t.v), at, v);
+// A thread's part of whole blocks with 8-bit states, copied ahead into places of its own: a block's arithmetic is long, and
+// so few bytes of it are on their way at once that the loads' latency would show (117M values: 255 us without masters).
+constexpr int kAdamStages = 2;
+constexpr int kAdamPlaces = 2 * 16 + 2 * 16 + 4 * 4 + 2 * 4;  // bytes of a thread and stage, at most
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void load_place(uint32_t from, float* f) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(from) : "memory");
   } else {
-    get_codes(static_cast<const uint8_t*>(t.m), at, t.m_scale[block >> 7], m);
-    get_codes(static_cast<const uint8_t*>(t.v), at, t.v_scale[block >> 7], v);
+    uint32_t a, b;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(from) : "memory");
+    f[0] = __uint_as_float(a << 16), f[1] = __uint_as_float(a & 0xFFFF0000u);
+    f[2] = __uint_as_float(b << 16), f[3] = __uint_as_float(b & 0xFFFF0000u);
   }
+}
+__device__ __forceinline__ uint32_t load_word(uint32_t from) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+  return v;
+}
+template <typename T, typename TG>  // T: of what the step starts from, the param or its master copy
+struct Ahead {
+  static constexpr int kP = 4 * static_cast<int>(sizeof(T)), kG = 4 * static_cast<int>(sizeof(TG));
+  static constexpr uint32_t kGrads = 2 * kP * kAdamThreads, kCodes = kGrads + 2 * kG * kAdamThreads;
+  uint32_t places;
+  __device__ __forceinline__ void copy(int stage, const AdamTensor& t, const void* from, int64_t block) const {
+    const int64_t first = block + 4 * (threadIdx.x & 15);
+    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x;
+    const T* p = static_cast<const T*>(from) + first;
+    const TG* g = static_cast<const TG*>(t.grad) + first;
+    const uint8_t *m = static_cast<const uint8_t*>(t.m) + first, *v = static_cast<const uint8_t*>(t.v) + first;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      copy_ahead<kP>(at + (i * kAdamThreads + x) * kP, p + 64 * i);
+      copy_ahead<kG>(at + kGrads + (i * kAdamThreads + x) * kG, g + 64 * i);
+      copy_ahead<4>(at + kCodes + (i * kAdamThreads + x) * 4, m + 64 * i);
+      copy_ahead<4>(at + kCodes + ((2 + i) * kAdamThreads + x) * 4, v + 64 * i);
+    }
+    copy_ahead<4>(at + kCodes + (4 * kAdamThreads + x) * 4, t.m_scale + (block >> 7));
+    copy_ahead<4>(at + kCodes + (5 * kAdamThreads + x) * 4, t.v_scale + (block >> 7));
+  }
+  __device__ __forceinline__ void load(int stage, float (&p)[8], float (&g)[8], float (&m)[8], float (&v)[8]) const {
+    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x;
+    uint32_t w[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      load_place<kP>(at + (i * kAdamThreads + x) * kP, p + 4 * i);
+      load_place<kG>(at + kGrads + (i * kAdamThreads + x) * kG, g + 4 * i);
+      w[0][i] = load_word(at + kCodes + (i * kAdamThreads + x) * 4);
+      w[1][i] = load_word(at + kCodes + ((2 + i) * kAdamThreads + x) * 4);
+    }
+    decode(w[0], __uint_as_float(load_word(at + kCodes + (4 * kAdamThreads + x) * 4)), m);
+    decode(w[1], __uint_as_float(load_word(at + kCodes + (5 * kAdamThreads + x) * 4)), v);
+  }
+};
+
+// The step of a lane's part of the block of 128 values of tensor t that starts at `block`.
+template <int BITS, typename TP, typename TG, bool MASTER, bool FULL>
+__device__ __forceinline__ void adam_apply(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block,
+                                           const Places<FULL>& at, float (&p)[8], float (&g)[8], float (&m)[8], float (&v)[8]) {
   float2 root[4];
   auto& p2 = reinterpret_cast<float2(&)[4]>(p);
   auto& g2 = reinterpret_cast<float2(&)[4]>(g);
@@ -289,7 +340,7 @@ __device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper
     m2[j] = add_apart(mul2(both(h.b1), m2[j]), mul2(both(h.nb1), gj));
     v2[j] = add_apart(mul2(both(h.b2), v2[j]), mul2(mul2(both(h.nb2), gj), gj));
   }
-  square_roots(v2, root);
+  const bool positive = square_roots(v2, root);
   const float shrink = -s.lr * t.decay;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -304,15 +355,54 @@ __device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper
     put8(static_cast<float*>(t.v), at, v);
   } else {
     put_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + (block >> 7), at, s.time, m);
-    put_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + (block >> 7), at, s.time, v);
+    put_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + (block >> 7), at, s.time, v, positive);
   }
+}
+
+template <int BITS, typename TP, typename TG, bool MASTER, bool FULL>
+__device__ __forceinline__ void adam_values(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block) {
+  const Places<FULL> at(block, t.numel);
+  float p[8], g[8], m[8], v[8];
+  get8(static_cast<const TG*>(t.grad), at, g);
+  if constexpr (MASTER) get8(t.master, at, p);
+  else get8(static_cast<const TP*>(t.param), at, p);
+  if constexpr (BITS == 32) {
+    get8(static_cast<const float*>(t.m), at, m);
+    get8(static_cast<const float*>(t.v), at, v);
+  } else {
+    get_codes(static_cast<const uint8_t*>(t.m), at, t.m_scale[block >> 7], m);
+    get_codes(static_cast<const uint8_t*>(t.v), at, t.v_scale[block >> 7], v);
+  }
+  adam_apply<BITS, TP, TG, MASTER, FULL>(t, h, s, block, at, p, g, m, v);
 }
 
 // The blocks of tensor t from `block` on, `step` values apart.
 template <int BITS, typename TP, typename TG, bool MASTER>
-__device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block, int64_t step) {
+__device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamHyper& h, const AdamStep& s, int64_t block, int64_t step,
+                                            uint32_t places) {
   const int64_t whole = t.kind & kVectors ? t.numel - 128 : -1;  // the last place where a whole block may start
-  for (; block <= whole; block += step) adam_values<BITS, TP, TG, MASTER, true>(t, h, s, block);
+  if constexpr (BITS == 8) {
+    const Ahead<std::conditional_t<MASTER, float, TP>, TG> ahead{places};
+    const void* from = MASTER ? static_cast<const void*>(t.master) : t.param;
+    int64_t next = block;
+    auto bring = [&](int stage) {
+      if (next <= whole) ahead.copy(stage, t, from, next);
+      next += step;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAdamStages; ++i) bring(i);
+    for (int stage = 0; block <= whole; block += step) {
+      float p[8], g[8], m[8], v[8];
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAdamStages - 1) : "memory");
+      ahead.load(stage, p, g, m, v);
+      bring(stage);
+      stage = stage + 1 == kAdamStages ? 0 : stage + 1;
+      adam_apply<BITS, TP, TG, MASTER, true>(t, h, s, block, Places<true>(block, t.numel), p, g, m, v);
+    }
+  } else {
+    for (; block <= whole; block += step) adam_values<BITS, TP, TG, MASTER, true>(t, h, s, block);
+  }
   for (; block < t.numel; block += step) adam_values<BITS, TP, TG, MASTER, false>(t, h, s, block);
 }
 
@@ -351,7 +441,8 @@ template <int CAP, int BITS>
 __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(const __grid_constant__ AdamTable<CAP> tab,
                                                                          const AdamHyper h,
                                                                          const AdamStep* __restrict__ step) {
-  const uint32_t chunks = tab.end[tab.n - 1];
+  __shared__ __align__(16) unsigned char shared[BITS == 8 ? kAdamStages * kAdamPlaces * kAdamThreads : 16];
+  const uint32_t places = smem_u32(shared), chunks = tab.end[tab.n - 1];
   adam_prefetch<BITS>(tab);  // (under the step's end: what was before that is complete)
   griddep_wait();
   AdamStep s;
@@ -366,12 +457,12 @@ __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(
     const int64_t block = static_cast<int64_t>(c - (i ? tab.end[i - 1] : 0u)) * kAdamPass + (threadIdx.x >> 4) * 128;
     c += (tab.end[i] - c + gridDim.x - 1) / gridDim.x * gridDim.x;  // the CTA's first chunk past this tensor's
     switch (t.kind & (kParamF32 | kGradF32 | kMaster)) {
-      case 0: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block, step_size); break;
-      case kGradF32: adam_blocks<BITS, __nv_bfloat16, float, false>(t, h, s, block, step_size); break;
-      case kMaster: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, true>(t, h, s, block, step_size); break;
-      case kMaster | kGradF32: adam_blocks<BITS, __nv_bfloat16, float, true>(t, h, s, block, step_size); break;
-      case kParamF32: adam_blocks<BITS, float, __nv_bfloat16, false>(t, h, s, block, step_size); break;
-      default: adam_blocks<BITS, float, float, false>(t, h, s, block, step_size); break;
+      case 0: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, false>(t, h, s, block, step_size, places); break;
+      case kGradF32: adam_blocks<BITS, __nv_bfloat16, float, false>(t, h, s, block, step_size, places); break;
+      case kMaster: adam_blocks<BITS, __nv_bfloat16, __nv_bfloat16, true>(t, h, s, block, step_size, places); break;
+      case kMaster | kGradF32: adam_blocks<BITS, __nv_bfloat16, float, true>(t, h, s, block, step_size, places); break;
+      case kParamF32: adam_blocks<BITS, float, __nv_bfloat16, false>(t, h, s, block, step_size, places); break;
+      default: adam_blocks<BITS, float, float, false>(t, h, s, block, step_size, places); break;
     }
   }
 }
