@@ -681,7 +681,7 @@ int route_launch(const RouteArgs& a, const DeviceInfo* dev, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(warps) * (8 * route_keys(a.E) + 4 * route_warp_words<VPL>(a.topk)) +
                       static_cast<size_t>((a.E + 3) / 4 * 4) * 4;
   auto kernel = moe_route_kernel<TL, VPL, LPR, KEYS16>;
-  const int st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
+  const int st = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem + 2048);  // (and what is static)
   if (st != FP8G_OK) return st;
   if (!single) moe_route_zero_kernel<<<1, 256, 0, s>>>(a.counts, a.E);
   RouteArgs args = a;

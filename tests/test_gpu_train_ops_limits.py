@@ -169,6 +169,12 @@ def test_route_where_every_row_is_close(T, E, groups, kept, score):
     assert np.allclose(_np(w), 0.25, rtol=1e-4, atol=0)  # (the chosen scores of a row are alike but for some 2^-20)
 
 
+@pytest.mark.parametrize("T,E,k", [(12700, 64, 6), (13300, 64, 3), (5400, 128, 2), (5800, 96, 1)])
+def test_route_where_shared_memory_is_just_below_48_kb(T, E, k):
+    """The dynamic part alone is within what needs no leave, with the static part it is not."""
+    _check_route(_draw((T, E), "f32", 1), k, _draw((E,), "f32", 2, 0.1))
+
+
 @pytest.mark.parametrize("T,E,groups,kept", [(90, 64, 8, 4), (3000, 256, 8, 4), (40, 800, 1, 1)])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_padding_of_nan(T, E, groups, kept, score):
