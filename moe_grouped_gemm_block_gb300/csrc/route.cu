@@ -22,6 +22,7 @@ constexpr int kRouteMaxExperts = 2048;
 constexpr int kRouteMaxTopk = 32;
 constexpr int kRouteMaxGroups = 32;
 constexpr int kRouteWarps = 4;
+constexpr int kRouteFewTopk = 16;  // of a row whose contenders are looked for (with 32 picks they are too many: 1000 instead of 740 us)
 
 struct RouteArgs {
   const void* logits;
@@ -37,11 +38,6 @@ struct RouteArgs {
   float scale;
 };
 
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -103,37 +99,57 @@ struct ExactRow {
   }
 };
 
+// The groups that stay, by the keys of their experts: lanes (groups rounded up to a power of 2, log_l bits of lanes each) as a
+// mask, bit g << log_l of group g among them.
+__device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const uint64_t* key) {
+  const int lane = threadIdx.x & 31, per = a.E / a.groups, log_l = 5 - a.log_groups, L = 1 << log_l, group = lane >> log_l;
+  uint64_t first = 0, second = 0;
+  if (group < a.groups)
+    for (int i = lane & (L - 1); i < per; i += L) {
+      const uint64_t v = key[group * per + i];
+      second = max(second, min(first, v));
+      first = max(first, v);
+    }
+  for (int off = 1; off < L; off <<= 1) {
+    const uint64_t o1 = __shfl_xor_sync(0xffffffffu, first, off), o2 = __shfl_xor_sync(0xffffffffu, second, off);
+    second = max(max(second, o2), min(first, o1));
+    first = max(first, o1);
+  }
+  const uint64_t mine = second <= kRuledOut ? first : order_key(key_value(first) + key_value(second));
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const uint64_t other = __shfl_sync(0xffffffffu, mine, g << log_l);
+    better += other > mine || (other == mine && g < group) ? 1 : 0;
+  }
+  return __ballot_sync(0xffffffffu, group < a.groups && better < a.kept);
+}
+
+// The score of expert e of a row whose softmax has these.
+__device__ __forceinline__ float route_weight(const RouteArgs& a, float l, int e, float mx, float inv) {
+  if (l == -INFINITY || (a.bias && a.bias[e] == -INFINITY)) return 0.0f;
+  if (a.softmax) return exp_below(l, mx) * inv;
+  const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
+  return l < 0.0f ? x * y : y;
+}
+
+// 1 / the sum of a softmax, for the weights.
+template <typename TL>
+__device__ __forceinline__ float route_inverse(const RouteArgs& a, const TL* row, float mx) {
+  float s = 0.0f;
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) s += exp_below(to_f32(row[e]), mx);
+  s = warp_sum(s);
+  return s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
+}
+
 // The choice of one warp from the keys: lane j < topk gets the j-th expert and its score.  (Without a bias and groups the keys
-// are not looked at.)
+// are not looked at, nor is inv.)
 template <typename TL>
 __device__ __noinline__ void route_choose(const RouteArgs& a, int64_t t, uint64_t* key, double mx, double inv, int& pick,
                                           float& weight) {
-  const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups;
+  const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups, log_l = 5 - a.log_groups;
   const TL* row = static_cast<const TL*>(a.logits) + t * a.ldl;
   const bool scored = a.bias || a.groups > 1;
-  uint32_t open = 0xffffffffu;
-  const int log_l = 5 - a.log_groups, L = 1 << log_l, group = lane >> log_l;
-  if (a.groups > 1) {
-    uint64_t first = 0, second = 0;
-    if (group < a.groups)
-      for (int i = lane & (L - 1); i < per; i += L) {
-        const uint64_t v = key[group * per + i];
-        second = max(second, min(first, v));
-        first = max(first, v);
-      }
-    for (int off = 1; off < L; off <<= 1) {
-      const uint64_t o1 = __shfl_xor_sync(0xffffffffu, first, off), o2 = __shfl_xor_sync(0xffffffffu, second, off);
-      second = max(max(second, o2), min(first, o1));
-      first = max(first, o1);
-    }
-    const uint64_t mine = second <= kRuledOut ? first : order_key(key_value(first) + key_value(second));
-    int better = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t other = __shfl_sync(0xffffffffu, mine, g << log_l);
-      better += other > mine || (other == mine && g < group) ? 1 : 0;
-    }
-    open = __ballot_sync(0xffffffffu, group < a.groups && better < a.kept);
-  }
+  const uint32_t open = a.groups > 1 ? route_groups(a, key) : 0xffffffffu;
   uint64_t best = 0;
   int at = kRouteMaxExperts;
   for (int e = lane; e < E; e += 32) {
@@ -143,6 +159,7 @@ __device__ __noinline__ void route_choose(const RouteArgs& a, int64_t t, uint64_
     key[e] = v;
     if (v > best) best = v, at = e;
   }
+  if (a.softmax && !scored) inv = route_inverse(a, row, static_cast<float>(mx));
   pick = 0;
   for (int j = 0; j < a.topk; ++j) {
     const uint32_t hi = static_cast<uint32_t>(best >> 32), top = __reduce_max_sync(0xffffffffu, hi);
@@ -159,19 +176,153 @@ __device__ __noinline__ void route_choose(const RouteArgs& a, int64_t t, uint64_
     }
     __syncwarp();
   }
-  weight = 0.0f;
-  if (lane < a.topk) {
-    const float l = to_f32(row[pick]);
-    if (!(l == -INFINITY || (a.bias && a.bias[pick] == -INFINITY))) {
-      if (a.softmax) {
-        weight = exp_below(l, static_cast<float>(mx)) * static_cast<float>(inv);
-      } else {
-        const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
-        weight = l < 0.0f ? x * y : y;
+  weight = lane < a.topk ? route_weight(a, to_f32(row[pick]), pick, static_cast<float>(mx), static_cast<float>(inv)) : 0.0f;
+  __syncwarp();
+}
+
+// The same choice where few experts can be it: their scores in fp32, off by less than 2^-24 (6 + |bias|), tell which groups
+// stay (or which are their two largest, for 64 bits to decide) and which experts may be among the topk, and 64 bits are
+// computed for those alone.  False: more than 64 of them, or a logit or bias that is NaN or +inf, or fewer than topk lanes
+// with an expert that is not ruled out; then nothing is chosen.  (Not for a softmax with a bias: its sum needs every
+// exponential.  Without one the order is that of the exponentials themselves.)
+template <typename TL>
+__device__ __noinline__ bool route_contenders(const ExactRow<TL>& r, uint64_t* key, int& pick) {
+  const RouteArgs& a = r.a;
+  const int lane = threadIdx.x & 31, E = a.E, per = E / a.groups, log_l = 5 - a.log_groups, L = 1 << log_l, group = lane >> log_l;
+  float* value = reinterpret_cast<float*>(key);          // words 2 e: fp32 scores
+  int32_t* list = reinterpret_cast<int32_t*>(key) + 1;   // words 2 i + 1: contenders
+  auto slack = [](float v) { return 0x1p-22f * (8.0f + fabsf(v)); };  // twice the error of two such scores, and more
+  auto approx = [&](int e) {
+    const float l = to_f32(r.row[e]), b = a.bias ? a.bias[e] : 0.0f;
+    if (l == -INFINITY || b == -INFINITY) return -INFINITY;
+    if (a.softmax) return exp_below(l, static_cast<float>(r.mx));
+    const float x = exp_below(-fabsf(l), 0.0f), y = recip_approx(1.0f + x);
+    return (l < 0.0f ? x * y : y) + b;
+  };
+  auto gather = [&](auto in) {  // the experts for which in(e); how many
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const bool mine = in(e) && e < E;
+      const uint32_t all = __ballot_sync(0xffffffffu, mine);
+      if (mine) list[2 * (n + __popc(all & ((1u << lane) - 1u)))] = e;
+      n += __popc(all);
+    }
+    __syncwarp();
+    return n;
+  };
+  uint32_t open = 0xffffffffu;
+  if (a.groups > 1) {
+    bool odd = false;
+    for (int e = lane; e < E; e += 32) {
+      const float v = approx(e);
+      value[2 * e] = v;
+      odd |= !(v < INFINITY);
+    }
+    if (__any_sync(0xffffffffu, odd)) return false;
+    __syncwarp();
+    float first = -INFINITY, second = -INFINITY;
+    if (group < a.groups)
+      for (int i = lane & (L - 1); i < per; i += L) {
+        const float v = value[2 * (group * per + i)];
+        second = fmaxf(second, fminf(first, v));
+        first = fmaxf(first, v);
       }
+    for (int off = 1; off < L; off <<= 1) {
+      const float o1 = __shfl_xor_sync(0xffffffffu, first, off), o2 = __shfl_xor_sync(0xffffffffu, second, off);
+      second = fmaxf(fmaxf(second, o2), fminf(first, o1));
+      first = fmaxf(first, o1);
+    }
+    const float sum = second == -INFINITY ? first : first + second;
+    const float off = first == -INFINITY ? 0.0f : slack(first) + (second == -INFINITY ? 0.0f : slack(second));
+    int better = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float other = __shfl_sync(0xffffffffu, sum, g << log_l);
+      better += other > sum || (other == sum && g < group) ? 1 : 0;
+    }
+    const bool stays = group < a.groups && better < a.kept;
+    open = __ballot_sync(0xffffffffu, stays);
+    float least = stays ? sum - off : INFINITY, most = group < a.groups && !stays ? sum + off : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    if (a.kept < a.groups && !(least > most)) {  // 64 bits decide
+      const float from = second == -INFINITY ? -INFINITY : second - slack(second);
+      const int n = gather([&](int e) {
+        const float mine = __shfl_sync(0xffffffffu, from, e < E ? e / per << log_l : 0);
+        return e < E && value[2 * e] > -INFINITY && value[2 * e] >= mine;
+      });
+      if (n > 64) return false;
+      const int e0 = lane < n ? list[2 * lane] : 0, e1 = lane + 32 < n ? list[2 * (lane + 32)] : 0;
+      __syncwarp();
+      for (int e = lane; e < E; e += 32) key[e] = value[2 * e] == -INFINITY ? kRuledOut : kRuledOut + 1;
+      __syncwarp();
+      if (lane < n) key[e0] = r.key(e0, r.exponential(e0), 1.0);
+      if (lane + 32 < n) key[e1] = r.key(e1, r.exponential(e1), 1.0);
+      __syncwarp();
+      open = route_groups(a, key);
+      __syncwarp();
     }
   }
+  // (without a bias the order is that of the logits, and nothing is off)
+  bool odd = false;
+  float best = -INFINITY;
+  for (int e = lane; e < E; e += 32) {
+    const bool in = open >> (e / per << log_l) & 1u;
+    const float v = !in ? -INFINITY : a.bias ? approx(e) : to_f32(r.row[e]);
+    value[2 * e] = v;
+    odd |= !(v < INFINITY);
+    best = fmaxf(best, v);
+  }
+  if (__any_sync(0xffffffffu, odd)) return false;
+  // the topk-th largest of the lanes' best is no larger than the topk-th of all
+  uint32_t o = best == -INFINITY ? 0u : fp8g::order_key(best), kth = 0u;  // (of floats)
+  for (int j = 0; j < a.topk; ++j) {
+    kth = __reduce_max_sync(0xffffffffu, o);
+    const uint32_t who = __ballot_sync(0xffffffffu, o == kth);
+    if (lane == __ffs(who) - 1) o = 0u;
+  }
+  if (kth == 0u) return false;
+  const float ref = fp8g::key_value(kth), from = a.bias ? ref - slack(ref) : ref;
   __syncwarp();
+  const int n = gather([&](int e) { return e < E && value[2 * e] > -INFINITY && value[2 * e] >= from; });
+  if (n > 64) return false;
+  const int e0 = lane < n ? list[2 * lane] : 0, e1 = lane + 32 < n ? list[2 * (lane + 32)] : 0;
+  auto exact = [&](int e) {
+    return a.bias ? r.key(e, r.exponential(e), 1.0) : order_key(static_cast<double>(to_f32(r.row[e])));
+  };
+  uint64_t k0 = lane < n ? exact(e0) : 0, k1 = n > 32 && lane + 32 < n ? exact(e1) : 0;
+  pick = 0;
+  for (int j = 0; j < a.topk; ++j) {
+    const uint64_t top = max(k0, k1);
+    const uint32_t hi = static_cast<uint32_t>(top >> 32), high = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = hi == high ? static_cast<uint32_t>(top) : 0u, low = __reduce_max_sync(0xffffffffu, lo);
+    const uint64_t best_key = static_cast<uint64_t>(high) << 32 | low;
+    const uint32_t own = min(k0 == best_key ? static_cast<uint32_t>(e0) : static_cast<uint32_t>(kRouteMaxExperts),
+                             k1 == best_key ? static_cast<uint32_t>(e1) : static_cast<uint32_t>(kRouteMaxExperts));
+    const int one = static_cast<int>(__reduce_min_sync(0xffffffffu, own));
+    if (lane == j) pick = min(one, E - 1);
+    if (k0 == best_key && e0 == one) k0 = 0;
+    else if (k1 == best_key && e1 == one) k1 = 0;
+  }
+  __syncwarp();
+  return true;
+}
+
+// A row by one warp, where few experts can be chosen (see route_contenders); false: it is not such a row.
+template <typename TL>
+__device__ __noinline__ bool route_few(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
+  const ExactRow<TL> r(a, t);
+  const int lane = threadIdx.x & 31;
+  if ((a.softmax && a.bias) || a.topk > kRouteFewTopk) return false;
+  const bool done = route_contenders<TL>(r, key, pick);
+  __syncwarp();
+  if (!done) return false;
+  const float mx = static_cast<float>(r.mx), inv = a.softmax ? route_inverse(a, r.row, mx) : 1.0f;
+  weight = lane < a.topk ? route_weight(a, to_f32(r.row[pick]), pick, mx, inv) : 0.0f;
+  return true;
 }
 
 // A row by one warp.
@@ -180,7 +331,7 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* 
   const ExactRow<TL> r(a, t);
   const int lane = threadIdx.x & 31;
   double inv = 1.0;
-  if (a.softmax) {
+  if (a.softmax && r.scored()) {
     double s = 0.0;
     for (int e = lane; e < a.E; e += 32) s += r.exponential(e);
     s = warp_sum(s);
@@ -205,7 +356,8 @@ __device__ __forceinline__ void put_row(const RouteArgs& a, int64_t t, int id, f
   }
 }
 
-// The general form: every row in 64 bits (2.7 ms for 65536 x 256).
+// The general form: a warp a row.  4096 rows of 1024, 8 picks: 53 us with a bias, 67 in groups too (with all scores in 64 bits,
+// as a softmax with a bias and more than 16 picks have them, 330 to 480; 37 without a bias and groups).
 template <typename TL>
 __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ __align__(16) uint64_t choice[];
@@ -213,7 +365,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += gridDim.x * kRouteWarps) {
     int id;
     float w;
-    route_row<TL>(a, t, choice + warp * a.E, id, w);
+    if (!route_few<TL>(a, t, choice + warp * a.E, id, w)) route_row<TL>(a, t, choice + warp * a.E, id, w);
     put_row(a, t, id, w, a.counts);
   }
 }
@@ -608,7 +760,7 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
     uint64_t* key = smem64 + slot * route_keys(E);
     const ExactRow<TL> r(a, t);
     double inv = 1.0;
-    if (a.softmax) {
+    if (a.softmax && r.scored()) {
       double sum = 0.0;
       if (mine_too)
         for (int e = part * 32 + lane; e < E; e += parts * 32) sum += r.exponential(e);

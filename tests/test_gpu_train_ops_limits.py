@@ -169,6 +169,37 @@ def test_route_where_every_row_is_close(T, E, groups, kept, score):
     assert np.allclose(_np(w), 0.25, rtol=1e-4, atol=0)  # (the chosen scores of a row are alike but for some 2^-20)
 
 
+@pytest.mark.parametrize("E,groups,kept,k", [(640, 1, 1, 8), (1024, 8, 3, 8), (600, 6, 2, 16), (2016, 9, 4, 5), (513, 27, 5, 12),
+                                             (576, 32, 7, 6), (2048, 1, 1, 17)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_many_experts_near_one_another(E, groups, kept, k, score):
+    """More experts than lanes hold: fp32 says whose scores are needed in 64 bits, whatever the biases' size and sign."""
+    T = 120
+    kw = dict(score=score, groups=groups, topk_groups=kept)
+    l, zero = torch.randn((T, E), generator=_gen(7), device="cuda"), torch.zeros(E, device="cuda")
+    few = _draw((T, E), "bf16", 8).mul_(2).round_().div_(2)
+    for logits in (few, l.bfloat16(), l * 4 + 18, l * 4 - 18, l):
+        for bias in (None, zero, _draw((E,), "f32", 9, 1e-7), _draw((E,), "f32", 10, 3.0) + 100.0, -1e5 - _draw((E,), "f32", 11)):
+            _check_route(logits, k, bias, **kw)
+    level = torch.sigmoid(l[0]) if score == "sigmoid" else torch.softmax(l[0], 0)
+    _check_route(l[:1].expand(T, E).contiguous(), k, 0.5 - level, **kw)  # every choice score is about 1/2
+    base = torch.randn((T, 1), generator=_gen(5), device="cuda")
+    near = base * (1 + torch.randint(0, 5, (T, E), generator=_gen(6), device="cuda") * 2.0 ** -23)
+    if groups == 1:
+        _check_route(near, k, zero, **kw)
+    # ruled out: a logit, a bias, whole groups, all but a few
+    l[torch.rand((T, E), generator=_gen(2), device="cuda") < 0.5] = -float("inf")
+    l[3], l[4, 2:], l[5, : E // 2] = -float("inf"), -float("inf"), -float("inf")
+    bias = _draw((E,), "f32", 3, 0.1)
+    bias[:5], bias[E // 3: E // 2] = -float("inf"), -float("inf")
+    for b in (None, bias):
+        _check_route(l, k, b, torch.arange(T, device="cuda") % 7 != 2, **kw)
+    l[7, 11], l[8, E - 1] = float("nan"), float("inf")
+    ids, w, _ = g.moe_route(l, k, bias=bias, **kw)
+    want, _, _ = ot.moe_route(_np(l), k, _np(bias), **kw)
+    assert np.array_equal(ids.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("T,E,k", [(12700, 64, 6), (13300, 64, 3), (5400, 128, 2), (5800, 96, 1)])
 def test_route_where_shared_memory_is_just_below_48_kb(T, E, k):
     """The dynamic part alone is within what needs no leave, with the static part it is not."""
