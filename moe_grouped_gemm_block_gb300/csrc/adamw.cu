@@ -262,7 +262,8 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places
   }
 }
 
-// A thread's part of whole blocks with 8-bit states, copied ahead into places of its own: a block's arithmetic is long, and
+// A thread's part of whole blocks with 8-bit states, copied ahead into places of its own in its warp's (warps are at tensors
+// of other types, whose places have other sizes): a block's arithmetic is long, and
 // so few bytes of it are on their way at once that the loads' latency would show (117M values with masters: 335 us).
 constexpr int kAdamStages = 2;
 constexpr int kAdamPlaces = 2 * 16 + 2 * 16 + 4 * 4 + 2 * 4;  // bytes of a thread and stage, at most
@@ -290,36 +291,36 @@ __device__ __forceinline__ uint32_t load_word(uint32_t from) {
 template <typename T, typename TG>  // T: of what the step starts from, the param or its master copy
 struct Ahead {
   static constexpr int kP = 4 * static_cast<int>(sizeof(T)), kG = 4 * static_cast<int>(sizeof(TG));
-  static constexpr uint32_t kGrads = 2 * kP * kAdamThreads, kCodes = kGrads + 2 * kG * kAdamThreads;
-  uint32_t places;
+  static constexpr uint32_t kGrads = 2 * kP * 32, kCodes = kGrads + 2 * kG * 32;
+  uint32_t places;  // of the warp
   __device__ __forceinline__ void copy(int stage, const AdamTensor& t, const void* from, int64_t block) const {
     const int64_t first = block + 4 * (threadIdx.x & 15);
-    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x;
+    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x & 31;
     const T* p = static_cast<const T*>(from) + first;
     const TG* g = static_cast<const TG*>(t.grad) + first;
     const uint8_t *m = static_cast<const uint8_t*>(t.m) + first, *v = static_cast<const uint8_t*>(t.v) + first;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      copy_ahead<kP>(at + (i * kAdamThreads + x) * kP, p + 64 * i);
-      copy_ahead<kG>(at + kGrads + (i * kAdamThreads + x) * kG, g + 64 * i);
-      copy_ahead<4>(at + kCodes + (i * kAdamThreads + x) * 4, m + 64 * i);
-      copy_ahead<4>(at + kCodes + ((2 + i) * kAdamThreads + x) * 4, v + 64 * i);
+      copy_ahead<kP>(at + (i * 32 + x) * kP, p + 64 * i);
+      copy_ahead<kG>(at + kGrads + (i * 32 + x) * kG, g + 64 * i);
+      copy_ahead<4>(at + kCodes + (i * 32 + x) * 4, m + 64 * i);
+      copy_ahead<4>(at + kCodes + ((2 + i) * 32 + x) * 4, v + 64 * i);
     }
-    copy_ahead<4>(at + kCodes + (4 * kAdamThreads + x) * 4, t.m_scale + (block >> 7));
-    copy_ahead<4>(at + kCodes + (5 * kAdamThreads + x) * 4, t.v_scale + (block >> 7));
+    copy_ahead<4>(at + kCodes + (4 * 32 + x) * 4, t.m_scale + (block >> 7));
+    copy_ahead<4>(at + kCodes + (5 * 32 + x) * 4, t.v_scale + (block >> 7));
   }
   __device__ __forceinline__ void load(int stage, float (&p)[8], float (&g)[8], float (&m)[8], float (&v)[8]) const {
-    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x;
+    const uint32_t at = places + stage * (kAdamPlaces * kAdamThreads), x = threadIdx.x & 31;
     uint32_t w[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      load_place<kP>(at + (i * kAdamThreads + x) * kP, p + 4 * i);
-      load_place<kG>(at + kGrads + (i * kAdamThreads + x) * kG, g + 4 * i);
-      w[0][i] = load_word(at + kCodes + (i * kAdamThreads + x) * 4);
-      w[1][i] = load_word(at + kCodes + ((2 + i) * kAdamThreads + x) * 4);
+      load_place<kP>(at + (i * 32 + x) * kP, p + 4 * i);
+      load_place<kG>(at + kGrads + (i * 32 + x) * kG, g + 4 * i);
+      w[0][i] = load_word(at + kCodes + (i * 32 + x) * 4);
+      w[1][i] = load_word(at + kCodes + ((2 + i) * 32 + x) * 4);
     }
-    decode(w[0], __uint_as_float(load_word(at + kCodes + (4 * kAdamThreads + x) * 4)), m);
-    decode(w[1], __uint_as_float(load_word(at + kCodes + (5 * kAdamThreads + x) * 4)), v);
+    decode(w[0], __uint_as_float(load_word(at + kCodes + (4 * 32 + x) * 4)), m);
+    decode(w[1], __uint_as_float(load_word(at + kCodes + (5 * 32 + x) * 4)), v);
   }
 };
 
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(
                                                                          const AdamHyper h,
                                                                          const AdamStep* __restrict__ step) {
   __shared__ __align__(16) unsigned char shared[BITS == 8 ? kAdamStages * kAdamPlaces * kAdamThreads : 16];
-  const uint32_t places = smem_u32(shared), chunks = tab.end[tab.n - 1];
+  const uint32_t places = smem_u32(shared) + (threadIdx.x >> 5) * (kAdamPlaces * 32), chunks = tab.end[tab.n - 1];
   adam_prefetch<BITS>(tab);  // (under the step's end: what was before that is complete)
   griddep_wait();
   AdamStep s;
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(kAdamThreads, adam_per_sm(BITS)) adamw_kernel(
       case kParamF32: adam_blocks<BITS, float, __nv_bfloat16, false>(t, h, s, block, step_size, places); break;
       default: adam_blocks<BITS, float, float, false>(t, h, s, block, step_size, places); break;
     }
+    __syncwarp();  // (the next tensor has other places)
   }
 }
 

@@ -291,6 +291,27 @@ def test_two_graphs_replayed_at_once():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_tensors_of_all_types_in_turn(bits):
+    """A CTA's warps are at tensors of different types at the same time."""
+    rng = np.random.default_rng(3)
+    sizes = [int(n) for n in rng.integers(0, 60000, 60)]
+    kinds = [(("bf16", "f32")[a], ("bf16", "f32")[b]) for a, b in rng.integers(0, 2, (60, 2))]
+    params = [_draw((n,), k[0], i, 0.1) for i, (n, k) in enumerate(zip(sizes, kinds))]
+    grads = [_draw((n,), k[1], 100 + i, 0.01) for i, (n, k) in enumerate(zip(sizes, kinds))]
+    before = [p.clone() for p in params]
+    masters = [p.float() if p.dtype == torch.bfloat16 and i % 3 == 0 else None for i, p in enumerate(params)]
+    first = [None if t is None else t.clone() for t in masters]
+    opt = g.AdamWList(params, grads, masters=masters, state_bits=bits)
+    g.adamw_step(opt, 1e-2)
+    check_status()
+    for i in range(60):
+        z, zs = torch.zeros_like(opt.m[i]), None if bits == 32 else torch.zeros_like(opt.m_scales[i])
+        _check_adam((before[i], first[i], z, z, zs, zs),
+                    (params[i], masters[i], opt.m[i], opt.v[i], opt.m_scales[i], opt.v_scales[i]), grads[i], 1, 1e-2, 0.9,
+                    0.999, 1e-8, float(np.float32(0.01)), 1.0, bits, f"tensor {i}")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_gradient_that_two_parameters_share(bits):
     d = _draw((3001,), "bf16", 1, 0.01)
     params = [_draw((3001,), "f32", 2, 0.1), _draw((3001,), "bf16", 3, 0.1)]
