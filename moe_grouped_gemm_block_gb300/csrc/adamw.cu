@@ -17,8 +17,8 @@
 // too large, which makes a step too small, never too large.  A block whose largest is below 2^-60 becomes 0.
 //
 // Bound by memory with states in 32 bits, by that and some 60 instructions a value in 8.  117M values, device times and the
-// share of the copy rate: 32 bits, fp32 with bf16 gradients 466 to 484 us (93 to 96%); 8 bits with masters 312 (89%),
-// without 250 (70%).  1M values: 9.5 and 11 us, of which the step's launch before is 2.
+// share of the copy rate: 32 bits, fp32 with bf16 gradients 466 to 484 us (93 to 96%); 8 bits with masters 319 (87%),
+// without 259 (67%).  1M values: 9.5 and 11 us, of which the step's launch before is 2.
 #include <algorithm>
 #include <cmath>
 #include <cuda_fp16.h>
