@@ -2,12 +2,13 @@
 // gradient.
 //
 //     h = g s(g) u,  s(g) = 1 / (1 + e^-g)        (a row of the first product is g [F], then u [F])
-//     e4m3 of h in 1 x 128 blocks: scale = amax / 448, code = e4m3(h / scale), as the quantisers' of unfused rows
+//     e4m3 of h in 1 x 128 blocks: scale = amax / 448, code = e4m3(h / scale), each quotient rounded as the quantisers' of
+//     unfused rows
 //     dg = dh u s (1 + g (1 - s)),  du = dh g s
 //
 // Everything is fp32 until the one rounding of a result.  Bound by memory: forward 4 bytes read and 1 written a value
 // (3 with h in bf16), backward 6 read and 4 written (6).  Device times, and the share of the copy rate:
-//   33024 x 4096: 113 us (89%), with h 156 (90%), backward with h 248 (96%);  64 rows of 32 experts, masked: 4.0
+//   33024 x 4096: 116 us (86%), with h 157 (89%), backward with h 248 (96%);  64 rows of 32 experts, masked: 4.0
 // Two or four blocks of 128 a group at once were slower (123 and 157 us without h).
 
 #include <algorithm>
@@ -47,7 +48,7 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 
 template <bool MASKED>
-__global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
+__global__ void __launch_bounds__(kGluThreads, kGluPerSm) swiglu_kernel(const GluArgs a) {
   const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
   uint32_t M = a.M;
   int64_t row0 = 0;
@@ -86,22 +87,31 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_kernel(const GluArgs a) {
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, off));
-    // top / 448, rounded: a product and a step on its exact remainder (Markstein), as an IEEE division where that could
-    // leave the normal range; there 1 / s is beyond fp32, and the block is taken 2^64 times larger
-    float s, inv;
-    if (top >= 0x1p-100f) {
+    // The scale is the rounded top / 448, the codes are those of the rounded quotients h / s.  Each by a product and a step on
+    // its exact remainder (Markstein), where every remainder that can move a code is in the normal range; else (top
+    // below 2^-60) by divisions.  (A product with 1 / s alone: 114 us without h in place of 116.)
+    float s, y[8];
+    if (top >= 0x1p-60f) {
       s = top * (1.0f / 448.0f);
       s = fmaf(fmaf(-448.0f, s, top), 1.0f / 448.0f, s);
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+      inv = fmaf(inv, fmaf(-s, inv, 1.0f), inv);
+      const float2 inv2 = make_float2(inv, inv), minus = make_float2(-s, -s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = make_float2(h[2 * j], h[2 * j + 1]), first = __fmul2_rn(x, inv2);
+        const float2 quotient = __ffma2_rn(__ffma2_rn(first, minus, x), inv2, first);
+        y[2 * j] = quotient.x, y[2 * j + 1] = quotient.y;
+      }
     } else {
       s = __fdiv_rn(top, 448.0f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] *= 0x1p64f;
+      for (int j = 0; j < 8; ++j) y[j] = s == 0.0f ? 0.0f : __fdiv_rn(h[j], s);
     }
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(top >= 0x1p-100f ? s : s * 0x1p64f));
-    inv = s == 0.0f ? 0.0f : inv;
     uint16_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(h[2 * j + 1] * inv, h[2 * j] * inv);
+    for (int j = 0; j < 4; ++j) c[j] = cvt_e4m3x2(y[2 * j + 1], y[2 * j]);
     *reinterpret_cast<uint2*>(a.q + row * a.ldq + col) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     if (lane == 0) a.sA[kb * a.ld_sa + row] = s;
   }

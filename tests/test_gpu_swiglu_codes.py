@@ -1,0 +1,60 @@
+"""The gated activation's codes and scales against the unfused quantiser's rule applied to the fp32 products: s = fp32(amax / 448),
+codes of the rounded quotients fp32(h / s).  Gates of 33 and more have s(g) = 1 in fp32, so h = g u is exact there (two
+significands of 8 bits)."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_block_gb300 as g
+from oracle.quantize import quantize_1x128
+from tests.gpu_util import check_status, need_gpu
+from tests.test_gpu_block_ops import _draw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    need_gpu()
+
+
+def _masked(gu):
+    """The masked form's codes and scales of the same rows, three experts of a third each."""
+    M, F = gu.shape[0] // 3 * 3, gu.shape[1] // 2
+    q = torch.zeros((3, M // 3, F), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((F // 128, (M + 3) // 4 * 4), device="cuda")
+    g.fp8_swiglu_quantize_1x128_masked(gu[:M].contiguous().view(3, M // 3, 2 * F), q, s,
+                                       torch.full((3,), M // 3, dtype=torch.int32, device="cuda"))
+    return q.view(M, F), s[:, :M]
+
+
+def _compare(gate, up):
+    gu = torch.cat([gate, up], 1).bfloat16()
+    M, F = gate.shape
+    assert torch.equal(gu.float(), torch.cat([gate, up], 1))
+    want_q, want_s = quantize_1x128((gate * up).cpu().numpy())
+    q, s, h = g.swiglu_quantize_1x128(gu, keep=True)
+    check_status()
+    assert np.array_equal(s[:, :M].cpu().numpy().T, want_s)
+    assert np.array_equal(q.cpu().numpy(), want_q)
+    assert torch.equal(h, (gate * up).bfloat16())
+    mq, ms = _masked(gu)
+    n = len(mq)
+    assert torch.equal(mq, q[:n]) and torch.equal(ms, s[:, :n])
+
+
+def test_codes_where_the_quotient_lies_between_two_codes():
+    """Rows of gate k with a largest up of 448 have the scale k, and ups halfway between two codes, whose quotients are
+    exactly that: they go to the even code."""
+    ups = [448.0] + [m * 2.0 ** e for e in range(-9, 5) for m in (17, 19, 21, 23, 25, 27, 29, 31)]
+    ups = ups + [-u for u in ups]
+    up = torch.tensor((ups + [0.0] * (256 - len(ups)))[:256], device="cuda").expand(223, 256).contiguous()
+    up[:, 0] = up[:, 128] = 448.0
+    _compare(torch.arange(33.0, 256.0, device="cuda")[:, None].expand(223, 256).contiguous(), up)
+
+
+@pytest.mark.parametrize("std", [1e-20, 1e-3, 1.0, 1e30])
+def test_codes_of_products_that_fp32_holds(std):
+    gate = (_draw((600, 384), "f32", 1).abs() * 30 + 40).bfloat16().float()
+    _compare(gate, _draw((600, 384), "bf16", 2, std).float())
