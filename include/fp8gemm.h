@@ -646,6 +646,7 @@ int fp8g_residual_rms_norm_backward(
  * fp8_swiglu_quantize_1x128 -- the gated activation between an expert's two matrix products, quantised for the second:
  *     h[m, n] = g s(g) u,  g = gu[m, n],  u = gu[m, F + n],  s(g) = 1 / (1 + e^-g)  (0 where below 2^-126)
  *     codes and scales of h in 1x128 blocks as fp8_quantize_1x128 writes them, formed from the fp32 h; h itself in bf16
+ * A block with a product beyond fp32 has the scale inf: its finite values get 0, its infinite ones the code of NaN.
  *
  *   gu    bf16 [M, 2F], row stride ldgu elements (>= 2F, % 8): a product whose first F columns are the gates
  *   q     e4m3 [M, F], row stride ldq bytes (>= F, % 16), or null;  sA  fp32 [F/128][ld_sa] (ld_sa >= M, % 4)

@@ -89,9 +89,9 @@ __global__ void __launch_bounds__(kGluThreads, kGluPerSm) swiglu_kernel(const Gl
     for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, off));
     // The scale is the rounded top / 448, the codes are those of the rounded quotients h / s.  Each by a product and a step on
     // its exact remainder (Markstein), where every remainder that can move a code is in the normal range; else (top
-    // below 2^-60) by divisions.  (A product with 1 / s alone: 114 us without h in place of 116.)
+    // below 2^-60, or infinite) by divisions.  (A product with 1 / s alone: 114 us without h in place of 116.)
     float s, y[8];
-    if (top >= 0x1p-60f) {
+    if (top >= 0x1p-60f && top < INFINITY) {
       s = top * (1.0f / 448.0f);
       s = fmaf(fmaf(-448.0f, s, top), 1.0f / 448.0f, s);
       float inv;

@@ -58,3 +58,25 @@ def test_codes_where_the_quotient_lies_between_two_codes():
 def test_codes_of_products_that_fp32_holds(std):
     gate = (_draw((600, 384), "f32", 1).abs() * 30 + 40).bfloat16().float()
     _compare(gate, _draw((600, 384), "bf16", 2, std).float())
+
+
+def test_a_block_with_a_product_beyond_fp32():
+    """Its scale is infinite, so finite values become 0 and the infinite one has no code but NaN; the blocks beside it do
+    not feel it."""
+    gate = torch.full((3, 256), 64.0, device="cuda")
+    up = _draw((3, 256), "bf16", 1).float()
+    gate[1, 7], up[1, 7] = 2.0 ** 100, -2.0 ** 100
+    gu = torch.cat([gate, up], 1).bfloat16()
+    q, s, h = g.swiglu_quantize_1x128(gu, keep=True)
+    check_status()
+    rest = [0, 2]
+    want_q, want_s = quantize_1x128((gate * up)[rest].cpu().numpy())
+    got = q.cpu().numpy()
+    assert np.array_equal(got[rest], want_q) and np.array_equal(s[:, rest].cpu().numpy().T, want_s)
+    want_q, want_s = quantize_1x128((gate * up)[1:2, 128:].cpu().numpy())
+    assert np.array_equal(got[1:2, 128:], want_q) and float(s[1, 1]) == want_s[0, 0]
+    assert float(s[0, 1]) == float("inf") and got[1, 7] & 0x7F == 0x7F
+    assert not (np.delete(got[1, :128], 7) & 0x7F).any()
+    assert float(h[1, 7]) == -float("inf") and int(torch.isinf(h).sum()) == 1
+    mq, ms = _masked(gu)
+    assert torch.equal(mq, q) and torch.equal(ms, s[:, :3])
