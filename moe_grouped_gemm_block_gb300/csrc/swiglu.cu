@@ -8,7 +8,7 @@
 //
 // Everything is fp32 until the one rounding of a result.  Bound by memory: forward 4 bytes read and 1 written a value
 // (3 with h in bf16), backward 6 read and 4 written (6).  Device times, and the share of the copy rate:
-//   33024 x 4096: 116 us (86%), with h 157 (89%), backward with h 248 (96%);  64 rows of 32 experts, masked: 4.0
+//   33024 x 4096: 116 us (86%), with h 157 (89%), backward with h 247 (96%);  64 rows of 32 experts, masked: 4.0
 // Two or four blocks of 128 a group at once were slower (123 and 157 us without h).
 
 #include <algorithm>
@@ -38,12 +38,19 @@ struct GluArgs {
   int32_t F;
 };
 
-// s(g).  e^-g as a power of two of a rounded exponent and the reciprocal are off by (4 + |g|) 2^-24 of themselves
-// together, far below the results' own rounding.  s below 2^-126 (g < -87) is 0.
-__device__ __forceinline__ float sigmoid(float g) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// s(g) = 1 / (1 + e^-g) of two gates.  A gate has 8 significant bits and the first part of log2(e) 16, so that the exponent
+// t of e^-g = 2^t e^(g c) is exact; of e^(g c), at most 2^-11 from 1, the first two terms.  So s is off by 8 u of itself
+// (u = 2^-24: exponential 4, product and sum 1 each, reciprocal 2), and by up to 1.5 more where g nears -87; 0 where below
+// 2^-126 (g < -87.3).  The library's exponential and a rounded reciprocal took 198 us (33024 x 4096 without h).
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 sigmoid(float2 g) {
+  const float2 t = __fmul2_rn(g, both(-0x1.7154p+0f)), c = __fmul2_rn(g, both(-4.888495e-6f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  const float2 d = __fadd2_rn(__ffma2_rn(e, c, e), both(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return r;
 }
 
@@ -75,8 +82,8 @@ __global__ void __launch_bounds__(kGluThreads, kGluPerSm) swiglu_kernel(const Gl
       ru.get(u);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[2 * j] = g[j].x * sigmoid(g[j].x) * u[j].x;
-        h[2 * j + 1] = g[j].y * sigmoid(g[j].y) * u[j].y;
+        const float2 p = __fmul2_rn(__fmul2_rn(g[j], sigmoid(g[j])), u[j]);
+        h[2 * j] = p.x, h[2 * j + 1] = p.y;
       }
       if (a.h) store8_stream(a.h + row * a.ldh + col, h);
     }
@@ -133,13 +140,13 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_backward_kernel(const GluA
     rd.get(d2);
     float dg[8], du[8], h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float g = j & 1 ? g2[j / 2].y : g2[j / 2].x, u = j & 1 ? u2[j / 2].y : u2[j / 2].x;
-      const float d = j & 1 ? d2[j / 2].y : d2[j / 2].x;
-      const float s = sigmoid(g), act = g * s;
-      h[j] = act * u;
-      dg[j] = d * u * s * (1.0f + g * (1.0f - s));
-      du[j] = d * act;
+    for (int j = 0; j < 4; ++j) {
+      const float2 s = sigmoid(g2[j]), act = __fmul2_rn(g2[j], s), p = __fmul2_rn(act, u2[j]), q = __fmul2_rn(d2[j], act);
+      const float2 rest = __ffma2_rn(s, both(-1.0f), both(1.0f)), slope = __ffma2_rn(g2[j], rest, both(1.0f));
+      const float2 r = __fmul2_rn(__fmul2_rn(__fmul2_rn(d2[j], u2[j]), s), slope);
+      h[2 * j] = p.x, h[2 * j + 1] = p.y;
+      dg[2 * j] = r.x, dg[2 * j + 1] = r.y;
+      du[2 * j] = q.x, du[2 * j + 1] = q.y;
     }
     store8_stream(a.dgu + m * a.lddgu + col, dg);
     store8_stream(a.dgu + m * a.lddgu + a.F + col, du);

@@ -9,7 +9,7 @@ import torch
 import moe_grouped_gemm_block_gb300 as g
 from oracle.quantize import quantize_1x128
 from tests.gpu_util import check_status, need_gpu
-from tests.test_gpu_block_ops import _draw
+from tests.test_gpu_block_ops import U, _draw
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,15 @@ def test_a_block_with_a_product_beyond_fp32():
     assert float(h[1, 7]) == -float("inf") and int(torch.isinf(h).sum()) == 1
     mq, ms = _masked(gu)
     assert torch.equal(mq, q) and torch.equal(ms, s[:, :3])
+
+
+def test_the_gates_own_error_does_not_grow_with_them():
+    """The scale of a block of equal products is their fp32 value over 448.  The exponential is off by 2 units in the last
+    place (4 u) and the 1.5 u that the next term of e^(g c) has at g = -87; its product, 1 + exp, two products and the scale
+    add a rounding each, the reciprocal a unit (2 u): 12.5 u.  (s(g) below 2^-126, of gates below -87.3, is 0.)"""
+    gates = torch.cat([torch.linspace(-87.0, 99.0, 500), torch.linspace(-3.0, 3.0, 500)]).bfloat16().double()
+    gu = torch.cat([gates[:, None].expand(-1, 128), torch.full((1000, 128), 64.0, dtype=torch.float64)], 1).bfloat16().cuda()
+    _, s, _ = g.swiglu_quantize_1x128(gu)
+    want = (gates / (1.0 + torch.exp(-gates)) * 64.0 / 448.0).abs().numpy()
+    got = s[0, :1000].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= 12.5 * U * 1.01 * want + 2.0 ** -149)
