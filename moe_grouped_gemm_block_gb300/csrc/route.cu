@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "shares.cuh"
 #include "topk.cuh"
 #include "vec.cuh"
 
@@ -752,29 +753,30 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
     tb = t0 + stride;
   }
   __syncthreads();
-  // the listed rows: an expert a lane, so as many warps a row as it has 32 experts, and several rows at once
-  const int parts = min((E + 31) / 32, warps), at_once = warps / parts, slot = warp / parts, part = warp % parts;
-  for (int r0 = 0, n = min(listed, kRouteListed); r0 < n; r0 += at_once) {
-    const bool mine_too = slot < at_once && r0 + slot < n;
-    const int64_t t = list_of_rows[min(r0 + slot, n - 1)];
-    uint64_t* key = smem64 + slot * route_keys(E);
+  // the listed rows
+  const RowShares share(E, warps, warp);
+  for (int r0 = 0, n = min(listed, kRouteListed); r0 < n; r0 += share.at_once) {
+    const bool mine_too = share.some() && r0 + share.slot < n;
+    const int64_t t = list_of_rows[min(r0 + share.slot, n - 1)];
+    uint64_t* key = smem64 + share.slot * route_keys(E);
     const ExactRow<TL> r(a, t);
     double inv = 1.0;
     if (a.softmax && r.scored()) {
       double sum = 0.0;
       if (mine_too)
-        for (int e = part * 32 + lane; e < E; e += parts * 32) sum += r.exponential(e);
+        for (int e = share.part * 32 + lane; e < E; e += share.parts * 32) sum += r.exponential(e);
       sum = warp_sum(sum);
       if (lane == 0) part_sum[warp] = sum;
       __syncthreads();
       sum = 0.0;
-      for (int i = 0; i < parts; ++i) sum += part_sum[warp - part + i];
+      if (mine_too)
+        for (int i = 0; i < share.parts; ++i) sum += part_sum[share.first() + i];
       inv = sum == 0.0 ? 0.0 : 1.0 / sum;
     }
     if (mine_too && r.scored())
-      for (int e = part * 32 + lane; e < E; e += parts * 32) key[e] = r.key(e, r.exponential(e), inv);
+      for (int e = share.part * 32 + lane; e < E; e += share.parts * 32) key[e] = r.key(e, r.exponential(e), inv);
     __syncthreads();
-    if (mine_too && part == 0) {
+    if (mine_too && share.part == 0) {
       int id;
       float w;
       route_choose<TL>(a, t, key, r.mx, inv, id, w);
