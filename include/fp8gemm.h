@@ -554,7 +554,8 @@ int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64
  *     one, where it has one).  The topk_groups best groups stay, ties to the lower group.
  *     topk_ids[t] = the topk largest c among their experts, in descending order, ties to the lower index.  Without a bias
  *     experts are ordered by their logits, as their scores are.
- *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where it is 0)
+ *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where all are ruled out).
+ *     A score may be as small as it likes for that; without renormalize one below 2^-126 may count as 0.
  *     counts[e] = how many (t, j) of the unmasked tokens chose e
  * The choice is that of scores in 64 bits (whose own roundings, 2^-50 of a score, decide where two lie that near).  The
  * bias takes part in the choice alone; a program balances its experts by moving it after each step, up where counts lie
@@ -579,7 +580,7 @@ int fp8g_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int6
 /*
  * fp8g_moe_route_backward -- the gradient of topk_weights with respect to the logits, the choice held fixed:
  *     d[t, j] = scale * dweights[t, j];  if renormalize, with S = sum_i s[t, topk_ids[t, i]]:
- *     d[t, j] = (d[t, j] - sum_i d[t, i] s[t, topk_ids[t, i]] / S) / S  (0 where S is 0)
+ *     d[t, j] = (d[t, j] - sum_i d[t, i] s[t, topk_ids[t, i]] / S) / S  (0 where all have a logit of -inf)
  *     G[t, e] = sum_j [topk_ids[t, j] == e] d[t, j]
  *     dlogits[t, e] = G s (1 - s) (sigmoid), or s[t, e] (G[t, e] - sum_e' G[t, e'] s[t, e']) (softmax)
  *
