@@ -557,9 +557,9 @@ int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64
  *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where all are ruled out).
  *     A score may be as small as it likes for that; without renormalize one below 2^-126 may count as 0.
  *     counts[e] = how many (t, j) of the unmasked tokens chose e
- * The choice is that of scores in 64 bits (whose own roundings, 2^-50 of a score, decide where two lie that near).  The
- * bias takes part in the choice alone; a program balances its experts by moving it after each step, up where counts lie
- * below their mean and down where above.
+ * The choice is that of scores in 64 bits (whose own roundings, 2^-50 of a score and 2^-53 of its sum with the bias, decide
+ * where two lie that near).  The bias takes part in the choice alone; a program balances its experts by moving it after
+ * each step, up where counts lie below their mean and down where above.
  *
  *   logits      [T, E] (dtype), row stride ldl elements (ldl >= E).  -inf rules an expert out whatever its bias, and so
  *               does a bias of -inf: it adds nothing to its group's score (a group of nothing else scores -inf) and is

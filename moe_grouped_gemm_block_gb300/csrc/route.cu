@@ -530,7 +530,8 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
   }
   if (!(low <= high)) low = high = 0.0f;
   const float range = 1.0f + (high - low);
-  all_exact |= !(range < INFINITY);
+  // Biases this far above their range round scores off in the 64-bit sums, and the grid, which starts at the lowest, does not.
+  all_exact |= !(fmaxf(fabsf(low), fabsf(high)) <= range * 0x1p20f) || !(range < INFINITY);
   const float K = __fdiv_rn(kGrid - 64.0f, range);
   const float near = a.softmax ? 48.0f : 12.0f;  // steps (see above)
   float place[VPL];

@@ -1,5 +1,5 @@
 """The router and its gradient where fp32 scores run out: chosen scores whose sum is below fp32's normal range, or below all
-of it."""
+of it, and biases so large that a score hardly shows in its sum with them."""
 
 import numpy as np
 import pytest
@@ -97,3 +97,20 @@ def test_gradient_of_scores_below_the_normal_range(E, k, score, dtype):
         np.add.at(lost, (np.arange(T)[:, None], at), gone * inside * (a + (p * a).sum(1, keepdims=True)))
         _within(got, want, (200 + 4 * d.max(1, keepdims=True)) * U * size + lost, dtype, f"dlogits at {offset}")
         assert not got[~mask].any()
+
+
+@pytest.mark.parametrize("E,groups,kept,k", [(64, 1, 1, 6), (64, 8, 4, 6), (256, 8, 4, 8), (512, 1, 1, 8), (700, 1, 1, 8),
+                                             (1024, 8, 2, 4)])
+@pytest.mark.parametrize("score,dtype", [("softmax", "f32"), ("sigmoid", "f32"), ("sigmoid", "bf16")])
+@pytest.mark.parametrize("level", [1e6, 1e9, 1e10, 1e12, -1e12, 1e16, 3e37])
+def test_choice_with_biases_far_above_the_scores(E, groups, kept, k, score, dtype, level):
+    """The choice is that of the sums in 64 bits, in every row alike: what they round off tells no experts apart."""
+    for T in (40, 900):
+        l = _draw((T, E), dtype, 1)
+        kw = dict(score=score, groups=groups, topk_groups=kept)
+        steps = torch.randint(0, 3, (E,), generator=_gen(2), device="cuda")
+        for bias in (torch.full((E,), level, device="cuda"), level * (1 + steps * 2.0 ** -22)):
+            ids, _, counts = g.moe_route(l, k, bias=bias, **kw)
+            check_status()
+            rids, _, rc = ot.moe_route(_np(l), k, _np(bias), **kw)
+            assert np.array_equal(ids.cpu().numpy(), rids) and np.array_equal(counts.cpu().numpy(), rc)
