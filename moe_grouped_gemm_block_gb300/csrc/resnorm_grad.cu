@@ -8,6 +8,7 @@
 // registers; 39 instructions a value, of which the unpacking of bf16, twice, is a fifth):
 //   8192 x 7168, fp32 stream and bf16 block: 192 us (81% of the copy rate);  16384 x 4096: 195 (91%)
 //   4096 x 7168 bf16: 87 (60%);  16384 x 2048 bf16: 84 (71%);  16384 x 64 bf16: 12 (16%)
+//   a plain residual, whose f is not read: 8192 x 7168, fp32 stream 158 us (88%), bf16 128 (68%)
 // What was slower: fp32 rows in eights a thread (a warp's accesses then touch twice the sectors: 252 us), both means from
 // one sum over the row (sum q k = sum p dh k + r (sum p g k - s sum p e k): as fast with fp32, 103 instead of 90 us with
 // bf16), bulk copies with a barrier a stage (equal, and 222 instead of 194 us at 16384 x 4096), a second stage for three of
@@ -159,18 +160,19 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
       for (int j = 0; j < H; ++j) sum = __ffma2_rn(dx[v][j], k[j], sum);
     }
     if (!a.df) continue;
-    float by = 1.0f, c = 0.0f;
     if (a.norm_f) {
-      by = rf;
-      c = -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * rf;
+      const float c = -res_sum<LPR>(sum.x + sum.y, red, phase, a.ranks) * a.inv_n * rf;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float2 k[H];
+        rk[v].get(k);
+#pragma unroll
+        for (int j = 0; j < H; ++j) dx[v][j] = __fmul2_rn(both(rf), __ffma2_rn(k[j], both(c), dx[v][j]));
+      }
     }
+    if (real) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float2 k[H];
-      rk[v].get(k);
-#pragma unroll
-      for (int j = 0; j < H; ++j) dx[v][j] = __fmul2_rn(both(by), __ffma2_rn(k[j], both(c), dx[v][j]));
-      if (real) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
+      for (int v = 0; v < V; ++v) col.store(static_cast<TB*>(a.df) + m * a.lddf, v, dx[v]);
     }
   }
   if (!LPR && a.ranks > 1) cluster_sync();  // (nobody leaves while it may still be written to)
@@ -408,13 +410,14 @@ extern "C" int fp8g_residual_rms_norm_backward(
   const int st = current_device(&dev);
   if (st != FP8G_OK) return st;
   ResArgs a{};
-  a.x = dy ? h : nullptr, a.ldx = ldh, a.f = f, a.ldf = ldf, a.w = weight, a.post = post_weight, a.gate = gate;
+  // (f is read where something depends on it: df of a plain residual does not, whatever f holds)
+  a.x = dy ? h : nullptr, a.ldx = ldh, a.f = post_norm || dgate ? f : nullptr, a.ldf = ldf, a.w = weight, a.post = post_weight, a.gate = gate;
   a.dy = dy, a.lddy = lddy, a.dh = dh, a.lddh = lddh, a.dx = dx, a.lddx = lddx, a.df = df, a.lddf = lddf;
   a.rstd = const_cast<float*>(rstd), a.rstd_f = const_cast<float*>(rstd_f);
   a.parts = sums ? static_cast<float*>(workspace) : nullptr;
   a.M = M, a.N = static_cast<int32_t>(N), a.w_kind = w_dtype, a.norm_f = post_norm;
   a.scale = scale, a.inv_n = 1.0f / static_cast<float>(N);
-  const ResMode mode = res_mode(M, N, {{a.x, ldh}, {f, ldf}, {dy, lddy}, {dh, lddh}, {dx, lddx}, {df, lddf}});
+  const ResMode mode = res_mode(M, N, {{a.x, ldh}, {a.f, ldf}, {dy, lddy}, {dh, lddh}, {dx, lddx}, {df, lddf}});
   const ResJoin j{a.parts, post_weight, gate, dweight, dgate, dpost, 0, a.N, w_dtype, scale};
   using B = __nv_bfloat16;
   auto pick = [mode](auto aligned, auto shifted, auto single) {
