@@ -16,6 +16,7 @@
 // Device times, forward, and the share of the copy rate (fp32 / bf16: the stream's and the block's type):
 //   8192 x 7168 fp32 / bf16: 124 us (84%);  4096 x 7168 bf16: 41 (84%);  16384 x 512 bf16: 12 (83%)
 //   4096 x 12288 fp32 / bf16 with both norms: 201 (44%), without the one after the block 134 (66%)
+//   4160 x 7168 fp32 / fp32: 84 us (84%);  58560 x 512 fp32 / bf16: 60 (88%)
 //   off the grid: 1021 x 4099 fp32 15.5 (64%), 4096 x 4099 bf16 36 (55%);  64 x 7168: 4.4
 
 #include "resnorm.cuh"
@@ -178,14 +179,10 @@ __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const
 
 template <typename TS, typename TB, int MODE>
 int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
-  constexpr ResMode kMode = static_cast<ResMode>(MODE);
-  const ResForm f = res_form(a.N, kMode, false);
-  const int per_sm = f.lpr < 0 ? 1 : f.ranks > 1 ? 2 : std::max(2, 1024 / f.threads);
-  const int64_t values = static_cast<int64_t>(f.threads) * f.v * 8;
-  const ResShared sh = res_shared(f.threads * res_thread_bytes(kMode, f.v, sizeof(TS)),
-                                  a.f ? f.threads * res_thread_bytes(kMode, f.v, sizeof(TB)) : 0, values * 4 * (a.f ? 2 : 1),
-                                  per_sm);
-  if (f.lpr < 0 || sh.stages == 0) {
+  const ResPlan plan = res_forward_plan(a.N, static_cast<ResMode>(MODE), sizeof(TS), sizeof(TB), a.f != nullptr);
+  const ResForm& f = plan.form;
+  const ResShared& sh = plan.shared;
+  if (sh.stages == 0) {
     residual_norm_any_kernel<TS, TB><<<static_cast<unsigned>(std::min<int64_t>(a.M, 2 * dev->sm_count)), kResMaxThreads, 0,
                                        s>>>(a);
     return cudaGetLastError() == cudaSuccess ? FP8G_OK : FP8G_ERR_CUDA;
@@ -198,7 +195,7 @@ int res_forward(ResArgs a, const DeviceInfo* dev, cudaStream_t s) {
                           : residual_norm_kernel<TS, TB, 0, 2, MODE>;
   a.stages = sh.stages, a.stages_f = sh.stages_f, a.ranks = f.ranks;
   // (row blocks: a multiple of 8 where a CTA takes more than one, see Columns)
-  const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count * per_sm / f.ranks / 8 * 8);
+  const int64_t blocks = std::min<int64_t>((a.M + f.rows - 1) / f.rows, int64_t{1} * dev->sm_count * plan.per_sm / f.ranks / 8 * 8);
   return res_launch(go, blocks * f.ranks, f.threads, sh.bytes, f.ranks, a, s);
 }
 

@@ -375,6 +375,27 @@ inline ResShared res_shared(int64_t stage, int64_t f, int64_t fixed, int per_sm)
       if (n * stage + k * f <= left) return {n * stage + k * f + fixed, n, k};
   return {0, 0, 0};
 }
+// bytes of a thread's places of a matrix whose values have `size` bytes
+inline int64_t res_thread_bytes(ResMode mode, int v, int64_t size) { return mode == kSingle && size == 2 ? 0 : v * 8 * size; }
+
+// The forward call's form, shared memory and resident CTAs an SM: as many as keep 1024 threads there (two at least, and two
+// clusters' CTAs), and fewer where their places do not fit beside one another.  stages 0: rows are taken as of any length.
+struct ResPlan {
+  ResForm form;
+  ResShared shared;
+  int per_sm;
+};
+inline ResPlan res_forward_plan(int64_t N, ResMode mode, int64_t stream_size, int64_t block_size, bool has_f) {
+  ResPlan p{res_form(N, mode, false), {0, 0, 0}, 1};
+  const ResForm& f = p.form;
+  if (f.lpr < 0) return p;
+  const int64_t stage = f.threads * res_thread_bytes(mode, f.v, stream_size);
+  const int64_t stage_f = has_f ? f.threads * res_thread_bytes(mode, f.v, block_size) : 0;
+  const int64_t weights = int64_t{4} * f.threads * f.v * 8 * (has_f ? 2 : 1);
+  p.per_sm = f.ranks > 1 ? 2 : std::max(2, 1024 / f.threads);
+  while ((p.shared = res_shared(stage, stage_f, weights, p.per_sm)).stages == 0 && p.per_sm > 1) --p.per_sm;
+  return p;
+}
 
 // Columns a row may have: the kernels count them, and twice as many, in 32 bits.
 constexpr int64_t kResMaxCols = int64_t{1} << 29;
@@ -390,9 +411,6 @@ inline ResMode res_mode(int64_t M, int64_t N, std::initializer_list<std::pair<co
   }
   return N % 8 == 0 && (M == 1 || ld % 8 == 0) ? kAligned : kShifted;
 }
-// bytes of a thread's places of a matrix whose values have `size` bytes
-inline int64_t res_thread_bytes(ResMode mode, int v, int64_t size) { return mode == kSingle && size == 2 ? 0 : v * 8 * size; }
-
 // Launches a kernel, as clusters where a row has several CTAs.
 template <typename Kernel>
 int res_launch(Kernel kernel, int64_t ctas, int threads, int64_t smem, int ranks, const ResArgs& a, cudaStream_t s) {
