@@ -27,14 +27,14 @@ namespace {
 template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
 __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE != kSingle ? 2 : 1)
     residual_norm_kernel(const ResArgs a) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   extern __shared__ __align__(16) unsigned char shared[];
   constexpr int G = res_unit<TS, TB>(), V = EIGHTS * 8 / G, H = G / 2;
   using Cols = Columns<MODE, G, V>;
   using SX = Source<TS, MODE, G, V>;
   using SF = Source<TB, MODE, G, V>;
   FP8G_RES_ROWS(a.ldx)
-  if (!LPR) res_sum_init<1>(red, a.ranks);
+  if (!LPR) res_sum_init(red, a.ranks);
   // the weights of y, and of f: post gate scale; the stages
   float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * EIGHTS * blockDim.x;
   col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR || MODE != kSi
 // Rows of any length: a CTA a row, which reads it again for each step.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_any_kernel(const ResArgs a) {
-  __shared__ float red[2][1][32];
-  res_sum_init<1>(red, 1);
+  __shared__ float red[2][32];
+  res_sum_init(red, 1);
   int phase = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const TS* x = static_cast<const TS*>(a.x) + m * a.ldx;

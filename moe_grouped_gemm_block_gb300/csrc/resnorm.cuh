@@ -31,10 +31,6 @@ struct ResArgs {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// 16 bytes, of which `bytes` are read and the others are zero.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All of this thread's groups of copies but the last `later` (at most 4) have landed.
 __device__ __forceinline__ void cp_async_wait(int later) {
@@ -268,71 +264,34 @@ struct Source {
   }
 };
 
-// Sums of NV values over the threads of a row: LPR lanes of a warp, or (LPR 0) the CTAs of a cluster, of which each warp
-// tells all its sums; entries of `red` past the warps are 0.
-template <int LPR, int NV>
-__device__ __forceinline__ void res_sum(float (&v)[NV], float (*red)[NV][32], int& phase, int ranks) {
+// The sum over the threads of a row: LPR lanes of a warp, or (LPR 0) the CTAs of a cluster, of which each warp tells all its
+// sum; entries of `red` past the warps are 0.
+template <int LPR>
+__device__ __forceinline__ float res_sum(float v, float (*red)[32], int& phase, int ranks) {
   if constexpr (LPR > 0) {
 #pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    for (int off = LPR / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
   } else {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if constexpr (NV == 4) {  // each half of the lanes goes on with two of the sums, each quarter with one
-      const bool half = lane & 16, quarter = lane & 8;
-      const float a = (half ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, half ? v[0] : v[2], 16);
-      const float b = (half ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, half ? v[1] : v[3], 16);
-      v[0] = (quarter ? b : a) + __shfl_xor_sync(0xffffffffu, quarter ? a : b, 8);
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
-    }
-    float(*r)[32] = red[phase & 1];
+    v = warp_sum(v);
+    float* r = red[phase & 1];
     ++phase;
-    const int each = 32 / NV;  // lane i each has sum i
-    const float mine = NV == 4 ? v[0] : v[lane / each % NV];
     if (ranks == 1) {
-      if (lane % each == 0) r[lane / each][warp] = mine;
+      if (lane == 0) r[warp] = v;
       __syncthreads();
     } else {
-      if (lane % each < ranks) {
-        const uint32_t to = mapa_shared(smem_u32(&r[lane / each][static_cast<int>(cluster_ctarank()) * (32 / ranks) + warp]), lane % each);
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(mine) : "memory");
+      if (lane < ranks) {
+        const uint32_t to = mapa_shared(smem_u32(r + static_cast<int>(cluster_ctarank()) * (32 / ranks) + warp), lane);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
       }
       cluster_sync();
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {  // (32 entries, a lane each: the same order in every warp)
-      const float s = r[i][lane];
-      v[i] = s;
-    }
-    if constexpr (NV == 4) {
-      const bool half = lane & 16, quarter = lane & 8;
-      const float a = (half ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, half ? v[0] : v[2], 16);
-      const float b = (half ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, half ? v[1] : v[3], 16);
-      float c = (quarter ? b : a) + __shfl_xor_sync(0xffffffffu, quarter ? a : b, 8);
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, c, 8 * i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = warp_sum(v[i]);
-    }
+    return warp_sum(r[lane]);  // (32 entries, a lane each: the same order in every warp)
   }
 }
-template <int LPR>
-__device__ __forceinline__ float res_sum(float v, float (*red)[1][32], int& phase, int ranks) {
-  float one[1] = {v};
-  res_sum<LPR, 1>(one, red, phase, ranks);
-  return one[0];
-}
-template <int NV>
-__device__ __forceinline__ void res_sum_init(float (*red)[NV][32], int ranks) {
-  for (int i = threadIdx.x; i < 64 * NV; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+__device__ __forceinline__ void res_sum_init(float (*red)[32], int ranks) {
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i >> 5][i & 31] = 0.0f;
   __syncthreads();
   if (ranks > 1) cluster_sync();
 }

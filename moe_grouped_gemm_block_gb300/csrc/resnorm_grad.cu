@@ -21,7 +21,7 @@ namespace {
 
 template <typename TS, typename TB, int LPR, int EIGHTS, int MODE>
 __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) residual_norm_backward_kernel(const ResArgs a) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   extern __shared__ __align__(16) unsigned char shared[];  // (in the end, LPR: [2][N] sums)
   constexpr int G = res_unit<TS, TB>(), V = EIGHTS * 8 / G, H = G / 2;
   using Cols = Columns<MODE, G, V>;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
   using SB = Source<TB, MODE, G, V>;
   griddep_launch_dependents();
   FP8G_RES_ROWS(a.lddx)
-  if (!LPR) res_sum_init<1>(red, a.ranks);
+  if (!LPR) res_sum_init(red, a.ranks);
   // the weights of dy, and of dx: post gate scale; zeros for a matrix that is not there; the stages
   float4 *w_at = reinterpret_cast<float4*>(shared), *f_at = w_at + 2 * EIGHTS * blockDim.x;
   col.keep_weights(w_at, a.w, nullptr, a.w_kind, 1.0f);
@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(LPR ? 256 : kResMaxThreads, LPR ? 2 : 1) resid
 // workspace.
 template <typename TS, typename TB>
 __global__ void __launch_bounds__(kResMaxThreads) residual_norm_backward_any_kernel(const ResArgs a) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   griddep_launch_dependents();
-  res_sum_init<1>(red, 1);
+  res_sum_init(red, 1);
   int phase = 0;
   float* out = a.parts ? a.parts + static_cast<int64_t>(blockIdx.x) * 2 * a.N : nullptr;
   if (out)
