@@ -60,7 +60,8 @@ struct AdamTable {
   uint32_t end[CAP];  // chunks of the tensors up to and with this one
   int32_t n;
 };
-constexpr int kAdamCap = 384;  // tensors a launch; tables of 64 and 160 are there for their size
+constexpr int kAdamCap = 384;  // tensors a launch
+constexpr int kAdamFew = 64;   // of a smaller table: 1 tensor 4.1 instead of 5.0 us, 64 8.0 instead of 8.7 (one of 160: 0.1 to 0.3)
 static_assert(sizeof(AdamTable<kAdamCap>) <= 32000, "kernel arguments hold 32764 bytes");
 
 struct AdamHyper {
@@ -555,7 +556,7 @@ extern "C" int fp8g_adamw(const fp8g_adamw_tensor* tensors, int32_t n, int32_t s
   if (cudaGetLastError() != cudaSuccess) return FP8G_ERR_CUDA;
   const AdamHyper h{static_cast<float>(beta1), static_cast<float>(1.0 - beta1), static_cast<float>(beta2),
                     static_cast<float>(1.0 - beta2), static_cast<float>(eps)};
-  auto go = state_bits == 32 ? (n <= 64 ? adamw_launch<64, 32> : n <= 160 ? adamw_launch<160, 32> : adamw_launch<kAdamCap, 32>)
-                             : (n <= 64 ? adamw_launch<64, 8> : n <= 160 ? adamw_launch<160, 8> : adamw_launch<kAdamCap, 8>);
+  auto go = state_bits == 32 ? (n <= kAdamFew ? adamw_launch<kAdamFew, 32> : adamw_launch<kAdamCap, 32>)
+                             : (n <= kAdamFew ? adamw_launch<kAdamFew, 8> : adamw_launch<kAdamCap, 8>);
   return go(tensors, n, h, out, dev, s);
 }
