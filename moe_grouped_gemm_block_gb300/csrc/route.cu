@@ -23,7 +23,10 @@ constexpr int kRouteMaxExperts = 2048;
 constexpr int kRouteMaxTopk = 32;
 constexpr int kRouteMaxGroups = 32;
 constexpr int kRouteWarps = 4;
-constexpr int kRouteFewTopk = 16;  // of a row whose contenders are looked for (with 32 picks they are too many: 1000 instead of 740 us)
+// Picks of a row whose contenders are looked for, with scores and where the logits decide alone.  4096 x 1024, us, all in 64 bits
+// and contenders first: 17 picks 333 and 56, 24 336 and 118, 28 338 and 243, 32 340 and 370 (contenders are too many then);
+// by the logits 17 58 and 42, 24 70 and 49, 28 76 and 84.
+constexpr int kRouteFewTopk = 28, kRouteFewLogits = 24;
 
 struct RouteArgs {
   const void* logits;
@@ -333,7 +336,7 @@ template <typename TL>
 __device__ __noinline__ bool route_few(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
   const ExactRow<TL> r(a, t);
   const int lane = threadIdx.x & 31;
-  if ((a.softmax && a.bias) || a.topk > kRouteFewTopk) return false;
+  if ((a.softmax && a.bias) || a.topk > (r.scored() ? kRouteFewTopk : kRouteFewLogits)) return false;
   const bool done = route_contenders<TL>(r, key, pick);
   __syncwarp();
   if (!done) return false;
@@ -383,8 +386,8 @@ __device__ __forceinline__ void put_row(const RouteArgs& a, int64_t t, int id, f
   }
 }
 
-// The general form: a warp a row.  4096 rows of 1024, 8 picks: 53 us with a bias, 67 in groups too (with all scores in 64 bits,
-// as a softmax with a bias and more than 16 picks have them, 330 to 480; 37 without a bias and groups).
+// The general form: a warp a row.  4096 rows of 1024, 8 picks: 53 us with a bias, 71 in groups too (with all scores in 64 bits,
+// as a softmax with a bias and more than 28 picks have them, 340 to 480; 37 without a bias and groups).
 template <typename TL>
 __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ __align__(16) uint64_t choice[];
