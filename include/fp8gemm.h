@@ -709,7 +709,8 @@ typedef struct {
  * states; they are then taken to one of the two codes next to them: for value i of its tensor with
  * y = |x| * (448 * (1 / amax)) between the codes a <= y < b, up where (y - a) / (b - a) + u >= 1 with
  * u = floor(((i * 0xC13FA9A9 + t * 0x91E10DA5 + z) mod 2^32) / 2^12) / 2^20, z = 0 (m) or 2^31 (the root), which is right
- * on the average of the steps; a root > 0 becomes at least the lowest code.
+ * on the average of the steps; a root > 0 becomes at least the lowest code.  The root is the rounded one but for about one
+ * value in 2^20, whose neighbour it is.
  *
  *   tensors   HOST array, read during the call only; the addresses travel as kernel arguments, so a captured graph keeps
  *             them.  Empty tensors (numel 0) may hold nulls.  No written tensor overlaps another one of the list.
