@@ -345,16 +345,19 @@ __device__ __noinline__ bool route_few(const RouteArgs& a, int64_t t, uint64_t* 
   return true;
 }
 
-// A row by one warp.
+// A row by one warp, whose softmax's sum is formed as `parts` warps form it: a row's bits are the same wherever it is decided.
 template <typename TL>
-__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int& pick, float& weight) {
+__device__ __noinline__ void route_row(const RouteArgs& a, int64_t t, uint64_t* key, int parts, int& pick, float& weight) {
   const ExactRow<TL> r(a, t);
   const int lane = threadIdx.x & 31;
   double inv = 1.0;
   if (a.softmax && r.scored()) {
     double s = 0.0;
-    for (int e = lane; e < a.E; e += 32) s += r.exponential(e);
-    s = warp_sum(s);
+    for (int p = 0; p < parts; ++p) {
+      double part = 0.0;
+      for (int e = p * 32 + lane; e < a.E; e += parts * 32) part += r.exponential(e);
+      s += warp_sum(part);
+    }
     inv = s == 0.0 ? 0.0 : 1.0 / s;
   }
   if (r.scored())
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += gridDim.x * kRouteWarps) {
     int id;
     float w;
-    if (!route_few<TL>(a, t, choice + warp * a.E, id, w)) route_row<TL>(a, t, choice + warp * a.E, id, w);
+    if (!route_few<TL>(a, t, choice + warp * a.E, id, w)) route_row<TL>(a, t, choice + warp * a.E, 1, id, w);
     put_row<TL>(a, t, id, w, a.counts);
   }
 }
@@ -781,7 +784,7 @@ __global__ void __launch_bounds__(32 * kRouteFastWarps, 1) moe_route_kernel(cons
       }
       int id;
       float w;
-      route_row<TL>(a, at, choice, id, w);
+      route_row<TL>(a, at, choice, RowShares(E, warps, warp).parts, id, w);
       put_row<TL>(a, at, id, w, cnt);
     }
     __syncwarp();
