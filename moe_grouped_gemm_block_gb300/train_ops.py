@@ -184,6 +184,8 @@ def residual_rms_norm(x, f=None, weight=None, gate=None, scale: float = 1.0, pos
     """x [M,N], f [M,N] or None -> (h [M,N] of x's type, y [M,N] of f's type (without f: out_dtype, or x's), rstd f32 [M],
     rstd_f f32 [M]).  Without f h is x; without post_norm rstd_f is None."""
     dev, shape = x.device, x.shape
+    if len(shape) != 2:
+        _refuse("x: 2-D, rows contiguous")
     block = out_dtype or x.dtype
     h, ptr_h, rstd_f = x, None, None
     if f is not None:
@@ -241,7 +243,7 @@ def residual_rms_norm_backward(dy, dh, h, f, rstd, rstd_f=None, weight=None, gat
                                post_norm: bool = False, post_weight=None, weight_grads: bool = True):
     """-> (dx of h's type, df of f's type or None, dweight, dgate, dpost f32 [N]); the last three are None for weights that
     there are none of, or without weight_grads.  dh may be None (nothing else uses h)."""
-    if h is None:
+    if h is None or h.dim() != 2:
         _refuse("h: as residual_rms_norm returned it")
     dev, N = h.device, h.shape[-1]
 
@@ -331,7 +333,8 @@ def swiglu_quantize_1x128(gu, ld_sa: int | None = None, keep: bool = False):
 
 def swiglu(gu):
     """bf16 [M,2F] -> h bf16 [M,F], not quantised."""
-    h = _empty((gu.shape[0], _gate_up(gu)), dtype=_BF16, device=gu.device)
+    F = _gate_up(gu)
+    h = _empty((gu.shape[0], F), dtype=_BF16, device=gu.device)
     fp8_swiglu_quantize_1x128(gu, h=h)
     return h
 
@@ -354,8 +357,9 @@ def fp8g_swiglu_backward(dh, gu, dgu, h=None) -> None:
 
 def swiglu_backward(dh, gu, keep: bool = True):
     """-> (dgu bf16 [M,2F], h bf16 [M,F] with keep, else None: what the second product's weight gradient needs)."""
+    F = _gate_up(gu)
     dgu = _empty(gu.shape, dtype=_BF16, device=gu.device)
-    h = _empty((gu.shape[0], gu.shape[1] // 2), dtype=_BF16, device=gu.device) if keep else None
+    h = _empty((gu.shape[0], F), dtype=_BF16, device=gu.device) if keep else None
     fp8g_swiglu_backward(dh, gu, dgu, h)
     return dgu, h
 
