@@ -16,9 +16,9 @@
 // steps and a call is repeatable.  And a root that is not 0 keeps the lowest code where it would round to 0: it is then
 // too large, which makes a step too small, never too large.  A block whose largest is below 2^-60 becomes 0.
 //
-// Bound by memory with states in 32 bits, by that and some 60 instructions a value in 8.  117M values, device times and the
-// share of the copy rate: 32 bits, fp32 with bf16 gradients 466 to 484 us (93 to 96%); 8 bits with masters 319 (87%),
-// without 259 (67%).  1M values: 9.5 and 11 us, of which the step's launch before is 2.
+// Bound by memory with states in 32 bits and in 8 with masters; without them by that and some 60 instructions a value.  117M
+// values in one tensor, device times and the share of the copy rate: 32 bits, fp32 with bf16 gradients 477 us (94%); 8 bits
+// with masters 321 (87%), without 260 (67%).  1M values: 9.5 and 11 us, of which the step's launch before is 2.
 #include <algorithm>
 #include <cmath>
 #include <cuda_fp16.h>
@@ -265,7 +265,8 @@ __device__ __forceinline__ void put_codes(uint8_t* p, float* scale, const Places
 
 // A thread's part of whole blocks with 8-bit states, copied ahead into places of its own in its warp's (warps are at tensors
 // of other types, whose places have other sizes): a block's arithmetic is long, and
-// so few bytes of it are on their way at once that the loads' latency would show (117M values with masters: 335 us).
+// so few bytes of it are on their way at once that the loads' latency would show (117M values with masters: 335 us in place
+// of 321).
 constexpr int kAdamStages = 2;
 constexpr int kAdamPlaces = 2 * 16 + 2 * 16 + 4 * 4 + 2 * 4;  // bytes of a thread and stage, at most
 template <int BYTES>

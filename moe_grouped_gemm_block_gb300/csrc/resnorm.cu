@@ -17,7 +17,9 @@
 //   8192 x 7168 fp32 / bf16: 124 us (84%);  4096 x 7168 bf16: 41 (84%);  16384 x 512 bf16: 12 (83%)
 //   4096 x 12288 fp32 / bf16 with both norms: 201 (44%), without the one after the block 134 (66%)
 //   4160 x 7168 fp32 / fp32: 84 us (84%);  58560 x 512 fp32 / bf16: 60 (88%)
-//   off the grid: 1021 x 4099 fp32 15.5 (64%), 4096 x 4099 bf16 36 (55%);  64 x 7168: 4.4
+//   off the grid alike: 1021 x 4099 fp32 with both norms 15.5 (64%), 4096 x 4099 bf16 28 (71%), with both norms 36 (54%)
+//   on grids of their own: 4096 x 4096 with both norms, bf16 102 (19%), fp32 71 (56%);  64 x 7168: 4.4
+//   read again for each step: 1024 x 20000 bf16 with both norms 189 (13%)
 
 #include "resnorm.cuh"
 

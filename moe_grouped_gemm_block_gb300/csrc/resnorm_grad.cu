@@ -8,6 +8,8 @@
 // registers; 39 instructions a value, of which the unpacking of bf16, twice, is a fifth):
 //   8192 x 7168, fp32 stream and bf16 block: 192 us (81% of the copy rate);  16384 x 4096: 195 (91%)
 //   4096 x 7168 bf16: 87 (60%);  16384 x 2048 bf16: 84 (71%);  16384 x 64 bf16: 12 (16%)
+//   with both norms: 4096 x 12288 bf16 203 (44%), fp32 stream 241 (55%);  4096 x 4099 bf16 92 (32%), fp32 118 (50%);  4096 x
+//   4096 on grids of their own bf16 119 (25%), fp32 126 (47%);  1024 x 20000 bf16 632 (6%)
 //   a plain residual, whose f is not read: 8192 x 7168, fp32 stream 158 us (88%), bf16 128 (68%)
 // What was slower: fp32 rows in eights a thread (a warp's accesses then touch twice the sectors: 252 us), both means from
 // one sum over the row (sum q k = sum p dh k + r (sum p g k - s sum p e k): as fast with fp32, 103 instead of 90 us with
@@ -316,9 +318,11 @@ __global__ void __launch_bounds__(32 * kJoinSlices) residual_norm_join_kernel(co
 // CTAs that are resident on an SM: 512 threads of 128 registers.
 int res_grad_per_sm(const ResForm& f) { return f.lpr > 0 ? 2 : f.lpr < 0 ? 1 : std::min(4, std::max(1, 512 / f.threads)); }
 // Blocks of rows, and partial sums, of a call: rows stay with their CTAs for the column sums, so no more than are resident
-// (and, where a block takes several rows, a multiple of 8 of them, see Columns).
+// (and, where a block takes several rows, a multiple of 8 of them, see Columns) on the 152 SMs of this GPU: the workspace's
+// size, which they are, is asked for without a device.
+constexpr int64_t kResGradSms = 152;
 int64_t res_grad_blocks(const ResForm& f, int64_t M) {
-  return std::min<int64_t>((M + f.rows - 1) / f.rows, 152 * res_grad_per_sm(f) / f.ranks / 8 * 8);
+  return std::min<int64_t>((M + f.rows - 1) / f.rows, kResGradSms * res_grad_per_sm(f) / f.ranks / 8 * 8);
 }
 
 template <typename TS, typename TB, int MODE>

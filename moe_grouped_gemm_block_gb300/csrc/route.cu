@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_any_kernel(const _
 // Rows with a logit that is NaN or +inf, with fewer experts left than are to be chosen, or with a group that has a single
 // one left, go there too.  65536 x 256 normal logits: one row in 1000.
 //
-// Bound by its instructions (some 600 of a warp a row of 256 in groups, 430 of bf16 without them; 70 to 84% of the issue
-// slots are taken) and by what the rows in 64 bits add at the end (8 us).  65536 x 256, 8 picks: bf16 in 8 groups 56 us,
+// Bound by its instructions (some 600 of a warp a row of 256 in groups, 430 of bf16 without them; 67 to 70% and 84% of the
+// issue slots are taken) and by what the rows in 64 bits add at the end (8 us).  65536 x 256, 8 picks: bf16 in 8 groups 56 us,
 // without groups 48, without a bias either 29; softmax in groups 77; 64 rows 5.5; 4096 rows 18.
 constexpr int kRouteFastWarps = 32;
 constexpr int kRouteCluster = 8;
