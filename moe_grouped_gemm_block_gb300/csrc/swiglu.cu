@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kGluThreads, kGluPerSm) swiglu_kernel(const Gl
     } else {
       s = __fdiv_rn(top, 448.0f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = s == 0.0f ? 0.0f : __fdiv_rn(h[j], s);
+      for (int j = 0; j < 8; ++j) y[j] = s != 0.0f ? __fdiv_rn(h[j], s) : h[j] == h[j] ? 0.0f : h[j];  // (what is no number stays)
     }
     uint16_t c[4];
 #pragma unroll

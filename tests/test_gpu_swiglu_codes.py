@@ -82,6 +82,18 @@ def test_a_block_with_a_product_beyond_fp32():
     assert torch.equal(mq, q) and torch.equal(ms, s[:, :3])
 
 
+def test_blocks_of_zeros_and_of_what_is_no_number():
+    """A block of zeros, of either sign, has the codes 0x00; one of NaN alone keeps them."""
+    gu = torch.full((4, 256), -0.0, dtype=torch.bfloat16, device="cuda")
+    gu[1, :128] = -1.0  # h = -0
+    gu[2, :128], gu[2, 128:] = 2.0, float("nan")
+    gu[3, :128], gu[3, 200] = 2.0, float("nan")
+    q, s, _ = g.swiglu_quantize_1x128(gu)
+    check_status()
+    assert not q[:2].any() and s[0, :4].tolist() == [0.0] * 4
+    assert (q[2] & 0x7F == 0x7F).all() and int((q[3] & 0x7F == 0x7F).sum()) == 1 and int(q[3, 72]) & 0x7F == 0x7F
+
+
 def test_the_gates_own_error_does_not_grow_with_them():
     """The scale of a block of equal products is their fp32 value over 448.  The exponential is off by 2 units in the last
     place (4 u) and the 1.5 u that the next term of e^(g c) has at g = -87; its product, 1 + exp, two products and the scale
