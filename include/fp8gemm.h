@@ -554,8 +554,8 @@ int fp8g_clip_grad_norm(const void* const* grads, void* const* outs, const int64
  *     one, where it has one).  The topk_groups best groups stay, ties to the lower group.
  *     topk_ids[t] = the topk largest c among their experts, in descending order, ties to the lower index.  Without a bias
  *     experts are ordered by their logits, as their scores are.
- *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where all are ruled out).
- *     A score may be as small as it likes for that; without renormalize one below 2^-126 may count as 0.
+ *     topk_weights[t, j] = scale * s[t, topk_ids[t, j]], divided by the sum of s over j if renormalize (0 where all are
+ *     ruled out): however small the scores are for that; without renormalize one below 2^-126 may count as 0
  *     counts[e] = how many (t, j) of the unmasked tokens chose e
  * The choice is that of scores in 64 bits (whose own roundings, 2^-50 of a score and 2^-53 of its sum with the bias, decide
  * where two lie that near).  The bias takes part in the choice alone; a program balances its experts by moving it after
